@@ -217,7 +217,7 @@ def _keep(s):
 
     k["B"] = B
     if c["op"] == "norm":
-        k["shape"] = B.norm_shape(T, K, eps=EPS, dtype=c["dtype"], grad_dtype=c["grad"])
+        k["shape"] = B.norm_shape(T, K, eps=EPS, dtype=c["dtype"], grad_dtype=c["grad"] if c["way"] == "bwd" else None)
         if c["way"] == "fwd":
             k["out"] = {"y": new(T, K)}
             if c["save"]:
@@ -228,7 +228,8 @@ def _keep(s):
             if c["bias"]:
                 k["out"]["db"] = new(K, dtype=gt)
         return k
-    k["shape"] = B.dense_shape(T, K, N, dtype=c["dtype"], act=c["act"], grad_dtype=c["grad"])
+    k["shape"] = B.dense_shape(T, K, N, dtype=c["dtype"], act=c["act"],
+                               grad_dtype=c["grad"] if c["way"] == "bwd" else None)
     call = {("gated", "fwd"): B.MOE_CALL_GATED_FORWARD, ("gated", "bwd"): B.MOE_CALL_GATED_BACKWARD,
             ("linear", "fwd"): B.MOE_CALL_LINEAR_FORWARD, ("linear", "bwd"): B.MOE_CALL_LINEAR_BACKWARD}
     k["ws"] = new(B.dense_workspace_bytes(k["shape"], call[c["op"], c["way"]]), dtype=torch.uint8)
