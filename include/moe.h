@@ -86,7 +86,7 @@
 extern "C" {
 #endif
 
-#define MOE_ABI_VERSION 5
+#define MOE_ABI_VERSION 6
 
 #ifndef MOE_API
 #define MOE_API __attribute__((visibility("default")))
@@ -415,6 +415,142 @@ MOE_API moe_status moe_layer_forward(const moe_layer_weights* w, const void* x, 
 MOE_API moe_status moe_layer_forward_noalloc(const moe_layer_weights* w, const void* x, float* logits,
                                              void* out, int out_dtype, const moe_shape* s,
                                              moe_layer_aux* aux, void** stage_events, void* stream);
+
+/*
+ * Dense operators around the layer
+ * --------------------------------
+ * The dense half of a transformer block next to the routed layer, forward and backward:
+ * the layer norm whose rows the router and the experts read, the gated feed-forward
+ * product of a dense layer (or of a shared expert trained on its own), and the linear
+ * projection that closes it:
+ *
+ *   n = layer_norm(x),  h = act(n w1^T) * (n w3^T),  y = h w2^T + bias + x
+ *
+ * The conventions at the top of this file hold, with these differences:
+ * - every size from 1 up is taken, whole tiles or not: T, K and N need no multiple of
+ *   anything (rows of a width that is no multiple of 8 are copied to padded rows in the
+ *   workspace first, or read element by element, which costs their bytes again);
+ * - T = 0 is a call on no rows: a forward pass does nothing, a backward pass writes zero
+ *   weight and bias gradients;
+ * - outputs may not overlap inputs, other outputs or the workspace, except that y of
+ *   moe_linear_forward may be its residual (MOE_ERR_INVALID_ARG);
+ * - results do not depend on what else runs: sums are formed in a fixed order, with no
+ *   atomics, in fp32.
+ *
+ * Limits: T <= 2^30, K and N (H) <= 2^22, no tensor above 2^35 elements (MOE_ERR_UNSUPPORTED).
+ */
+typedef enum moe_act {
+  MOE_ACT_NONE = 0,      /* a */
+  MOE_ACT_RELU = 1,      /* max(a, 0), slope 0 at 0 */
+  MOE_ACT_SILU = 2,      /* a / (1 + e^-a) */
+  MOE_ACT_GELU = 3,      /* a (1 + erf(a / sqrt 2)) / 2 */
+  MOE_ACT_GELU_TANH = 4  /* a (1 + tanh(sqrt(2/pi) (a + 0.044715 a^3))) / 2 */
+} moe_act;
+
+typedef struct moe_dense_shape {
+  int64_t T;           /* rows (tokens) */
+  int64_t K;           /* input width */
+  int64_t N;           /* output width */
+  int32_t dtype;       /* moe_dtype of activations, weights and outputs */
+  int32_t act;         /* moe_act */
+  int32_t grad_dtype;  /* moe_dtype of weight and bias gradients: dtype, or MOE_F32.  With
+                        * MOE_F32 in a bf16 layer the gradient before the activation enters
+                        * the weight gradients' products as three bf16 terms that hold its
+                        * fp32 value exactly, which triples those products' work wherever
+                        * there is an activation to go through; with MOE_BF16 as its rounded
+                        * value. */
+  int32_t reserved;    /* 0 */
+} moe_dense_shape;
+
+typedef struct moe_norm_shape {
+  int64_t T;           /* rows */
+  int64_t H;           /* row width */
+  float eps;           /* added to the variance; finite, >= 0 */
+  int32_t dtype;       /* moe_dtype of rows, weight and bias */
+  int32_t grad_dtype;  /* moe_dtype of dw and db: dtype, or MOE_F32 */
+  int32_t reserved;    /* 0 */
+} moe_norm_shape;
+
+typedef enum moe_dense_call {
+  MOE_CALL_GATED_FORWARD = 0,
+  MOE_CALL_GATED_BACKWARD = 1,
+  MOE_CALL_LINEAR_FORWARD = 2,
+  MOE_CALL_LINEAR_BACKWARD = 3
+} moe_dense_call;
+
+/* Workspace bytes of a dense call / of moe_layer_norm_backward on shape s (0 if the shape is
+ * invalid, and where the call needs none). Host only. */
+MOE_API size_t moe_dense_workspace_bytes(const moe_dense_shape* s, int call);
+MOE_API size_t moe_norm_workspace_bytes(const moe_norm_shape* s);
+
+/*
+ * Layer norm: m = mean(x[t]), v = mean((x[t] - m)^2), r = 1 / sqrt(v + eps),
+ * y[t] = (x[t] - m) r w + b, statistics in fp32 from the centred row.
+ *
+ * x, y [T x H] (dtype), w [H] and b [H] (dtype; b nullable).
+ * mean, rstd [T] fp32 out, each nullable (a backward pass needs both).
+ */
+MOE_API moe_status moe_layer_norm_forward(const void* x, const void* w, const void* b, void* y,
+                                          float* mean, float* rstd, const moe_norm_shape* s,
+                                          void* stream);
+
+/*
+ * With n = (x - mean) rstd and e = dy w:
+ *   dx = rstd (e - mean(e) - n mean(e n)),  dw = sum_t dy n,  db = sum_t dy.
+ * dx [T x H] (dtype), dw and db [H] (grad_dtype) out, each nullable (not all of them).
+ * x is what the forward pass read, mean and rstd what it wrote.
+ */
+MOE_API moe_status moe_layer_norm_backward(const void* dy, const void* x, const void* w,
+                                           const float* mean, const float* rstd, void* dx, void* dw,
+                                           void* db, const moe_norm_shape* s, void* ws,
+                                           size_t ws_bytes, void* stream);
+
+/*
+ * Gated feed-forward product: g = x w1^T, u = x w3^T, h = act(g) u from the fp32 sums,
+ * rounded once.
+ *
+ * x [T x K], w1 and w3 [N x K] (dtype).  h [T x N] (dtype) out.
+ * g, u [T x N] (dtype) out, both or neither: the rounded projections, which a backward
+ * pass reads.
+ */
+MOE_API moe_status moe_gated_forward(const void* x, const void* w1, const void* w3, void* h, void* g,
+                                     void* u, const moe_dense_shape* s, void* ws, size_t ws_bytes,
+                                     void* stream);
+
+/*
+ * With dg = dh u act'(g) and du = dh act(g) (fp32, rounded to dtype as operands of the
+ * products; see grad_dtype):
+ *   dx = dg w1 + du w3,  dw1 = dg^T x,  dw3 = du^T x.
+ * dx [T x K] (dtype) out, dw1 and dw3 [N x K] (grad_dtype) out, dx nullable, dw1 and dw3
+ * both or neither.
+ */
+MOE_API moe_status moe_gated_backward(const void* dh, const void* x, const void* w1, const void* w3,
+                                      const void* g, const void* u, void* dx, void* dw1, void* dw3,
+                                      const moe_dense_shape* s, void* ws, size_t ws_bytes,
+                                      void* stream);
+
+/*
+ * Linear projection: z = x w^T + bias, y = act(z) + residual from the fp32 sums, rounded once.
+ *
+ * x [T x K], w [N x K], bias [N] (nullable), residual [T x N] (nullable, may be y) (dtype).
+ * y [T x N] (dtype) out.  z [T x N] (dtype) out, nullable: the rounded pre-activation, which
+ * a backward pass through an activation reads.
+ */
+MOE_API moe_status moe_linear_forward(const void* x, const void* w, const void* bias,
+                                      const void* residual, void* y, void* z, const moe_dense_shape* s,
+                                      void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * With dz = dy act'(z) (dy itself for MOE_ACT_NONE; fp32, rounded to dtype as an operand of
+ * the products; see grad_dtype):
+ *   dx = dz w,  dw = dz^T x,  dbias = sum_t dz (unrounded dz);  the residual's gradient is dy.
+ * z [T x N] as the forward pass wrote it; NULL for MOE_ACT_NONE.
+ * dx [T x K] (dtype), dw [N x K] and dbias [N] (grad_dtype) out, each nullable (not all of
+ * them); x may be NULL without dw, w without dx.
+ */
+MOE_API moe_status moe_linear_backward(const void* dy, const void* x, const void* w, const void* z,
+                                       void* dx, void* dw, void* dbias, const moe_dense_shape* s,
+                                       void* ws, size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

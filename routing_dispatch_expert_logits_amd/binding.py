@@ -21,8 +21,13 @@ MOE_COMBINE_FUSED, MOE_COMBINE_UNFUSED = 0, 1
 MOE_DISPATCH_DTYPE, MOE_DISPATCH_MXFP8 = 0, 1
 MOE_NUM_STAGE_EVENTS = 10
 NOALLOC_SCRATCH_BYTES = 64 << 20
-ABI_VERSION = 5
+ABI_VERSION = 6
 MOE_PLAN_GATE, MOE_PLAN_X_PERM = 1, 2
+MOE_ACT_NONE, MOE_ACT_RELU, MOE_ACT_SILU, MOE_ACT_GELU, MOE_ACT_GELU_TANH = range(5)
+(MOE_CALL_GATED_FORWARD, MOE_CALL_GATED_BACKWARD, MOE_CALL_LINEAR_FORWARD,
+ MOE_CALL_LINEAR_BACKWARD) = range(4)
+ACT_NAMES = {"none": MOE_ACT_NONE, "relu": MOE_ACT_RELU, "silu": MOE_ACT_SILU, "gelu": MOE_ACT_GELU,
+             "gelu_tanh": MOE_ACT_GELU_TANH}
 
 STAGE_NAMES = ["latent_down", "gate", "route", "permute", "gemm_gate_up", "gemm_down",
                "shared_expert", "combine", "latent_up"]
@@ -54,6 +59,16 @@ class MoeLayerAux(ctypes.Structure):
     _fields_ = [("topk_ids", _vp), ("topk_w", _vp), ("counts", _vp), ("offsets", _vp),
                 ("row_token", _vp), ("token_row", _vp), ("x_perm", _vp), ("y_perm", _vp),
                 ("z", _vp), ("out_latent", _vp), ("x_perm_scale", _vp)]
+
+
+class MoeDenseShape(ctypes.Structure):
+    _fields_ = [("T", _i64), ("K", _i64), ("N", _i64), ("dtype", _i32), ("act", _i32),
+                ("grad_dtype", _i32), ("reserved", _i32)]
+
+
+class MoeNormShape(ctypes.Structure):
+    _fields_ = [("T", _i64), ("H", _i64), ("eps", ctypes.c_float), ("dtype", _i32),
+                ("grad_dtype", _i32), ("reserved", _i32)]
 
 
 class MoePlan(ctypes.Structure):
@@ -93,8 +108,20 @@ def _load() -> ctypes.CDLL:
                                       P(MoeShape), P(MoeLayerAux), P(_vp), _vp, sz, _vp]
     lib.moe_layer_forward_noalloc.argtypes = [P(MoeLayerWeights), _vp, _vp, _vp, ctypes.c_int,
                                               P(MoeShape), P(MoeLayerAux), P(_vp), _vp]
+    lib.moe_dense_workspace_bytes.restype = sz
+    lib.moe_dense_workspace_bytes.argtypes = [P(MoeDenseShape), ctypes.c_int]
+    lib.moe_norm_workspace_bytes.restype = sz
+    lib.moe_norm_workspace_bytes.argtypes = [P(MoeNormShape)]
+    lib.moe_layer_norm_forward.argtypes = [_vp] * 6 + [P(MoeNormShape), _vp]
+    lib.moe_layer_norm_backward.argtypes = [_vp] * 8 + [P(MoeNormShape), _vp, sz, _vp]
+    lib.moe_gated_forward.argtypes = [_vp] * 6 + [P(MoeDenseShape), _vp, sz, _vp]
+    lib.moe_gated_backward.argtypes = [_vp] * 9 + [P(MoeDenseShape), _vp, sz, _vp]
+    lib.moe_linear_forward.argtypes = [_vp] * 6 + [P(MoeDenseShape), _vp, sz, _vp]
+    lib.moe_linear_backward.argtypes = [_vp] * 7 + [P(MoeDenseShape), _vp, sz, _vp]
     for f in ("moe_route_topk", "moe_dispatch_permute", "moe_grouped_ffn", "moe_combine",
-              "moe_layer_forward", "moe_quantize_mxfp8", "moe_layer_forward_noalloc"):
+              "moe_layer_forward", "moe_quantize_mxfp8", "moe_layer_forward_noalloc",
+              "moe_layer_norm_forward", "moe_layer_norm_backward", "moe_gated_forward",
+              "moe_gated_backward", "moe_linear_forward", "moe_linear_backward"):
         getattr(lib, f).restype = ctypes.c_int
     v = lib.moe_abi_version()
     if v != ABI_VERSION:
@@ -223,3 +250,136 @@ def layer_forward_noalloc(weights: dict, x, logits, out, out_dtype: int, s: MoeS
     _check("moe_layer_forward_noalloc", lib.moe_layer_forward_noalloc(
         ctypes.byref(w), _p(x), _p(logits), _p(out), int(out_dtype), ctypes.byref(s), ctypes.byref(a), ev,
         _stream(stream)))
+
+
+# ---- dense operators around the layer (layer norm, gated product, linear projection)
+#
+# These take whole tensors of the shape's sizes.  Beyond what the C call checks they refuse a
+# tensor of another size, type or device, and one that is not dense row-major (its strides
+# cannot be passed on), as MOE_ERR_INVALID_ARG.  They run on the tensors' device: on `stream`,
+# or on that device's current stream.  bf16 tensors may be torch.bfloat16 or raw bits (int16).
+
+
+def _dtype_code(name: str) -> int:
+    return {"bf16": MOE_BF16, "f32": MOE_F32}[name]
+
+
+def dense_shape(T: int, K: int, N: int, dtype: str = "bf16", act: str = "none",
+                grad_dtype: Optional[str] = None) -> MoeDenseShape:
+    """T rows, K input columns, N output columns; grad_dtype: of weight and bias gradients (default dtype)."""
+    return MoeDenseShape(T, K, N, _dtype_code(dtype), ACT_NAMES[act], _dtype_code(grad_dtype or dtype), 0)
+
+
+def norm_shape(T: int, H: int, eps: float = 1e-5, dtype: str = "bf16",
+               grad_dtype: Optional[str] = None) -> MoeNormShape:
+    return MoeNormShape(T, H, eps, _dtype_code(dtype), _dtype_code(grad_dtype or dtype), 0)
+
+
+def dense_workspace_bytes(s: MoeDenseShape, call: int) -> int:
+    return int(lib.moe_dense_workspace_bytes(ctypes.byref(s), call))
+
+
+def norm_workspace_bytes(s: MoeNormShape) -> int:
+    return int(lib.moe_norm_workspace_bytes(ctypes.byref(s)))
+
+
+class _Args:
+    """Checks one call's tensors and hands out their pointers."""
+
+    def __init__(self, call: str, stream):
+        self.call, self.stream, self.device = call, stream, None
+
+    def _bad(self, name: str, why: str):
+        raise MoeError(f"{self.call} ({name}: {why})", MOE_ERR_INVALID_ARG)
+
+    def __call__(self, name: str, t, shape: tuple, code: int):
+        if t is None:
+            return None
+        if isinstance(t, int):
+            return t
+        import torch
+        if tuple(t.shape) != shape:
+            self._bad(name, f"shape {tuple(t.shape)}, expected {shape}")
+        if not (t.dtype == torch.float32 if code == MOE_F32 else t.dtype in (torch.bfloat16, torch.int16)):
+            self._bad(name, f"type {t.dtype}")
+        return self._ptr(name, t)
+
+    def _ptr(self, name: str, t):
+        if not t.is_cuda:
+            self._bad(name, "not on a GPU")
+        if not t.is_contiguous():
+            self._bad(name, "not dense row-major")
+        if self.device is None:
+            self.device = t.device
+        elif t.device != self.device:
+            self._bad(name, f"on {t.device}, others on {self.device}")
+        return t.data_ptr()
+
+    def ws(self, t):
+        return t if t is None or isinstance(t, int) else self._ptr("ws", t)
+
+    def run(self, fn, *args):
+        import torch
+        if self.device is None or self.device.index == torch.cuda.current_device():
+            _check(self.call, fn(*args, _stream(self.stream)))
+        else:
+            with torch.cuda.device(self.device):
+                _check(self.call, fn(*args, _stream(self.stream)))
+
+
+def layer_norm_forward(x, w, b, y, s: MoeNormShape, mean=None, rstd=None, stream=None):
+    """y = (x - mean(x)) / sqrt(var(x) + eps) w + b per row; mean and rstd [T] fp32 are kept where given."""
+    a = _Args("moe_layer_norm_forward", stream)
+    rows, cols = (s.T, s.H), (s.H,)
+    a.run(lib.moe_layer_norm_forward, a("x", x, rows, s.dtype), a("w", w, cols, s.dtype),
+          a("b", b, cols, s.dtype), a("y", y, rows, s.dtype), a("mean", mean, (s.T,), MOE_F32),
+          a("rstd", rstd, (s.T,), MOE_F32), ctypes.byref(s))
+
+
+def layer_norm_backward(dy, x, w, mean, rstd, dx, dw, db, s: MoeNormShape, ws, stream=None):
+    """Gradients dx (dtype), dw and db (grad_dtype) of layer_norm_forward; each may be None."""
+    a = _Args("moe_layer_norm_backward", stream)
+    rows, cols = (s.T, s.H), (s.H,)
+    a.run(lib.moe_layer_norm_backward, a("dy", dy, rows, s.dtype), a("x", x, rows, s.dtype),
+          a("w", w, cols, s.dtype), a("mean", mean, (s.T,), MOE_F32), a("rstd", rstd, (s.T,), MOE_F32),
+          a("dx", dx, rows, s.dtype), a("dw", dw, cols, s.grad_dtype), a("db", db, cols, s.grad_dtype),
+          ctypes.byref(s), a.ws(ws), _nbytes(ws))
+
+
+def gated_forward(x, w1, w3, h, s: MoeDenseShape, ws, g=None, u=None, stream=None):
+    """h = act(x w1^T) * (x w3^T); g and u (both or neither) receive the two projections."""
+    a = _Args("moe_gated_forward", stream)
+    wide, wt = (s.T, s.N), (s.N, s.K)
+    a.run(lib.moe_gated_forward, a("x", x, (s.T, s.K), s.dtype), a("w1", w1, wt, s.dtype),
+          a("w3", w3, wt, s.dtype), a("h", h, wide, s.dtype), a("g", g, wide, s.dtype),
+          a("u", u, wide, s.dtype), ctypes.byref(s), a.ws(ws), _nbytes(ws))
+
+
+def gated_backward(dh, x, w1, w3, g, u, dx, dw1, dw3, s: MoeDenseShape, ws, stream=None):
+    """Gradients dx (dtype), dw1 and dw3 (grad_dtype) of gated_forward from the g and u it kept."""
+    a = _Args("moe_gated_backward", stream)
+    wide, wt, rows = (s.T, s.N), (s.N, s.K), (s.T, s.K)
+    a.run(lib.moe_gated_backward, a("dh", dh, wide, s.dtype), a("x", x, rows, s.dtype),
+          a("w1", w1, wt, s.dtype), a("w3", w3, wt, s.dtype), a("g", g, wide, s.dtype),
+          a("u", u, wide, s.dtype), a("dx", dx, rows, s.dtype), a("dw1", dw1, wt, s.grad_dtype),
+          a("dw3", dw3, wt, s.grad_dtype), ctypes.byref(s), a.ws(ws), _nbytes(ws))
+
+
+def linear_forward(x, w, bias, residual, y, s: MoeDenseShape, ws, z=None, stream=None):
+    """y = act(x w^T + bias) + residual (residual may be y itself); z receives the pre-activation."""
+    a = _Args("moe_linear_forward", stream)
+    wide = (s.T, s.N)
+    a.run(lib.moe_linear_forward, a("x", x, (s.T, s.K), s.dtype), a("w", w, (s.N, s.K), s.dtype),
+          a("bias", bias, (s.N,), s.dtype), a("residual", residual, wide, s.dtype), a("y", y, wide, s.dtype),
+          a("z", z, wide, s.dtype), ctypes.byref(s), a.ws(ws), _nbytes(ws))
+
+
+def linear_backward(dy, x, w, z, dx, dw, dbias, s: MoeDenseShape, ws, stream=None):
+    """Gradients dx (dtype), dw and dbias (grad_dtype) of linear_forward; z as it kept it (None without
+    an activation).  The residual's gradient is dy."""
+    a = _Args("moe_linear_backward", stream)
+    wide = (s.T, s.N)
+    a.run(lib.moe_linear_backward, a("dy", dy, wide, s.dtype), a("x", x, (s.T, s.K), s.dtype),
+          a("w", w, (s.N, s.K), s.dtype), a("z", z, wide, s.dtype), a("dx", dx, (s.T, s.K), s.dtype),
+          a("dw", dw, (s.N, s.K), s.grad_dtype), a("dbias", dbias, (s.N,), s.grad_dtype), ctypes.byref(s),
+          a.ws(ws), _nbytes(ws))

@@ -1,0 +1,360 @@
+// Host side of the dense operators' C ABI: argument validation, workspace carve-up and the
+// launch sequence of each call.  No call allocates, synchronises or reads device memory.
+#include <cmath>
+
+#include "dense_kernels.h"
+#include "moe.h"
+#include "moe_host.h"
+
+using namespace moe;
+
+namespace {
+
+constexpr int64_t kMaxRows = 1ll << 30, kMaxWidth = 1ll << 22, kMaxElems = 1ll << 35;
+
+struct DenseDims {
+  int T, K, N, act;
+  bool bf16, grad_f32;
+  size_t es, ges;   // element bytes of the layer, of the weight gradients
+};
+
+moe_status check_types(int dtype, int grad_dtype) {
+  if (dtype != MOE_F32 && dtype != MOE_BF16) return MOE_ERR_INVALID_ARG;
+  if (grad_dtype != dtype && grad_dtype != MOE_F32) return MOE_ERR_INVALID_ARG;
+  return MOE_OK;
+}
+
+moe_status check_dense(const moe_dense_shape* s, DenseDims& d) {
+  if (!s || s->T < 0 || s->K < 1 || s->N < 1 || s->reserved != 0) return MOE_ERR_INVALID_ARG;
+  if (s->act < MOE_ACT_NONE || s->act > MOE_ACT_GELU_TANH) return MOE_ERR_INVALID_ARG;
+  if (check_types(s->dtype, s->grad_dtype) != MOE_OK) return MOE_ERR_INVALID_ARG;
+  if (s->T > kMaxRows || s->K > kMaxWidth || s->N > kMaxWidth) return MOE_ERR_UNSUPPORTED;
+  if (s->T * s->K > kMaxElems || s->T * s->N > kMaxElems || s->N * s->K > kMaxElems)
+    return MOE_ERR_UNSUPPORTED;
+  d.T = (int)s->T; d.K = (int)s->K; d.N = (int)s->N; d.act = s->act;
+  d.bf16 = s->dtype == MOE_BF16;
+  d.grad_f32 = s->grad_dtype == MOE_F32;
+  d.es = d.bf16 ? 2 : 4;
+  d.ges = d.grad_f32 ? 4 : 2;
+  return MOE_OK;
+}
+
+struct NormDims {
+  int T, H;
+  bool bf16, grad_f32;
+  size_t es, ges;
+};
+
+moe_status check_norm(const moe_norm_shape* s, NormDims& d) {
+  if (!s || s->T < 0 || s->H < 1 || s->reserved != 0) return MOE_ERR_INVALID_ARG;
+  if (!(s->eps >= 0.f) || std::isinf(s->eps)) return MOE_ERR_INVALID_ARG;
+  if (check_types(s->dtype, s->grad_dtype) != MOE_OK) return MOE_ERR_INVALID_ARG;
+  if (s->T > kMaxRows || s->H > kMaxWidth || s->T * s->H > kMaxElems) return MOE_ERR_UNSUPPORTED;
+  d.T = (int)s->T; d.H = (int)s->H;
+  d.bf16 = s->dtype == MOE_BF16;
+  d.grad_f32 = s->grad_dtype == MOE_F32;
+  d.es = d.bf16 ? 2 : 4;
+  d.ges = d.grad_f32 ? 4 : 2;
+  return MOE_OK;
+}
+
+// The buffers of one call: every one given is 16-byte aligned, and no output overlaps
+// another buffer.
+struct Buffers {
+  struct One { uintptr_t lo, hi; bool out; } v[12];
+  int n = 0;
+  bool ok = true;
+  void add(const void* p, size_t bytes, bool out, bool required) {
+    if (!p) { ok = ok && !required; return; }
+    ok = ok && al16(p);
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+    v[n++] = One{a, a + bytes, out};
+  }
+  void in(const void* p, size_t bytes, bool required = true) { add(p, bytes, false, required); }
+  void out(const void* p, size_t bytes, bool required = true) { add(p, bytes, true, required); }
+  moe_status status() const {
+    if (!ok) return MOE_ERR_INVALID_ARG;
+    for (int a = 0; a < n; ++a)
+      for (int b = a + 1; b < n; ++b)
+        if ((v[a].out || v[b].out) && v[a].lo < v[b].hi && v[b].lo < v[a].hi) return MOE_ERR_INVALID_ARG;
+    return MOE_OK;
+  }
+};
+
+moe_status check_ws(Buffers& b, const void* ws, size_t ws_bytes, size_t need) {
+  if (b.status() != MOE_OK) return MOE_ERR_INVALID_ARG;
+  if (need == 0) return MOE_OK;
+  if (!ws || ws_bytes < need) return MOE_ERR_WORKSPACE;
+  b.out(ws, need);
+  return b.status();
+}
+
+// ---- workspaces
+
+// Backward: the gradient before the activation as operand of the products (three bf16 terms of
+// each value, lo elements apart, where fp32 weight gradients are asked for), and the row
+// blocks' column sums.
+struct GradWs {
+  size_t d0, d1, part, total;
+  int terms;
+  int64_t lo, ld;
+};
+GradWs grad_ws(const DenseDims& d, bool gated) {
+  Carve c; GradWs w;
+  w.ld = d.N;
+  const bool through = gated || d.act != MOE_ACT_NONE;
+  w.terms = d.bf16 && d.grad_f32 ? 3 : 1;
+  w.lo = (int64_t)(align_up((size_t)d.T * w.ld * d.es) / d.es);
+  const size_t bytes = through ? (size_t)w.lo * d.es * w.terms : 0;
+  w.d0 = c.take(bytes);
+  w.d1 = c.take(gated ? bytes : 0);
+  w.part = c.take(gated || d.T == 0 ? 0 : (size_t)grad_row_blocks(d.T, d.N) * d.N * 4);
+  w.total = c.cur;
+  return w;
+}
+
+size_t norm_ws(const NormDims& d) {
+  return d.T == 0 ? 0 : align_up((size_t)norm_row_blocks(d.T, d.H) * 2 * d.H * 4);
+}
+
+DenseJob forward_job(const DenseDims& d, const void* x, const void* w0, const void* w1) {
+  DenseJob j{};
+  j.M = d.T; j.N = d.N; j.K = d.K;
+  j.segs = 1; j.batch = 1;
+  j.pair = w1 != nullptr;
+  j.A[0][0] = x; j.lda = d.K;
+  j.B[0][0] = w0; j.B[1][0] = w1; j.ldb = d.K;
+  return j;
+}
+
+// dx = d0 w0 (+ d1 w1): the contraction runs over N, which is across the weights' rows.
+moe_status input_grad(const DenseDims& d, const void* d0, const void* d1, int64_t ld, const void* w0,
+                      const void* w1, void* dx, hipStream_t st) {
+  DenseJob j{};
+  j.M = d.T; j.N = d.K; j.K = d.N;
+  j.segs = d1 ? 2 : 1; j.batch = 1;
+  j.b_col = true;
+  j.A[0][0] = d0; j.A[0][1] = d1; j.lda = ld;
+  j.B[0][0] = w0; j.B[0][1] = w1; j.ldb = d.K;
+  DenseEpi e{};
+  e.kind = DENSE_STORE;
+  e.out_f32 = !d.bf16;
+  e.out[0] = dx;
+  MOE_HIP(launch_dense(j, e, d.bf16, st));
+  return MOE_OK;
+}
+
+// dw_z = (sum of d_z's terms)^T x: the contraction runs over the tokens, across both operands' rows.
+moe_status weight_grad(const DenseDims& d, const void* d0, const void* d1, int terms, int64_t lo, int64_t ld,
+                       const void* x, void* dw0, void* dw1, hipStream_t st) {
+  DenseJob j{};
+  j.M = d.N; j.N = d.K; j.K = d.T;
+  j.segs = terms; j.batch = d1 ? 2 : 1;
+  j.a_col = j.b_col = true;
+  for (int q = 0; q < terms; ++q) {
+    j.A[0][q] = static_cast<const char*>(d0) + q * lo * d.es;
+    if (d1) j.A[1][q] = static_cast<const char*>(d1) + q * lo * d.es;
+    j.B[0][q] = j.B[1][q] = x;
+  }
+  j.lda = ld;
+  j.ldb = d.K;
+  DenseEpi e{};
+  e.kind = DENSE_STORE;
+  e.out_f32 = d.grad_f32;
+  e.out[0] = dw0; e.out[1] = dw1;
+  MOE_HIP(launch_dense(j, e, d.bf16, st));
+  return MOE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t moe_dense_workspace_bytes(const moe_dense_shape* s, int call) {
+  DenseDims d;
+  if (check_dense(s, d) != MOE_OK) return 0;
+  switch (call) {
+    case MOE_CALL_GATED_BACKWARD: return grad_ws(d, true).total;
+    case MOE_CALL_LINEAR_BACKWARD: return grad_ws(d, false).total;
+    default: return 0;
+  }
+}
+
+size_t moe_norm_workspace_bytes(const moe_norm_shape* s) {
+  NormDims d;
+  return check_norm(s, d) == MOE_OK ? norm_ws(d) : 0;
+}
+
+moe_status moe_layer_norm_forward(const void* x, const void* w, const void* b, void* y, float* mean,
+                                  float* rstd, const moe_norm_shape* s, void* stream) {
+  NormDims d;
+  if (const moe_status st = check_norm(s, d); st != MOE_OK) return st;
+  const size_t rows = (size_t)d.T * d.H * d.es;
+  Buffers bufs;
+  bufs.in(x, rows, d.T > 0);
+  bufs.in(w, d.H * d.es);
+  bufs.in(b, d.H * d.es, false);
+  bufs.out(y, rows, d.T > 0);
+  bufs.out(mean, (size_t)d.T * 4, false);
+  bufs.out(rstd, (size_t)d.T * 4, false);
+  if (bufs.status() != MOE_OK) return MOE_ERR_INVALID_ARG;
+  if (d.T == 0) return MOE_OK;
+  MOE_HIP(launch_norm_forward(x, w, b, y, mean, rstd, d.T, d.H, s->eps, d.bf16, (hipStream_t)stream));
+  return MOE_OK;
+}
+
+moe_status moe_layer_norm_backward(const void* dy, const void* x, const void* w, const float* mean,
+                                   const float* rstd, void* dx, void* dw, void* db,
+                                   const moe_norm_shape* s, void* ws, size_t ws_bytes, void* stream) {
+  NormDims d;
+  if (const moe_status st = check_norm(s, d); st != MOE_OK) return st;
+  const size_t rows = (size_t)d.T * d.H * d.es;
+  Buffers bufs;
+  bufs.in(dy, rows, d.T > 0);
+  bufs.in(x, rows, d.T > 0);
+  bufs.in(w, d.H * d.es);
+  bufs.in(mean, (size_t)d.T * 4, d.T > 0);
+  bufs.in(rstd, (size_t)d.T * 4, d.T > 0);
+  bufs.out(dx, rows, false);
+  bufs.out(dw, d.H * d.ges, false);
+  bufs.out(db, d.H * d.ges, false);
+  if (!dx && !dw && !db) return MOE_ERR_INVALID_ARG;
+  if (const moe_status st = check_ws(bufs, ws, ws_bytes, norm_ws(d)); st != MOE_OK) return st;
+  const hipStream_t st = (hipStream_t)stream;
+  if (d.T == 0) {
+    if (dw) MOE_HIP(launch_fill_zero(dw, d.H * d.ges, st));
+    if (db) MOE_HIP(launch_fill_zero(db, d.H * d.ges, st));
+    return MOE_OK;
+  }
+  float* part = dw || db ? static_cast<float*>(ws) : nullptr;
+  MOE_HIP(launch_norm_backward(dy, x, w, mean, rstd, dx, part, d.T, d.H, d.bf16, st));
+  if (part) MOE_HIP(launch_col_sum(part, norm_row_blocks(d.T, d.H), d.H, 2 * d.H, dw, db, d.grad_f32, st));
+  return MOE_OK;
+}
+
+moe_status moe_gated_forward(const void* x, const void* w1, const void* w3, void* h, void* g, void* u,
+                             const moe_dense_shape* s, void* ws, size_t ws_bytes, void* stream) {
+  DenseDims d;
+  if (const moe_status st = check_dense(s, d); st != MOE_OK) return st;
+  const size_t wide = (size_t)d.T * d.N * d.es, wb = (size_t)d.N * d.K * d.es;
+  Buffers bufs;
+  bufs.in(x, (size_t)d.T * d.K * d.es, d.T > 0);
+  bufs.in(w1, wb);
+  bufs.in(w3, wb);
+  bufs.out(h, wide, d.T > 0);
+  bufs.out(g, wide, false);
+  bufs.out(u, wide, false);
+  if (!g != !u) return MOE_ERR_INVALID_ARG;
+  if (const moe_status st = check_ws(bufs, ws, ws_bytes, 0); st != MOE_OK) return st;
+  if (d.T == 0) return MOE_OK;
+  const DenseJob j = forward_job(d, x, w1, w3);
+  DenseEpi e{};
+  e.kind = DENSE_GATED;
+  e.act = d.act;
+  e.out[0] = h; e.save[0] = g; e.save[1] = u;
+  MOE_HIP(launch_dense(j, e, d.bf16, (hipStream_t)stream));
+  return MOE_OK;
+}
+
+moe_status moe_gated_backward(const void* dh, const void* x, const void* w1, const void* w3, const void* g,
+                              const void* u, void* dx, void* dw1, void* dw3, const moe_dense_shape* s,
+                              void* ws, size_t ws_bytes, void* stream) {
+  DenseDims d;
+  if (const moe_status st = check_dense(s, d); st != MOE_OK) return st;
+  const size_t wide = (size_t)d.T * d.N * d.es, wb = (size_t)d.N * d.K * d.es;
+  const size_t gb = (size_t)d.N * d.K * d.ges, xb = (size_t)d.T * d.K * d.es;
+  Buffers bufs;
+  bufs.in(dh, wide, d.T > 0);
+  bufs.in(x, xb, d.T > 0);
+  bufs.in(w1, wb);
+  bufs.in(w3, wb);
+  bufs.in(g, wide, d.T > 0);
+  bufs.in(u, wide, d.T > 0);
+  bufs.out(dx, xb, false);
+  bufs.out(dw1, gb, false);
+  bufs.out(dw3, gb, false);
+  if (!dw1 != !dw3 || (!dx && !dw1)) return MOE_ERR_INVALID_ARG;
+  const GradWs w = grad_ws(d, true);
+  if (const moe_status st = check_ws(bufs, ws, ws_bytes, w.total); st != MOE_OK) return st;
+  const hipStream_t st = (hipStream_t)stream;
+  if (d.T == 0) {
+    if (dw1) MOE_HIP(launch_fill_zero(dw1, gb, st));
+    if (dw3) MOE_HIP(launch_fill_zero(dw3, gb, st));
+    return MOE_OK;
+  }
+  const int terms = dw1 ? w.terms : 1;
+  void *d0 = at<void>(ws, w.d0), *d1 = at<void>(ws, w.d1);
+  MOE_HIP(launch_act_grad(dh, g, u, d.act, d.bf16, d.T, d.N, d0, d1, terms, w.lo, w.ld, nullptr, st));
+  if (dx)
+    if (const moe_status r = input_grad(d, d0, d1, w.ld, w1, w3, dx, st); r != MOE_OK) return r;
+  return dw1 ? weight_grad(d, d0, d1, terms, w.lo, w.ld, x, dw1, dw3, st) : MOE_OK;
+}
+
+moe_status moe_linear_forward(const void* x, const void* w, const void* bias, const void* residual, void* y,
+                              void* z, const moe_dense_shape* s, void* ws, size_t ws_bytes, void* stream) {
+  DenseDims d;
+  if (const moe_status st = check_dense(s, d); st != MOE_OK) return st;
+  const size_t wide = (size_t)d.T * d.N * d.es;
+  Buffers bufs;
+  bufs.in(x, (size_t)d.T * d.K * d.es, d.T > 0);
+  bufs.in(w, (size_t)d.N * d.K * d.es);
+  bufs.in(bias, d.N * d.es, false);
+  if (residual != y) bufs.in(residual, wide, false);  // y in place of its residual
+  bufs.out(y, wide, d.T > 0);
+  bufs.out(z, wide, false);
+  if (const moe_status st = check_ws(bufs, ws, ws_bytes, 0); st != MOE_OK) return st;
+  if (d.T == 0) return MOE_OK;
+  const DenseJob j = forward_job(d, x, w, nullptr);
+  DenseEpi e{};
+  e.kind = DENSE_LINEAR;
+  e.act = d.act;
+  e.bias = bias; e.residual = residual;
+  e.out[0] = y; e.save[0] = z;
+  MOE_HIP(launch_dense(j, e, d.bf16, (hipStream_t)stream));
+  return MOE_OK;
+}
+
+moe_status moe_linear_backward(const void* dy, const void* x, const void* w, const void* z, void* dx, void* dw,
+                               void* dbias, const moe_dense_shape* s, void* ws, size_t ws_bytes,
+                               void* stream) {
+  DenseDims d;
+  if (const moe_status st = check_dense(s, d); st != MOE_OK) return st;
+  const size_t wide = (size_t)d.T * d.N * d.es, gb = (size_t)d.N * d.K * d.ges, xb = (size_t)d.T * d.K * d.es;
+  const bool through = d.act != MOE_ACT_NONE;
+  Buffers bufs;
+  bufs.in(dy, wide, d.T > 0);
+  bufs.in(x, xb, d.T > 0 && dw);
+  bufs.in(w, (size_t)d.N * d.K * d.es, d.T > 0 && dx);
+  bufs.in(z, wide, d.T > 0 && through);
+  bufs.out(dx, xb, false);
+  bufs.out(dw, gb, false);
+  bufs.out(dbias, d.N * d.ges, false);
+  if ((!dx && !dw && !dbias) || (!through && z)) return MOE_ERR_INVALID_ARG;
+  const GradWs g = grad_ws(d, false);
+  if (const moe_status st = check_ws(bufs, ws, ws_bytes, g.total); st != MOE_OK) return st;
+  const hipStream_t st = (hipStream_t)stream;
+  if (d.T == 0) {
+    if (dw) MOE_HIP(launch_fill_zero(dw, gb, st));
+    if (dbias) MOE_HIP(launch_fill_zero(dbias, d.N * d.ges, st));
+    return MOE_OK;
+  }
+  const void* d0 = dy;
+  int terms = 1;
+  int64_t ld = d.N;
+  const bool operand = through && (dx || dw);
+  if (operand || dbias) {
+    void* o0 = operand ? at<void>(ws, g.d0) : nullptr;
+    if (through && dw) terms = g.terms;
+    float* part = dbias ? at<float>(ws, g.part) : nullptr;
+    MOE_HIP(launch_act_grad(dy, through ? z : nullptr, nullptr, d.act, d.bf16, d.T, d.N, o0, nullptr, terms, g.lo,
+                            g.ld, part, st));
+    if (dbias)
+      MOE_HIP(launch_col_sum(part, grad_row_blocks(d.T, d.N), d.N, d.N, dbias, nullptr, d.grad_f32, st));
+    if (operand) { d0 = o0; ld = g.ld; }
+  }
+  if (dx)
+    if (const moe_status r = input_grad(d, d0, nullptr, ld, w, nullptr, dx, st); r != MOE_OK) return r;
+  return dw ? weight_grad(d, d0, nullptr, terms, g.lo, ld, x, dw, nullptr, st) : MOE_OK;
+}
+
+}  // extern "C"

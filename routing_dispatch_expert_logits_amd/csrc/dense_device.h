@@ -1,0 +1,146 @@
+// Device helpers of the dense operators: activations, their slopes and guarded loads.
+#pragma once
+
+#include "moe.h"
+#include "moe_device.h"
+
+namespace moe {
+
+// e^a through the hardware exp2 (about one fp32 ulp of the argument's scale), or the
+// library's correctly scaled one.
+template <bool FAST>
+__device__ __forceinline__ float exp_of(float a) {
+  if constexpr (FAST) return __builtin_amdgcn_exp2f(a * 1.4426950408889634f);
+  else return expf(a);
+}
+template <bool FAST>
+__device__ __forceinline__ float recip(float a) {
+  if constexpr (FAST) return __builtin_amdgcn_rcpf(a);
+  else return 1.f / a;
+}
+
+// erfc(a) / 2, the normal distribution's mass right of sqrt(2) a.  FAST: Abramowitz and
+// Stegun 7.1.26, erf(x) = 1 - (a1 t + .. + a5 t^5) e^(-x^2) with t = 1 / (1 + p x), within
+// 1.5e-7 for x >= 0, far below a bf16 rounding; 14 operations where the library's takes
+// several times that, and a 256 x 256 tile's epilogue spends about 1000 cycles for each
+// operation per value.
+template <bool FAST>
+__device__ __forceinline__ float half_erfc(float a) {
+  if constexpr (!FAST) {
+    return 0.5f * erfcf(a);
+  } else {
+    const float x = fabsf(a);
+    const float t = recip<true>(1.f + 0.3275911f * x);
+    const float p = t * (0.254829592f + t * (-0.284496736f + t * (1.421413741f + t * (-1.453152027f +
+                    t * 1.061405429f))));
+    const float h = 0.5f * p * exp_of<true>(-x * x);
+    return a >= 0.f ? h : 1.f - h;
+  }
+}
+
+constexpr float kSqrtHalf = 0.70710678118654752f;
+constexpr float kInvSqrt2Pi = 0.39894228040143268f;
+constexpr float kTanhC = 1.5957691216057308f;  // 2 sqrt(2 / pi)
+constexpr float kTanhA = 0.044715f;
+
+// act(a).  ReLU keeps NaN.  The tanh form uses (1 + tanh q) / 2 = 1 / (1 + e^(-2 q)).
+template <bool FAST>
+__device__ __forceinline__ float act_value(float a, int act) {
+  switch (act) {
+    case MOE_ACT_RELU: return a < 0.f ? 0.f : a;
+    case MOE_ACT_SILU: return a * recip<FAST>(1.f + exp_of<FAST>(-a));
+    case MOE_ACT_GELU: return a * half_erfc<FAST>(-a * kSqrtHalf);
+    case MOE_ACT_GELU_TANH:
+      return a * recip<FAST>(1.f + exp_of<FAST>(-kTanhC * (a + kTanhA * a * a * a)));
+    default: return a;
+  }
+}
+
+// act(a) and act'(a).
+template <bool FAST>
+__device__ __forceinline__ float act_value_slope(float a, int act, float* slope) {
+  switch (act) {
+    case MOE_ACT_RELU: *slope = a > 0.f ? 1.f : 0.f; return a < 0.f ? 0.f : a;
+    case MOE_ACT_SILU: {
+      const float s = recip<FAST>(1.f + exp_of<FAST>(-a));
+      *slope = s * (1.f + a * (1.f - s));
+      return a * s;
+    }
+    case MOE_ACT_GELU: {
+      const float p = half_erfc<FAST>(-a * kSqrtHalf);
+      *slope = p + a * kInvSqrt2Pi * exp_of<FAST>(-0.5f * a * a);
+      return a * p;
+    }
+    case MOE_ACT_GELU_TANH: {
+      // e^(-2q) overflows to inf for very negative a: p = 0, and p (1 - p) = 0
+      const float p = recip<FAST>(1.f + exp_of<FAST>(-kTanhC * (a + kTanhA * a * a * a)));
+      *slope = p + a * p * (1.f - p) * kTanhC * (1.f + 3.f * kTanhA * a * a);
+      return a * p;
+    }
+    default: *slope = 1.f; return a;
+  }
+}
+
+// One element of the layer's type as fp32.
+template <typename T>
+__device__ __forceinline__ float load1(const T* p) {
+  if constexpr (sizeof(T) == 2) return bf16_to_f32(*p);
+  else return *p;
+}
+template <typename T>
+__device__ __forceinline__ void store1(T* p, float v) {
+  if constexpr (sizeof(T) == 2) *p = f32_to_bf16(v);
+  else *p = v;
+}
+
+// Eight consecutive elements at any element-aligned address (rows of odd widths).
+struct __attribute__((packed, aligned(2))) Bytes16of2 { uint32_t v[4]; };
+struct __attribute__((packed, aligned(4))) Bytes16of4 { uint32_t v[4]; };
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, float* f) {
+  if constexpr (sizeof(T) == 2) {
+    const Bytes16of2 b = *reinterpret_cast<const Bytes16of2*>(p);
+    unpack_bf16x8(make_uint4(b.v[0], b.v[1], b.v[2], b.v[3]), f);
+  } else {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const Bytes16of4 b = reinterpret_cast<const Bytes16of4*>(p)[h];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) f[4 * h + i] = __uint_as_float(b.v[i]);
+    }
+  }
+}
+template <typename T>
+__device__ __forceinline__ void store8(T* p, const float* f) {
+  if constexpr (sizeof(T) == 2) {
+    Bytes16of2 b;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      b.v[i] = f32_to_bf16(f[2 * i]) | (static_cast<uint32_t>(f32_to_bf16(f[2 * i + 1])) << 16);
+    *reinterpret_cast<Bytes16of2*>(p) = b;
+  } else {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      Bytes16of4 b;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) b.v[i] = __float_as_uint(f[4 * h + i]);
+      reinterpret_cast<Bytes16of4*>(p)[h] = b;
+    }
+  }
+}
+// The first n of eight elements (n may be <= 0 or >= 8); the others read as 0 / stay as they are.
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, int n, float* f) {
+  if (n >= 8) return load8(p, f);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) f[i] = i < n ? load1(p + i) : 0.f;
+}
+template <typename T>
+__device__ __forceinline__ void store8(T* p, int n, const float* f) {
+  if (n >= 8) return store8(p, f);
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (i < n) store1(p + i, f[i]);
+}
+
+}  // namespace moe

@@ -1,0 +1,132 @@
+// Gradients before an activation, column sums and zero fills of the dense backward passes.
+#include "dense_device.h"
+#include "dense_kernels.h"
+
+namespace moe {
+
+constexpr int kGradCols = 256;  // columns per workgroup: 32 lanes of 8
+constexpr int kGradSub = 8;     // rows in flight per workgroup
+
+// Row blocks: enough workgroups for the device, at least 32 rows each so that the partial
+// sums stay a small part of what is read.
+int grad_row_blocks(int T, int N) {
+  const int cb = ceil_div(N, kGradCols);
+  const int want = ceil_div(2048, cb);
+  const int most = ceil_div(T, 32);
+  return want < most ? (want > 0 ? want : 1) : (most > 0 ? most : 1);
+}
+
+// One pass over dh, g (and u): d0 = dh u act'(g), d1 = dh act(g) in fp32, rounded on store.
+// Workgroup (column block, row block); a thread owns 8 columns and every kGradSub-th row of
+// its block; the column sums of d0 go through LDS in row-lane order.
+template <typename T, bool GATED>
+__global__ __launch_bounds__(256) void k_act_grad(const T* __restrict__ dh, const T* __restrict__ g,
+                                                  const T* __restrict__ u, int act, int rows, int N,
+                                                  T* __restrict__ d0, T* __restrict__ d1, int terms, int64_t lo,
+                                                  int64_t ld, float* __restrict__ part) {
+  constexpr bool FAST = sizeof(T) == 2;
+  const int tid = threadIdx.x, cl = tid & 31, sub = tid >> 5;
+  const int c0 = (int)blockIdx.x * kGradCols + cl * 8;
+  const int per = ceil_div(rows, (int)gridDim.y);
+  const int r0 = min(rows, (int)blockIdx.y * per), r1 = min(rows, r0 + per);
+  const int nc = N - c0;                                          // columns of this thread in N
+  const int np = (int)min<int64_t>(8, max<int64_t>(0, ld - c0));  // and in an output row, padding included
+  float sum[8] = {};
+  if (nc > 0) {
+    for (int r = r0 + sub; r < r1; r += kGradSub) {
+      const int64_t in = (int64_t)r * N + c0, out = (int64_t)r * ld + c0;
+      float vdh[8], vg[8], vu[8], v0[8], v1[8];
+      load8(dh + in, nc, vdh);
+      if (g) load8(g + in, nc, vg);
+      if (GATED) load8(u + in, nc, vu);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        float slope = 1.f, a = 0.f;
+        if (g) a = act_value_slope<FAST>(vg[i], act, &slope);
+        v0[i] = i < nc ? vdh[i] * (GATED ? vu[i] * slope : slope) : 0.f;
+        v1[i] = i < nc ? vdh[i] * a : 0.f;
+        sum[i] += v0[i];
+      }
+      if (d0) store8(d0 + out, np, v0);
+      if (GATED) store8(d1 + out, np, v1);
+      if constexpr (sizeof(T) == 2) {
+        for (int q = 1; q < terms; ++q) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v0[i] -= bf16_to_f32(f32_to_bf16(v0[i]));
+          store8(d0 + q * lo + out, np, v0);
+          if (GATED) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v1[i] -= bf16_to_f32(f32_to_bf16(v1[i]));
+            store8(d1 + q * lo + out, np, v1);
+          }
+        }
+      }
+    }
+  }
+  if (part) {
+    __shared__ float s[kGradSub][kGradCols];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s[sub][cl * 8 + i] = sum[i];
+    __syncthreads();
+    const int n = (int)blockIdx.x * kGradCols + tid;
+    if (n < N) {
+      float v = 0.f;
+#pragma unroll
+      for (int q = 0; q < kGradSub; ++q) v += s[q][tid];
+      part[(int64_t)blockIdx.y * N + n] = v;
+    }
+  }
+}
+
+hipError_t launch_act_grad(const void* dh, const void* g, const void* u, int act, bool bf16, int T, int N,
+                           void* d0, void* d1, int terms, int64_t lo, int64_t ld, float* part, hipStream_t st) {
+  const dim3 grid(ceil_div(N, kGradCols), grad_row_blocks(T, N));
+  auto go = [&](auto* t) {
+    using E = std::remove_pointer_t<decltype(t)>;
+    const E *a = static_cast<const E*>(dh), *b = static_cast<const E*>(g), *c = static_cast<const E*>(u);
+    E *p0 = static_cast<E*>(d0), *p1 = static_cast<E*>(d1);
+    if (u) k_act_grad<E, true><<<grid, 256, 0, st>>>(a, b, c, act, T, N, p0, p1, terms, lo, ld, part);
+    else k_act_grad<E, false><<<grid, 256, 0, st>>>(a, b, c, act, T, N, p0, p1, terms, lo, ld, part);
+  };
+  if (bf16) go(static_cast<uint16_t*>(nullptr));
+  else go(static_cast<float*>(nullptr));
+  return hipGetLastError();
+}
+
+// Column n of the partial sums: 4 groups of the P rows in ascending order, then the groups.
+__global__ __launch_bounds__(256) void k_col_sum(const float* __restrict__ part, int P, int N, int64_t stride,
+                                                 void* __restrict__ out0, void* __restrict__ out1, bool out_f32) {
+  __shared__ float s[4][64];
+  void* out = blockIdx.y ? out1 : out0;
+  if (!out) return;
+  const float* src = part + (int64_t)blockIdx.y * N;
+  const int n = (int)blockIdx.x * 64 + (threadIdx.x & 63), q = threadIdx.x >> 6;
+  float v = 0.f;
+  if (n < N)
+    for (int p = q; p < P; p += 4) v += src[p * stride + n];
+  s[q][threadIdx.x & 63] = v;
+  __syncthreads();
+  if (q == 0 && n < N) {
+    v = (s[0][threadIdx.x] + s[1][threadIdx.x]) + (s[2][threadIdx.x] + s[3][threadIdx.x]);
+    if (out_f32) static_cast<float*>(out)[n] = v;
+    else static_cast<uint16_t*>(out)[n] = f32_to_bf16(v);
+  }
+}
+
+hipError_t launch_col_sum(const float* part, int P, int N, int64_t stride, void* out0, void* out1, bool out_f32,
+                          hipStream_t st) {
+  k_col_sum<<<dim3(ceil_div(N, 64), out1 ? 2 : 1), 256, 0, st>>>(part, P, N, stride, out0, out1, out_f32);
+  return hipGetLastError();
+}
+
+__global__ __launch_bounds__(256) void k_fill_zero(uint16_t* p, size_t n) {
+  for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (size_t)gridDim.x * 256) p[i] = 0;
+}
+
+hipError_t launch_fill_zero(void* p, size_t bytes, hipStream_t st) {
+  const size_t n = bytes / 2, want = (n + 255) / 256;
+  k_fill_zero<<<(unsigned)(want < 4096 ? want : 4096), 256, 0, st>>>(static_cast<uint16_t*>(p), n);
+  return hipGetLastError();
+}
+
+}  // namespace moe

@@ -1,0 +1,66 @@
+// Internal launchers of the dense operators' kernels (layer norm, gated product, linear
+// projection and their backward passes; not part of the C ABI).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "moe_device.h"
+
+namespace moe {
+
+// One dense product: for z < batch, C_z[m][n] = sum_{s < segs} sum_{k < K} A_zs(m, k) B_zs(n, k).
+// An operand stored with the contraction index along its rows' length (A(m, k) = A[m * ld + k])
+// is a row operand; one stored the other way (A(m, k) = A[k * ld + m]) is a column operand.
+// With pair, batch is 1 and B[0][0], B[1][0] are the two projections of one output.
+struct DenseJob {
+  int M, N, K;
+  int segs, batch;
+  bool pair;
+  bool a_col, b_col;
+  const void* A[2][3];
+  const void* B[2][3];
+  int64_t lda, ldb;
+};
+
+enum DenseEpiKind {
+  DENSE_STORE = 0,   // out[z] = acc, fp32 or the layer's type
+  DENSE_LINEAR = 1,  // z = acc + bias, out[0] = act(z) + residual
+  DENSE_GATED = 2    // out[0] = act(acc0) * acc1
+};
+struct DenseEpi {
+  int kind, act;
+  bool out_f32;          // DENSE_STORE: fp32 output
+  const void* bias;      // [N], nullable
+  const void* residual;  // [M x N], nullable
+  void* out[2];
+  void* save[2];         // z, or g and u; nullable
+};
+
+// bf16: element type of the operands and of what the epilogue reads and writes.
+hipError_t launch_dense(const DenseJob& j, const DenseEpi& e, bool bf16, hipStream_t st);
+
+// The gradient before an activation, [T x N]:
+//   linear (dh == dy, u == NULL): d0 = dy act'(g);  gated: d0 = dh u act'(g), d1 = dh act(g).
+// d0, d1 (nullable) get them in the layer's type with rows of ld elements.  With terms = 3
+// (bf16) the second and third bf16 terms of each value follow at d + lo and d + 2 lo: the
+// three hold its 24 bits exactly.  part (nullable) receives fp32 column sums of the
+// unrounded d0, one row of N for each of the grad_row_blocks(T, N) row blocks.
+int grad_row_blocks(int T, int N);
+hipError_t launch_act_grad(const void* dh, const void* g, const void* u, int act, bool bf16, int T, int N,
+                           void* d0, void* d1, int terms, int64_t lo, int64_t ld, float* part, hipStream_t st);
+// out0[n] = sum_p part[p * stride + n], out1[n] = sum_p part[p * stride + N + n] for n < N (each
+// nullable), in a fixed order; in fp32 or bf16.
+hipError_t launch_col_sum(const float* part, int P, int N, int64_t stride, void* out0, void* out1, bool out_f32,
+                          hipStream_t st);
+hipError_t launch_fill_zero(void* p, size_t bytes, hipStream_t st);
+
+hipError_t launch_norm_forward(const void* x, const void* w, const void* b, void* y, float* mean, float* rstd,
+                               int T, int H, float eps, bool bf16, hipStream_t st);
+// part: norm_row_blocks(T, H) rows of 2 H fp32 column sums (dy n, then dy).
+int norm_row_blocks(int T, int H);
+hipError_t launch_norm_backward(const void* dy, const void* x, const void* w, const float* mean,
+                                const float* rstd, void* dx, float* part, int T, int H, bool bf16,
+                                hipStream_t st);
+
+}  // namespace moe
