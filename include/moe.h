@@ -437,7 +437,7 @@ MOE_API moe_status moe_layer_forward_noalloc(const moe_layer_weights* w, const v
  * - results do not depend on what else runs: sums are formed in a fixed order, with no
  *   atomics, in fp32.
  *
- * Limits: T <= 2^30, K and N (H) <= 2^22, no tensor above 2^35 elements (MOE_ERR_UNSUPPORTED).
+ * Limits: T <= 2^30, K and N (H) <= 2^21, no tensor above 2^35 elements (MOE_ERR_UNSUPPORTED).
  */
 typedef enum moe_act {
   MOE_ACT_NONE = 0,      /* a */

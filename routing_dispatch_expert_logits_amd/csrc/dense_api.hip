@@ -10,7 +10,7 @@ using namespace moe;
 
 namespace {
 
-constexpr int64_t kMaxRows = 1ll << 30, kMaxWidth = 1ll << 22, kMaxElems = 1ll << 35;
+constexpr int64_t kMaxRows = 1ll << 30, kMaxWidth = 1ll << 21, kMaxElems = 1ll << 35;
 
 struct DenseDims {
   int T, K, N, act;
@@ -91,51 +91,84 @@ moe_status check_ws(Buffers& b, const void* ws, size_t ws_bytes, size_t need) {
 
 // ---- workspaces
 
+// The bf16 kernels read rows whose length is a multiple of 8 elements; operands with other
+// widths are copied to such rows first.
+int64_t padded(const DenseDims& d, int cols) { return d.bf16 ? ((int64_t)cols + 7) / 8 * 8 : cols; }
+
 // Backward: the gradient before the activation as operand of the products (three bf16 terms of
 // each value, lo elements apart, where fp32 weight gradients are asked for), and the row
-// blocks' column sums.
-struct GradWs {
-  size_t d0, d1, part, total;
+// blocks' column sums.  x, w[2]: padded copies (0 bytes where the operand is read in place).
+struct DenseWs {
+  size_t x, w[2], d0, d1, part, total;
   int terms;
-  int64_t lo, ld;
+  int64_t lo, ldk, ldn;
 };
-GradWs grad_ws(const DenseDims& d, bool gated) {
-  Carve c; GradWs w;
-  w.ld = d.N;
-  const bool through = gated || d.act != MOE_ACT_NONE;
-  w.terms = d.bf16 && d.grad_f32 ? 3 : 1;
-  w.lo = (int64_t)(align_up((size_t)d.T * w.ld * d.es) / d.es);
-  const size_t bytes = through ? (size_t)w.lo * d.es * w.terms : 0;
-  w.d0 = c.take(bytes);
-  w.d1 = c.take(gated ? bytes : 0);
-  w.part = c.take(gated || d.T == 0 ? 0 : (size_t)grad_row_blocks(d.T, d.N) * d.N * 4);
+DenseWs dense_ws(const DenseDims& d, bool gated, bool backward) {
+  Carve c; DenseWs w{};
+  w.ldk = padded(d, d.K);
+  w.ldn = padded(d, d.N);
+  const bool pad_k = w.ldk != d.K && d.T > 0;
+  w.x = c.take(pad_k ? (size_t)d.T * w.ldk * d.es : 0);
+  w.w[0] = c.take(pad_k ? (size_t)d.N * w.ldk * d.es : 0);
+  w.w[1] = c.take(pad_k && gated ? (size_t)d.N * w.ldk * d.es : 0);
+  if (backward) {
+    const bool through = gated || d.act != MOE_ACT_NONE;
+    w.terms = through && d.bf16 && d.grad_f32 ? 3 : 1;
+    w.lo = (int64_t)(align_up((size_t)d.T * w.ldn * d.es) / d.es);
+    const size_t bytes = through || w.ldn != d.N ? (size_t)w.lo * d.es * w.terms : 0;
+    w.d0 = c.take(bytes);
+    w.d1 = c.take(gated ? bytes : 0);
+    w.part = c.take(gated || d.T == 0 ? 0 : (size_t)grad_row_blocks(d.T, d.N) * d.N * 4);
+  }
   w.total = c.cur;
   return w;
+}
+
+// An operand's rows of `cols` elements at row length ld: in place, or copied to ws + off.
+moe_status in_rows(const DenseDims& d, const void** p, int64_t rows, int cols, int64_t ld, void* ws, size_t off,
+                   hipStream_t st) {
+  if (!*p || ld == cols) return MOE_OK;
+  MOE_HIP(launch_pad_rows(*p, rows, cols, at<void>(ws, off), ld, st));
+  *p = at<void>(ws, off);
+  return MOE_OK;
 }
 
 size_t norm_ws(const NormDims& d) {
   return d.T == 0 ? 0 : align_up((size_t)norm_row_blocks(d.T, d.H) * 2 * d.H * 4);
 }
 
-DenseJob forward_job(const DenseDims& d, const void* x, const void* w0, const void* w1) {
+#define MOE_TRY(call)                                         \
+  do {                                                        \
+    if (const moe_status r = (call); r != MOE_OK) return r;   \
+  } while (0)
+
+// z = x w0^T (and x w1^T) with epilogue e.
+moe_status forward(const DenseDims& d, const DenseWs& w, const void* x, const void* w0, const void* w1,
+                   const DenseEpi& e, void* ws, hipStream_t st) {
+  MOE_TRY(in_rows(d, &x, d.T, d.K, w.ldk, ws, w.x, st));
+  MOE_TRY(in_rows(d, &w0, d.N, d.K, w.ldk, ws, w.w[0], st));
+  MOE_TRY(in_rows(d, &w1, d.N, d.K, w.ldk, ws, w.w[1], st));
   DenseJob j{};
   j.M = d.T; j.N = d.N; j.K = d.K;
   j.segs = 1; j.batch = 1;
   j.pair = w1 != nullptr;
-  j.A[0][0] = x; j.lda = d.K;
-  j.B[0][0] = w0; j.B[1][0] = w1; j.ldb = d.K;
-  return j;
+  j.A[0][0] = x; j.lda = w.ldk;
+  j.B[0][0] = w0; j.B[1][0] = w1; j.ldb = w.ldk;
+  MOE_HIP(launch_dense(j, e, d.bf16, st));
+  return MOE_OK;
 }
 
 // dx = d0 w0 (+ d1 w1): the contraction runs over N, which is across the weights' rows.
-moe_status input_grad(const DenseDims& d, const void* d0, const void* d1, int64_t ld, const void* w0,
-                      const void* w1, void* dx, hipStream_t st) {
+moe_status input_grad(const DenseDims& d, const DenseWs& w, const void* d0, const void* d1, const void* w0,
+                      const void* w1, void* dx, void* ws, hipStream_t st) {
+  MOE_TRY(in_rows(d, &w0, d.N, d.K, w.ldk, ws, w.w[0], st));
+  MOE_TRY(in_rows(d, &w1, d.N, d.K, w.ldk, ws, w.w[1], st));
   DenseJob j{};
   j.M = d.T; j.N = d.K; j.K = d.N;
   j.segs = d1 ? 2 : 1; j.batch = 1;
   j.b_col = true;
-  j.A[0][0] = d0; j.A[0][1] = d1; j.lda = ld;
-  j.B[0][0] = w0; j.B[0][1] = w1; j.ldb = d.K;
+  j.A[0][0] = d0; j.A[0][1] = d1; j.lda = w.ldn;
+  j.B[0][0] = w0; j.B[0][1] = w1; j.ldb = w.ldk;
   DenseEpi e{};
   e.kind = DENSE_STORE;
   e.out_f32 = !d.bf16;
@@ -145,19 +178,20 @@ moe_status input_grad(const DenseDims& d, const void* d0, const void* d1, int64_
 }
 
 // dw_z = (sum of d_z's terms)^T x: the contraction runs over the tokens, across both operands' rows.
-moe_status weight_grad(const DenseDims& d, const void* d0, const void* d1, int terms, int64_t lo, int64_t ld,
-                       const void* x, void* dw0, void* dw1, hipStream_t st) {
+moe_status weight_grad(const DenseDims& d, const DenseWs& w, const void* d0, const void* d1, int terms,
+                       const void* x, void* dw0, void* dw1, void* ws, hipStream_t st) {
+  MOE_TRY(in_rows(d, &x, d.T, d.K, w.ldk, ws, w.x, st));
   DenseJob j{};
   j.M = d.N; j.N = d.K; j.K = d.T;
   j.segs = terms; j.batch = d1 ? 2 : 1;
   j.a_col = j.b_col = true;
   for (int q = 0; q < terms; ++q) {
-    j.A[0][q] = static_cast<const char*>(d0) + q * lo * d.es;
-    if (d1) j.A[1][q] = static_cast<const char*>(d1) + q * lo * d.es;
+    j.A[0][q] = static_cast<const char*>(d0) + q * w.lo * d.es;
+    if (d1) j.A[1][q] = static_cast<const char*>(d1) + q * w.lo * d.es;
     j.B[0][q] = j.B[1][q] = x;
   }
-  j.lda = ld;
-  j.ldb = d.K;
+  j.lda = w.ldn;
+  j.ldb = w.ldk;
   DenseEpi e{};
   e.kind = DENSE_STORE;
   e.out_f32 = d.grad_f32;
@@ -174,8 +208,10 @@ size_t moe_dense_workspace_bytes(const moe_dense_shape* s, int call) {
   DenseDims d;
   if (check_dense(s, d) != MOE_OK) return 0;
   switch (call) {
-    case MOE_CALL_GATED_BACKWARD: return grad_ws(d, true).total;
-    case MOE_CALL_LINEAR_BACKWARD: return grad_ws(d, false).total;
+    case MOE_CALL_GATED_FORWARD: return dense_ws(d, true, false).total;
+    case MOE_CALL_GATED_BACKWARD: return dense_ws(d, true, true).total;
+    case MOE_CALL_LINEAR_FORWARD: return dense_ws(d, false, false).total;
+    case MOE_CALL_LINEAR_BACKWARD: return dense_ws(d, false, true).total;
     default: return 0;
   }
 }
@@ -188,7 +224,7 @@ size_t moe_norm_workspace_bytes(const moe_norm_shape* s) {
 moe_status moe_layer_norm_forward(const void* x, const void* w, const void* b, void* y, float* mean,
                                   float* rstd, const moe_norm_shape* s, void* stream) {
   NormDims d;
-  if (const moe_status st = check_norm(s, d); st != MOE_OK) return st;
+  MOE_TRY(check_norm(s, d));
   const size_t rows = (size_t)d.T * d.H * d.es;
   Buffers bufs;
   bufs.in(x, rows, d.T > 0);
@@ -207,7 +243,7 @@ moe_status moe_layer_norm_backward(const void* dy, const void* x, const void* w,
                                    const float* rstd, void* dx, void* dw, void* db,
                                    const moe_norm_shape* s, void* ws, size_t ws_bytes, void* stream) {
   NormDims d;
-  if (const moe_status st = check_norm(s, d); st != MOE_OK) return st;
+  MOE_TRY(check_norm(s, d));
   const size_t rows = (size_t)d.T * d.H * d.es;
   Buffers bufs;
   bufs.in(dy, rows, d.T > 0);
@@ -219,7 +255,7 @@ moe_status moe_layer_norm_backward(const void* dy, const void* x, const void* w,
   bufs.out(dw, d.H * d.ges, false);
   bufs.out(db, d.H * d.ges, false);
   if (!dx && !dw && !db) return MOE_ERR_INVALID_ARG;
-  if (const moe_status st = check_ws(bufs, ws, ws_bytes, norm_ws(d)); st != MOE_OK) return st;
+  MOE_TRY(check_ws(bufs, ws, ws_bytes, norm_ws(d)));
   const hipStream_t st = (hipStream_t)stream;
   if (d.T == 0) {
     if (dw) MOE_HIP(launch_fill_zero(dw, d.H * d.ges, st));
@@ -235,7 +271,7 @@ moe_status moe_layer_norm_backward(const void* dy, const void* x, const void* w,
 moe_status moe_gated_forward(const void* x, const void* w1, const void* w3, void* h, void* g, void* u,
                              const moe_dense_shape* s, void* ws, size_t ws_bytes, void* stream) {
   DenseDims d;
-  if (const moe_status st = check_dense(s, d); st != MOE_OK) return st;
+  MOE_TRY(check_dense(s, d));
   const size_t wide = (size_t)d.T * d.N * d.es, wb = (size_t)d.N * d.K * d.es;
   Buffers bufs;
   bufs.in(x, (size_t)d.T * d.K * d.es, d.T > 0);
@@ -245,22 +281,21 @@ moe_status moe_gated_forward(const void* x, const void* w1, const void* w3, void
   bufs.out(g, wide, false);
   bufs.out(u, wide, false);
   if (!g != !u) return MOE_ERR_INVALID_ARG;
-  if (const moe_status st = check_ws(bufs, ws, ws_bytes, 0); st != MOE_OK) return st;
+  const DenseWs w = dense_ws(d, true, false);
+  MOE_TRY(check_ws(bufs, ws, ws_bytes, w.total));
   if (d.T == 0) return MOE_OK;
-  const DenseJob j = forward_job(d, x, w1, w3);
   DenseEpi e{};
   e.kind = DENSE_GATED;
   e.act = d.act;
   e.out[0] = h; e.save[0] = g; e.save[1] = u;
-  MOE_HIP(launch_dense(j, e, d.bf16, (hipStream_t)stream));
-  return MOE_OK;
+  return forward(d, w, x, w1, w3, e, ws, (hipStream_t)stream);
 }
 
 moe_status moe_gated_backward(const void* dh, const void* x, const void* w1, const void* w3, const void* g,
                               const void* u, void* dx, void* dw1, void* dw3, const moe_dense_shape* s,
                               void* ws, size_t ws_bytes, void* stream) {
   DenseDims d;
-  if (const moe_status st = check_dense(s, d); st != MOE_OK) return st;
+  MOE_TRY(check_dense(s, d));
   const size_t wide = (size_t)d.T * d.N * d.es, wb = (size_t)d.N * d.K * d.es;
   const size_t gb = (size_t)d.N * d.K * d.ges, xb = (size_t)d.T * d.K * d.es;
   Buffers bufs;
@@ -274,8 +309,8 @@ moe_status moe_gated_backward(const void* dh, const void* x, const void* w1, con
   bufs.out(dw1, gb, false);
   bufs.out(dw3, gb, false);
   if (!dw1 != !dw3 || (!dx && !dw1)) return MOE_ERR_INVALID_ARG;
-  const GradWs w = grad_ws(d, true);
-  if (const moe_status st = check_ws(bufs, ws, ws_bytes, w.total); st != MOE_OK) return st;
+  const DenseWs w = dense_ws(d, true, true);
+  MOE_TRY(check_ws(bufs, ws, ws_bytes, w.total));
   const hipStream_t st = (hipStream_t)stream;
   if (d.T == 0) {
     if (dw1) MOE_HIP(launch_fill_zero(dw1, gb, st));
@@ -284,16 +319,15 @@ moe_status moe_gated_backward(const void* dh, const void* x, const void* w1, con
   }
   const int terms = dw1 ? w.terms : 1;
   void *d0 = at<void>(ws, w.d0), *d1 = at<void>(ws, w.d1);
-  MOE_HIP(launch_act_grad(dh, g, u, d.act, d.bf16, d.T, d.N, d0, d1, terms, w.lo, w.ld, nullptr, st));
-  if (dx)
-    if (const moe_status r = input_grad(d, d0, d1, w.ld, w1, w3, dx, st); r != MOE_OK) return r;
-  return dw1 ? weight_grad(d, d0, d1, terms, w.lo, w.ld, x, dw1, dw3, st) : MOE_OK;
+  MOE_HIP(launch_act_grad(dh, g, u, d.act, d.bf16, d.T, d.N, d0, d1, terms, w.lo, w.ldn, nullptr, st));
+  if (dx) MOE_TRY(input_grad(d, w, d0, d1, w1, w3, dx, ws, st));
+  return dw1 ? weight_grad(d, w, d0, d1, terms, x, dw1, dw3, ws, st) : MOE_OK;
 }
 
 moe_status moe_linear_forward(const void* x, const void* w, const void* bias, const void* residual, void* y,
                               void* z, const moe_dense_shape* s, void* ws, size_t ws_bytes, void* stream) {
   DenseDims d;
-  if (const moe_status st = check_dense(s, d); st != MOE_OK) return st;
+  MOE_TRY(check_dense(s, d));
   const size_t wide = (size_t)d.T * d.N * d.es;
   Buffers bufs;
   bufs.in(x, (size_t)d.T * d.K * d.es, d.T > 0);
@@ -302,23 +336,22 @@ moe_status moe_linear_forward(const void* x, const void* w, const void* bias, co
   if (residual != y) bufs.in(residual, wide, false);  // y in place of its residual
   bufs.out(y, wide, d.T > 0);
   bufs.out(z, wide, false);
-  if (const moe_status st = check_ws(bufs, ws, ws_bytes, 0); st != MOE_OK) return st;
+  const DenseWs p = dense_ws(d, false, false);
+  MOE_TRY(check_ws(bufs, ws, ws_bytes, p.total));
   if (d.T == 0) return MOE_OK;
-  const DenseJob j = forward_job(d, x, w, nullptr);
   DenseEpi e{};
   e.kind = DENSE_LINEAR;
   e.act = d.act;
   e.bias = bias; e.residual = residual;
   e.out[0] = y; e.save[0] = z;
-  MOE_HIP(launch_dense(j, e, d.bf16, (hipStream_t)stream));
-  return MOE_OK;
+  return forward(d, p, x, w, nullptr, e, ws, (hipStream_t)stream);
 }
 
 moe_status moe_linear_backward(const void* dy, const void* x, const void* w, const void* z, void* dx, void* dw,
                                void* dbias, const moe_dense_shape* s, void* ws, size_t ws_bytes,
                                void* stream) {
   DenseDims d;
-  if (const moe_status st = check_dense(s, d); st != MOE_OK) return st;
+  MOE_TRY(check_dense(s, d));
   const size_t wide = (size_t)d.T * d.N * d.es, gb = (size_t)d.N * d.K * d.ges, xb = (size_t)d.T * d.K * d.es;
   const bool through = d.act != MOE_ACT_NONE;
   Buffers bufs;
@@ -330,31 +363,28 @@ moe_status moe_linear_backward(const void* dy, const void* x, const void* w, con
   bufs.out(dw, gb, false);
   bufs.out(dbias, d.N * d.ges, false);
   if ((!dx && !dw && !dbias) || (!through && z)) return MOE_ERR_INVALID_ARG;
-  const GradWs g = grad_ws(d, false);
-  if (const moe_status st = check_ws(bufs, ws, ws_bytes, g.total); st != MOE_OK) return st;
+  const DenseWs p = dense_ws(d, false, true);
+  MOE_TRY(check_ws(bufs, ws, ws_bytes, p.total));
   const hipStream_t st = (hipStream_t)stream;
   if (d.T == 0) {
     if (dw) MOE_HIP(launch_fill_zero(dw, gb, st));
     if (dbias) MOE_HIP(launch_fill_zero(dbias, d.N * d.ges, st));
     return MOE_OK;
   }
-  const void* d0 = dy;
-  int terms = 1;
-  int64_t ld = d.N;
-  const bool operand = through && (dx || dw);
+  // the operand of the products: dy itself, or dz (or padded rows of dy) in the workspace
+  const bool operand = (through || p.ldn != d.N) && (dx || dw);
+  void* d0 = operand ? at<void>(ws, p.d0) : nullptr;
+  const int terms = dw ? p.terms : 1;
+  float* part = dbias ? at<float>(ws, p.part) : nullptr;
   if (operand || dbias) {
-    void* o0 = operand ? at<void>(ws, g.d0) : nullptr;
-    if (through && dw) terms = g.terms;
-    float* part = dbias ? at<float>(ws, g.part) : nullptr;
-    MOE_HIP(launch_act_grad(dy, through ? z : nullptr, nullptr, d.act, d.bf16, d.T, d.N, o0, nullptr, terms, g.lo,
-                            g.ld, part, st));
+    MOE_HIP(launch_act_grad(dy, through ? z : nullptr, nullptr, d.act, d.bf16, d.T, d.N, d0, nullptr, terms, p.lo,
+                            p.ldn, part, st));
     if (dbias)
       MOE_HIP(launch_col_sum(part, grad_row_blocks(d.T, d.N), d.N, d.N, dbias, nullptr, d.grad_f32, st));
-    if (operand) { d0 = o0; ld = g.ld; }
   }
-  if (dx)
-    if (const moe_status r = input_grad(d, d0, nullptr, ld, w, nullptr, dx, st); r != MOE_OK) return r;
-  return dw ? weight_grad(d, d0, nullptr, terms, g.lo, ld, x, dw, nullptr, st) : MOE_OK;
+  const void* dz = operand ? d0 : dy;
+  if (dx) MOE_TRY(input_grad(d, p, dz, nullptr, w, nullptr, dx, ws, st));
+  return dw ? weight_grad(d, p, dz, nullptr, terms, x, dw, nullptr, ws, st) : MOE_OK;
 }
 
 }  // extern "C"

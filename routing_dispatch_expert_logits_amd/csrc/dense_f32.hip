@@ -1,4 +1,4 @@
-// Dense products of the gated and linear operators and of their backward passes.
+// fp32 dense products of the gated and linear operators and of their backward passes.
 //
 // C(m, n) = sum_k A(m, k) B(n, k) for the three layouts these need: y = x w^T (both operands
 // with k along their rows), dx = d w (the weight with k across its rows) and dw = d^T x (both).
@@ -8,33 +8,31 @@
 namespace moe {
 
 // What the epilogue does with one output value (and the second projection's, for the
-// gated product), from fp32.
-template <typename T>
-__device__ __forceinline__ void dense_out(const DenseEpi& e, int z, int64_t idx, int n, float v0, float v1) {
-  constexpr bool FAST = sizeof(T) == 2;
+// gated product).
+__device__ __forceinline__ void f32_out(const DenseEpi& e, int z, int64_t idx, int n, float v0, float v1) {
+  float* out = static_cast<float*>(e.out[z]);
   if (e.kind == DENSE_STORE) {
-    if (e.out_f32) static_cast<float*>(e.out[z])[idx] = v0;
-    else store1(static_cast<T*>(e.out[z]) + idx, v0);
+    out[idx] = v0;
   } else if (e.kind == DENSE_LINEAR) {
-    const float a = e.bias ? v0 + load1(static_cast<const T*>(e.bias) + n) : v0;
-    if (e.save[0]) store1(static_cast<T*>(e.save[0]) + idx, a);
-    float y = act_value<FAST>(a, e.act);
-    if (e.residual) y += load1(static_cast<const T*>(e.residual) + idx);
-    store1(static_cast<T*>(e.out[0]) + idx, y);
+    const float a = e.bias ? v0 + static_cast<const float*>(e.bias)[n] : v0;
+    if (e.save[0]) static_cast<float*>(e.save[0])[idx] = a;
+    float y = act_value<false>(a, e.act);
+    if (e.residual) y += static_cast<const float*>(e.residual)[idx];
+    out[idx] = y;
   } else {
     if (e.save[0]) {
-      store1(static_cast<T*>(e.save[0]) + idx, v0);
-      store1(static_cast<T*>(e.save[1]) + idx, v1);
+      static_cast<float*>(e.save[0])[idx] = v0;
+      static_cast<float*>(e.save[1])[idx] = v1;
     }
-    store1(static_cast<T*>(e.out[0]) + idx, act_value<FAST>(v0, e.act) * v1);
+    out[idx] = act_value<false>(v0, e.act) * v1;
   }
 }
 
-// Tile 64 x 64, four waves in 2 x 2, K-steps of 16 staged through LDS as fp32 with k across
-// the rows, v_mfma_f32_16x16x4_f32: lane l supplies A[l % 16][l / 16] and B[l / 16][l % 16]
+// Tile 64 x 64, four waves in 2 x 2, K-steps of 16 staged through LDS with k across the
+// rows, v_mfma_f32_16x16x4_f32: lane l supplies A[l % 16][l / 16] and B[l / 16][l % 16]
 // and receives D[4 (l / 16) + i][l % 16].  B's columns take the A side, so a lane holds four
 // neighbouring output columns.
-template <typename T, bool PAIR>
+template <bool PAIR>
 __global__ __launch_bounds__(256) void k_dense_f32(DenseJob j, DenseEpi e) {
   constexpr int BK = 16, LD = 68, NB = PAIR ? 2 : 1;
   __shared__ float sA[BK * LD];
@@ -50,24 +48,24 @@ __global__ __launch_bounds__(256) void k_dense_f32(DenseJob j, DenseEpi e) {
 #pragma unroll
     for (int f = 0; f < 4; ++f) acc[b][f >> 1][f & 1] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  auto fill = [&](float* dst, const T* src, int64_t ld, bool col, int r0, int rows, int k0) {
+  auto fill = [&](float* dst, const float* src, int64_t ld, bool col, int r0, int rows, int k0) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int q = tid + 256 * i;  // of 64 x 16 elements, the stored-along index fastest
       const int r = col ? q & 63 : q >> 4, k = col ? q >> 6 : q & 15;
       float v = 0.f;
       if (r0 + r < rows && k0 + k < j.K)
-        v = load1(src + (col ? (int64_t)(k0 + k) * ld + (r0 + r) : (int64_t)(r0 + r) * ld + (k0 + k)));
+        v = src[col ? (int64_t)(k0 + k) * ld + (r0 + r) : (int64_t)(r0 + r) * ld + (k0 + k)];
       dst[k * LD + r] = v;
     }
   };
   for (int s = 0; s < j.segs; ++s)
     for (int k0 = 0; k0 < j.K; k0 += BK) {
       __syncthreads();
-      fill(sA, static_cast<const T*>(j.A[z][s]), j.lda, j.a_col, m0, j.M, k0);
+      fill(sA, static_cast<const float*>(j.A[z][s]), j.lda, j.a_col, m0, j.M, k0);
 #pragma unroll
       for (int b = 0; b < NB; ++b)
-        fill(sB[b], static_cast<const T*>(PAIR ? j.B[b][0] : j.B[z][s]), j.ldb, j.b_col, n0, j.N, k0);
+        fill(sB[b], static_cast<const float*>(PAIR ? j.B[b][0] : j.B[z][s]), j.ldb, j.b_col, n0, j.N, k0);
       __syncthreads();
 #pragma unroll
       for (int kk = 0; kk < BK; kk += 4) {
@@ -91,19 +89,15 @@ __global__ __launch_bounds__(256) void k_dense_f32(DenseJob j, DenseEpi e) {
       for (int i = 0; i < 4; ++i) {
         const int m = m0 + wm + 16 * fm + (lane & 15), n = n0 + wn + 16 * fn + 4 * (lane >> 4) + i;
         if (m < j.M && n < j.N)
-          dense_out<T>(e, z, (int64_t)m * j.N + n, n, acc[0][fm][fn][i], acc[NB - 1][fm][fn][i]);
+          f32_out(e, z, (int64_t)m * j.N + n, n, acc[0][fm][fn][i], acc[NB - 1][fm][fn][i]);
       }
 }
 
 hipError_t launch_dense(const DenseJob& j, const DenseEpi& e, bool bf16, hipStream_t st) {
+  if (bf16) return launch_dense_mm(j, e, st);
   const dim3 grid((unsigned)((int64_t)ceil_div(j.M, 64) * ceil_div(j.N, 64)), j.batch);
-  if (bf16) {
-    if (j.pair) k_dense_f32<uint16_t, true><<<grid, 256, 0, st>>>(j, e);
-    else k_dense_f32<uint16_t, false><<<grid, 256, 0, st>>>(j, e);
-  } else {
-    if (j.pair) k_dense_f32<float, true><<<grid, 256, 0, st>>>(j, e);
-    else k_dense_f32<float, false><<<grid, 256, 0, st>>>(j, e);
-  }
+  if (j.pair) k_dense_f32<true><<<grid, 256, 0, st>>>(j, e);
+  else k_dense_f32<false><<<grid, 256, 0, st>>>(j, e);
   return hipGetLastError();
 }
 

@@ -119,6 +119,25 @@ hipError_t launch_col_sum(const float* part, int P, int N, int64_t stride, void*
   return hipGetLastError();
 }
 
+// One 16-byte chunk of a padded row per thread.
+__global__ __launch_bounds__(256) void k_pad_rows(const uint16_t* __restrict__ src, int64_t chunks, int cols,
+                                                  uint16_t* __restrict__ dst, int cpr) {
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < chunks; i += (int64_t)gridDim.x * 256) {
+    const int64_t r = i / cpr;
+    const int c = (int)(i - r * cpr) * 8;
+    float v[8];
+    load8(src + r * cols + c, cols - c, v);
+    store8(dst + i * 8, v);
+  }
+}
+
+hipError_t launch_pad_rows(const void* src, int64_t rows, int cols, void* dst, int64_t ld, hipStream_t st) {
+  const int64_t chunks = rows * (ld / 8), want = (chunks + 255) / 256;
+  k_pad_rows<<<(unsigned)(want < 16384 ? want : 16384), 256, 0, st>>>(static_cast<const uint16_t*>(src), chunks, cols,
+                                                                     static_cast<uint16_t*>(dst), (int)(ld / 8));
+  return hipGetLastError();
+}
+
 __global__ __launch_bounds__(256) void k_fill_zero(uint16_t* p, size_t n) {
   for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (size_t)gridDim.x * 256) p[i] = 0;
 }

@@ -37,7 +37,9 @@ struct DenseEpi {
   void* save[2];         // z, or g and u; nullable
 };
 
-// bf16: element type of the operands and of what the epilogue reads and writes.
+// bf16: element type of the operands and of what the epilogue reads and writes; bf16 operands'
+// lda and ldb are multiples of 8, their rows zero from the contraction length on.
+hipError_t launch_dense_mm(const DenseJob& j, const DenseEpi& e, hipStream_t st);
 hipError_t launch_dense(const DenseJob& j, const DenseEpi& e, bool bf16, hipStream_t st);
 
 // The gradient before an activation, [T x N]:
@@ -53,6 +55,8 @@ hipError_t launch_act_grad(const void* dh, const void* g, const void* u, int act
 // nullable), in a fixed order; in fp32 or bf16.
 hipError_t launch_col_sum(const float* part, int P, int N, int64_t stride, void* out0, void* out1, bool out_f32,
                           hipStream_t st);
+// dst[r][0 .. ld) = src[r][0 .. cols) and zeros; bf16, ld a multiple of 8.
+hipError_t launch_pad_rows(const void* src, int64_t rows, int cols, void* dst, int64_t ld, hipStream_t st);
 hipError_t launch_fill_zero(void* p, size_t bytes, hipStream_t st);
 
 hipError_t launch_norm_forward(const void* x, const void* w, const void* b, void* y, float* mean, float* rstd,
