@@ -283,103 +283,112 @@ def norm_workspace_bytes(s: MoeNormShape) -> int:
     return int(lib.moe_norm_workspace_bytes(ctypes.byref(s)))
 
 
-class _Args:
-    """Checks one call's tensors and hands out their pointers."""
+def _refuse(call: str, name: str, t, shape: tuple, code: int, device: int):
+    import torch
+    if tuple(t.shape) != tuple(shape):
+        why = f"shape {tuple(t.shape)}, expected {tuple(shape)}"
+    elif t.dtype not in _tensor_types()[code]:
+        why = f"type {t.dtype}"
+    elif not t.is_cuda:
+        why = "not on a GPU"
+    elif not t.is_contiguous():
+        why = "not dense row-major"
+    else:
+        why = f"on {t.device}, others on {torch.device('cuda', device)}"
+    raise MoeError(f"{call} ({name}: {why})", MOE_ERR_INVALID_ARG)
 
-    def __init__(self, call: str, stream):
-        self.call, self.stream, self.device = call, stream, None
 
-    def _bad(self, name: str, why: str):
-        raise MoeError(f"{self.call} ({name}: {why})", MOE_ERR_INVALID_ARG)
+_types = None
 
-    def __call__(self, name: str, t, shape: tuple, code: int):
+
+def _tensor_types() -> dict:
+    global _types
+    if _types is None:
+        import torch
+        _types = {MOE_F32: (torch.float32,), MOE_BF16: (torch.bfloat16, torch.int16), None: (torch.uint8,)}
+    return _types
+
+
+def _dense_call(call: str, fn, s, tensors: tuple, stream, ws=()):
+    """Check `tensors`, (name, tensor, shape, dtype code) in the call's order, and make the call; ws: () for a
+    call that takes no workspace, else (tensor,)."""
+    import torch
+    types, device, args = _tensor_types(), -1, []
+    for name, t, shape, code in tensors:
+        if t is None or isinstance(t, int):
+            args.append(t)
+            continue
+        d = t.get_device()
+        if t.shape != shape or t.dtype not in types[code] or d < 0 or not t.is_contiguous() or d != device >= 0:
+            _refuse(call, name, t, shape, code, device)
+        device = d
+        args.append(t.data_ptr())
+    args.append(ctypes.byref(s))
+    if ws:
+        t = ws[0]
         if t is None:
-            return None
-        if isinstance(t, int):
-            return t
-        import torch
-        if tuple(t.shape) != shape:
-            self._bad(name, f"shape {tuple(t.shape)}, expected {shape}")
-        if not (t.dtype == torch.float32 if code == MOE_F32 else t.dtype in (torch.bfloat16, torch.int16)):
-            self._bad(name, f"type {t.dtype}")
-        return self._ptr(name, t)
-
-    def _ptr(self, name: str, t):
-        if not t.is_cuda:
-            self._bad(name, "not on a GPU")
-        if not t.is_contiguous():
-            self._bad(name, "not dense row-major")
-        if self.device is None:
-            self.device = t.device
-        elif t.device != self.device:
-            self._bad(name, f"on {t.device}, others on {self.device}")
-        return t.data_ptr()
-
-    def ws(self, t):
-        return t if t is None or isinstance(t, int) else self._ptr("ws", t)
-
-    def run(self, fn, *args):
-        import torch
-        if self.device is None or self.device.index == torch.cuda.current_device():
-            _check(self.call, fn(*args, _stream(self.stream)))
+            args += (None, 0)
         else:
-            with torch.cuda.device(self.device):
-                _check(self.call, fn(*args, _stream(self.stream)))
+            d = t.get_device()
+            if d < 0 or not t.is_contiguous() or d != device >= 0:
+                _refuse(call, "ws", t, t.shape, None, device)
+            args += (t.data_ptr(), t.numel() * t.element_size())
+    if device < 0 or device == torch.cuda.current_device():
+        args.append(_stream(stream) if stream is not None or device < 0 else torch._C._cuda_getCurrentRawStream(device))
+        rc = fn(*args)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, _stream(stream))
+    if rc != MOE_OK:
+        raise MoeError(call, rc)
 
 
 def layer_norm_forward(x, w, b, y, s: MoeNormShape, mean=None, rstd=None, stream=None):
     """y = (x - mean(x)) / sqrt(var(x) + eps) w + b per row; mean and rstd [T] fp32 are kept where given."""
-    a = _Args("moe_layer_norm_forward", stream)
-    rows, cols = (s.T, s.H), (s.H,)
-    a.run(lib.moe_layer_norm_forward, a("x", x, rows, s.dtype), a("w", w, cols, s.dtype),
-          a("b", b, cols, s.dtype), a("y", y, rows, s.dtype), a("mean", mean, (s.T,), MOE_F32),
-          a("rstd", rstd, (s.T,), MOE_F32), ctypes.byref(s))
+    T, H, dt = s.T, s.H, s.dtype
+    _dense_call("moe_layer_norm_forward", lib.moe_layer_norm_forward, s, (
+        ("x", x, (T, H), dt), ("w", w, (H,), dt), ("b", b, (H,), dt), ("y", y, (T, H), dt),
+        ("mean", mean, (T,), MOE_F32), ("rstd", rstd, (T,), MOE_F32)), stream)
 
 
 def layer_norm_backward(dy, x, w, mean, rstd, dx, dw, db, s: MoeNormShape, ws, stream=None):
     """Gradients dx (dtype), dw and db (grad_dtype) of layer_norm_forward; each may be None."""
-    a = _Args("moe_layer_norm_backward", stream)
-    rows, cols = (s.T, s.H), (s.H,)
-    a.run(lib.moe_layer_norm_backward, a("dy", dy, rows, s.dtype), a("x", x, rows, s.dtype),
-          a("w", w, cols, s.dtype), a("mean", mean, (s.T,), MOE_F32), a("rstd", rstd, (s.T,), MOE_F32),
-          a("dx", dx, rows, s.dtype), a("dw", dw, cols, s.grad_dtype), a("db", db, cols, s.grad_dtype),
-          ctypes.byref(s), a.ws(ws), _nbytes(ws))
+    T, H, dt, gt = s.T, s.H, s.dtype, s.grad_dtype
+    _dense_call("moe_layer_norm_backward", lib.moe_layer_norm_backward, s, (
+        ("dy", dy, (T, H), dt), ("x", x, (T, H), dt), ("w", w, (H,), dt), ("mean", mean, (T,), MOE_F32),
+        ("rstd", rstd, (T,), MOE_F32), ("dx", dx, (T, H), dt), ("dw", dw, (H,), gt), ("db", db, (H,), gt)),
+        stream, (ws,))
 
 
 def gated_forward(x, w1, w3, h, s: MoeDenseShape, ws, g=None, u=None, stream=None):
     """h = act(x w1^T) * (x w3^T); g and u (both or neither) receive the two projections."""
-    a = _Args("moe_gated_forward", stream)
-    wide, wt = (s.T, s.N), (s.N, s.K)
-    a.run(lib.moe_gated_forward, a("x", x, (s.T, s.K), s.dtype), a("w1", w1, wt, s.dtype),
-          a("w3", w3, wt, s.dtype), a("h", h, wide, s.dtype), a("g", g, wide, s.dtype),
-          a("u", u, wide, s.dtype), ctypes.byref(s), a.ws(ws), _nbytes(ws))
+    T, K, N, dt = s.T, s.K, s.N, s.dtype
+    _dense_call("moe_gated_forward", lib.moe_gated_forward, s, (
+        ("x", x, (T, K), dt), ("w1", w1, (N, K), dt), ("w3", w3, (N, K), dt), ("h", h, (T, N), dt),
+        ("g", g, (T, N), dt), ("u", u, (T, N), dt)), stream, (ws,))
 
 
 def gated_backward(dh, x, w1, w3, g, u, dx, dw1, dw3, s: MoeDenseShape, ws, stream=None):
     """Gradients dx (dtype), dw1 and dw3 (grad_dtype) of gated_forward from the g and u it kept."""
-    a = _Args("moe_gated_backward", stream)
-    wide, wt, rows = (s.T, s.N), (s.N, s.K), (s.T, s.K)
-    a.run(lib.moe_gated_backward, a("dh", dh, wide, s.dtype), a("x", x, rows, s.dtype),
-          a("w1", w1, wt, s.dtype), a("w3", w3, wt, s.dtype), a("g", g, wide, s.dtype),
-          a("u", u, wide, s.dtype), a("dx", dx, rows, s.dtype), a("dw1", dw1, wt, s.grad_dtype),
-          a("dw3", dw3, wt, s.grad_dtype), ctypes.byref(s), a.ws(ws), _nbytes(ws))
+    T, K, N, dt, gt = s.T, s.K, s.N, s.dtype, s.grad_dtype
+    _dense_call("moe_gated_backward", lib.moe_gated_backward, s, (
+        ("dh", dh, (T, N), dt), ("x", x, (T, K), dt), ("w1", w1, (N, K), dt), ("w3", w3, (N, K), dt),
+        ("g", g, (T, N), dt), ("u", u, (T, N), dt), ("dx", dx, (T, K), dt), ("dw1", dw1, (N, K), gt),
+        ("dw3", dw3, (N, K), gt)), stream, (ws,))
 
 
 def linear_forward(x, w, bias, residual, y, s: MoeDenseShape, ws, z=None, stream=None):
     """y = act(x w^T + bias) + residual (residual may be y itself); z receives the pre-activation."""
-    a = _Args("moe_linear_forward", stream)
-    wide = (s.T, s.N)
-    a.run(lib.moe_linear_forward, a("x", x, (s.T, s.K), s.dtype), a("w", w, (s.N, s.K), s.dtype),
-          a("bias", bias, (s.N,), s.dtype), a("residual", residual, wide, s.dtype), a("y", y, wide, s.dtype),
-          a("z", z, wide, s.dtype), ctypes.byref(s), a.ws(ws), _nbytes(ws))
+    T, K, N, dt = s.T, s.K, s.N, s.dtype
+    _dense_call("moe_linear_forward", lib.moe_linear_forward, s, (
+        ("x", x, (T, K), dt), ("w", w, (N, K), dt), ("bias", bias, (N,), dt),
+        ("residual", residual, (T, N), dt), ("y", y, (T, N), dt), ("z", z, (T, N), dt)), stream, (ws,))
 
 
 def linear_backward(dy, x, w, z, dx, dw, dbias, s: MoeDenseShape, ws, stream=None):
     """Gradients dx (dtype), dw and dbias (grad_dtype) of linear_forward; z as it kept it (None without
     an activation).  The residual's gradient is dy."""
-    a = _Args("moe_linear_backward", stream)
-    wide = (s.T, s.N)
-    a.run(lib.moe_linear_backward, a("dy", dy, wide, s.dtype), a("x", x, (s.T, s.K), s.dtype),
-          a("w", w, (s.N, s.K), s.dtype), a("z", z, wide, s.dtype), a("dx", dx, (s.T, s.K), s.dtype),
-          a("dw", dw, (s.N, s.K), s.grad_dtype), a("dbias", dbias, (s.N,), s.grad_dtype), ctypes.byref(s),
-          a.ws(ws), _nbytes(ws))
+    T, K, N, dt, gt = s.T, s.K, s.N, s.dtype, s.grad_dtype
+    _dense_call("moe_linear_backward", lib.moe_linear_backward, s, (
+        ("dy", dy, (T, N), dt), ("x", x, (T, K), dt), ("w", w, (N, K), dt), ("z", z, (T, N), dt),
+        ("dx", dx, (T, K), dt), ("dw", dw, (N, K), gt), ("dbias", dbias, (N,), gt)), stream, (ws,))

@@ -97,9 +97,9 @@ int64_t padded(const DenseDims& d, int cols) { return d.bf16 ? ((int64_t)cols + 
 
 // Backward: the gradient before the activation as operand of the products (three bf16 terms of
 // each value, lo elements apart, where fp32 weight gradients are asked for), and the row
-// blocks' column sums.  x, w[2]: padded copies (0 bytes where the operand is read in place).
+// blocks' column sums.  slices: the products' contraction slices.  x, w[2]: padded copies (0 bytes where the operand is read in place).
 struct DenseWs {
-  size_t x, w[2], d0, d1, part, total;
+  size_t x, w[2], d0, d1, part, slices, total;
   int terms;
   int64_t lo, ldk, ldn;
 };
@@ -107,7 +107,9 @@ DenseWs dense_ws(const DenseDims& d, bool gated, bool backward) {
   Carve c; DenseWs w{};
   w.ldk = padded(d, d.K);
   w.ldn = padded(d, d.N);
-  const bool pad_k = w.ldk != d.K && d.T > 0;
+  const bool decode = !backward && d.T <= kDecodeRows;
+  if (decode) w.ldk = d.K;  // its kernel takes rows of any length
+  const bool pad_k = w.ldk != d.K;
   w.x = c.take(pad_k ? (size_t)d.T * w.ldk * d.es : 0);
   w.w[0] = c.take(pad_k ? (size_t)d.N * w.ldk * d.es : 0);
   w.w[1] = c.take(pad_k && gated ? (size_t)d.N * w.ldk * d.es : 0);
@@ -119,6 +121,18 @@ DenseWs dense_ws(const DenseDims& d, bool gated, bool backward) {
     w.d0 = c.take(bytes);
     w.d1 = c.take(gated ? bytes : 0);
     w.part = c.take(gated || d.T == 0 ? 0 : (size_t)grad_row_blocks(d.T, d.N) * d.N * 4);
+  }
+  if (d.bf16 && d.T > 0 && !decode) {
+    const int z = gated ? 2 : 1;
+    size_t n;
+    if (backward) {
+      const size_t dx = dense_mm_part_bytes(d.T, d.K, d.N, z, 1, false);
+      const size_t dw = dense_mm_part_bytes(d.N, d.K, d.T, w.terms, z, false);
+      n = dx > dw ? dx : dw;
+    } else {
+      n = dense_mm_part_bytes(d.T, d.N, d.K, 1, 1, gated);
+    }
+    w.slices = c.take(n);
   }
   w.total = c.cur;
   return w;
@@ -154,7 +168,8 @@ moe_status forward(const DenseDims& d, const DenseWs& w, const void* x, const vo
   j.pair = w1 != nullptr;
   j.A[0][0] = x; j.lda = w.ldk;
   j.B[0][0] = w0; j.B[1][0] = w1; j.ldb = w.ldk;
-  MOE_HIP(launch_dense(j, e, d.bf16, st));
+  MOE_HIP(d.T <= kDecodeRows ? launch_dense_decode(j, e, d.bf16, st)
+                                : launch_dense(j, e, d.bf16, at<float>(ws, w.slices), st));
   return MOE_OK;
 }
 
@@ -173,7 +188,7 @@ moe_status input_grad(const DenseDims& d, const DenseWs& w, const void* d0, cons
   e.kind = DENSE_STORE;
   e.out_f32 = !d.bf16;
   e.out[0] = dx;
-  MOE_HIP(launch_dense(j, e, d.bf16, st));
+  MOE_HIP(launch_dense(j, e, d.bf16, at<float>(ws, w.slices), st));
   return MOE_OK;
 }
 
@@ -196,7 +211,7 @@ moe_status weight_grad(const DenseDims& d, const DenseWs& w, const void* d0, con
   e.kind = DENSE_STORE;
   e.out_f32 = d.grad_f32;
   e.out[0] = dw0; e.out[1] = dw1;
-  MOE_HIP(launch_dense(j, e, d.bf16, st));
+  MOE_HIP(launch_dense(j, e, d.bf16, at<float>(ws, w.slices), st));
   return MOE_OK;
 }
 

@@ -93,8 +93,8 @@ __global__ __launch_bounds__(256) void k_dense_f32(DenseJob j, DenseEpi e) {
       }
 }
 
-hipError_t launch_dense(const DenseJob& j, const DenseEpi& e, bool bf16, hipStream_t st) {
-  if (bf16) return launch_dense_mm(j, e, st);
+hipError_t launch_dense(const DenseJob& j, const DenseEpi& e, bool bf16, float* part, hipStream_t st) {
+  if (bf16) return launch_dense_mm(j, e, part, st);
   const dim3 grid((unsigned)((int64_t)ceil_div(j.M, 64) * ceil_div(j.N, 64)), j.batch);
   if (j.pair) k_dense_f32<true><<<grid, 256, 0, st>>>(j, e);
   else k_dense_f32<false><<<grid, 256, 0, st>>>(j, e);

@@ -39,8 +39,17 @@ struct DenseEpi {
 
 // bf16: element type of the operands and of what the epilogue reads and writes; bf16 operands'
 // lda and ldb are multiples of 8, their rows zero from the contraction length on.
-hipError_t launch_dense_mm(const DenseJob& j, const DenseEpi& e, hipStream_t st);
-hipError_t launch_dense(const DenseJob& j, const DenseEpi& e, bool bf16, hipStream_t st);
+//
+// Forward products of at most kDecodeRows rows read each weight once, straight into operands,
+// and take rows of any length.
+constexpr int kDecodeRows = 16;
+hipError_t launch_dense_decode(const DenseJob& j, const DenseEpi& e, bool bf16, hipStream_t st);
+//
+// Products whose tiles are too few for the device are cut along the contraction; the slices'
+// sums meet in `part`, dense_mm_part_bytes of scratch for the same sizes.
+size_t dense_mm_part_bytes(int M, int N, int K, int segs, int batch, bool pair);
+hipError_t launch_dense_mm(const DenseJob& j, const DenseEpi& e, float* part, hipStream_t st);
+hipError_t launch_dense(const DenseJob& j, const DenseEpi& e, bool bf16, float* part, hipStream_t st);
 
 // The gradient before an activation, [T x N]:
 //   linear (dh == dy, u == NULL): d0 = dy act'(g);  gated: d0 = dh u act'(g), d1 = dh act(g).

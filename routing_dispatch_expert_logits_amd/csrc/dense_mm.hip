@@ -51,112 +51,119 @@ struct MmTile {
     }
   }
 
-  // Operand of rows row0 + 16 i .. + 16 (row0 a multiple of 16), contraction half h.
-  static __device__ __forceinline__ bf16x8 read(const uint16_t* t, int row0, int i, int h, int lane) {
+  // Operand of rows row0 + 16 i .. + 16 (row0 a multiple of 16), contraction half h, of the tile
+  // at element `at` of a stage.  One pointer addition from the stage's array: the compiler
+  // follows only a few when it derives what a read can alias.
+  static __device__ __forceinline__ bf16x8 read(const uint16_t* stage, int at, int row0, int i, int h, int lane) {
     if constexpr (COL) {
       const int g = lane >> 4, j = (lane >> 2) & 3;
       const int k = 32 * h + 8 * g + j, u = ((row0 >> 4) + i) ^ f(8 * g + j);
-      const uint16_t* p = t + k * R + u * 16 + (lane & 3) * 4;
+      const int o = at + k * R + u * 16 + (lane & 3) * 4;
       s16x4 v[2];
-      v[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)p);
-      v[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(p + 4 * R));
+      v[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(stage + o));
+      v[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(stage + (o + 4 * R)));
       return __builtin_bit_cast(bf16x8, v);
     } else {
       const int r = row0 + (lane & 15);
-      return as_bf16x8(*reinterpret_cast<const u32x4*>(t + (r + 16 * i) * kMBK +
-                                                       (((4 * h + (lane >> 4)) ^ (lane & 7)) << 3)));
+      const int o = at + (r + 16 * i) * kMBK + (((4 * h + (lane >> 4)) ^ (lane & 7)) << 3);
+      return as_bf16x8(*reinterpret_cast<const u32x4*>(stage + o));
     }
   }
 };
 
-// Four neighbouring output columns n .. n + 3 of row m.
+// Eight neighbouring output columns n .. n + 7 of row m (the first `left` of them), from the
+// fp32 sums; rows of odd widths are stored at element alignment.
 template <int KIND>
-__device__ __forceinline__ void mm_out4(const DenseEpi& e, int z, int m, int n, int N, f32x4 v0, f32x4 v1) {
+__device__ __forceinline__ void mm_out8(const DenseEpi& e, int z, int m, int n, int N, float* a, const float* b) {
   const int64_t idx = (int64_t)m * N + n;
-  const bool vec = (N & 3) == 0;
-  auto put = [&](void* p, const float* v, bool f32) {
-    if (f32) {
-      if (vec) *reinterpret_cast<f32x4*>(static_cast<float*>(p) + idx) = f32x4{v[0], v[1], v[2], v[3]};
-      else for (int i = 0; i < 4; ++i) { if (n + i < N) static_cast<float*>(p)[idx + i] = v[i]; }
-    } else {
-      uint16_t* o = static_cast<uint16_t*>(p) + idx;
-      if (vec)
-        *reinterpret_cast<uint2*>(o) = make_uint2(f32_to_bf16(v[0]) | (uint32_t)f32_to_bf16(v[1]) << 16,
-                                                  f32_to_bf16(v[2]) | (uint32_t)f32_to_bf16(v[3]) << 16);
-      else for (int i = 0; i < 4; ++i) { if (n + i < N) o[i] = f32_to_bf16(v[i]); }
-    }
-  };
-  auto get = [&](const void* p, int64_t at, float* v) {
-    const uint16_t* o = static_cast<const uint16_t*>(p) + at;
-    if (vec) {
-      const uint2 w = *reinterpret_cast<const uint2*>(o);
-      v[0] = __uint_as_float(w.x << 16); v[1] = __uint_as_float(w.x & 0xffff0000u);
-      v[2] = __uint_as_float(w.y << 16); v[3] = __uint_as_float(w.y & 0xffff0000u);
-    } else {
-      for (int i = 0; i < 4; ++i) v[i] = n + i < N ? bf16_to_f32(o[i]) : 0.f;
-    }
-  };
-  float a[4] = {v0[0], v0[1], v0[2], v0[3]}, y[4];
+  const int left = N - n;
+  float y[8];
   if constexpr (KIND == DENSE_STORE) {
-    put(e.out[z], a, e.out_f32);
+    if (e.out_f32) store8(static_cast<float*>(e.out[z]) + idx, left, a);
+    else store8(static_cast<uint16_t*>(e.out[z]) + idx, left, a);
   } else if constexpr (KIND == DENSE_LINEAR) {
+    float res[8];
+    if (e.residual) load8(static_cast<const uint16_t*>(e.residual) + idx, left, res);
     if (e.bias) {
-      get(e.bias, n, y);
-      for (int i = 0; i < 4; ++i) a[i] += y[i];
+      load8(static_cast<const uint16_t*>(e.bias) + n, left, y);
+      for (int i = 0; i < 8; ++i) a[i] += y[i];
     }
-    if (e.save[0]) put(e.save[0], a, false);
-    for (int i = 0; i < 4; ++i) y[i] = act_value<true>(a[i], e.act);
+    if (e.save[0]) store8(static_cast<uint16_t*>(e.save[0]) + idx, left, a);
+    if (e.act != MOE_ACT_NONE) {
+      for (int i = 0; i < 8; ++i) a[i] = act_value<true>(a[i], e.act);
+    }
     if (e.residual) {
-      get(e.residual, idx, a);
-      for (int i = 0; i < 4; ++i) y[i] += a[i];
+      for (int i = 0; i < 8; ++i) a[i] += res[i];
     }
-    put(e.out[0], y, false);
+    store8(static_cast<uint16_t*>(e.out[0]) + idx, left, a);
   } else {
-    const float b[4] = {v1[0], v1[1], v1[2], v1[3]};
     if (e.save[0]) {
-      put(e.save[0], a, false);
-      put(e.save[1], b, false);
+      store8(static_cast<uint16_t*>(e.save[0]) + idx, left, a);
+      store8(static_cast<uint16_t*>(e.save[1]) + idx, left, b);
     }
-    for (int i = 0; i < 4; ++i) y[i] = act_value<true>(a[i], e.act) * b[i];
-    put(e.out[0], y, false);
+    for (int i = 0; i < 8; ++i) y[i] = act_value<true>(a[i], e.act) * b[i];
+    store8(static_cast<uint16_t*>(e.out[0]) + idx, left, y);
   }
 }
 
-// Tile (m-tile, n-tile, batch) of a workgroup: tiles are dealt to the 8 XCDs in contiguous
-// chunks, within which groups of 8 m-tiles run down their n-tiles, so that the tiles an XCD
-// works on at a time share rows and columns in its L2.
-struct MmWhere { int mt, nt, z; bool ok; };
-__device__ __forceinline__ MmWhere mm_where(int tm, int tn, int batch) {
-  const int total = tm * tn * batch, per = ceil_div(total, 8);
+// Tile (m-tile, n-tile, batch) and contraction slice of a workgroup: work items are dealt to
+// the 8 XCDs in contiguous chunks, within which groups of 8 m-tiles run down their n-tiles, so
+// that the tiles an XCD works on at a time share rows and columns in its L2.
+struct MmWhere { int mt, nt, z, slice; bool ok; };
+__device__ __forceinline__ MmWhere mm_where(int tm, int tn, int batch, int slices) {
+  const int total = tm * tn * batch * slices, per = ceil_div(total, 8);
   const int slot = blockIdx.x >> 3, L = (blockIdx.x & 7) * per + slot;
-  MmWhere w{0, 0, 0, slot < per && L < total};
-  w.z = L / (tm * tn);
-  const int t = L - w.z * (tm * tn), grp = t / (8 * tn), first = grp * 8, r = t - grp * (8 * tn);
+  MmWhere w{0, 0, 0, 0, slot < per && L < total};
+  const int q = L / (tm * tn);
+  w.slice = q / batch;
+  w.z = q - w.slice * batch;
+  const int t = L - q * (tm * tn), grp = t / (8 * tn), first = grp * 8, r = t - grp * (8 * tn);
   const int gsz = min(8, tm - first);
   w.nt = r / gsz;
   w.mt = first + (r - w.nt * gsz);
   return w;
 }
 
-// BM x BN tile by WM x WN waves, two LDS stages: the next step's loads fill one while the
-// other is multiplied.  With PAIR the tile's first BN / 2 rows of B come from the first weight
+// The fp32 sums of one contraction slice: rows of ldp (N rounded up to 8) columns, a plane per
+// batch entry or projection, planes of a slice together.
+struct MmSlices {
+  float* part;   // NULL: one slice, straight to the epilogue
+  int slices, planes, ldp;
+  __device__ __forceinline__ f32x4* at(int slice, int plane, int m, int n, int M) const {  // n: a multiple of 8
+    return reinterpret_cast<f32x4*>(part + (((int64_t)slice * planes + plane) * M + m) * ldp + n);
+  }
+};
+
+// s_waitcnt immediate: at most n vector-memory operations outstanding (bits [3:0] and
+// [15:14]), no LDS operation (bits [11:8]), exports as they are.
+constexpr int mm_waitcnt(int n) { return (n & 0xF) | ((n >> 4) << 14) | (0x7 << 4); }
+
+// BM x BN tile by WM x WN waves, S LDS stages: up to S - 1 steps' loads are in flight while one
+// stage is multiplied.  With PAIR the tile's first BN / 2 rows of B come from the first weight
 // and the rest from the second, for the same BN / 2 output columns.
-template <int BM, int BN, int WM, int WN, bool A_COL, bool B_COL, bool PAIR, int KIND>
-__global__ __launch_bounds__(WM* WN * 64, 2) void k_dense_mm(DenseJob j, DenseEpi e) {
+//
+// The stages are separate arrays, used in an unrolled ring: the compiler then knows which
+// loads into LDS a read has to wait for, and waits for no later ones.
+template <int BM, int BN, int WM, int WN, int S, bool A_COL, bool B_COL, bool PAIR, int KIND>
+__global__ __launch_bounds__(WM* WN * 64, 2) void k_dense_mm(DenseJob j, DenseEpi e, MmSlices sl) {
   using TA = MmTile<BM, A_COL>;
   using TB = MmTile<BN, B_COL>;
   constexpr int W = WM * WN, TM = BM / WM, TN = BN / WN, FM = TM / 16, FN = TN / 16;
   constexpr int QA = TA::INSTR / W, QB = TB::INSTR / W;
   constexpr int ON = PAIR ? BN / 2 : BN;   // output columns of a tile
   static_assert(QA >= 1 && QB >= 1 && !(PAIR && (B_COL || FN % 2)), "tile");
-  __shared__ __attribute__((aligned(1024))) uint16_t sA0[TA::ELEMS], sB0[TB::ELEMS], sA1[TA::ELEMS], sB1[TB::ELEMS];
+  static_assert(S >= 2 && S <= 4, "stages");
+  constexpr int STAGE = TA::ELEMS + TB::ELEMS;
+  __shared__ __attribute__((aligned(1024))) uint16_t s0[STAGE], s1[STAGE], s2[S > 2 ? STAGE : 1], s3[S > 3 ? STAGE : 1];
 
-  const MmWhere w = mm_where(ceil_div(j.M, BM), ceil_div(j.N, ON), j.batch);
+  const MmWhere w = mm_where(ceil_div(j.M, BM), ceil_div(j.N, ON), j.batch, sl.slices);
   if (!w.ok) return;
   const int m0 = uniform(w.mt * BM), n0 = uniform(w.nt * ON), z = uniform(w.z);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / WN, wn = wave % WN;
-  const int nk = ceil_div(j.K, kMBK), steps = nk * j.segs;
+  const int nk = ceil_div(j.K, kMBK), slice = uniform(w.slice);
+  const int first = (int)((int64_t)nk * j.segs * slice / sl.slices);  // this slice's steps
+  const int steps = (int)((int64_t)nk * j.segs * (slice + 1) / sl.slices) - first;
 
   // fill: this wave's instructions are wave * Q .. + Q of each tile
   uint32_t va[QA], vb[QB];
@@ -170,7 +177,7 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void k_dense_mm(DenseJob j, DenseEp
   // of the next step to load: where the tile starts and how many bytes from there are the
   // operand's (whole rows of it, none past its last one)
   const char *pa, *pb;
-  int na, nb, left = 0, seg = 0;                      // left: contraction elements to load of this segment
+  int na, nb, left, seg = first / nk;                   // left: contraction elements to load of this segment
   auto segment = [&]() __attribute__((always_inline)) {
     const void* b = PAIR ? (second ? j.B[1][0] : j.B[0][0]) : j.B[z][seg];
     pa = uniform(static_cast<const char*>(j.A[z][seg]) + (A_COL ? (int64_t)m0 : (int64_t)m0 * j.lda) * 2);
@@ -179,34 +186,36 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void k_dense_mm(DenseJob j, DenseEp
     nb = min(ON, j.N - n0) * (int)j.ldb * 2;
     left = j.K;
   };
-  auto fill = [&](uint16_t* la, uint16_t* lb) __attribute__((always_inline)) {
-    if (left <= 0) {
+  auto advance = [&](int n) __attribute__((always_inline)) {
+    left -= n * kMBK;
+    pa += n * (A_COL ? (int64_t)kMBK * j.lda * 2 : kMBK * 2);
+    pb += n * (B_COL ? (int64_t)kMBK * j.ldb * 2 : kMBK * 2);
+    na -= n * kMBK * 2;
+    nb -= n * kMBK * 2;
+  };
+  // The next step's loads.  Past the last step they are issued all the same with an empty
+  // buffer (zeros, no memory read), so that the count of loads in flight is the same at every
+  // wait, which the compiler's own waits need too.
+  int filled = 0;
+  auto fill = [&](uint16_t* st) __attribute__((always_inline)) {
+    const bool live = filled++ < steps;
+    if (left <= 0 && live) {
       ++seg;
       segment();
     }
     const int rows = min(kMBK, left);
-    auto one = [&](const char* p, int n, bool col, const uint32_t* v, int Q, uint16_t* dst)
+    auto one = [&](const char* p, int n, bool col, const uint32_t* v, int Q, int dst)
         __attribute__((always_inline)) {
       const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
-          const_cast<char*>(p), 0, __builtin_amdgcn_readfirstlane(n), 0x00020000);
-      if (col || rows == kMBK) {
+          const_cast<char*>(p), 0, uniform(live ? n : 0), 0x00020000);
 #pragma unroll
-        for (int q = 0; q < Q; ++q)
-          __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_dst)(dst + q * 512), 16, v[q], 0, 0, 0);
-      } else {
-#pragma unroll
-        for (int q = 0; q < Q; ++q)
-          __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_dst)(dst + q * 512), 16,
-                                                   kchunk < rows ? v[q] : kOutOfRange, 0, 0, 0);
-      }
+      for (int q = 0; q < Q; ++q)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_dst)(st + (dst + q * 512)), 16,
+                                                 col || kchunk < rows ? v[q] : kOutOfRange, 0, 0, 0);
     };
-    one(pa, A_COL ? (rows * (int)j.lda - m0) * 2 : na, A_COL, va, QA, la + wave * QA * 512);
-    one(pb, B_COL ? (rows * (int)j.ldb - n0) * 2 : nb, B_COL, vb, QB, lb + wave * QB * 512);
-    left -= kMBK;
-    pa += A_COL ? (int64_t)kMBK * j.lda * 2 : kMBK * 2;
-    pb += B_COL ? (int64_t)kMBK * j.ldb * 2 : kMBK * 2;
-    na -= kMBK * 2;
-    nb -= kMBK * 2;
+    one(pa, A_COL ? (rows * (int)j.lda - m0) * 2 : na, A_COL, va, QA, wave * QA * 512);
+    one(pb, B_COL ? (rows * (int)j.ldb - n0) * 2 : nb, B_COL, vb, QB, TA::ELEMS + wave * QB * 512);
+    advance(1);
   };
 
   f32x4 acc[FM][FN];
@@ -214,7 +223,7 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void k_dense_mm(DenseJob j, DenseEp
   for (int a = 0; a < FM; ++a)
 #pragma unroll
     for (int b = 0; b < FN; ++b) acc[a][b] = f32x4{0.f, 0.f, 0.f, 0.f};
-  auto multiply = [&](const uint16_t* la, const uint16_t* lb) __attribute__((always_inline)) {
+  auto multiply = [&](const uint16_t* st) __attribute__((always_inline)) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       bf16x8 fb[FN];
@@ -222,62 +231,201 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void k_dense_mm(DenseJob j, DenseEp
       for (int b = 0; b < FN; ++b) {
         // with PAIR, the wave's first half of columns in the first weight's rows, then the second's
         const int row0 = PAIR ? wn * (TN / 2) + (b / (FN / 2)) * ON : wn * TN;
-        fb[b] = TB::read(lb, row0, PAIR ? b % (FN / 2) : b, h, lane);
+        fb[b] = TB::read(st, TA::ELEMS, row0, PAIR ? b % (FN / 2) : b, h, lane);
       }
 #pragma unroll
       for (int a = 0; a < FM; ++a) {
-        const bf16x8 fa = TA::read(la, wm * TM, a, h, lane);
+        const bf16x8 fa = TA::read(st, 0, wm * TM, a, h, lane);
 #pragma unroll
         for (int b = 0; b < FN; ++b)
           acc[a][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[b], fa, acc[a][b], 0, 0, 0);
       }
     }
   };
-  // every load into LDS of this wave has landed and every read from it is done; then all waves
-  auto hand_over = [&]() __attribute__((always_inline)) {
-    __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
+  // One step: the stage's loads have landed (behind them at most S - 2 later stages' are in
+  // flight) and this wave's reads of the stage before are done; then so for every wave, and
+  // that earlier stage takes the loads of S - 1 steps on.
+  auto step = [&](const uint16_t* cur, uint16_t* last) __attribute__((always_inline)) {
+    __builtin_amdgcn_s_waitcnt(mm_waitcnt((S - 2) * (QA + QB)));
     asm volatile("" ::: "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
+    fill(last);
+    // with two stages the loads go first: moved among the products they would come too late
+    // (8192 x 7168 x 2 * 2048 gated, operands in memory: 381 us, else 448); deeper rings have
+    // the time, and lose 8 % by it (4096^3 on 256 x 128: 115 us, else 123)
+    if (S == 2) __builtin_amdgcn_sched_barrier(0);
+    multiply(cur);
   };
 
   segment();
-  fill(sA0, sB0);
-  hand_over();
-  for (int s = 0; s < steps; s += 2) {
-    if (s + 1 < steps) fill(sA1, sB1);
-    multiply(sA0, sB0);
-    hand_over();
-    if (s + 1 < steps) {
-      if (s + 2 < steps) fill(sA0, sB0);
-      multiply(sA1, sB1);
-      hand_over();
+  advance(first - seg * nk);
+  fill(s0);
+  if (S > 2) fill(s1);
+  if (S > 3) fill(s2);
+  if constexpr (S == 2) {
+    for (int s = 0;;) {
+      step(s0, s1);
+      if (++s >= steps) break;
+      step(s1, s0);
+      if (++s >= steps) break;
     }
+  } else {
+    // whole rounds of the ring, then the rest of one: with exits inside the round the compiler
+    // merges their states and waits for the newest loads at the loop's head
+    int s = 0;
+    for (; s + S <= steps; s += S) {
+      step(s0, S == 3 ? s2 : s3);
+      step(s1, s0);
+      step(s2, s1);
+      if (S > 3) step(s3, s2);
+    }
+    if (s < steps) step(s0, S == 3 ? s2 : s3);
+    if (s + 1 < steps) step(s1, s0);
+    if (S > 3 && s + 2 < steps) step(s2, s1);
   }
+  __builtin_amdgcn_s_waitcnt(mm_waitcnt(0));
 
+  // Epilogue through LDS, the stages being free now: a wave's sums go to a 16 KB region of its
+  // own (in passes where they are more), rows of TN columns whose 16-byte chunks are rotated
+  // by row, and come back eight columns of a row per lane: whole cache lines per store, and one
+  // copy of the epilogue's code in a loop, where straight from the accumulators it would be
+  // FM * FN copies (which cost 12 us of a 120 us product, 4096^3, in instruction fetches and
+  // scattered stores).
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+  constexpr int PASSES = TM * TN * 4 * W > S * STAGE * 2 ? 2 : 1, PM = TM / PASSES, PF = FM / PASSES;
+  constexpr int CH = TN / 4;                       // chunks per row
+  constexpr int OC = PAIR ? TN / 2 : TN;           // output columns of the wave
+  constexpr int LPR = OC / 8, RPI = 64 / LPR;      // lanes per row, rows per iteration
+  constexpr int PER = STAGE * 2 / (PM * TN * 4);   // regions per stage array
+  static_assert(PER * S >= W, "epilogue regions");
+  uint16_t* stage = wave < PER ? s0 : wave < 2 * PER ? s1 : wave < 3 * PER ? s2 : s3;
+  float* reg = reinterpret_cast<float*>(stage) + (wave % PER) * (PM * TN);
+  const int nw = n0 + wn * OC, lr = lane / LPR, lc = lane % LPR;
 #pragma unroll
-  for (int a = 0; a < FM; ++a) {
-    const int m = m0 + wm * TM + 16 * a + (lane & 15);
+  for (int p = 0; p < PASSES; ++p) {
 #pragma unroll
-    for (int b = 0; b < (PAIR ? FN / 2 : FN); ++b) {
-      const int n = n0 + wn * (PAIR ? TN / 2 : TN) + 16 * b + 4 * (lane >> 4);
-      if (m < j.M && n < j.N) mm_out4<KIND>(e, z, m, n, j.N, acc[a][b], acc[a][PAIR ? b + FN / 2 : b]);
+    for (int a = 0; a < PF; ++a)
+#pragma unroll
+      for (int b = 0; b < FN; ++b)
+        *reinterpret_cast<f32x4*>(reg + (16 * a + (lane & 15)) * TN +
+                                  (((4 * b + (lane >> 4)) ^ (lane & (CH - 1) & 15)) << 2)) = acc[p * PF + a][b];
+    asm volatile("" ::: "memory");  // the region is this wave's, and its LDS operations stay in order
+    __builtin_amdgcn_wave_barrier();
+    const int mp = m0 + wm * TM + p * PM, n = nw + 8 * lc;
+#pragma unroll 1
+    for (int r = lr; r < PM; r += RPI) {
+      auto chunk = [&](int c) { return *reinterpret_cast<const f32x4*>(reg + r * TN + ((c ^ (r & (CH - 1) & 15)) << 2)); };
+      f32x4 v[2] = {chunk(2 * lc), chunk(2 * lc + 1)}, u[2] = {v[0], v[1]};
+      if (PAIR) u[0] = chunk(CH / 2 + 2 * lc), u[1] = chunk(CH / 2 + 2 * lc + 1);
+      const int m = mp + r;
+      if (m >= j.M || n >= j.N) continue;
+      if (sl.part) {
+        f32x4* o = sl.at(slice, z, m, n, j.M);
+        o[0] = v[0];
+        o[1] = v[1];
+        if (PAIR) {
+          o = sl.at(slice, 1, m, n, j.M);
+          o[0] = u[0];
+          o[1] = u[1];
+        }
+      } else {
+        mm_out8<KIND>(e, z, m, n, j.N, reinterpret_cast<float*>(v), reinterpret_cast<const float*>(u));
+      }
     }
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_wave_barrier();
   }
 }
 
-template <int BM, int BN, int WM, int WN>
-static void mm_go(const DenseJob& j, const DenseEpi& e, hipStream_t st) {
-  const int64_t tiles = (int64_t)ceil_div(j.M, BM) * ceil_div(j.N, j.pair ? BN / 2 : BN) * j.batch;
-  const dim3 grid((unsigned)((tiles + 7) / 8 * 8)), block(WM * WN * 64);
-  if (j.pair) k_dense_mm<BM, BN, WM, WN, false, false, true, DENSE_GATED><<<grid, block, 0, st>>>(j, e);
-  else if (e.kind == DENSE_LINEAR) k_dense_mm<BM, BN, WM, WN, false, false, false, DENSE_LINEAR><<<grid, block, 0, st>>>(j, e);
-  else if (!j.a_col) k_dense_mm<BM, BN, WM, WN, false, true, false, DENSE_STORE><<<grid, block, 0, st>>>(j, e);
-  else k_dense_mm<BM, BN, WM, WN, true, true, false, DENSE_STORE><<<grid, block, 0, st>>>(j, e);
+// The slices' sums in ascending order, then the epilogue; eight columns per thread.
+template <int KIND>
+__global__ __launch_bounds__(256) void k_dense_join(int M, int N, int batch, DenseEpi e, MmSlices sl) {
+  const int n8 = sl.ldp / 8;
+  const int64_t total = (int64_t)batch * M * n8;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+    const int64_t row = i / n8;
+    const int n = (int)(i - row * n8) * 8, z = (int)(row / M), m = (int)(row - (int64_t)z * M);
+    float a[8] = {}, b[8] = {};
+    for (int s = 0; s < sl.slices; ++s) {
+      const f32x4* p = sl.at(s, z, m, n, M);
+      for (int k = 0; k < 8; ++k) a[k] += p[k >> 2][k & 3];
+      if (KIND == DENSE_GATED) {
+        p = sl.at(s, 1, m, n, M);
+        for (int k = 0; k < 8; ++k) b[k] += p[k >> 2][k & 3];
+      }
+    }
+    mm_out8<KIND>(e, z, m, n, N, a, b);
+  }
 }
 
-hipError_t launch_dense_mm(const DenseJob& j, const DenseEpi& e, hipStream_t st) {
-  mm_go<256, 256, 2, 4>(j, e, st);
+template <int BM, int BN, int WM, int WN, int S>
+static void mm_go(const DenseJob& j, const DenseEpi& e, const MmSlices& sl, hipStream_t st) {
+  const int64_t items = (int64_t)ceil_div(j.M, BM) * ceil_div(j.N, j.pair ? BN / 2 : BN) * j.batch * sl.slices;
+  const dim3 grid((unsigned)((items + 7) / 8 * 8)), block(WM * WN * 64);
+  if (j.pair) k_dense_mm<BM, BN, WM, WN, S, false, false, true, DENSE_GATED><<<grid, block, 0, st>>>(j, e, sl);
+  else if (e.kind == DENSE_LINEAR) k_dense_mm<BM, BN, WM, WN, S, false, false, false, DENSE_LINEAR><<<grid, block, 0, st>>>(j, e, sl);
+  else if (!j.a_col) k_dense_mm<BM, BN, WM, WN, S, false, true, false, DENSE_STORE><<<grid, block, 0, st>>>(j, e, sl);
+  else k_dense_mm<BM, BN, WM, WN, S, true, true, false, DENSE_STORE><<<grid, block, 0, st>>>(j, e, sl);
+}
+
+// Tile and slice count of one product, by estimated time.  A tile's constants are what its
+// kernel takes per contraction step with every CU busy and per workgroup beside the steps,
+// measured with operands that come from memory (MI355X): 4096^3 takes 109 us on 256 x 256
+// tiles, 116 on 256 x 128, 133 on 128 x 128 and 193 on 64 x 64; 2048^3, an eighth of the work
+// with a quarter of the tiles, 54, 27, 21 and 27; 512 x 2048 x 2048 52, 26, 16 and 10.
+struct MmTileCost {
+  int bm, bn, at_once;   // workgroups per CU
+  double step, alone, fixed;   // us; step when at_once workgroups share a CU, alone when one has it
+};
+constexpr MmTileCost kMmTiles[] = {
+    {256, 256, 1, 1.62, 1.62, 7.0}, {256, 128, 1, 0.88, 0.80, 4.5}, {128, 128, 1, 0.50, 0.47, 3.0}, {64, 64, 2, 0.33, 0.19, 2.5}};
+struct MmPlan {
+  int tile;    // index into kMmTiles
+  int slices, planes, ldp;
+};
+static MmPlan mm_plan(int M, int N, int K, int segs, int batch, bool pair) {
+  constexpr int CUS = 256;
+  MmPlan best{-1, 1, pair ? 2 : batch, (N + 7) / 8 * 8};
+  double least = 0;
+  const int steps = ceil_div(K, kMBK) * segs;
+  for (int t = 0; t < 4; ++t) {
+    const MmTileCost& c = kMmTiles[t];
+    const int64_t tiles = (int64_t)ceil_div(M, c.bm) * ceil_div(N, pair ? c.bn / 2 : c.bn) * batch;
+    for (int s = 1; s <= 32 && s <= ceil_div(steps, 4); s += s < 4 ? 1 : s / 2) {
+      const int64_t items = tiles * s, rounds = (items + CUS * c.at_once - 1) / (CUS * c.at_once);
+      double us = rounds * (ceil_div(steps, s) * (items <= CUS ? c.alone : c.step) + c.fixed);
+      // the slices' sums are written and read again, and joined by a launch of their own
+      if (s > 1) us += 3.0 + (double)s * best.planes * M * N * 8 / 5e6;
+      if (best.tile < 0 || us < least) {
+        least = us;
+        best.tile = t;
+        best.slices = s;
+      }
+    }
+  }
+  return best;
+}
+
+size_t dense_mm_part_bytes(int M, int N, int K, int segs, int batch, bool pair) {
+  const MmPlan p = mm_plan(M, N, K, segs, batch, pair);
+  return p.slices > 1 ? (size_t)p.slices * p.planes * M * p.ldp * 4 : 0;
+}
+
+hipError_t launch_dense_mm(const DenseJob& j, const DenseEpi& e, float* part, hipStream_t st) {
+  const MmPlan p = mm_plan(j.M, j.N, j.K, j.segs, j.batch, j.pair);
+  const MmSlices sl{p.slices > 1 ? part : nullptr, p.slices, p.planes, p.ldp};
+  if (p.tile == 0) mm_go<256, 256, 2, 4, 2>(j, e, sl, st);
+  else if (p.tile == 1) mm_go<256, 128, 4, 2, 3>(j, e, sl, st);
+  else if (p.tile == 2) mm_go<128, 128, 2, 4, 4>(j, e, sl, st);
+  else mm_go<64, 64, 2, 2, 4>(j, e, sl, st);
+  if (const hipError_t r = hipGetLastError(); r != hipSuccess || p.slices == 1) return r;
+  const int64_t want = ((int64_t)j.batch * j.M * (p.ldp / 8) + 255) / 256;
+  const unsigned grid = (unsigned)(want < 4096 ? want : 4096);
+  if (j.pair) k_dense_join<DENSE_GATED><<<grid, 256, 0, st>>>(j.M, j.N, j.batch, e, sl);
+  else if (e.kind == DENSE_LINEAR) k_dense_join<DENSE_LINEAR><<<grid, 256, 0, st>>>(j.M, j.N, j.batch, e, sl);
+  else k_dense_join<DENSE_STORE><<<grid, 256, 0, st>>>(j.M, j.N, j.batch, e, sl);
   return hipGetLastError();
 }
 
