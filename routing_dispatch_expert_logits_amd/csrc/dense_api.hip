@@ -91,9 +91,12 @@ moe_status check_ws(Buffers& b, const void* ws, size_t ws_bytes, size_t need) {
 
 // ---- workspaces
 
-// The bf16 kernels read rows whose length is a multiple of 8 elements; operands with other
-// widths are copied to such rows first.
-int64_t padded(const DenseDims& d, int cols) { return d.bf16 ? ((int64_t)cols + 7) / 8 * 8 : cols; }
+// The products read rows of whole 16-byte chunks; operands with other widths are copied to
+// such rows first.
+int64_t padded(const DenseDims& d, int cols) {
+  const int64_t c = 16 / d.es;
+  return (cols + c - 1) / c * c;
+}
 
 // Backward: the gradient before the activation as operand of the products (three bf16 terms of
 // each value, lo elements apart, where fp32 weight gradients are asked for), and the row
@@ -122,15 +125,15 @@ DenseWs dense_ws(const DenseDims& d, bool gated, bool backward) {
     w.d1 = c.take(gated ? bytes : 0);
     w.part = c.take(gated || d.T == 0 ? 0 : (size_t)grad_row_blocks(d.T, d.N) * d.N * 4);
   }
-  if (d.bf16 && d.T > 0 && !decode) {
+  if (d.T > 0 && !decode) {
     const int z = gated ? 2 : 1;
     size_t n;
     if (backward) {
-      const size_t dx = dense_mm_part_bytes(d.T, d.K, d.N, z, 1, false);
-      const size_t dw = dense_mm_part_bytes(d.N, d.K, d.T, w.terms, z, false);
+      const size_t dx = dense_part_bytes(d.bf16, d.T, d.K, d.N, z, 1, false);
+      const size_t dw = dense_part_bytes(d.bf16, d.N, d.K, d.T, w.terms, z, false);
       n = dx > dw ? dx : dw;
     } else {
-      n = dense_mm_part_bytes(d.T, d.N, d.K, 1, 1, gated);
+      n = dense_part_bytes(d.bf16, d.T, d.N, d.K, 1, 1, gated);
     }
     w.slices = c.take(n);
   }
@@ -138,12 +141,22 @@ DenseWs dense_ws(const DenseDims& d, bool gated, bool backward) {
   return w;
 }
 
-// An operand's rows of `cols` elements at row length ld: in place, or copied to ws + off.
-moe_status in_rows(const DenseDims& d, const void** p, int64_t rows, int cols, int64_t ld, void* ws, size_t off,
+// x and the weights (each nullable) at row length w.ldk: in place, or copied to the workspace.
+moe_status in_rows(const DenseDims& d, const DenseWs& w, const void** x, const void** w0, const void** w1, void* ws,
                    hipStream_t st) {
-  if (!*p || ld == cols) return MOE_OK;
-  MOE_HIP(launch_pad_rows(*p, rows, cols, at<void>(ws, off), ld, st));
-  *p = at<void>(ws, off);
+  if (w.ldk == d.K) return MOE_OK;
+  PadRows p{};
+  auto one = [&](int i, const void** v, int64_t rows, size_t off) {
+    if (!v || !*v) return;
+    p.src[i] = *v;
+    p.dst[i] = at<void>(ws, off);
+    p.rows[i] = rows;
+    *v = p.dst[i];
+  };
+  one(0, x, d.T, w.x);
+  one(1, w0, d.N, w.w[0]);
+  one(2, w1, d.N, w.w[1]);
+  MOE_HIP(launch_pad_rows(p, d.bf16, d.K, w.ldk, st));
   return MOE_OK;
 }
 
@@ -159,9 +172,7 @@ size_t norm_ws(const NormDims& d) {
 // z = x w0^T (and x w1^T) with epilogue e.
 moe_status forward(const DenseDims& d, const DenseWs& w, const void* x, const void* w0, const void* w1,
                    const DenseEpi& e, void* ws, hipStream_t st) {
-  MOE_TRY(in_rows(d, &x, d.T, d.K, w.ldk, ws, w.x, st));
-  MOE_TRY(in_rows(d, &w0, d.N, d.K, w.ldk, ws, w.w[0], st));
-  MOE_TRY(in_rows(d, &w1, d.N, d.K, w.ldk, ws, w.w[1], st));
+  MOE_TRY(in_rows(d, w, &x, &w0, &w1, ws, st));
   DenseJob j{};
   j.M = d.T; j.N = d.N; j.K = d.K;
   j.segs = 1; j.batch = 1;
@@ -175,9 +186,7 @@ moe_status forward(const DenseDims& d, const DenseWs& w, const void* x, const vo
 
 // dx = d0 w0 (+ d1 w1): the contraction runs over N, which is across the weights' rows.
 moe_status input_grad(const DenseDims& d, const DenseWs& w, const void* d0, const void* d1, const void* w0,
-                      const void* w1, void* dx, void* ws, hipStream_t st) {
-  MOE_TRY(in_rows(d, &w0, d.N, d.K, w.ldk, ws, w.w[0], st));
-  MOE_TRY(in_rows(d, &w1, d.N, d.K, w.ldk, ws, w.w[1], st));
+                      const void* w1, void* dx, void* ws, hipStream_t st) {  // w0, w1 at row length w.ldk
   DenseJob j{};
   j.M = d.T; j.N = d.K; j.K = d.N;
   j.segs = d1 ? 2 : 1; j.batch = 1;
@@ -194,8 +203,7 @@ moe_status input_grad(const DenseDims& d, const DenseWs& w, const void* d0, cons
 
 // dw_z = (sum of d_z's terms)^T x: the contraction runs over the tokens, across both operands' rows.
 moe_status weight_grad(const DenseDims& d, const DenseWs& w, const void* d0, const void* d1, int terms,
-                       const void* x, void* dw0, void* dw1, void* ws, hipStream_t st) {
-  MOE_TRY(in_rows(d, &x, d.T, d.K, w.ldk, ws, w.x, st));
+                       const void* x, void* dw0, void* dw1, void* ws, hipStream_t st) {  // x at row length w.ldk
   DenseJob j{};
   j.M = d.N; j.N = d.K; j.K = d.T;
   j.segs = terms; j.batch = d1 ? 2 : 1;
@@ -335,6 +343,7 @@ moe_status moe_gated_backward(const void* dh, const void* x, const void* w1, con
   const int terms = dw1 ? w.terms : 1;
   void *d0 = at<void>(ws, w.d0), *d1 = at<void>(ws, w.d1);
   MOE_HIP(launch_act_grad(dh, g, u, d.act, d.bf16, d.T, d.N, d0, d1, terms, w.lo, w.ldn, nullptr, st));
+  MOE_TRY(in_rows(d, w, dw1 ? &x : nullptr, dx ? &w1 : nullptr, dx ? &w3 : nullptr, ws, st));
   if (dx) MOE_TRY(input_grad(d, w, d0, d1, w1, w3, dx, ws, st));
   return dw1 ? weight_grad(d, w, d0, d1, terms, x, dw1, dw3, ws, st) : MOE_OK;
 }
@@ -397,7 +406,9 @@ moe_status moe_linear_backward(const void* dy, const void* x, const void* w, con
     if (dbias)
       MOE_HIP(launch_col_sum(part, grad_row_blocks(d.T, d.N), d.N, d.N, dbias, nullptr, d.grad_f32, st));
   }
+  if (!dx && !dw) return MOE_OK;
   const void* dz = operand ? d0 : dy;
+  MOE_TRY(in_rows(d, p, dw ? &x : nullptr, dx ? &w : nullptr, nullptr, ws, st));
   if (dx) MOE_TRY(input_grad(d, p, dz, nullptr, w, nullptr, dx, ws, st));
   return dw ? weight_grad(d, p, dz, nullptr, terms, x, dw, nullptr, ws, st) : MOE_OK;
 }

@@ -143,4 +143,40 @@ __device__ __forceinline__ void store8(T* p, int n, const float* f) {
     if (i < n) store1(p + i, f[i]);
 }
 
+
+// Eight elements as they are in memory: what a load in flight costs in registers.
+template <typename T>
+struct Raw8 {
+  uint32_t v[2 * sizeof(T)];
+  __device__ __forceinline__ void load(const T* p, int n) {  // the first n, zeros behind
+    if (n >= 8) {
+#pragma unroll
+      for (int h = 0; h < (int)sizeof(T) / 2; ++h) {
+        if constexpr (sizeof(T) == 2) {
+          const Bytes16of2 b = *reinterpret_cast<const Bytes16of2*>(p);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[i] = b.v[i];
+        } else {
+          const Bytes16of4 b = reinterpret_cast<const Bytes16of4*>(p)[h];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[4 * h + i] = b.v[i];
+        }
+      }
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < (int)(2 * sizeof(T)); ++i) v[i] = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) {
+        if constexpr (sizeof(T) == 2) v[i / 2] |= (uint32_t)p[i] << (16 * (i & 1));
+        else v[i] = __float_as_uint(p[i]);
+      }
+  }
+  __device__ __forceinline__ float get(int i) const {
+    if constexpr (sizeof(T) == 2) return __uint_as_float(i & 1 ? v[i / 2] & 0xffff0000u : v[i / 2] << 16);
+    else return __uint_as_float(v[i]);
+  }
+};
+
 }  // namespace moe

@@ -93,21 +93,28 @@ hipError_t launch_act_grad(const void* dh, const void* g, const void* u, int act
   return hipGetLastError();
 }
 
-// Column n of the partial sums: 4 groups of the P rows in ascending order, then the groups.
-__global__ __launch_bounds__(256) void k_col_sum(const float* __restrict__ part, int P, int N, int64_t stride,
-                                                 void* __restrict__ out0, void* __restrict__ out1, bool out_f32) {
-  __shared__ float s[4][64];
+// Column n of the partial sums: 16 groups of the P rows (each in ascending order, four loads at
+// a time), then the groups.
+__global__ __launch_bounds__(1024) void k_col_sum(const float* __restrict__ part, int P, int N, int64_t stride,
+                                                  void* __restrict__ out0, void* __restrict__ out1, bool out_f32) {
+  __shared__ float s[16][64];
   void* out = blockIdx.y ? out1 : out0;
   if (!out) return;
-  const float* src = part + (int64_t)blockIdx.y * N;
   const int n = (int)blockIdx.x * 64 + (threadIdx.x & 63), q = threadIdx.x >> 6;
+  const float* src = part + (int64_t)blockIdx.y * N + min(n, N - 1);
   float v = 0.f;
-  if (n < N)
-    for (int p = q; p < P; p += 4) v += src[p * stride + n];
+  int p = q;
+  for (; p + 48 < P; p += 64) {
+    const float a = src[p * stride], b = src[(p + 16) * stride], c = src[(p + 32) * stride], d = src[(p + 48) * stride];
+    v = (((v + a) + b) + c) + d;
+  }
+  for (; p < P; p += 16) v += src[p * stride];
   s[q][threadIdx.x & 63] = v;
   __syncthreads();
   if (q == 0 && n < N) {
-    v = (s[0][threadIdx.x] + s[1][threadIdx.x]) + (s[2][threadIdx.x] + s[3][threadIdx.x]);
+    v = 0.f;
+#pragma unroll
+    for (int g = 0; g < 16; ++g) v += s[g][threadIdx.x];
     if (out_f32) static_cast<float*>(out)[n] = v;
     else static_cast<uint16_t*>(out)[n] = f32_to_bf16(v);
   }
@@ -115,26 +122,34 @@ __global__ __launch_bounds__(256) void k_col_sum(const float* __restrict__ part,
 
 hipError_t launch_col_sum(const float* part, int P, int N, int64_t stride, void* out0, void* out1, bool out_f32,
                           hipStream_t st) {
-  k_col_sum<<<dim3(ceil_div(N, 64), out1 ? 2 : 1), 256, 0, st>>>(part, P, N, stride, out0, out1, out_f32);
+  k_col_sum<<<dim3(ceil_div(N, 64), out1 ? 2 : 1), 1024, 0, st>>>(part, P, N, stride, out0, out1, out_f32);
   return hipGetLastError();
 }
 
-// One 16-byte chunk of a padded row per thread.
-__global__ __launch_bounds__(256) void k_pad_rows(const uint16_t* __restrict__ src, int64_t chunks, int cols,
-                                                  uint16_t* __restrict__ dst, int cpr) {
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < chunks; i += (int64_t)gridDim.x * 256) {
-    const int64_t r = i / cpr;
-    const int c = (int)(i - r * cpr) * 8;
+// Eight elements of a padded row per thread (fp32 rows may end in half of them).
+template <typename T>
+__global__ __launch_bounds__(256) void k_pad_rows(PadRows p, int cols, int ld) {
+  const T* src = static_cast<const T*>(p.src[blockIdx.y]);
+  T* dst = static_cast<T*>(p.dst[blockIdx.y]);
+  if (!src) return;
+  const int per = ceil_div(ld, 8);
+  const int64_t total = p.rows[blockIdx.y] * per;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+    const int64_t r = i / per;
+    const int c = (int)(i - r * per) * 8;
     float v[8];
     load8(src + r * cols + c, cols - c, v);
-    store8(dst + i * 8, v);
+    store8(dst + r * ld + c, ld - c, v);
   }
 }
 
-hipError_t launch_pad_rows(const void* src, int64_t rows, int cols, void* dst, int64_t ld, hipStream_t st) {
-  const int64_t chunks = rows * (ld / 8), want = (chunks + 255) / 256;
-  k_pad_rows<<<(unsigned)(want < 16384 ? want : 16384), 256, 0, st>>>(static_cast<const uint16_t*>(src), chunks, cols,
-                                                                     static_cast<uint16_t*>(dst), (int)(ld / 8));
+hipError_t launch_pad_rows(const PadRows& p, bool bf16, int cols, int64_t ld, hipStream_t st) {
+  int64_t most = 1;
+  for (int64_t r : p.rows) most = r > most ? r : most;
+  const int64_t want = (most * ((ld + 7) / 8) + 255) / 256;
+  const dim3 grid((unsigned)(want < 8192 ? want : 8192), 3);
+  if (bf16) k_pad_rows<uint16_t><<<grid, 256, 0, st>>>(p, cols, (int)ld);
+  else k_pad_rows<float><<<grid, 256, 0, st>>>(p, cols, (int)ld);
   return hipGetLastError();
 }
 

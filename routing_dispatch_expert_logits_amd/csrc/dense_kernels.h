@@ -37,8 +37,8 @@ struct DenseEpi {
   void* save[2];         // z, or g and u; nullable
 };
 
-// bf16: element type of the operands and of what the epilogue reads and writes; bf16 operands'
-// lda and ldb are multiples of 8, their rows zero from the contraction length on.
+// bf16: element type of the operands and of what the epilogue reads and writes (else fp32).
+// lda and ldb are whole 16-byte chunks, row operands zero from the contraction length on.
 //
 // Forward products of at most kDecodeRows rows read each weight once, straight into operands,
 // and take rows of any length.
@@ -46,9 +46,8 @@ constexpr int kDecodeRows = 16;
 hipError_t launch_dense_decode(const DenseJob& j, const DenseEpi& e, bool bf16, hipStream_t st);
 //
 // Products whose tiles are too few for the device are cut along the contraction; the slices'
-// sums meet in `part`, dense_mm_part_bytes of scratch for the same sizes.
-size_t dense_mm_part_bytes(int M, int N, int K, int segs, int batch, bool pair);
-hipError_t launch_dense_mm(const DenseJob& j, const DenseEpi& e, float* part, hipStream_t st);
+// sums meet in `part`, dense_part_bytes of scratch for the same sizes.
+size_t dense_part_bytes(bool bf16, int M, int N, int K, int segs, int batch, bool pair);
 hipError_t launch_dense(const DenseJob& j, const DenseEpi& e, bool bf16, float* part, hipStream_t st);
 
 // The gradient before an activation, [T x N]:
@@ -64,8 +63,14 @@ hipError_t launch_act_grad(const void* dh, const void* g, const void* u, int act
 // nullable), in a fixed order; in fp32 or bf16.
 hipError_t launch_col_sum(const float* part, int P, int N, int64_t stride, void* out0, void* out1, bool out_f32,
                           hipStream_t st);
-// dst[r][0 .. ld) = src[r][0 .. cols) and zeros; bf16, ld a multiple of 8.
-hipError_t launch_pad_rows(const void* src, int64_t rows, int cols, void* dst, int64_t ld, hipStream_t st);
+// dst[r][0 .. ld) = src[r][0 .. cols) and zeros for up to three operands of the same width (src
+// NULL: none) in one launch; ld the next whole number of 16-byte chunks.
+struct PadRows {
+  const void* src[3];
+  void* dst[3];
+  int64_t rows[3];
+};
+hipError_t launch_pad_rows(const PadRows& p, bool bf16, int cols, int64_t ld, hipStream_t st);
 hipError_t launch_fill_zero(void* p, size_t bytes, hipStream_t st);
 
 hipError_t launch_norm_forward(const void* x, const void* w, const void* b, void* y, float* mean, float* rstd,

@@ -1,5 +1,5 @@
-// bf16 dense products on v_mfma_f32_16x16x32_bf16, fp32 accumulate (the layouts are described
-// in dense_kernels.h).
+// Dense products on the matrix cores, fp32 accumulate (the layouts are described in
+// dense_kernels.h): v_mfma_f32_16x16x32_bf16, or for fp32 operands v_mfma_f32_16x16x4_f32.
 #include "dense_device.h"
 #include "dense_kernels.h"
 
@@ -9,7 +9,7 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) void* lds_dst;
 typedef __attribute__((address_space(3))) s16x4* lds_s16x4;
 
-constexpr int kMBK = 64;                       // contraction step
+constexpr int kStepBytes = 128;                // contraction step: 64 bf16 or 32 fp32 elements
 constexpr uint32_t kOutOfRange = 0x80000000u;  // a lane offset no buffer of ours reaches: reads 0
 
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
@@ -18,24 +18,31 @@ __device__ __forceinline__ const char* uniform(const char* p) {
   return reinterpret_cast<const char*>(((uint64_t)(uint32_t)uniform((int)(a >> 32)) << 32) | (uint32_t)uniform((int)a));
 }
 
-// A tile of R rows (m or n) by 64 contraction elements in LDS, filled by 16-byte buffer loads
-// straight into LDS (1 KB per instruction, lane i to byte 16 i) and read as MFMA operands: lane
-// l holds row l % 16, contraction elements 8 (l / 16) .. + 8 of each 32.
+// A tile of R rows (m or n) by one contraction step in LDS, filled by 16-byte buffer loads
+// straight into LDS (1 KB per instruction, lane i to byte 16 i) and read as MFMA operands in two
+// halves: lane l holds row l % 16, the (l / 16)-th 16 bytes of the half's contraction elements.
+// For bf16 that is one instruction's operand; for fp32 the i-th of four instructions takes
+// element i of every lane's four, an order of the contraction that both sides share.
 //
 // Row operands (contraction along memory): LDS row r is 128 bytes, its 16-byte chunk c sits at
 // slot c ^ (r & 7), so the 16 rows one ds_read_b128 touches at one chunk index cover all banks.
 //
-// Column operands (contraction across memory): LDS row k holds R elements, and
+// bf16 column operands (contraction across memory): LDS row k holds R elements, and
 // ds_read_b64_tr_b16 turns 4 x 16 blocks into operand order: of each 16 lanes, lane i reads
 // 8 bytes of row i / 4 at 4 (i % 4) and receives element i of rows 0..3.  The 32-byte unit u
 // of row k sits at u ^ f(k) with f(k) = (k & 3) | (k >> 1 & 4), which spreads the 16 rows one
-// instruction touches over all banks.
-template <int R, bool COL>
+// instruction touches over all banks.  fp32 column operands are read a dword per element, 16
+// lanes to a 64-byte unit of one row; unit u of row k sits at u ^ (k >> 2 & 3).
+template <typename T, int R, bool COL>
 struct MmTile {
-  static constexpr int ELEMS = R * kMBK;
-  static constexpr int INSTR = R / 8;           // fill instructions
-  static constexpr int CPR = R / 8;             // column operand: 16-byte chunks per LDS row
-  static __device__ __forceinline__ int f(int k) { return ((k & 3) | ((k >> 1) & 4)) & (R / 16 - 1); }
+  static constexpr int ES = sizeof(T);
+  static constexpr int HALFS = R * kStepBytes / 2;  // 16-bit words of the tile
+  static constexpr int INSTR = R / 8;               // fill instructions
+  static constexpr int CPR = R * ES / 16;           // column operand: 16-byte chunks per LDS row
+  static constexpr int UC = ES;                     // and chunks per unit (16 elements)
+  static __device__ __forceinline__ int f(int k) {
+    return (ES == 2 ? (k & 3) | ((k >> 1) & 4) : (k >> 2) & 3) & (R / 16 - 1);
+  }
 
   // Byte offset of lane's 16 bytes of fill instruction q, from the tile's first row at
   // contraction 0 (row operand; rows >= valid are out of range) or from the tile's first
@@ -43,66 +50,73 @@ struct MmTile {
   static __device__ __forceinline__ uint32_t src(int q, int lane, int64_t ld, int valid) {
     if constexpr (COL) {
       const int k = q * (64 / CPR) + lane / CPR, s = lane % CPR;
-      const int chunk = (((s >> 1) ^ f(k)) << 1) | (s & 1);
-      return (uint32_t)(k * ld * 2 + chunk * 16);
+      const int chunk = ((s / UC) ^ f(k)) * UC + s % UC;
+      return (uint32_t)(k * ld * ES + chunk * 16);
     } else {
       const int r = q * 8 + (lane >> 3);
-      return r < valid ? (uint32_t)(r * ld * 2 + (((lane & 7) ^ (lane >> 3)) << 4)) : kOutOfRange;
+      return r < valid ? (uint32_t)(r * ld * ES + (((lane & 7) ^ (lane >> 3)) << 4)) : kOutOfRange;
     }
   }
 
   // Operand of rows row0 + 16 i .. + 16 (row0 a multiple of 16), contraction half h, of the tile
-  // at element `at` of a stage.  One pointer addition from the stage's array: the compiler
+  // at 16-bit word `at` of a stage.  One pointer addition from the stage's array: the compiler
   // follows only a few when it derives what a read can alias.
-  static __device__ __forceinline__ bf16x8 read(const uint16_t* stage, int at, int row0, int i, int h, int lane) {
-    if constexpr (COL) {
+  static __device__ __forceinline__ u32x4 read(const uint16_t* stage, int at, int row0, int i, int h, int lane) {
+    if constexpr (COL && ES == 4) {
+      const int g = lane >> 4, k = 16 * h + 4 * g, u = ((row0 >> 4) + i) ^ f(k);
+      const int o = at + 2 * (k * R + u * 16 + (lane & 15));
+      u32x4 v;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = *reinterpret_cast<const uint32_t*>(stage + (o + 2 * e * R));
+      return v;
+    } else if constexpr (COL) {
       const int g = lane >> 4, j = (lane >> 2) & 3;
       const int k = 32 * h + 8 * g + j, u = ((row0 >> 4) + i) ^ f(8 * g + j);
       const int o = at + k * R + u * 16 + (lane & 3) * 4;
       s16x4 v[2];
       v[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(stage + o));
       v[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(stage + (o + 4 * R)));
-      return __builtin_bit_cast(bf16x8, v);
+      return __builtin_bit_cast(u32x4, v);
     } else {
       const int r = row0 + (lane & 15);
-      const int o = at + (r + 16 * i) * kMBK + (((4 * h + (lane >> 4)) ^ (lane & 7)) << 3);
-      return as_bf16x8(*reinterpret_cast<const u32x4*>(stage + o));
+      const int o = at + (r + 16 * i) * (kStepBytes / 2) + (((4 * h + (lane >> 4)) ^ (lane & 7)) << 3);
+      return *reinterpret_cast<const u32x4*>(stage + o);
     }
   }
 };
 
 // Eight neighbouring output columns n .. n + 7 of row m (the first `left` of them), from the
 // fp32 sums; rows of odd widths are stored at element alignment.
-template <int KIND>
+template <typename T, int KIND>
 __device__ __forceinline__ void mm_out8(const DenseEpi& e, int z, int m, int n, int N, float* a, const float* b) {
   const int64_t idx = (int64_t)m * N + n;
   const int left = N - n;
   float y[8];
   if constexpr (KIND == DENSE_STORE) {
     if (e.out_f32) store8(static_cast<float*>(e.out[z]) + idx, left, a);
-    else store8(static_cast<uint16_t*>(e.out[z]) + idx, left, a);
+    else store8(static_cast<T*>(e.out[z]) + idx, left, a);
   } else if constexpr (KIND == DENSE_LINEAR) {
     float res[8];
-    if (e.residual) load8(static_cast<const uint16_t*>(e.residual) + idx, left, res);
+    if (e.residual) load8(static_cast<const T*>(e.residual) + idx, left, res);
     if (e.bias) {
-      load8(static_cast<const uint16_t*>(e.bias) + n, left, y);
+      load8(static_cast<const T*>(e.bias) + n, left, y);
       for (int i = 0; i < 8; ++i) a[i] += y[i];
     }
-    if (e.save[0]) store8(static_cast<uint16_t*>(e.save[0]) + idx, left, a);
+    if (e.save[0]) store8(static_cast<T*>(e.save[0]) + idx, left, a);
     if (e.act != MOE_ACT_NONE) {
-      for (int i = 0; i < 8; ++i) a[i] = act_value<true>(a[i], e.act);
+      for (int i = 0; i < 8; ++i) a[i] = act_value<sizeof(T) == 2>(a[i], e.act);
     }
     if (e.residual) {
       for (int i = 0; i < 8; ++i) a[i] += res[i];
     }
-    store8(static_cast<uint16_t*>(e.out[0]) + idx, left, a);
+    store8(static_cast<T*>(e.out[0]) + idx, left, a);
   } else {
     if (e.save[0]) {
-      store8(static_cast<uint16_t*>(e.save[0]) + idx, left, a);
-      store8(static_cast<uint16_t*>(e.save[1]) + idx, left, b);
+      store8(static_cast<T*>(e.save[0]) + idx, left, a);
+      store8(static_cast<T*>(e.save[1]) + idx, left, b);
     }
-    for (int i = 0; i < 8; ++i) y[i] = act_value<true>(a[i], e.act) * b[i];
-    store8(static_cast<uint16_t*>(e.out[0]) + idx, left, y);
+    for (int i = 0; i < 8; ++i) y[i] = act_value<sizeof(T) == 2>(a[i], e.act) * b[i];
+    store8(static_cast<T*>(e.out[0]) + idx, left, y);
   }
 }
 
@@ -144,16 +158,17 @@ constexpr int mm_waitcnt(int n) { return (n & 0xF) | ((n >> 4) << 14) | (0x7 << 
 //
 // The stages are separate arrays, used in an unrolled ring: the compiler then knows which
 // loads into LDS a read has to wait for, and waits for no later ones.
-template <int BM, int BN, int WM, int WN, int S, bool A_COL, bool B_COL, bool PAIR, int KIND>
+template <typename T, int BM, int BN, int WM, int WN, int S, bool A_COL, bool B_COL, bool PAIR, int KIND>
 __global__ __launch_bounds__(WM* WN * 64, 2) void k_dense_mm(DenseJob j, DenseEpi e, MmSlices sl) {
-  using TA = MmTile<BM, A_COL>;
-  using TB = MmTile<BN, B_COL>;
+  using TA = MmTile<T, BM, A_COL>;
+  using TB = MmTile<T, BN, B_COL>;
+  constexpr int ES = sizeof(T), BK = kStepBytes / ES;
   constexpr int W = WM * WN, TM = BM / WM, TN = BN / WN, FM = TM / 16, FN = TN / 16;
   constexpr int QA = TA::INSTR / W, QB = TB::INSTR / W;
   constexpr int ON = PAIR ? BN / 2 : BN;   // output columns of a tile
   static_assert(QA >= 1 && QB >= 1 && !(PAIR && (B_COL || FN % 2)), "tile");
   static_assert(S >= 2 && S <= 4, "stages");
-  constexpr int STAGE = TA::ELEMS + TB::ELEMS;
+  constexpr int STAGE = TA::HALFS + TB::HALFS;
   __shared__ __attribute__((aligned(1024))) uint16_t s0[STAGE], s1[STAGE], s2[S > 2 ? STAGE : 1], s3[S > 3 ? STAGE : 1];
 
   const MmWhere w = mm_where(ceil_div(j.M, BM), ceil_div(j.N, ON), j.batch, sl.slices);
@@ -161,7 +176,7 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void k_dense_mm(DenseJob j, DenseEp
   const int m0 = uniform(w.mt * BM), n0 = uniform(w.nt * ON), z = uniform(w.z);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / WN, wn = wave % WN;
-  const int nk = ceil_div(j.K, kMBK), slice = uniform(w.slice);
+  const int nk = ceil_div(j.K, BK), slice = uniform(w.slice);
   const int first = (int)((int64_t)nk * j.segs * slice / sl.slices);  // this slice's steps
   const int steps = (int)((int64_t)nk * j.segs * (slice + 1) / sl.slices) - first;
 
@@ -173,25 +188,25 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void k_dense_mm(DenseJob j, DenseEp
 #pragma unroll
   for (int q = 0; q < QB; ++q)
     vb[q] = TB::src((PAIR ? wave % (W / 2) : wave) * QB + q, lane, j.ldb, j.N - n0);
-  const int kchunk = ((lane & 7) ^ (lane >> 3)) * 8;  // row operands: this lane's first element in a step
+  const int kchunk = ((lane & 7) ^ (lane >> 3)) * (16 / ES);  // row operands: this lane's first element in a step
   // of the next step to load: where the tile starts and how many bytes from there are the
   // operand's (whole rows of it, none past its last one)
   const char *pa, *pb;
   int na, nb, left, seg = first / nk;                   // left: contraction elements to load of this segment
   auto segment = [&]() __attribute__((always_inline)) {
     const void* b = PAIR ? (second ? j.B[1][0] : j.B[0][0]) : j.B[z][seg];
-    pa = uniform(static_cast<const char*>(j.A[z][seg]) + (A_COL ? (int64_t)m0 : (int64_t)m0 * j.lda) * 2);
-    pb = uniform(static_cast<const char*>(b) + (B_COL ? (int64_t)n0 : (int64_t)n0 * j.ldb) * 2);
-    na = min(BM, j.M - m0) * (int)j.lda * 2;
-    nb = min(ON, j.N - n0) * (int)j.ldb * 2;
+    pa = uniform(static_cast<const char*>(j.A[z][seg]) + (A_COL ? (int64_t)m0 : (int64_t)m0 * j.lda) * ES);
+    pb = uniform(static_cast<const char*>(b) + (B_COL ? (int64_t)n0 : (int64_t)n0 * j.ldb) * ES);
+    na = min(BM, j.M - m0) * (int)j.lda * ES;
+    nb = min(ON, j.N - n0) * (int)j.ldb * ES;
     left = j.K;
   };
   auto advance = [&](int n) __attribute__((always_inline)) {
-    left -= n * kMBK;
-    pa += n * (A_COL ? (int64_t)kMBK * j.lda * 2 : kMBK * 2);
-    pb += n * (B_COL ? (int64_t)kMBK * j.ldb * 2 : kMBK * 2);
-    na -= n * kMBK * 2;
-    nb -= n * kMBK * 2;
+    left -= n * BK;
+    pa += n * (A_COL ? (int64_t)kStepBytes * j.lda : kStepBytes);
+    pb += n * (B_COL ? (int64_t)kStepBytes * j.ldb : kStepBytes);
+    na -= n * kStepBytes;
+    nb -= n * kStepBytes;
   };
   // The next step's loads.  Past the last step they are issued all the same with an empty
   // buffer (zeros, no memory read), so that the count of loads in flight is the same at every
@@ -203,7 +218,7 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void k_dense_mm(DenseJob j, DenseEp
       ++seg;
       segment();
     }
-    const int rows = min(kMBK, left);
+    const int rows = min(BK, left);
     auto one = [&](const char* p, int n, bool col, const uint32_t* v, int Q, int dst)
         __attribute__((always_inline)) {
       const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
@@ -213,8 +228,8 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void k_dense_mm(DenseJob j, DenseEp
         __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_dst)(st + (dst + q * 512)), 16,
                                                  col || kchunk < rows ? v[q] : kOutOfRange, 0, 0, 0);
     };
-    one(pa, A_COL ? (rows * (int)j.lda - m0) * 2 : na, A_COL, va, QA, wave * QA * 512);
-    one(pb, B_COL ? (rows * (int)j.ldb - n0) * 2 : nb, B_COL, vb, QB, TA::ELEMS + wave * QB * 512);
+    one(pa, A_COL ? (rows * (int)j.lda - m0) * ES : na, A_COL, va, QA, wave * QA * 512);
+    one(pb, B_COL ? (rows * (int)j.ldb - n0) * ES : nb, B_COL, vb, QB, TA::HALFS + wave * QB * 512);
     advance(1);
   };
 
@@ -226,19 +241,33 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void k_dense_mm(DenseJob j, DenseEp
   auto multiply = [&](const uint16_t* st) __attribute__((always_inline)) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      bf16x8 fb[FN];
+      u32x4 fb[FN];
 #pragma unroll
       for (int b = 0; b < FN; ++b) {
         // with PAIR, the wave's first half of columns in the first weight's rows, then the second's
         const int row0 = PAIR ? wn * (TN / 2) + (b / (FN / 2)) * ON : wn * TN;
-        fb[b] = TB::read(st, TA::ELEMS, row0, PAIR ? b % (FN / 2) : b, h, lane);
+        fb[b] = TB::read(st, TA::HALFS, row0, PAIR ? b % (FN / 2) : b, h, lane);
       }
+      if constexpr (ES == 2) {
 #pragma unroll
-      for (int a = 0; a < FM; ++a) {
-        const bf16x8 fa = TA::read(st, 0, wm * TM, a, h, lane);
+        for (int a = 0; a < FM; ++a) {
+          const u32x4 fa = TA::read(st, 0, wm * TM, a, h, lane);
 #pragma unroll
-        for (int b = 0; b < FN; ++b)
-          acc[a][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[b], fa, acc[a][b], 0, 0, 0);
+          for (int b = 0; b < FN; ++b)
+            acc[a][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(fb[b]), as_bf16x8(fa), acc[a][b], 0, 0, 0);
+        }
+      } else {
+        u32x4 fa[FM];
+#pragma unroll
+        for (int a = 0; a < FM; ++a) fa[a] = TA::read(st, 0, wm * TM, a, h, lane);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)  // FM * FN independent sums between two products of one
+#pragma unroll
+          for (int a = 0; a < FM; ++a)
+#pragma unroll
+            for (int b = 0; b < FN; ++b)
+              acc[a][b] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(fb[b][e]), __uint_as_float(fa[a][e]),
+                                                               acc[a][b], 0, 0, 0);
       }
     }
   };
@@ -331,7 +360,7 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void k_dense_mm(DenseJob j, DenseEp
           o[1] = u[1];
         }
       } else {
-        mm_out8<KIND>(e, z, m, n, j.N, reinterpret_cast<float*>(v), reinterpret_cast<const float*>(u));
+        mm_out8<T, KIND>(e, z, m, n, j.N, reinterpret_cast<float*>(v), reinterpret_cast<const float*>(u));
       }
     }
     asm volatile("" ::: "memory");
@@ -340,7 +369,7 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void k_dense_mm(DenseJob j, DenseEp
 }
 
 // The slices' sums in ascending order, then the epilogue; eight columns per thread.
-template <int KIND>
+template <typename T, int KIND>
 __global__ __launch_bounds__(256) void k_dense_join(int M, int N, int batch, DenseEpi e, MmSlices sl) {
   const int n8 = sl.ldp / 8;
   const int64_t total = (int64_t)batch * M * n8;
@@ -356,51 +385,58 @@ __global__ __launch_bounds__(256) void k_dense_join(int M, int N, int batch, Den
         for (int k = 0; k < 8; ++k) b[k] += p[k >> 2][k & 3];
       }
     }
-    mm_out8<KIND>(e, z, m, n, N, a, b);
+    mm_out8<T, KIND>(e, z, m, n, N, a, b);
   }
 }
 
-template <int BM, int BN, int WM, int WN, int S>
+template <typename T, int BM, int BN, int WM, int WN, int S>
 static void mm_go(const DenseJob& j, const DenseEpi& e, const MmSlices& sl, hipStream_t st) {
   const int64_t items = (int64_t)ceil_div(j.M, BM) * ceil_div(j.N, j.pair ? BN / 2 : BN) * j.batch * sl.slices;
   const dim3 grid((unsigned)((items + 7) / 8 * 8)), block(WM * WN * 64);
-  if (j.pair) k_dense_mm<BM, BN, WM, WN, S, false, false, true, DENSE_GATED><<<grid, block, 0, st>>>(j, e, sl);
-  else if (e.kind == DENSE_LINEAR) k_dense_mm<BM, BN, WM, WN, S, false, false, false, DENSE_LINEAR><<<grid, block, 0, st>>>(j, e, sl);
-  else if (!j.a_col) k_dense_mm<BM, BN, WM, WN, S, false, true, false, DENSE_STORE><<<grid, block, 0, st>>>(j, e, sl);
-  else k_dense_mm<BM, BN, WM, WN, S, true, true, false, DENSE_STORE><<<grid, block, 0, st>>>(j, e, sl);
+  if (j.pair) k_dense_mm<T, BM, BN, WM, WN, S, false, false, true, DENSE_GATED><<<grid, block, 0, st>>>(j, e, sl);
+  else if (e.kind == DENSE_LINEAR) k_dense_mm<T, BM, BN, WM, WN, S, false, false, false, DENSE_LINEAR><<<grid, block, 0, st>>>(j, e, sl);
+  else if (!j.a_col) k_dense_mm<T, BM, BN, WM, WN, S, false, true, false, DENSE_STORE><<<grid, block, 0, st>>>(j, e, sl);
+  else k_dense_mm<T, BM, BN, WM, WN, S, true, true, false, DENSE_STORE><<<grid, block, 0, st>>>(j, e, sl);
 }
 
 // Tile and slice count of one product, by estimated time.  A tile's constants are what its
-// kernel takes per contraction step with every CU busy and per workgroup beside the steps,
-// measured with operands that come from memory (MI355X): 4096^3 takes 109 us on 256 x 256
-// tiles, 116 on 256 x 128, 133 on 128 x 128 and 193 on 64 x 64; 2048^3, an eighth of the work
-// with a quarter of the tiles, 54, 27, 21 and 27; 512 x 2048 x 2048 52, 26, 16 and 10.
+// kernel takes per contraction step and per workgroup beside the steps, on a CU that works
+// through several (at_once of them together) or has just one, measured with operands that
+// come from memory (MI355X).  bf16: 4096^3 takes 109 us on 256 x 256 tiles, 116 on 256 x 128,
+// 133 on 128 x 128 and 193 on 64 x 64; 2048^3, an eighth of the work with a quarter of the
+// tiles, 54, 27, 21 and 27; 512 x 2048 x 2048 52, 26, 16 and 10.  fp32 is bound by its matrix
+// instructions on 64 x 64 tiles already (4096^3: 967 us, 142 TFLOP/s; 128 x 128 the same).
 struct MmTileCost {
-  int bm, bn, at_once;   // workgroups per CU
-  double step, alone, fixed;   // us; step when at_once workgroups share a CU, alone when one has it
+  int bm, bn;
+  double step, fixed;              // us, several workgroups after or beside each other
+  double step_alone, fixed_alone;  // us, one
 };
-constexpr MmTileCost kMmTiles[] = {
-    {256, 256, 1, 1.62, 1.62, 7.0}, {256, 128, 1, 0.88, 0.80, 4.5}, {128, 128, 1, 0.50, 0.47, 3.0}, {64, 64, 2, 0.33, 0.19, 2.5}};
+constexpr MmTileCost kTilesBf16[] = {{256, 256, 1.62, 7.0, 1.62, 7.0},
+                                     {256, 128, 0.88, 4.5, 0.80, 4.5},
+                                     {128, 128, 0.50, 3.0, 0.47, 3.0},
+                                     {64, 64, 0.165, 1.3, 0.19, 2.5}};
+constexpr MmTileCost kTilesF32[] = {{64, 64, 0.42, 1.0, 0.50, 2.5}};
 struct MmPlan {
-  int tile;    // index into kMmTiles
+  MmTileCost tile;
   int slices, planes, ldp;
 };
-static MmPlan mm_plan(int M, int N, int K, int segs, int batch, bool pair) {
+static MmPlan mm_plan(bool bf16, int M, int N, int K, int segs, int batch, bool pair) {
   constexpr int CUS = 256;
-  MmPlan best{-1, 1, pair ? 2 : batch, (N + 7) / 8 * 8};
+  MmPlan best{{}, 1, pair ? 2 : batch, (N + 7) / 8 * 8};
   double least = 0;
-  const int steps = ceil_div(K, kMBK) * segs;
-  for (int t = 0; t < 4; ++t) {
-    const MmTileCost& c = kMmTiles[t];
+  const int steps = ceil_div(K, kStepBytes / (bf16 ? 2 : 4)) * segs;
+  for (int t = 0; t < (bf16 ? 4 : 1); ++t) {
+    const MmTileCost& c = bf16 ? kTilesBf16[t] : kTilesF32[t];
     const int64_t tiles = (int64_t)ceil_div(M, c.bm) * ceil_div(N, pair ? c.bn / 2 : c.bn) * batch;
     for (int s = 1; s <= 32 && s <= ceil_div(steps, 4); s += s < 4 ? 1 : s / 2) {
-      const int64_t items = tiles * s, rounds = (items + CUS * c.at_once - 1) / (CUS * c.at_once);
-      double us = rounds * (ceil_div(steps, s) * (items <= CUS ? c.alone : c.step) + c.fixed);
+      const int64_t rounds = (tiles * s + CUS - 1) / CUS;
+      double us = rounds == 1 ? ceil_div(steps, s) * c.step_alone + c.fixed_alone
+                              : rounds * (ceil_div(steps, s) * c.step + c.fixed);
       // the slices' sums are written and read again, and joined by a launch of their own
       if (s > 1) us += 3.0 + (double)s * best.planes * M * N * 8 / 5e6;
-      if (best.tile < 0 || us < least) {
+      if (!best.tile.bm || us < least) {
         least = us;
-        best.tile = t;
+        best.tile = c;
         best.slices = s;
       }
     }
@@ -408,25 +444,38 @@ static MmPlan mm_plan(int M, int N, int K, int segs, int batch, bool pair) {
   return best;
 }
 
-size_t dense_mm_part_bytes(int M, int N, int K, int segs, int batch, bool pair) {
-  const MmPlan p = mm_plan(M, N, K, segs, batch, pair);
+size_t dense_part_bytes(bool bf16, int M, int N, int K, int segs, int batch, bool pair) {
+  const MmPlan p = mm_plan(bf16, M, N, K, segs, batch, pair);
   return p.slices > 1 ? (size_t)p.slices * p.planes * M * p.ldp * 4 : 0;
 }
 
-hipError_t launch_dense_mm(const DenseJob& j, const DenseEpi& e, float* part, hipStream_t st) {
-  const MmPlan p = mm_plan(j.M, j.N, j.K, j.segs, j.batch, j.pair);
-  const MmSlices sl{p.slices > 1 ? part : nullptr, p.slices, p.planes, p.ldp};
-  if (p.tile == 0) mm_go<256, 256, 2, 4, 2>(j, e, sl, st);
-  else if (p.tile == 1) mm_go<256, 128, 4, 2, 3>(j, e, sl, st);
-  else if (p.tile == 2) mm_go<128, 128, 2, 4, 4>(j, e, sl, st);
-  else mm_go<64, 64, 2, 2, 4>(j, e, sl, st);
-  if (const hipError_t r = hipGetLastError(); r != hipSuccess || p.slices == 1) return r;
-  const int64_t want = ((int64_t)j.batch * j.M * (p.ldp / 8) + 255) / 256;
+template <typename T>
+static hipError_t mm_join(const DenseJob& j, const DenseEpi& e, const MmSlices& sl, hipStream_t st) {
+  const int64_t want = ((int64_t)j.batch * j.M * (sl.ldp / 8) + 255) / 256;
   const unsigned grid = (unsigned)(want < 4096 ? want : 4096);
-  if (j.pair) k_dense_join<DENSE_GATED><<<grid, 256, 0, st>>>(j.M, j.N, j.batch, e, sl);
-  else if (e.kind == DENSE_LINEAR) k_dense_join<DENSE_LINEAR><<<grid, 256, 0, st>>>(j.M, j.N, j.batch, e, sl);
-  else k_dense_join<DENSE_STORE><<<grid, 256, 0, st>>>(j.M, j.N, j.batch, e, sl);
+  if (j.pair) k_dense_join<T, DENSE_GATED><<<grid, 256, 0, st>>>(j.M, j.N, j.batch, e, sl);
+  else if (e.kind == DENSE_LINEAR) k_dense_join<T, DENSE_LINEAR><<<grid, 256, 0, st>>>(j.M, j.N, j.batch, e, sl);
+  else k_dense_join<T, DENSE_STORE><<<grid, 256, 0, st>>>(j.M, j.N, j.batch, e, sl);
   return hipGetLastError();
+}
+
+hipError_t launch_dense(const DenseJob& j, const DenseEpi& e, bool bf16, float* part, hipStream_t st) {
+  const MmPlan p = mm_plan(bf16, j.M, j.N, j.K, j.segs, j.batch, j.pair);
+  const MmSlices sl{p.slices > 1 ? part : nullptr, p.slices, p.planes, p.ldp};
+  const int bm = p.tile.bm, bn = p.tile.bn;
+  if (!bf16) {
+    mm_go<float, 64, 64, 2, 2, 3>(j, e, sl, st);
+  } else if (bn == 256) {
+    mm_go<uint16_t, 256, 256, 2, 4, 2>(j, e, sl, st);
+  } else if (bm == 256) {
+    mm_go<uint16_t, 256, 128, 4, 2, 3>(j, e, sl, st);
+  } else if (bm == 128) {
+    mm_go<uint16_t, 128, 128, 2, 4, 4>(j, e, sl, st);
+  } else {
+    mm_go<uint16_t, 64, 64, 2, 2, 4>(j, e, sl, st);
+  }
+  if (const hipError_t r = hipGetLastError(); r != hipSuccess || p.slices == 1) return r;
+  return bf16 ? mm_join<uint16_t>(j, e, sl, st) : mm_join<float>(j, e, sl, st);
 }
 
 }  // namespace moe

@@ -1,49 +1,102 @@
-// Layer norm, forward and backward.
+// Layer norm, forward and backward.  Both are bound by memory: a row is read once, kept in
+// registers while its sums are formed, and written once.
 #include "dense_device.h"
 #include "dense_kernels.h"
 
 namespace moe {
 
-// Sum over the 256 threads of a workgroup, in a fixed order, in every thread.
+// Forward rows up to kRowChunks * 8 elements stay in registers, at most 4 chunks of 8 per thread.
+constexpr int kRowChunks = 4096;
+
+// Sum over a workgroup of up to 16 waves, in a fixed order, in every thread.  s: 16 floats of
+// LDS that no earlier sum of the caller still reads.
 __device__ __forceinline__ float block_sum(float v, float* s) {
   v = wave_sum_f32(v);
-  __syncthreads();
   if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = v;
   __syncthreads();
-  return (s[0] + s[1]) + (s[2] + s[3]);
+  const int waves = blockDim.x >> 6;
+  v = 0.f;
+  for (int i = 0; i < waves; ++i) v += s[i];
+  return v;
 }
 
-// Workgroups of a kernel that takes a row at a time.
-static unsigned norm_grid(int T) { return T < (1 << 20) ? T : 1 << 20; }
-
-// One workgroup per row; the variance is taken from the centred row.
-template <typename T>
-__global__ __launch_bounds__(256) void k_norm_forward(const T* __restrict__ x, const T* __restrict__ w,
-                                                      const T* __restrict__ b, T* __restrict__ y,
-                                                      float* __restrict__ mean, float* __restrict__ rstd, int rows,
-                                                      int H, float eps) {
-  __shared__ float s[4];
-  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
+// A row per workgroup (or per wave, blockDim.y rows to a workgroup, where 64 threads hold it):
+// thread i holds the chunks of 8 elements i, i + blockDim.x, ..; the variance is taken from the
+// centred row.
+template <typename T, int NCH, bool WAVE>
+__global__ __launch_bounds__(WAVE ? 256 : 1024) void k_norm_forward(const T* __restrict__ x, const T* __restrict__ w,
+                                                                    const T* __restrict__ b, T* __restrict__ y,
+                                                                    float* __restrict__ mean,
+                                                                    float* __restrict__ rstd, int rows, int H,
+                                                                    float eps) {
+  __shared__ float s[2][16];
+  const int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+  if (WAVE && row >= rows) return;
   const T* xr = x + row * H;
-  float v[8], sum = 0.f;
-  for (int c = threadIdx.x * 8; c < H; c += 2048) {
-    load8(xr + c, H - c, v);
+  float v[NCH][8], sum = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) sum += v[i];
+  for (int i = 0; i < NCH; ++i) {
+    const int c = ((int)threadIdx.x + i * (int)blockDim.x) * 8;
+    load8(xr + c, H - c, v[i]);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) sum += v[i][k];
   }
-  const float m = block_sum(sum, s) / H;
+  const float m = (WAVE ? wave_sum_f32(sum) : block_sum(sum, s[0])) / (float)H;  // not by 1 / H: a constant row's mean is the constant
   sum = 0.f;
-  for (int c = threadIdx.x * 8; c < H; c += 2048) {
-    load8(xr + c, H - c, v);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) sum += c + i < H ? (v[i] - m) * (v[i] - m) : 0.f;
+  for (int i = 0; i < NCH; ++i) {
+    const int c = ((int)threadIdx.x + i * (int)blockDim.x) * 8;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      v[i][k] -= m;
+      sum += c + k < H ? v[i][k] * v[i][k] : 0.f;
+    }
   }
-  const float r = 1.f / sqrtf(block_sum(sum, s) / H + eps);
+  const float r = 1.f / sqrtf((WAVE ? wave_sum_f32(sum) : block_sum(sum, s[1])) / (float)H + eps);
   if (threadIdx.x == 0) {
     if (mean) mean[row] = m;
     if (rstd) rstd[row] = r;
   }
-  for (int c = threadIdx.x * 8; c < H; c += 2048) {
+#pragma unroll
+  for (int i = 0; i < NCH; ++i) {
+    const int c = ((int)threadIdx.x + i * (int)blockDim.x) * 8;
+    float vw[8], vb[8] = {};
+    load8(w + c, H - c, vw);
+    if (b) load8(b + c, H - c, vb);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[i][k] = v[i][k] * r * vw[k] + vb[k];
+    store8(y + row * H + c, H - c, v[i]);
+  }
+}
+
+// Longer rows: read three times.
+template <typename T>
+__global__ __launch_bounds__(1024) void k_norm_forward_long(const T* __restrict__ x, const T* __restrict__ w,
+                                                            const T* __restrict__ b, T* __restrict__ y,
+                                                            float* __restrict__ mean, float* __restrict__ rstd, int H,
+                                                            float eps) {
+  __shared__ float s[2][16];
+  const int64_t row = blockIdx.x;
+  const T* xr = x + row * H;
+  float v[8], sum = 0.f;
+  for (int c = threadIdx.x * 8; c < H; c += 8192) {
+    load8(xr + c, H - c, v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum += v[i];
+  }
+  const float m = block_sum(sum, s[0]) / H;
+  sum = 0.f;
+  for (int c = threadIdx.x * 8; c < H; c += 8192) {
+    load8(xr + c, H - c, v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum += c + i < H ? (v[i] - m) * (v[i] - m) : 0.f;
+  }
+  const float r = 1.f / sqrtf(block_sum(sum, s[1]) / H + eps);
+  if (threadIdx.x == 0) {
+    if (mean) mean[row] = m;
+    if (rstd) rstd[row] = r;
+  }
+  for (int c = threadIdx.x * 8; c < H; c += 8192) {
     float vw[8], vb[8] = {};
     load8(xr + c, H - c, v);
     load8(w + c, H - c, vw);
@@ -52,31 +105,161 @@ __global__ __launch_bounds__(256) void k_norm_forward(const T* __restrict__ x, c
     for (int i = 0; i < 8; ++i) v[i] = (v[i] - m) * r * vw[i] + vb[i];
     store8(y + row * H + c, H - c, v);
   }
+}
+
+template <typename T>
+static void norm_forward(const void* x_, const void* w_, const void* b_, void* y_, float* mean, float* rstd, int rows,
+                         int H, float eps, hipStream_t st) {
+  const T *x = static_cast<const T*>(x_), *w = static_cast<const T*>(w_), *b = static_cast<const T*>(b_);
+  T* y = static_cast<T*>(y_);
+  const int chunks = ceil_div(H, 8);
+  if (chunks <= 256) {
+    const dim3 block(64, 4);
+    const unsigned grid = ceil_div(rows, 4);
+    if (chunks <= 64) k_norm_forward<T, 1, true><<<grid, block, 0, st>>>(x, w, b, y, mean, rstd, rows, H, eps);
+    else if (chunks <= 128) k_norm_forward<T, 2, true><<<grid, block, 0, st>>>(x, w, b, y, mean, rstd, rows, H, eps);
+    else k_norm_forward<T, 4, true><<<grid, block, 0, st>>>(x, w, b, y, mean, rstd, rows, H, eps);
+  } else if (chunks <= kRowChunks) {
+    // two chunks a thread up to 8192 elements, then four
+    const int n = chunks <= 1024 ? 2 : 4, threads = ceil_div(ceil_div(chunks, n), 64) * 64;
+    if (n == 2) k_norm_forward<T, 2, false><<<rows, threads, 0, st>>>(x, w, b, y, mean, rstd, rows, H, eps);
+    else k_norm_forward<T, 4, false><<<rows, threads, 0, st>>>(x, w, b, y, mean, rstd, rows, H, eps);
+  } else {
+    k_norm_forward_long<T><<<rows, 1024, 0, st>>>(x, w, b, y, mean, rstd, H, eps);
   }
 }
 
 hipError_t launch_norm_forward(const void* x, const void* w, const void* b, void* y, float* mean, float* rstd,
                                int T, int H, float eps, bool bf16, hipStream_t st) {
-  if (bf16)
-    k_norm_forward<uint16_t><<<norm_grid(T), 256, 0, st>>>(static_cast<const uint16_t*>(x), static_cast<const uint16_t*>(w),
-                                                static_cast<const uint16_t*>(b), static_cast<uint16_t*>(y), mean,
-                                                rstd, T, H, eps);
-  else
-    k_norm_forward<float><<<norm_grid(T), 256, 0, st>>>(static_cast<const float*>(x), static_cast<const float*>(w),
-                                             static_cast<const float*>(b), static_cast<float*>(y), mean, rstd, T,
-                                             H, eps);
+  // a grid has fewer than 2^32 threads: batches of rows, 2^21 workgroups of up to 1024 at a time
+  const int64_t row_bytes = (int64_t)H * (bf16 ? 2 : 4);
+  for (int t = 0; t < T;) {
+    const int n = T - t < (1 << 21) ? T - t : 1 << 21;
+    const void* xt = static_cast<const char*>(x) + t * row_bytes;
+    void* yt = static_cast<char*>(y) + t * row_bytes;
+    float *mt = mean ? mean + t : nullptr, *rt = rstd ? rstd + t : nullptr;
+    if (bf16) norm_forward<uint16_t>(xt, w, b, yt, mt, rt, n, H, eps, st);
+    else norm_forward<float>(xt, w, b, yt, mt, rt, n, H, eps, st);
+    t += n;
+  }
   return hipGetLastError();
 }
 
+// Backward in one pass over dy and x.  A workgroup takes a block of consecutive rows, RB at a
+// time; a thread owns NCH chunks of 8 columns, whose dw and db sums it keeps in registers over
+// all its rows (rows in order), while the two sums of a row that dx needs meet in LDS.  The
+// next rows' loads are in flight while these are worked on.
+template <typename T, int NCH, int RB, int MAXT>
+__global__ __launch_bounds__(MAXT) void k_norm_backward(const T* __restrict__ dy, const T* __restrict__ x,
+                                                        const T* __restrict__ w, const float* __restrict__ mean,
+                                                        const float* __restrict__ rstd, T* __restrict__ dx,
+                                                        float* __restrict__ part, int rows, int per, int H) {
+  __shared__ float s[2][16][2 * RB];
+  const int r0 = (int)blockIdx.x * per, r1 = min(rows, r0 + per);
+  const int wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+  const float inv = 1.f / (float)H;
+  float vw[NCH][8], sw[NCH][8] = {}, sb[NCH][8] = {};
+  int col[NCH];
+#pragma unroll
+  for (int i = 0; i < NCH; ++i) {
+    col[i] = ((int)threadIdx.x + i * (int)blockDim.x) * 8;
+    load8(w + col[i], H - col[i], vw[i]);
+  }
+  Raw8<T> nx[RB][NCH], nd[RB][NCH];
+  float nm[RB], nr[RB];
+  auto load = [&](int r) __attribute__((always_inline)) {
+#pragma unroll
+    for (int q = 0; q < RB; ++q) {
+      const bool in = r + q < r1;
+      const int64_t at = (int64_t)min(r + q, r1 - 1) * H;
+      nm[q] = mean[min(r + q, r1 - 1)];
+      nr[q] = in ? rstd[r + q] : 0.f;
+#pragma unroll
+      for (int i = 0; i < NCH; ++i) {
+        nx[q][i].load(x + at + col[i], H - col[i]);
+        nd[q][i].load(dy + at + col[i], in ? H - col[i] : 0);
+      }
+    }
+  };
+  load(r0);
+  for (int r = r0, odd = 0; r < r1; r += RB, odd ^= 1) {
+    float n[RB][NCH][8], d[RB][NCH][8], rs[RB], s1[RB], s2[RB];
+#pragma unroll
+    for (int q = 0; q < RB; ++q) {
+      rs[q] = nr[q];
+      s1[q] = s2[q] = 0.f;
+#pragma unroll
+      for (int i = 0; i < NCH; ++i)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          n[q][i][k] = (nx[q][i].get(k) - nm[q]) * rs[q];
+          d[q][i][k] = nd[q][i].get(k);
+        }
+    }
+    if (r + RB < r1) load(r + RB);
+#pragma unroll
+    for (int q = 0; q < RB; ++q) {
+#pragma unroll
+      for (int i = 0; i < NCH; ++i)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          sw[i][k] += d[q][i][k] * n[q][i][k];
+          sb[i][k] += d[q][i][k];
+          d[q][i][k] *= vw[i][k];
+          s1[q] += d[q][i][k];
+          s2[q] += d[q][i][k] * n[q][i][k];
+        }
+      s1[q] = wave_sum_f32(s1[q]);
+      s2[q] = wave_sum_f32(s2[q]);
+    }
+    if (!dx) continue;  // the same for every thread of the launch
+    if ((threadIdx.x & 63) == 0)
+#pragma unroll
+      for (int q = 0; q < RB; ++q) {
+        s[odd][wave][2 * q] = s1[q];
+        s[odd][wave][2 * q + 1] = s2[q];
+      }
+    __syncthreads();  // the other buffer's readers are past the sync before this one
+#pragma unroll
+    for (int q = 0; q < RB; ++q) {
+      s1[q] = s2[q] = 0.f;
+      for (int v = 0; v < waves; ++v) {
+        s1[q] += s[odd][v][2 * q];
+        s2[q] += s[odd][v][2 * q + 1];
+      }
+      s1[q] *= inv;
+      s2[q] *= inv;
+      if (r + q < r1) {
+#pragma unroll
+        for (int i = 0; i < NCH; ++i) {
+          float o[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) o[k] = rs[q] * (d[q][i][k] - s1[q] - n[q][i][k] * s2[q]);
+          store8(dx + (int64_t)(r + q) * H + col[i], H - col[i], o);
+        }
+      }
+    }
+  }
+  if (part) {
+    float* p = part + (int64_t)blockIdx.x * 2 * H;
+#pragma unroll
+    for (int i = 0; i < NCH; ++i) {
+      store8(p + col[i], H - col[i], sw[i]);
+      store8(p + H + col[i], H - col[i], sb[i]);
+    }
+  }
+}
+
+// Rows of more than 16384 elements (fp32: 8192): dx by a workgroup per row, the column sums by a second kernel.
 template <typename T>
-__global__ __launch_bounds__(256) void k_norm_dx(const T* __restrict__ dy, const T* __restrict__ x,
-                                                 const T* __restrict__ w, const float* __restrict__ mean,
-                                                 const float* __restrict__ rstd, T* __restrict__ dx, int rows, int H) {
-  __shared__ float s[4];
-  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
+__global__ __launch_bounds__(1024) void k_norm_dx_long(const T* __restrict__ dy, const T* __restrict__ x,
+                                                       const T* __restrict__ w, const float* __restrict__ mean,
+                                                       const float* __restrict__ rstd, T* __restrict__ dx, int H) {
+  __shared__ float s[2][16];
+  const int64_t row = blockIdx.x;
   const float m = mean[row], r = rstd[row];
   float vx[8], vd[8], vw[8], s1 = 0.f, s2 = 0.f;
-  for (int c = threadIdx.x * 8; c < H; c += 2048) {
+  for (int c = threadIdx.x * 8; c < H; c += 8192) {
     load8(x + row * H + c, H - c, vx);
     load8(dy + row * H + c, H - c, vd);
     load8(w + c, H - c, vw);
@@ -87,9 +270,9 @@ __global__ __launch_bounds__(256) void k_norm_dx(const T* __restrict__ dy, const
       s2 += e * ((vx[i] - m) * r);
     }
   }
-  s1 = block_sum(s1, s) / H;
-  s2 = block_sum(s2, s) / H;
-  for (int c = threadIdx.x * 8; c < H; c += 2048) {
+  s1 = block_sum(s1, s[0]) / H;
+  s2 = block_sum(s2, s[1]) / H;
+  for (int c = threadIdx.x * 8; c < H; c += 8192) {
     load8(x + row * H + c, H - c, vx);
     load8(dy + row * H + c, H - c, vd);
     load8(w + c, H - c, vw);
@@ -97,18 +280,15 @@ __global__ __launch_bounds__(256) void k_norm_dx(const T* __restrict__ dy, const
     for (int i = 0; i < 8; ++i) vx[i] = r * (vd[i] * vw[i] - s1 - (vx[i] - m) * r * s2);
     store8(dx + row * H + c, H - c, vx);
   }
-  }
 }
 
-// Column sums of dy n and dy over one block of rows (rows of 2 H partial sums).
 template <typename T>
-__global__ __launch_bounds__(256) void k_norm_dw(const T* __restrict__ dy, const T* __restrict__ x,
-                                                 const float* __restrict__ mean, const float* __restrict__ rstd,
-                                                 float* __restrict__ part, int rows, int H) {
+__global__ __launch_bounds__(256) void k_norm_dw_long(const T* __restrict__ dy, const T* __restrict__ x,
+                                                      const float* __restrict__ mean, const float* __restrict__ rstd,
+                                                      float* __restrict__ part, int rows, int per, int H) {
   const int c = (int)blockIdx.x * 256 + threadIdx.x;
   if (c >= H) return;
-  const int per = ceil_div(rows, (int)gridDim.y);
-  const int r0 = (int)min<int64_t>(rows, (int64_t)blockIdx.y * per), r1 = min(rows, r0 + per);
+  const int r0 = (int)blockIdx.y * per, r1 = min(rows, r0 + per);
   float sw = 0.f, sb = 0.f;
   for (int r = r0; r < r1; ++r) {
     const float d = load1(dy + (int64_t)r * H + c);
@@ -119,23 +299,58 @@ __global__ __launch_bounds__(256) void k_norm_dw(const T* __restrict__ dy, const
   part[((int64_t)blockIdx.y * 2 + 1) * H + c] = sb;
 }
 
-int norm_row_blocks(int T, int) {
-  const int n = ceil_div(T, 32);
-  return n < 256 ? n : 256;
+// Chunks of 8 columns per thread and threads per workgroup of the one-pass kernel.
+static void backward_shape(int H, int* nch, int* threads) {
+  const int chunks = ceil_div(H, 8);
+  *nch = chunks <= 1024 ? 1 : 4;
+  *threads = ceil_div(ceil_div(chunks, *nch), 64) * 64;
+}
+// Consecutive rows of one workgroup: the column sums of a block cost 4 H bytes twice over, a
+// row of it 2 H bytes or more three times, so at least 8 rows where there are that many, and
+// no more blocks than the device holds at a time.
+static int rows_per_block(int T, int H) {
+  int nch, threads;
+  backward_shape(H, &nch, &threads);
+  const int blocks = 256 * (threads >= 512 ? 1 : 512 / threads);
+  const int per = ceil_div(T, blocks);
+  return per > 8 ? per : T < 8 ? T : T < 2048 ? 4 : 8;
+}
+int norm_row_blocks(int T, int H) { return ceil_div(T, rows_per_block(T, H)); }
+
+template <typename T>
+static void norm_backward(const void* dy_, const void* x_, const void* w_, const float* mean, const float* rstd,
+                          void* dx_, float* part, int rows, int H, hipStream_t st) {
+  const T *dy = static_cast<const T*>(dy_), *x = static_cast<const T*>(x_), *w = static_cast<const T*>(w_);
+  T* dx = static_cast<T*>(dx_);
+  const int per = rows_per_block(rows, H);
+  int nch, threads;
+  backward_shape(H, &nch, &threads);
+  const int grid = ceil_div(rows, per);
+  if (nch == 1) {
+    k_norm_backward<T, 1, sizeof(T) == 2 ? 2 : 1, 1024><<<grid, threads, 0, st>>>(dy, x, w, mean, rstd, dx, part, rows, per, H);
+    return;
+  }
+  if constexpr (sizeof(T) == 2) {  // fp32 would not fit the registers
+    if (threads <= 512) {
+      k_norm_backward<T, 4, 1, 512><<<grid, threads, 0, st>>>(dy, x, w, mean, rstd, dx, part, rows, per, H);
+      return;
+    }
+  }
+  if (dx)
+    for (int t = 0; t < rows; t += 1 << 21) {  // a grid has fewer than 2^32 threads
+      const int n = rows - t < (1 << 21) ? rows - t : 1 << 21;
+      const int64_t at = (int64_t)t * H;
+      k_norm_dx_long<T><<<n, 1024, 0, st>>>(dy + at, x + at, w, mean + t, rstd + t, dx + at, H);
+    }
+  if (part)
+    k_norm_dw_long<T><<<dim3(ceil_div(H, 256), ceil_div(rows, per)), 256, 0, st>>>(dy, x, mean, rstd, part, rows, per, H);
 }
 
 hipError_t launch_norm_backward(const void* dy, const void* x, const void* w, const float* mean,
                                 const float* rstd, void* dx, float* part, int T, int H, bool bf16,
                                 hipStream_t st) {
-  auto go = [&](auto* t) {
-    using E = std::remove_pointer_t<decltype(t)>;
-    const E *a = static_cast<const E*>(dy), *b = static_cast<const E*>(x), *c = static_cast<const E*>(w);
-    if (dx) k_norm_dx<E><<<norm_grid(T), 256, 0, st>>>(a, b, c, mean, rstd, static_cast<E*>(dx), T, H);
-    if (part)
-      k_norm_dw<E><<<dim3(ceil_div(H, 256), norm_row_blocks(T, H)), 256, 0, st>>>(a, b, mean, rstd, part, T, H);
-  };
-  if (bf16) go(static_cast<uint16_t*>(nullptr));
-  else go(static_cast<float*>(nullptr));
+  if (bf16) norm_backward<uint16_t>(dy, x, w, mean, rstd, dx, part, T, H, st);
+  else norm_backward<float>(dy, x, w, mean, rstd, dx, part, T, H, st);
   return hipGetLastError();
 }
 
