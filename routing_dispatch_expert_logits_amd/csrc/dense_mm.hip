@@ -1,5 +1,7 @@
 // Dense products on the matrix cores, fp32 accumulate (the layouts are described in
 // dense_kernels.h): v_mfma_f32_16x16x32_bf16, or for fp32 operands v_mfma_f32_16x16x4_f32.
+#include <type_traits>
+
 #include "dense_device.h"
 #include "dense_kernels.h"
 
@@ -86,9 +88,12 @@ struct MmTile {
 };
 
 // Eight neighbouring output columns n .. n + 7 of row m (the first `left` of them), from the
-// fp32 sums; rows of odd widths are stored at element alignment.
-template <typename T, int KIND>
-__device__ __forceinline__ void mm_out8(const DenseEpi& e, int z, int m, int n, int N, float* a, const float* b) {
+// fp32 sums; rows of odd widths are stored at element alignment.  ACT: the activation; res: the
+// residual's eight, where there is one.
+template <typename T, int KIND, int ACT>
+__device__ __forceinline__ void mm_out8(const DenseEpi& e, int z, int m, int n, int N, float* a, const float* b,
+                                        const Raw8<T>& res) {
+  constexpr bool FAST = sizeof(T) == 2;
   const int64_t idx = (int64_t)m * N + n;
   const int left = N - n;
   float y[8];
@@ -96,18 +101,14 @@ __device__ __forceinline__ void mm_out8(const DenseEpi& e, int z, int m, int n, 
     if (e.out_f32) store8(static_cast<float*>(e.out[z]) + idx, left, a);
     else store8(static_cast<T*>(e.out[z]) + idx, left, a);
   } else if constexpr (KIND == DENSE_LINEAR) {
-    float res[8];
-    if (e.residual) load8(static_cast<const T*>(e.residual) + idx, left, res);
     if (e.bias) {
       load8(static_cast<const T*>(e.bias) + n, left, y);
       for (int i = 0; i < 8; ++i) a[i] += y[i];
     }
     if (e.save[0]) store8(static_cast<T*>(e.save[0]) + idx, left, a);
-    if (e.act != MOE_ACT_NONE) {
-      for (int i = 0; i < 8; ++i) a[i] = act_value<sizeof(T) == 2>(a[i], e.act);
-    }
+    for (int i = 0; i < 8; ++i) a[i] = act_value<FAST>(a[i], ACT);
     if (e.residual) {
-      for (int i = 0; i < 8; ++i) a[i] += res[i];
+      for (int i = 0; i < 8; ++i) a[i] += res.get(i);
     }
     store8(static_cast<T*>(e.out[0]) + idx, left, a);
   } else {
@@ -115,9 +116,29 @@ __device__ __forceinline__ void mm_out8(const DenseEpi& e, int z, int m, int n, 
       store8(static_cast<T*>(e.save[0]) + idx, left, a);
       store8(static_cast<T*>(e.save[1]) + idx, left, b);
     }
-    for (int i = 0; i < 8; ++i) y[i] = act_value<sizeof(T) == 2>(a[i], e.act) * b[i];
+    for (int i = 0; i < 8; ++i) y[i] = act_value<FAST>(a[i], ACT) * b[i];
     store8(static_cast<T*>(e.out[0]) + idx, left, y);
   }
+}
+
+template <typename T, int KIND>
+__device__ __forceinline__ void load_residual(const DenseEpi& e, int m, int n, int M, int N, Raw8<T>* res) {
+  if (KIND == DENSE_LINEAR && e.residual)
+    res->load(static_cast<const T*>(e.residual) + (int64_t)min(m, M - 1) * N + n, m < M ? N - n : 0);
+}
+
+// f(std::integral_constant<int, act>) for the activation of a launch.
+template <int KIND, typename F>
+__device__ __forceinline__ void with_act(int act, F&& f) {
+  if constexpr (KIND != DENSE_STORE) {
+    switch (act) {
+      case MOE_ACT_RELU: return f(std::integral_constant<int, MOE_ACT_RELU>{});
+      case MOE_ACT_SILU: return f(std::integral_constant<int, MOE_ACT_SILU>{});
+      case MOE_ACT_GELU: return f(std::integral_constant<int, MOE_ACT_GELU>{});
+      case MOE_ACT_GELU_TANH: return f(std::integral_constant<int, MOE_ACT_GELU_TANH>{});
+    }
+  }
+  f(std::integral_constant<int, MOE_ACT_NONE>{});
 }
 
 // Tile (m-tile, n-tile, batch) and contraction slice of a workgroup: work items are dealt to
@@ -342,26 +363,43 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void k_dense_mm(DenseJob j, DenseEp
                                   (((4 * b + (lane >> 4)) ^ (lane & (CH - 1) & 15)) << 2)) = acc[p * PF + a][b];
     asm volatile("" ::: "memory");  // the region is this wave's, and its LDS operations stay in order
     __builtin_amdgcn_wave_barrier();
-    const int mp = m0 + wm * TM + p * PM, n = nw + 8 * lc;
-#pragma unroll 1
-    for (int r = lr; r < PM; r += RPI) {
-      auto chunk = [&](int c) { return *reinterpret_cast<const f32x4*>(reg + r * TN + ((c ^ (r & (CH - 1) & 15)) << 2)); };
-      f32x4 v[2] = {chunk(2 * lc), chunk(2 * lc + 1)}, u[2] = {v[0], v[1]};
-      if (PAIR) u[0] = chunk(CH / 2 + 2 * lc), u[1] = chunk(CH / 2 + 2 * lc + 1);
-      const int m = mp + r;
-      if (m >= j.M || n >= j.N) continue;
-      if (sl.part) {
+    const int mp = m0 + wm * TM + p * PM + lr, n = nw + 8 * lc;
+    auto chunk = [&](int r, int c) __attribute__((always_inline)) {
+      return *reinterpret_cast<const f32x4*>(reg + r * TN + ((c ^ (r & (CH - 1) & 15)) << 2));
+    };
+    if (sl.part) {
+      for (int r = lr; r < PM; r += RPI) {
+        const int m = mp + r - lr;
+        if (m >= j.M || n >= j.N) continue;
         f32x4* o = sl.at(slice, z, m, n, j.M);
-        o[0] = v[0];
-        o[1] = v[1];
+        o[0] = chunk(r, 2 * lc);
+        o[1] = chunk(r, 2 * lc + 1);
         if (PAIR) {
           o = sl.at(slice, 1, m, n, j.M);
-          o[0] = u[0];
-          o[1] = u[1];
+          o[0] = chunk(r, CH / 2 + 2 * lc);
+          o[1] = chunk(r, CH / 2 + 2 * lc + 1);
         }
-      } else {
-        mm_out8<T, KIND>(e, z, m, n, j.N, reinterpret_cast<float*>(v), reinterpret_cast<const float*>(u));
       }
+    } else {
+      with_act<KIND>(e.act, [&](auto act) __attribute__((always_inline)) {
+        // a residual's rows are all on their way before the first is used: taken one iteration
+        // at a time their latency is most of the epilogue (8192 x 2048 x 7168: 40 us of 273)
+        constexpr int U = KIND == DENSE_LINEAR ? PM / RPI : 1;
+        Raw8<T> res[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i) load_residual<T, KIND>(e, mp + i * RPI, n, j.M, j.N, &res[i]);
+        for (int r0 = 0; r0 < PM; r0 += U * RPI) {
+#pragma unroll
+          for (int i = 0; i < U; ++i) {
+            const int r = r0 + i * RPI + lr, m = mp + r - lr;
+            if (m >= j.M || n >= j.N) continue;
+            f32x4 v[2] = {chunk(r, 2 * lc), chunk(r, 2 * lc + 1)}, u[2] = {v[0], v[1]};
+            if (PAIR) u[0] = chunk(r, CH / 2 + 2 * lc), u[1] = chunk(r, CH / 2 + 2 * lc + 1);
+            mm_out8<T, KIND, act()>(e, z, m, n, j.N, reinterpret_cast<float*>(v), reinterpret_cast<const float*>(u),
+                                    res[i]);
+          }
+        }
+      });
     }
     asm volatile("" ::: "memory");
     __builtin_amdgcn_wave_barrier();
@@ -385,7 +423,9 @@ __global__ __launch_bounds__(256) void k_dense_join(int M, int N, int batch, Den
         for (int k = 0; k < 8; ++k) b[k] += p[k >> 2][k & 3];
       }
     }
-    mm_out8<T, KIND>(e, z, m, n, N, a, b);
+    Raw8<T> res;
+    load_residual<T, KIND>(e, m, n, M, N, &res);
+    with_act<KIND>(e.act, [&](auto act) __attribute__((always_inline)) { mm_out8<T, KIND, act()>(e, z, m, n, N, a, b, res); });
   }
 }
 

@@ -5,8 +5,8 @@
 
 namespace moe {
 
-// Forward rows up to kRowChunks * 8 elements stay in registers, at most 4 chunks of 8 per thread.
-constexpr int kRowChunks = 4096;
+// Forward rows up to kRowChunks * 8 elements stay in registers.
+constexpr int kRowChunks = 2048;
 
 // Sum over a workgroup of up to 16 waves, in a fixed order, in every thread.  s: 16 floats of
 // LDS that no earlier sum of the caller still reads.
@@ -20,52 +20,66 @@ __device__ __forceinline__ float block_sum(float v, float* s) {
   return v;
 }
 
-// A row per workgroup (or per wave, blockDim.y rows to a workgroup, where 64 threads hold it):
-// thread i holds the chunks of 8 elements i, i + blockDim.x, ..; the variance is taken from the
-// centred row.
+// A row per workgroup at a time (or per wave, blockDim.y of them in a workgroup, where 64
+// threads hold it): thread i holds the chunks of 8 elements i, i + blockDim.x, ..  Weight and
+// bias stay in registers over all rows of the workgroup: read again for each row they would be
+// as many bytes from L2 as the row itself.  The next row's loads are in flight while one is
+// worked on; the variance is taken from the centred row.
 template <typename T, int NCH, bool WAVE>
 __global__ __launch_bounds__(WAVE ? 256 : 1024) void k_norm_forward(const T* __restrict__ x, const T* __restrict__ w,
                                                                     const T* __restrict__ b, T* __restrict__ y,
                                                                     float* __restrict__ mean,
-                                                                    float* __restrict__ rstd, int rows, int H,
-                                                                    float eps) {
-  __shared__ float s[2][16];
-  const int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
-  if (WAVE && row >= rows) return;
-  const T* xr = x + row * H;
-  float v[NCH][8], sum = 0.f;
+                                                                    float* __restrict__ rstd, int rows, int per,
+                                                                    int H, float eps) {
+  __shared__ float s[4][16];
+  const int first = ((int)blockIdx.x * (int)blockDim.y + (int)threadIdx.y) * per;
+  const int last = min(rows, first + per);
+  int col[NCH];
+  Raw8<T> next[NCH], vw[NCH], vb[NCH];
+  auto load = [&](int row) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < NCH; ++i) next[i].load(x + (int64_t)row * H + col[i], H - col[i]);
+  };
+#pragma unroll
+  for (int i = 0; i < NCH; ++i) col[i] = ((int)threadIdx.x + i * (int)blockDim.x) * 8;
+  if (first < last) load(first);
 #pragma unroll
   for (int i = 0; i < NCH; ++i) {
-    const int c = ((int)threadIdx.x + i * (int)blockDim.x) * 8;
-    load8(xr + c, H - c, v[i]);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) sum += v[i][k];
+    vw[i].load(w + col[i], H - col[i]);
+    vb[i].load(b + col[i], b ? H - col[i] : 0);
   }
-  const float m = (WAVE ? wave_sum_f32(sum) : block_sum(sum, s[0])) / (float)H;  // not by 1 / H: a constant row's mean is the constant
-  sum = 0.f;
+  for (int row = first, q = 0; row < last; ++row, q ^= 2) {
+    float v[NCH][8], sum = 0.f;
 #pragma unroll
-  for (int i = 0; i < NCH; ++i) {
-    const int c = ((int)threadIdx.x + i * (int)blockDim.x) * 8;
+    for (int i = 0; i < NCH; ++i)
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      v[i][k] -= m;
-      sum += c + k < H ? v[i][k] * v[i][k] : 0.f;
+      for (int k = 0; k < 8; ++k) {
+        v[i][k] = next[i].get(k);
+        sum += v[i][k];
+      }
+    if (row + 1 < last) load(row + 1);
+    // divided by H, not multiplied by 1 / H: a constant row's mean is the constant.  The sums'
+    // LDS alternates between rows: its readers are one sync behind the next row's writers.
+    const float m = (WAVE ? wave_sum_f32(sum) : block_sum(sum, s[q])) / (float)H;
+    sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < NCH; ++i)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        v[i][k] -= m;
+        sum += col[i] + k < H ? v[i][k] * v[i][k] : 0.f;
+      }
+    const float r = 1.f / sqrtf((WAVE ? wave_sum_f32(sum) : block_sum(sum, s[q + 1])) / (float)H + eps);
+    if (threadIdx.x == 0) {
+      if (mean) mean[row] = m;
+      if (rstd) rstd[row] = r;
     }
-  }
-  const float r = 1.f / sqrtf((WAVE ? wave_sum_f32(sum) : block_sum(sum, s[1])) / (float)H + eps);
-  if (threadIdx.x == 0) {
-    if (mean) mean[row] = m;
-    if (rstd) rstd[row] = r;
-  }
 #pragma unroll
-  for (int i = 0; i < NCH; ++i) {
-    const int c = ((int)threadIdx.x + i * (int)blockDim.x) * 8;
-    float vw[8], vb[8] = {};
-    load8(w + c, H - c, vw);
-    if (b) load8(b + c, H - c, vb);
+    for (int i = 0; i < NCH; ++i) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[i][k] = v[i][k] * r * vw[k] + vb[k];
-    store8(y + row * H + c, H - c, v[i]);
+      for (int k = 0; k < 8; ++k) v[i][k] = v[i][k] * r * vw[i].get(k) + vb[i].get(k);
+      store8(y + (int64_t)row * H + col[i], H - col[i], v[i]);
+    }
   }
 }
 
@@ -73,37 +87,38 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void k_norm_forward(const T* __r
 template <typename T>
 __global__ __launch_bounds__(1024) void k_norm_forward_long(const T* __restrict__ x, const T* __restrict__ w,
                                                             const T* __restrict__ b, T* __restrict__ y,
-                                                            float* __restrict__ mean, float* __restrict__ rstd, int H,
-                                                            float eps) {
+                                                            float* __restrict__ mean, float* __restrict__ rstd,
+                                                            int rows, int H, float eps) {
   __shared__ float s[2][16];
-  const int64_t row = blockIdx.x;
-  const T* xr = x + row * H;
-  float v[8], sum = 0.f;
-  for (int c = threadIdx.x * 8; c < H; c += 8192) {
-    load8(xr + c, H - c, v);
+  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
+    const T* xr = x + row * H;
+    float v[8], sum = 0.f;
+    for (int c = threadIdx.x * 8; c < H; c += 8192) {
+      load8(xr + c, H - c, v);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) sum += v[i];
-  }
-  const float m = block_sum(sum, s[0]) / H;
-  sum = 0.f;
-  for (int c = threadIdx.x * 8; c < H; c += 8192) {
-    load8(xr + c, H - c, v);
+      for (int i = 0; i < 8; ++i) sum += v[i];
+    }
+    const float m = block_sum(sum, s[0]) / H;
+    sum = 0.f;
+    for (int c = threadIdx.x * 8; c < H; c += 8192) {
+      load8(xr + c, H - c, v);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) sum += c + i < H ? (v[i] - m) * (v[i] - m) : 0.f;
-  }
-  const float r = 1.f / sqrtf(block_sum(sum, s[1]) / H + eps);
-  if (threadIdx.x == 0) {
-    if (mean) mean[row] = m;
-    if (rstd) rstd[row] = r;
-  }
-  for (int c = threadIdx.x * 8; c < H; c += 8192) {
-    float vw[8], vb[8] = {};
-    load8(xr + c, H - c, v);
-    load8(w + c, H - c, vw);
-    if (b) load8(b + c, H - c, vb);
+      for (int i = 0; i < 8; ++i) sum += c + i < H ? (v[i] - m) * (v[i] - m) : 0.f;
+    }
+    const float r = 1.f / sqrtf(block_sum(sum, s[1]) / H + eps);
+    if (threadIdx.x == 0) {
+      if (mean) mean[row] = m;
+      if (rstd) rstd[row] = r;
+    }
+    for (int c = threadIdx.x * 8; c < H; c += 8192) {
+      float vw[8], vb[8] = {};
+      load8(xr + c, H - c, v);
+      load8(w + c, H - c, vw);
+      if (b) load8(b + c, H - c, vb);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = (v[i] - m) * r * vw[i] + vb[i];
-    store8(y + row * H + c, H - c, v);
+      for (int i = 0; i < 8; ++i) v[i] = (v[i] - m) * r * vw[i] + vb[i];
+      store8(y + row * H + c, H - c, v);
+    }
   }
 }
 
@@ -114,34 +129,26 @@ static void norm_forward(const void* x_, const void* w_, const void* b_, void* y
   T* y = static_cast<T*>(y_);
   const int chunks = ceil_div(H, 8);
   if (chunks <= 256) {
+    // 8 waves per SIMD of 256 CUs, then several rows each
+    const int per = ceil_div(rows, 8192), grid = ceil_div(ceil_div(rows, per), 4);
     const dim3 block(64, 4);
-    const unsigned grid = ceil_div(rows, 4);
-    if (chunks <= 64) k_norm_forward<T, 1, true><<<grid, block, 0, st>>>(x, w, b, y, mean, rstd, rows, H, eps);
-    else if (chunks <= 128) k_norm_forward<T, 2, true><<<grid, block, 0, st>>>(x, w, b, y, mean, rstd, rows, H, eps);
-    else k_norm_forward<T, 4, true><<<grid, block, 0, st>>>(x, w, b, y, mean, rstd, rows, H, eps);
+    if (chunks <= 64) k_norm_forward<T, 1, true><<<grid, block, 0, st>>>(x, w, b, y, mean, rstd, rows, per, H, eps);
+    else if (chunks <= 128) k_norm_forward<T, 2, true><<<grid, block, 0, st>>>(x, w, b, y, mean, rstd, rows, per, H, eps);
+    else k_norm_forward<T, 4, true><<<grid, block, 0, st>>>(x, w, b, y, mean, rstd, rows, per, H, eps);
   } else if (chunks <= kRowChunks) {
-    // two chunks a thread up to 8192 elements, then four
-    const int n = chunks <= 1024 ? 2 : 4, threads = ceil_div(ceil_div(chunks, n), 64) * 64;
-    if (n == 2) k_norm_forward<T, 2, false><<<rows, threads, 0, st>>>(x, w, b, y, mean, rstd, rows, H, eps);
-    else k_norm_forward<T, 4, false><<<rows, threads, 0, st>>>(x, w, b, y, mean, rstd, rows, H, eps);
+    // two chunks a thread; up to four workgroups per CU
+    const int threads = ceil_div(ceil_div(chunks, 2), 64) * 64;
+    const int per = ceil_div(rows, 1024), grid = ceil_div(rows, per);
+    k_norm_forward<T, 2, false><<<grid, threads, 0, st>>>(x, w, b, y, mean, rstd, rows, per, H, eps);
   } else {
-    k_norm_forward_long<T><<<rows, 1024, 0, st>>>(x, w, b, y, mean, rstd, H, eps);
+    k_norm_forward_long<T><<<rows < 4096 ? rows : 4096, 1024, 0, st>>>(x, w, b, y, mean, rstd, rows, H, eps);
   }
 }
 
 hipError_t launch_norm_forward(const void* x, const void* w, const void* b, void* y, float* mean, float* rstd,
                                int T, int H, float eps, bool bf16, hipStream_t st) {
-  // a grid has fewer than 2^32 threads: batches of rows, 2^21 workgroups of up to 1024 at a time
-  const int64_t row_bytes = (int64_t)H * (bf16 ? 2 : 4);
-  for (int t = 0; t < T;) {
-    const int n = T - t < (1 << 21) ? T - t : 1 << 21;
-    const void* xt = static_cast<const char*>(x) + t * row_bytes;
-    void* yt = static_cast<char*>(y) + t * row_bytes;
-    float *mt = mean ? mean + t : nullptr, *rt = rstd ? rstd + t : nullptr;
-    if (bf16) norm_forward<uint16_t>(xt, w, b, yt, mt, rt, n, H, eps, st);
-    else norm_forward<float>(xt, w, b, yt, mt, rt, n, H, eps, st);
-    t += n;
-  }
+  if (bf16) norm_forward<uint16_t>(x, w, b, y, mean, rstd, T, H, eps, st);
+  else norm_forward<float>(x, w, b, y, mean, rstd, T, H, eps, st);
   return hipGetLastError();
 }
 
@@ -254,31 +261,33 @@ __global__ __launch_bounds__(MAXT) void k_norm_backward(const T* __restrict__ dy
 template <typename T>
 __global__ __launch_bounds__(1024) void k_norm_dx_long(const T* __restrict__ dy, const T* __restrict__ x,
                                                        const T* __restrict__ w, const float* __restrict__ mean,
-                                                       const float* __restrict__ rstd, T* __restrict__ dx, int H) {
+                                                       const float* __restrict__ rstd, T* __restrict__ dx, int rows,
+                                                       int H) {
   __shared__ float s[2][16];
-  const int64_t row = blockIdx.x;
-  const float m = mean[row], r = rstd[row];
-  float vx[8], vd[8], vw[8], s1 = 0.f, s2 = 0.f;
-  for (int c = threadIdx.x * 8; c < H; c += 8192) {
-    load8(x + row * H + c, H - c, vx);
-    load8(dy + row * H + c, H - c, vd);
-    load8(w + c, H - c, vw);
+  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
+    const float m = mean[row], r = rstd[row];
+    float vx[8], vd[8], vw[8], s1 = 0.f, s2 = 0.f;
+    for (int c = threadIdx.x * 8; c < H; c += 8192) {
+      load8(x + row * H + c, H - c, vx);
+      load8(dy + row * H + c, H - c, vd);
+      load8(w + c, H - c, vw);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float e = vd[i] * vw[i];
-      s1 += e;
-      s2 += e * ((vx[i] - m) * r);
+      for (int i = 0; i < 8; ++i) {
+        const float e = vd[i] * vw[i];
+        s1 += e;
+        s2 += e * ((vx[i] - m) * r);
+      }
     }
-  }
-  s1 = block_sum(s1, s[0]) / H;
-  s2 = block_sum(s2, s[1]) / H;
-  for (int c = threadIdx.x * 8; c < H; c += 8192) {
-    load8(x + row * H + c, H - c, vx);
-    load8(dy + row * H + c, H - c, vd);
-    load8(w + c, H - c, vw);
+    s1 = block_sum(s1, s[0]) / H;
+    s2 = block_sum(s2, s[1]) / H;
+    for (int c = threadIdx.x * 8; c < H; c += 8192) {
+      load8(x + row * H + c, H - c, vx);
+      load8(dy + row * H + c, H - c, vd);
+      load8(w + c, H - c, vw);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) vx[i] = r * (vd[i] * vw[i] - s1 - (vx[i] - m) * r * s2);
-    store8(dx + row * H + c, H - c, vx);
+      for (int i = 0; i < 8; ++i) vx[i] = r * (vd[i] * vw[i] - s1 - (vx[i] - m) * r * s2);
+      store8(dx + row * H + c, H - c, vx);
+    }
   }
 }
 
@@ -312,8 +321,8 @@ static int rows_per_block(int T, int H) {
   int nch, threads;
   backward_shape(H, &nch, &threads);
   const int blocks = 256 * (threads >= 512 ? 1 : 512 / threads);
-  const int per = ceil_div(T, blocks);
-  return per > 8 ? per : T < 8 ? T : T < 2048 ? 4 : 8;
+  const int per = ceil_div(T, blocks), least = T < 4096 ? 4 : 8;
+  return per > least ? per : least;
 }
 int norm_row_blocks(int T, int H) { return ceil_div(T, rows_per_block(T, H)); }
 
@@ -326,6 +335,10 @@ static void norm_backward(const void* dy_, const void* x_, const void* w_, const
   int nch, threads;
   backward_shape(H, &nch, &threads);
   const int grid = ceil_div(rows, per);
+  if (nch == 1 && threads <= 256) {
+    k_norm_backward<T, 1, 4, 256><<<grid, threads, 0, st>>>(dy, x, w, mean, rstd, dx, part, rows, per, H);
+    return;
+  }
   if (nch == 1) {
     k_norm_backward<T, 1, sizeof(T) == 2 ? 2 : 1, 1024><<<grid, threads, 0, st>>>(dy, x, w, mean, rstd, dx, part, rows, per, H);
     return;
@@ -336,12 +349,7 @@ static void norm_backward(const void* dy_, const void* x_, const void* w_, const
       return;
     }
   }
-  if (dx)
-    for (int t = 0; t < rows; t += 1 << 21) {  // a grid has fewer than 2^32 threads
-      const int n = rows - t < (1 << 21) ? rows - t : 1 << 21;
-      const int64_t at = (int64_t)t * H;
-      k_norm_dx_long<T><<<n, 1024, 0, st>>>(dy + at, x + at, w, mean + t, rstd + t, dx + at, H);
-    }
+  if (dx) k_norm_dx_long<T><<<rows < 4096 ? rows : 4096, 1024, 0, st>>>(dy, x, w, mean, rstd, dx, rows, H);
   if (part)
     k_norm_dw_long<T><<<dim3(ceil_div(H, 256), ceil_div(rows, per)), 256, 0, st>>>(dy, x, mean, rstd, part, rows, per, H);
 }
