@@ -100,9 +100,10 @@ int64_t padded(const DenseDims& d, int cols) {
 
 // Backward: the gradient before the activation as operand of the products (three bf16 terms of
 // each value, lo elements apart, where fp32 weight gradients are asked for), and the row
-// blocks' column sums.  slices: the products' contraction slices.  x, w[2]: padded copies (0 bytes where the operand is read in place).
+// blocks' column sums.  slices, slices_w: the products' contraction
+// slices (dw's in slices_w).  x, w[2]: padded copies (0 bytes where the operand is read in place).
 struct DenseWs {
-  size_t x, w[2], d0, d1, part, slices, total;
+  size_t x, w[2], d0, d1, part, slices, slices_w, total;
   int terms;
   int64_t lo, ldk, ldn;
 };
@@ -127,15 +128,9 @@ DenseWs dense_ws(const DenseDims& d, bool gated, bool backward) {
   }
   if (d.T > 0 && !decode) {
     const int z = gated ? 2 : 1;
-    size_t n;
-    if (backward) {
-      const size_t dx = dense_part_bytes(d.bf16, d.T, d.K, d.N, z, 1, false);
-      const size_t dw = dense_part_bytes(d.bf16, d.N, d.K, d.T, w.terms, z, false);
-      n = dx > dw ? dx : dw;
-    } else {
-      n = dense_part_bytes(d.bf16, d.T, d.N, d.K, 1, 1, gated);
-    }
-    w.slices = c.take(n);
+    w.slices = c.take(backward ? dense_part_bytes(d.bf16, d.T, d.K, d.N, z, 1, false)
+                               : dense_part_bytes(d.bf16, d.T, d.N, d.K, 1, 1, gated));
+    w.slices_w = c.take(backward ? dense_part_bytes(d.bf16, d.N, d.K, d.T, w.terms, z, false) : 0);
   }
   w.total = c.cur;
   return w;
@@ -184,42 +179,39 @@ moe_status forward(const DenseDims& d, const DenseWs& w, const void* x, const vo
   return MOE_OK;
 }
 
-// dx = d0 w0 (+ d1 w1): the contraction runs over N, which is across the weights' rows.
-moe_status input_grad(const DenseDims& d, const DenseWs& w, const void* d0, const void* d1, const void* w0,
-                      const void* w1, void* dx, void* ws, hipStream_t st) {  // w0, w1 at row length w.ldk
-  DenseJob j{};
-  j.M = d.T; j.N = d.K; j.K = d.N;
-  j.segs = d1 ? 2 : 1; j.batch = 1;
-  j.b_col = true;
-  j.A[0][0] = d0; j.A[0][1] = d1; j.lda = w.ldn;
-  j.B[0][0] = w0; j.B[0][1] = w1; j.ldb = w.ldk;
-  DenseEpi e{};
-  e.kind = DENSE_STORE;
-  e.out_f32 = !d.bf16;
-  e.out[0] = dx;
-  MOE_HIP(launch_dense(j, e, d.bf16, at<float>(ws, w.slices), st));
-  return MOE_OK;
-}
-
-// dw_z = (sum of d_z's terms)^T x: the contraction runs over the tokens, across both operands' rows.
-moe_status weight_grad(const DenseDims& d, const DenseWs& w, const void* d0, const void* d1, int terms,
-                       const void* x, void* dw0, void* dw1, void* ws, hipStream_t st) {  // x at row length w.ldk
-  DenseJob j{};
-  j.M = d.N; j.N = d.K; j.K = d.T;
-  j.segs = terms; j.batch = d1 ? 2 : 1;
-  j.a_col = j.b_col = true;
+// dx = d0 w0 (+ d1 w1), the contraction over N, across the weights' rows, and dw_z = (sum of
+// d_z's terms)^T x, the contraction over the tokens, across both operands' rows.  dx or dw0
+// may be NULL.
+moe_status gradients(const DenseDims& d, const DenseWs& w, const void* d0, const void* d1, int terms, const void* x,
+                     const void* w0, const void* w1, void* dx, void* dw0, void* dw1, void* ws, hipStream_t st) {
+  MOE_TRY(in_rows(d, w, dw0 ? &x : nullptr, dx ? &w0 : nullptr, dx ? &w1 : nullptr, ws, st));
+  DenseJob jx{}, jw{};
+  DenseEpi ex{}, ew{};
+  jx.M = d.T; jx.N = d.K; jx.K = d.N;
+  jx.segs = d1 ? 2 : 1; jx.batch = 1;
+  jx.b_col = true;
+  jx.A[0][0] = d0; jx.A[0][1] = d1; jx.lda = w.ldn;
+  jx.B[0][0] = w0; jx.B[0][1] = w1; jx.ldb = w.ldk;
+  ex.kind = DENSE_STORE;
+  ex.out_f32 = !d.bf16;
+  ex.out[0] = dx;
+  jw.M = d.N; jw.N = d.K; jw.K = d.T;
+  jw.segs = terms; jw.batch = d1 ? 2 : 1;
+  jw.a_col = jw.b_col = true;
   for (int q = 0; q < terms; ++q) {
-    j.A[0][q] = static_cast<const char*>(d0) + q * w.lo * d.es;
-    if (d1) j.A[1][q] = static_cast<const char*>(d1) + q * w.lo * d.es;
-    j.B[0][q] = j.B[1][q] = x;
+    jw.A[0][q] = static_cast<const char*>(d0) + q * w.lo * d.es;
+    if (d1) jw.A[1][q] = static_cast<const char*>(d1) + q * w.lo * d.es;
+    jw.B[0][q] = jw.B[1][q] = x;
   }
-  j.lda = w.ldn;
-  j.ldb = w.ldk;
-  DenseEpi e{};
-  e.kind = DENSE_STORE;
-  e.out_f32 = d.grad_f32;
-  e.out[0] = dw0; e.out[1] = dw1;
-  MOE_HIP(launch_dense(j, e, d.bf16, at<float>(ws, w.slices), st));
+  jw.lda = w.ldn;
+  jw.ldb = w.ldk;
+  ew.kind = DENSE_STORE;
+  ew.out_f32 = d.grad_f32;
+  ew.out[0] = dw0; ew.out[1] = dw1;
+  float *px = at<float>(ws, w.slices), *pw = at<float>(ws, w.slices_w);
+  if (dx && dw0) MOE_HIP(launch_dense_two(jx, ex, jw, ew, d.bf16, px, pw, st));
+  else if (dx) MOE_HIP(launch_dense(jx, ex, d.bf16, px, st));
+  else MOE_HIP(launch_dense(jw, ew, d.bf16, pw, st));
   return MOE_OK;
 }
 
@@ -342,10 +334,9 @@ moe_status moe_gated_backward(const void* dh, const void* x, const void* w1, con
   }
   const int terms = dw1 ? w.terms : 1;
   void *d0 = at<void>(ws, w.d0), *d1 = at<void>(ws, w.d1);
-  MOE_HIP(launch_act_grad(dh, g, u, d.act, d.bf16, d.T, d.N, d0, d1, terms, w.lo, w.ldn, nullptr, st));
-  MOE_TRY(in_rows(d, w, dw1 ? &x : nullptr, dx ? &w1 : nullptr, dx ? &w3 : nullptr, ws, st));
-  if (dx) MOE_TRY(input_grad(d, w, d0, d1, w1, w3, dx, ws, st));
-  return dw1 ? weight_grad(d, w, d0, d1, terms, x, dw1, dw3, ws, st) : MOE_OK;
+  MOE_HIP(launch_act_grad(dh, g, u, d.act, d.bf16, d.T, d.N, d0, d1, terms, w.lo, w.ldn, nullptr, nullptr,
+                          false, st));
+  return gradients(d, w, d0, d1, terms, x, w1, w3, dx, dw1, dw3, ws, st);
 }
 
 moe_status moe_linear_forward(const void* x, const void* w, const void* bias, const void* residual, void* y,
@@ -399,18 +390,11 @@ moe_status moe_linear_backward(const void* dy, const void* x, const void* w, con
   const bool operand = (through || p.ldn != d.N) && (dx || dw);
   void* d0 = operand ? at<void>(ws, p.d0) : nullptr;
   const int terms = dw ? p.terms : 1;
-  float* part = dbias ? at<float>(ws, p.part) : nullptr;
-  if (operand || dbias) {
+  if (operand || dbias)
     MOE_HIP(launch_act_grad(dy, through ? z : nullptr, nullptr, d.act, d.bf16, d.T, d.N, d0, nullptr, terms, p.lo,
-                            p.ldn, part, st));
-    if (dbias)
-      MOE_HIP(launch_col_sum(part, grad_row_blocks(d.T, d.N), d.N, d.N, dbias, nullptr, d.grad_f32, st));
-  }
+                            p.ldn, at<float>(ws, p.part), dbias, d.grad_f32, st));
   if (!dx && !dw) return MOE_OK;
-  const void* dz = operand ? d0 : dy;
-  MOE_TRY(in_rows(d, p, dw ? &x : nullptr, dx ? &w : nullptr, nullptr, ws, st));
-  if (dx) MOE_TRY(input_grad(d, p, dz, nullptr, w, nullptr, dx, ws, st));
-  return dw ? weight_grad(d, p, dz, nullptr, terms, x, dw, nullptr, ws, st) : MOE_OK;
+  return gradients(d, p, operand ? d0 : dy, nullptr, terms, x, w, nullptr, dx, dw, nullptr, ws, st);
 }
 
 }  // extern "C"

@@ -1,4 +1,6 @@
 // Gradients before an activation, column sums and zero fills of the dense backward passes.
+#include <type_traits>
+
 #include "dense_device.h"
 #include "dense_kernels.h"
 
@@ -23,7 +25,8 @@ template <typename T, bool GATED>
 __global__ __launch_bounds__(256) void k_act_grad(const T* __restrict__ dh, const T* __restrict__ g,
                                                   const T* __restrict__ u, int act, int rows, int N,
                                                   T* __restrict__ d0, T* __restrict__ d1, int terms, int64_t lo,
-                                                  int64_t ld, float* __restrict__ part) {
+                                                  int64_t ld, float* __restrict__ part, void* __restrict__ out,
+                                                  bool out_f32) {
   constexpr bool FAST = sizeof(T) == 2;
   const int tid = threadIdx.x, cl = tid & 31, sub = tid >> 5;
   const int c0 = (int)blockIdx.x * kGradCols + cl * 8;
@@ -73,24 +76,11 @@ __global__ __launch_bounds__(256) void k_act_grad(const T* __restrict__ dh, cons
       float v = 0.f;
 #pragma unroll
       for (int q = 0; q < kGradSub; ++q) v += s[q][tid];
-      part[(int64_t)blockIdx.y * N + n] = v;
+      if (gridDim.y > 1) part[(int64_t)blockIdx.y * N + n] = v;
+      else if (out_f32) static_cast<float*>(out)[n] = v;
+      else static_cast<uint16_t*>(out)[n] = f32_to_bf16(v);
     }
   }
-}
-
-hipError_t launch_act_grad(const void* dh, const void* g, const void* u, int act, bool bf16, int T, int N,
-                           void* d0, void* d1, int terms, int64_t lo, int64_t ld, float* part, hipStream_t st) {
-  const dim3 grid(ceil_div(N, kGradCols), grad_row_blocks(T, N));
-  auto go = [&](auto* t) {
-    using E = std::remove_pointer_t<decltype(t)>;
-    const E *a = static_cast<const E*>(dh), *b = static_cast<const E*>(g), *c = static_cast<const E*>(u);
-    E *p0 = static_cast<E*>(d0), *p1 = static_cast<E*>(d1);
-    if (u) k_act_grad<E, true><<<grid, 256, 0, st>>>(a, b, c, act, T, N, p0, p1, terms, lo, ld, part);
-    else k_act_grad<E, false><<<grid, 256, 0, st>>>(a, b, c, act, T, N, p0, p1, terms, lo, ld, part);
-  };
-  if (bf16) go(static_cast<uint16_t*>(nullptr));
-  else go(static_cast<float*>(nullptr));
-  return hipGetLastError();
 }
 
 // Column n of the partial sums: 16 groups of the P rows (each in ascending order, four loads at
@@ -124,6 +114,24 @@ hipError_t launch_col_sum(const float* part, int P, int N, int64_t stride, void*
                           hipStream_t st) {
   k_col_sum<<<dim3(ceil_div(N, 64), out1 ? 2 : 1), 1024, 0, st>>>(part, P, N, stride, out0, out1, out_f32);
   return hipGetLastError();
+}
+
+hipError_t launch_act_grad(const void* dh, const void* g, const void* u, int act, bool bf16, int T, int N,
+                           void* d0, void* d1, int terms, int64_t lo, int64_t ld, float* part, void* sum, bool sum_f32,
+                           hipStream_t st) {
+  const dim3 grid(ceil_div(N, kGradCols), grad_row_blocks(T, N));
+  if (!sum) part = nullptr;
+  auto go = [&](auto* t) {
+    using E = std::remove_pointer_t<decltype(t)>;
+    const E *a = static_cast<const E*>(dh), *b = static_cast<const E*>(g), *c = static_cast<const E*>(u);
+    E *p0 = static_cast<E*>(d0), *p1 = static_cast<E*>(d1);
+    if (u) k_act_grad<E, true><<<grid, 256, 0, st>>>(a, b, c, act, T, N, p0, p1, terms, lo, ld, part, sum, sum_f32);
+    else k_act_grad<E, false><<<grid, 256, 0, st>>>(a, b, c, act, T, N, p0, p1, terms, lo, ld, part, sum, sum_f32);
+  };
+  if (bf16) go(static_cast<uint16_t*>(nullptr));
+  else go(static_cast<float*>(nullptr));
+  if (const hipError_t r = hipGetLastError(); r != hipSuccess || !sum || grid.y == 1) return r;
+  return launch_col_sum(part, (int)grid.y, N, N, sum, nullptr, sum_f32, st);
 }
 
 // Eight elements of a padded row per thread (fp32 rows may end in half of them).

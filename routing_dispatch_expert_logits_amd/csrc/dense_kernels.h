@@ -49,16 +49,21 @@ hipError_t launch_dense_decode(const DenseJob& j, const DenseEpi& e, bool bf16, 
 // sums meet in `part`, dense_part_bytes of scratch for the same sizes.
 size_t dense_part_bytes(bool bf16, int M, int N, int K, int segs, int batch, bool pair);
 hipError_t launch_dense(const DenseJob& j, const DenseEpi& e, bool bf16, float* part, hipStream_t st);
+// A backward pass's dx and dw products, in one launch where both are small; each with its scratch.
+hipError_t launch_dense_two(const DenseJob& jx, const DenseEpi& ex, const DenseJob& jw, const DenseEpi& ew, bool bf16,
+                            float* part_x, float* part_w, hipStream_t st);
 
 // The gradient before an activation, [T x N]:
 //   linear (dh == dy, u == NULL): d0 = dy act'(g);  gated: d0 = dh u act'(g), d1 = dh act(g).
 // d0, d1 (nullable) get them in the layer's type with rows of ld elements.  With terms = 3
 // (bf16) the second and third bf16 terms of each value follow at d + lo and d + 2 lo: the
-// three hold its 24 bits exactly.  part (nullable) receives fp32 column sums of the
-// unrounded d0, one row of N for each of the grad_row_blocks(T, N) row blocks.
+// three hold its 24 bits exactly.  sum (nullable) receives the column sums of the unrounded d0
+// (fp32 or bf16), by way of part: a row of N floats for each of the grad_row_blocks(T, N) row
+// blocks.
 int grad_row_blocks(int T, int N);
 hipError_t launch_act_grad(const void* dh, const void* g, const void* u, int act, bool bf16, int T, int N,
-                           void* d0, void* d1, int terms, int64_t lo, int64_t ld, float* part, hipStream_t st);
+                           void* d0, void* d1, int terms, int64_t lo, int64_t ld, float* part, void* sum, bool sum_f32,
+                           hipStream_t st);
 // out0[n] = sum_p part[p * stride + n], out1[n] = sum_p part[p * stride + N + n] for n < N (each
 // nullable), in a fixed order; in fp32 or bf16.
 hipError_t launch_col_sum(const float* part, int P, int N, int64_t stride, void* out0, void* out1, bool out_f32,

@@ -145,9 +145,9 @@ __device__ __forceinline__ void with_act(int act, F&& f) {
 // the 8 XCDs in contiguous chunks, within which groups of 8 m-tiles run down their n-tiles, so
 // that the tiles an XCD works on at a time share rows and columns in its L2.
 struct MmWhere { int mt, nt, z, slice; bool ok; };
-__device__ __forceinline__ MmWhere mm_where(int tm, int tn, int batch, int slices) {
+__device__ __forceinline__ MmWhere mm_where(int block, int tm, int tn, int batch, int slices) {
   const int total = tm * tn * batch * slices, per = ceil_div(total, 8);
-  const int slot = blockIdx.x >> 3, L = (blockIdx.x & 7) * per + slot;
+  const int slot = block >> 3, L = (block & 7) * per + slot;
   MmWhere w{0, 0, 0, 0, slot < per && L < total};
   const int q = L / (tm * tn);
   w.slice = q / batch;
@@ -179,8 +179,11 @@ constexpr int mm_waitcnt(int n) { return (n & 0xF) | ((n >> 4) << 14) | (0x7 << 
 //
 // The stages are separate arrays, used in an unrolled ring: the compiler then knows which
 // loads into LDS a read has to wait for, and waits for no later ones.
+template <int BM, int BN>
+constexpr int kMmStage = (BM + BN) * kStepBytes / 2;  // 16-bit words of a stage
 template <typename T, int BM, int BN, int WM, int WN, int S, bool A_COL, bool B_COL, bool PAIR, int KIND>
-__global__ __launch_bounds__(WM* WN * 64, 2) void k_dense_mm(DenseJob j, DenseEpi e, MmSlices sl) {
+__device__ __forceinline__ void mm_body(const DenseJob& j, const DenseEpi& e, const MmSlices& sl, int block,
+                                        uint16_t* s0, uint16_t* s1, uint16_t* s2, uint16_t* s3) {
   using TA = MmTile<T, BM, A_COL>;
   using TB = MmTile<T, BN, B_COL>;
   constexpr int ES = sizeof(T), BK = kStepBytes / ES;
@@ -189,10 +192,9 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void k_dense_mm(DenseJob j, DenseEp
   constexpr int ON = PAIR ? BN / 2 : BN;   // output columns of a tile
   static_assert(QA >= 1 && QB >= 1 && !(PAIR && (B_COL || FN % 2)), "tile");
   static_assert(S >= 2 && S <= 4, "stages");
-  constexpr int STAGE = TA::HALFS + TB::HALFS;
-  __shared__ __attribute__((aligned(1024))) uint16_t s0[STAGE], s1[STAGE], s2[S > 2 ? STAGE : 1], s3[S > 3 ? STAGE : 1];
+  constexpr int STAGE = kMmStage<BM, BN>;
 
-  const MmWhere w = mm_where(ceil_div(j.M, BM), ceil_div(j.N, ON), j.batch, sl.slices);
+  const MmWhere w = mm_where(block, ceil_div(j.M, BM), ceil_div(j.N, ON), j.batch, sl.slices);
   if (!w.ok) return;
   const int m0 = uniform(w.mt * BM), n0 = uniform(w.nt * ON), z = uniform(w.z);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -406,6 +408,26 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void k_dense_mm(DenseJob j, DenseEp
   }
 }
 
+template <typename T, int BM, int BN, int WM, int WN, int S, bool A_COL, bool B_COL, bool PAIR, int KIND>
+__global__ __launch_bounds__(WM* WN * 64, 2) void k_dense_mm(DenseJob j, DenseEpi e, MmSlices sl) {
+  constexpr int STAGE = kMmStage<BM, BN>;
+  __shared__ __attribute__((aligned(1024))) uint16_t s0[STAGE], s1[STAGE], s2[S > 2 ? STAGE : 1], s3[S > 3 ? STAGE : 1];
+  mm_body<T, BM, BN, WM, WN, S, A_COL, B_COL, PAIR, KIND>(j, e, sl, blockIdx.x, s0, s1, s2, s3);
+}
+
+// A small backward pass's two products, dx on the first `first` workgroups and dw on the others:
+// neither fills the device, and a launch of its own costs each about 5 us.
+template <typename T, int S>
+__global__ __launch_bounds__(256, 2) void k_dense_mm_two(DenseJob jx, DenseEpi ex, MmSlices sx, int first, DenseJob jw,
+                                                         DenseEpi ew, MmSlices sw) {
+  constexpr int STAGE = kMmStage<64, 64>;
+  __shared__ __attribute__((aligned(1024))) uint16_t s0[STAGE], s1[STAGE], s2[STAGE], s3[S > 3 ? STAGE : 1];
+  if ((int)blockIdx.x < first)
+    mm_body<T, 64, 64, 2, 2, S, false, true, false, DENSE_STORE>(jx, ex, sx, blockIdx.x, s0, s1, s2, s3);
+  else
+    mm_body<T, 64, 64, 2, 2, S, true, true, false, DENSE_STORE>(jw, ew, sw, blockIdx.x - first, s0, s1, s2, s3);
+}
+
 // The slices' sums in ascending order, then the epilogue; eight columns per thread.
 template <typename T, int KIND>
 __global__ __launch_bounds__(256) void k_dense_join(int M, int N, int batch, DenseEpi e, MmSlices sl) {
@@ -429,10 +451,15 @@ __global__ __launch_bounds__(256) void k_dense_join(int M, int N, int batch, Den
   }
 }
 
+// Workgroups of a product: its tiles' slices, a whole number for each of the 8 XCDs.
+static unsigned mm_grid(const DenseJob& j, const MmSlices& sl, int bm, int bn) {
+  const int64_t items = (int64_t)ceil_div(j.M, bm) * ceil_div(j.N, j.pair ? bn / 2 : bn) * j.batch * sl.slices;
+  return (unsigned)((items + 7) / 8 * 8);
+}
+
 template <typename T, int BM, int BN, int WM, int WN, int S>
 static void mm_go(const DenseJob& j, const DenseEpi& e, const MmSlices& sl, hipStream_t st) {
-  const int64_t items = (int64_t)ceil_div(j.M, BM) * ceil_div(j.N, j.pair ? BN / 2 : BN) * j.batch * sl.slices;
-  const dim3 grid((unsigned)((items + 7) / 8 * 8)), block(WM * WN * 64);
+  const dim3 grid(mm_grid(j, sl, BM, BN)), block(WM * WN * 64);
   if (j.pair) k_dense_mm<T, BM, BN, WM, WN, S, false, false, true, DENSE_GATED><<<grid, block, 0, st>>>(j, e, sl);
   else if (e.kind == DENSE_LINEAR) k_dense_mm<T, BM, BN, WM, WN, S, false, false, false, DENSE_LINEAR><<<grid, block, 0, st>>>(j, e, sl);
   else if (!j.a_col) k_dense_mm<T, BM, BN, WM, WN, S, false, true, false, DENSE_STORE><<<grid, block, 0, st>>>(j, e, sl);
@@ -490,18 +517,22 @@ size_t dense_part_bytes(bool bf16, int M, int N, int K, int segs, int batch, boo
 }
 
 template <typename T>
-static hipError_t mm_join(const DenseJob& j, const DenseEpi& e, const MmSlices& sl, hipStream_t st) {
+static void mm_join(const DenseJob& j, const DenseEpi& e, const MmSlices& sl, hipStream_t st) {
   const int64_t want = ((int64_t)j.batch * j.M * (sl.ldp / 8) + 255) / 256;
   const unsigned grid = (unsigned)(want < 4096 ? want : 4096);
   if (j.pair) k_dense_join<T, DENSE_GATED><<<grid, 256, 0, st>>>(j.M, j.N, j.batch, e, sl);
   else if (e.kind == DENSE_LINEAR) k_dense_join<T, DENSE_LINEAR><<<grid, 256, 0, st>>>(j.M, j.N, j.batch, e, sl);
   else k_dense_join<T, DENSE_STORE><<<grid, 256, 0, st>>>(j.M, j.N, j.batch, e, sl);
-  return hipGetLastError();
+}
+
+static MmPlan plan_of(const DenseJob& j, bool bf16) { return mm_plan(bf16, j.M, j.N, j.K, j.segs, j.batch, j.pair); }
+static MmSlices slices_of(const MmPlan& p, float* part) {
+  return MmSlices{p.slices > 1 ? part : nullptr, p.slices, p.planes, p.ldp};
 }
 
 hipError_t launch_dense(const DenseJob& j, const DenseEpi& e, bool bf16, float* part, hipStream_t st) {
-  const MmPlan p = mm_plan(bf16, j.M, j.N, j.K, j.segs, j.batch, j.pair);
-  const MmSlices sl{p.slices > 1 ? part : nullptr, p.slices, p.planes, p.ldp};
+  const MmPlan p = plan_of(j, bf16);
+  const MmSlices sl = slices_of(p, part);
   const int bm = p.tile.bm, bn = p.tile.bn;
   if (!bf16) {
     mm_go<float, 64, 64, 2, 2, 3>(j, e, sl, st);
@@ -514,8 +545,33 @@ hipError_t launch_dense(const DenseJob& j, const DenseEpi& e, bool bf16, float* 
   } else {
     mm_go<uint16_t, 64, 64, 2, 2, 4>(j, e, sl, st);
   }
-  if (const hipError_t r = hipGetLastError(); r != hipSuccess || p.slices == 1) return r;
-  return bf16 ? mm_join<uint16_t>(j, e, sl, st) : mm_join<float>(j, e, sl, st);
+  if (hipError_t r = hipGetLastError(); r != hipSuccess || p.slices == 1) return r;
+  if (bf16) mm_join<uint16_t>(j, e, sl, st);
+  else mm_join<float>(j, e, sl, st);
+  return hipGetLastError();
+}
+
+hipError_t launch_dense_two(const DenseJob& jx, const DenseEpi& ex, const DenseJob& jw, const DenseEpi& ew, bool bf16,
+                            float* part_x, float* part_w, hipStream_t st) {
+  const MmPlan px = plan_of(jx, bf16), pw = plan_of(jw, bf16);
+  if (px.tile.bm != 64 || pw.tile.bm != 64) {
+    if (hipError_t r = launch_dense(jx, ex, bf16, part_x, st); r != hipSuccess) return r;
+    return launch_dense(jw, ew, bf16, part_w, st);
+  }
+  const MmSlices sx = slices_of(px, part_x), sw = slices_of(pw, part_w);
+  const unsigned first = mm_grid(jx, sx, 64, 64), all = first + mm_grid(jw, sw, 64, 64);
+  if (bf16) k_dense_mm_two<uint16_t, 4><<<all, 256, 0, st>>>(jx, ex, sx, (int)first, jw, ew, sw);
+  else k_dense_mm_two<float, 3><<<all, 256, 0, st>>>(jx, ex, sx, (int)first, jw, ew, sw);
+  if (hipError_t r = hipGetLastError(); r != hipSuccess) return r;
+  if (px.slices > 1) {
+    if (bf16) mm_join<uint16_t>(jx, ex, sx, st);
+    else mm_join<float>(jx, ex, sx, st);
+  }
+  if (pw.slices > 1) {
+    if (bf16) mm_join<uint16_t>(jw, ew, sw, st);
+    else mm_join<float>(jw, ew, sw, st);
+  }
+  return hipGetLastError();
 }
 
 }  // namespace moe
