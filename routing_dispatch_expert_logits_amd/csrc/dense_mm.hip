@@ -11,7 +11,6 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) void* lds_dst;
 typedef __attribute__((address_space(3))) s16x4* lds_s16x4;
 
-constexpr int kStepBytes = 128;                // contraction step: 64 bf16 or 32 fp32 elements
 constexpr uint32_t kOutOfRange = 0x80000000u;  // a lane offset no buffer of ours reaches: reads 0
 
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
@@ -21,13 +20,14 @@ __device__ __forceinline__ const char* uniform(const char* p) {
 }
 
 // A tile of R rows (m or n) by one contraction step in LDS, filled by 16-byte buffer loads
-// straight into LDS (1 KB per instruction, lane i to byte 16 i) and read as MFMA operands in two
-// halves: lane l holds row l % 16, the (l / 16)-th 16 bytes of the half's contraction elements.
+// straight into LDS (1 KB per instruction, lane i to byte 16 i) and read as MFMA operands in
+// pieces of 64 bytes of contraction, of which a step has one or two (SB = 64 or 128): lane l
+// holds row l % 16, the (l / 16)-th 16 bytes of the piece's contraction elements.
 // For bf16 that is one instruction's operand; for fp32 the i-th of four instructions takes
 // element i of every lane's four, an order of the contraction that both sides share.
 //
-// Row operands (contraction along memory): LDS row r is 128 bytes, its 16-byte chunk c sits at
-// slot c ^ (r & 7), so the 16 rows one ds_read_b128 touches at one chunk index cover all banks.
+// Row operands (contraction along memory): LDS row r is SB bytes, its 16-byte chunk c sits at
+// slot c ^ swz(r), so the 16 rows one ds_read_b128 touches at one chunk index cover all banks.
 //
 // bf16 column operands (contraction across memory): LDS row k holds R elements, and
 // ds_read_b64_tr_b16 turns 4 x 16 blocks into operand order: of each 16 lanes, lane i reads
@@ -35,13 +35,17 @@ __device__ __forceinline__ const char* uniform(const char* p) {
 // of row k sits at u ^ f(k) with f(k) = (k & 3) | (k >> 1 & 4), which spreads the 16 rows one
 // instruction touches over all banks.  fp32 column operands are read a dword per element, 16
 // lanes to a 64-byte unit of one row; unit u of row k sits at u ^ (k >> 2 & 3).
-template <typename T, int R, bool COL>
+template <typename T, int R, bool COL, int SB>
 struct MmTile {
   static constexpr int ES = sizeof(T);
-  static constexpr int HALFS = R * kStepBytes / 2;  // 16-bit words of the tile
-  static constexpr int INSTR = R / 8;               // fill instructions
-  static constexpr int CPR = R * ES / 16;           // column operand: 16-byte chunks per LDS row
-  static constexpr int UC = ES;                     // and chunks per unit (16 elements)
+  static constexpr int HALFS = R * SB / 2;       // 16-bit words of the tile
+  static constexpr int INSTR = R * SB / 1024;    // fill instructions
+  static constexpr int CPR = R * ES / 16;        // column operand: 16-byte chunks per LDS row
+  static constexpr int UC = ES;                  // and chunks per unit (16 elements)
+  static constexpr int RC = SB / 16, RPI = 64 / RC;  // row operand: chunks per LDS row, rows per instruction
+  static __device__ __forceinline__ int swz(int r) { return SB == 128 ? r & 7 : (r >> 1) & 3; }
+  // Row operand: the chunk of its row that a lane fills.
+  static __device__ __forceinline__ int chunk(int lane) { return (lane % RC) ^ swz(lane / RC); }
   static __device__ __forceinline__ int f(int k) {
     return (ES == 2 ? (k & 3) | ((k >> 1) & 4) : (k >> 2) & 3) & (R / 16 - 1);
   }
@@ -55,12 +59,12 @@ struct MmTile {
       const int chunk = ((s / UC) ^ f(k)) * UC + s % UC;
       return (uint32_t)(k * ld * ES + chunk * 16);
     } else {
-      const int r = q * 8 + (lane >> 3);
-      return r < valid ? (uint32_t)(r * ld * ES + (((lane & 7) ^ (lane >> 3)) << 4)) : kOutOfRange;
+      const int r = q * RPI + lane / RC;
+      return r < valid ? (uint32_t)(r * ld * ES + (chunk(lane) << 4)) : kOutOfRange;
     }
   }
 
-  // Operand of rows row0 + 16 i .. + 16 (row0 a multiple of 16), contraction half h, of the tile
+  // Operand of rows row0 + 16 i .. + 16 (row0 a multiple of 16), contraction piece h, of the tile
   // at 16-bit word `at` of a stage.  One pointer addition from the stage's array: the compiler
   // follows only a few when it derives what a read can alias.
   static __device__ __forceinline__ u32x4 read(const uint16_t* stage, int at, int row0, int i, int h, int lane) {
@@ -81,7 +85,7 @@ struct MmTile {
       return __builtin_bit_cast(u32x4, v);
     } else {
       const int r = row0 + (lane & 15);
-      const int o = at + (r + 16 * i) * (kStepBytes / 2) + (((4 * h + (lane >> 4)) ^ (lane & 7)) << 3);
+      const int o = at + (r + 16 * i) * (SB / 2) + (((4 * h + (lane >> 4)) ^ swz(lane & 15)) << 3);
       return *reinterpret_cast<const u32x4*>(stage + o);
     }
   }
@@ -179,20 +183,24 @@ constexpr int mm_waitcnt(int n) { return (n & 0xF) | ((n >> 4) << 14) | (0x7 << 
 //
 // The stages are separate arrays, used in an unrolled ring: the compiler then knows which
 // loads into LDS a read has to wait for, and waits for no later ones.
-template <int BM, int BN>
-constexpr int kMmStage = (BM + BN) * kStepBytes / 2;  // 16-bit words of a stage
-template <typename T, int BM, int BN, int WM, int WN, int S, bool A_COL, bool B_COL, bool PAIR, int KIND>
+//
+// Steps of 128 bytes: all waves read a stage's operands and multiply at their own pace, one
+// barrier per step.  Steps of 64 bytes (8 waves, two per SIMD): the waves of a SIMD take turns,
+// one reading a step's operands while the other multiplies, a barrier after each turn.
+template <int BM, int BN, int SB>
+constexpr int kMmStage = (BM + BN) * SB / 2;  // 16-bit words of a stage
+template <typename T, int BM, int BN, int WM, int WN, int S, int SB, bool A_COL, bool B_COL, bool PAIR, int KIND>
 __device__ __forceinline__ void mm_body(const DenseJob& j, const DenseEpi& e, const MmSlices& sl, int block,
                                         uint16_t* s0, uint16_t* s1, uint16_t* s2, uint16_t* s3) {
-  using TA = MmTile<T, BM, A_COL>;
-  using TB = MmTile<T, BN, B_COL>;
-  constexpr int ES = sizeof(T), BK = kStepBytes / ES;
+  using TA = MmTile<T, BM, A_COL, SB>;
+  using TB = MmTile<T, BN, B_COL, SB>;
+  constexpr int ES = sizeof(T), BK = SB / ES;
   constexpr int W = WM * WN, TM = BM / WM, TN = BN / WN, FM = TM / 16, FN = TN / 16;
   constexpr int QA = TA::INSTR / W, QB = TB::INSTR / W;
   constexpr int ON = PAIR ? BN / 2 : BN;   // output columns of a tile
   static_assert(QA >= 1 && QB >= 1 && !(PAIR && (B_COL || FN % 2)), "tile");
   static_assert(S >= 2 && S <= 4, "stages");
-  constexpr int STAGE = kMmStage<BM, BN>;
+  constexpr int STAGE = kMmStage<BM, BN, SB>;
 
   const MmWhere w = mm_where(block, ceil_div(j.M, BM), ceil_div(j.N, ON), j.batch, sl.slices);
   if (!w.ok) return;
@@ -211,7 +219,7 @@ __device__ __forceinline__ void mm_body(const DenseJob& j, const DenseEpi& e, co
 #pragma unroll
   for (int q = 0; q < QB; ++q)
     vb[q] = TB::src((PAIR ? wave % (W / 2) : wave) * QB + q, lane, j.ldb, j.N - n0);
-  const int kchunk = ((lane & 7) ^ (lane >> 3)) * (16 / ES);  // row operands: this lane's first element in a step
+  const int kchunk = TA::chunk(lane) * (16 / ES);  // row operands: this lane's first element in a step
   // of the next step to load: where the tile starts and how many bytes from there are the
   // operand's (whole rows of it, none past its last one)
   const char *pa, *pb;
@@ -226,10 +234,10 @@ __device__ __forceinline__ void mm_body(const DenseJob& j, const DenseEpi& e, co
   };
   auto advance = [&](int n) __attribute__((always_inline)) {
     left -= n * BK;
-    pa += n * (A_COL ? (int64_t)kStepBytes * j.lda : kStepBytes);
-    pb += n * (B_COL ? (int64_t)kStepBytes * j.ldb : kStepBytes);
-    na -= n * kStepBytes;
-    nb -= n * kStepBytes;
+    pa += n * (A_COL ? (int64_t)SB * j.lda : SB);
+    pb += n * (B_COL ? (int64_t)SB * j.ldb : SB);
+    na -= n * SB;
+    nb -= n * SB;
   };
   // The next step's loads.  Past the last step they are issued all the same with an empty
   // buffer (zeros, no memory read), so that the count of loads in flight is the same at every
@@ -263,7 +271,7 @@ __device__ __forceinline__ void mm_body(const DenseJob& j, const DenseEpi& e, co
     for (int b = 0; b < FN; ++b) acc[a][b] = f32x4{0.f, 0.f, 0.f, 0.f};
   auto multiply = [&](const uint16_t* st) __attribute__((always_inline)) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int h = 0; h < SB / 64; ++h) {
       u32x4 fb[FN];
 #pragma unroll
       for (int b = 0; b < FN; ++b) {
@@ -310,12 +318,68 @@ __device__ __forceinline__ void mm_body(const DenseJob& j, const DenseEpi& e, co
     multiply(cur);
   };
 
+  // The same in turns.  In a wave's reading turn of step s it issues the loads of step s + 3 into
+  // the stage of step s - 1 (whose readers are done: the other wave's turn ended with the last
+  // barrier) and reads its operands; in the next turn it multiplies.  The early waves read step
+  // s + 1 two turns after they read s, so every wave's loads of it must have landed (with the 2
+  // later steps' in flight) by the end of the turn between: there the early waves multiply and
+  // the late ones read.
+  const bool late = wave >= W / 2;
+  auto turn = [&](const uint16_t* cur, uint16_t* last) __attribute__((always_inline)) {
+    constexpr int flight = 2 * (QA + QB);
+    u32x4 fa[FM], fb[FN];
+    fill(last);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int b = 0; b < FN; ++b)
+      fb[b] = TB::read(cur, TA::HALFS, PAIR ? wn * (TN / 2) + (b / (FN / 2)) * ON : wn * TN, PAIR ? b % (FN / 2) : b, 0, lane);
+#pragma unroll
+    for (int a = 0; a < FM; ++a) fa[a] = TA::read(cur, 0, wm * TM, a, 0, lane);
+    __builtin_amdgcn_sched_barrier(0);
+    if (late) __builtin_amdgcn_s_waitcnt(mm_waitcnt(flight));
+    else __builtin_amdgcn_s_waitcnt(mm_waitcnt(63));
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+    for (int a = 0; a < FM; ++a)
+#pragma unroll
+      for (int b = 0; b < FN; ++b)
+        acc[a][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(fb[b]), as_bf16x8(fa[a]), acc[a][b], 0, 0, 0);
+    __builtin_amdgcn_s_setprio(0);
+    __builtin_amdgcn_sched_barrier(0);
+    if (!late) __builtin_amdgcn_s_waitcnt(mm_waitcnt(flight));
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+  };
+
   segment();
   advance(first - seg * nk);
   fill(s0);
   if (S > 2) fill(s1);
   if (S > 3) fill(s2);
-  if constexpr (S == 2) {
+  if constexpr (SB == 64) {
+    static_assert(S == 4 && W == 8 && ES == 2, "turns");
+    __builtin_amdgcn_s_waitcnt(mm_waitcnt(2 * (QA + QB)));
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    if (late) __builtin_amdgcn_s_barrier();  // a turn behind
+    asm volatile("" ::: "memory");
+    int s = 0;
+    for (; s + S <= steps; s += S) {
+      turn(s0, s3);
+      turn(s1, s0);
+      turn(s2, s1);
+      turn(s3, s2);
+    }
+    if (s < steps) turn(s0, s3);
+    if (s + 1 < steps) turn(s1, s0);
+    if (s + 2 < steps) turn(s2, s1);
+    if (!late) __builtin_amdgcn_s_barrier();
+  } else if constexpr (S == 2) {
     for (int s = 0;;) {
       step(s0, s1);
       if (++s >= steps) break;
@@ -355,8 +419,8 @@ __device__ __forceinline__ void mm_body(const DenseJob& j, const DenseEpi& e, co
   uint16_t* stage = wave < PER ? s0 : wave < 2 * PER ? s1 : wave < 3 * PER ? s2 : s3;
   float* reg = reinterpret_cast<float*>(stage) + (wave % PER) * (PM * TN);
   const int nw = n0 + wn * OC, lr = lane / LPR, lc = lane % LPR;
-#pragma unroll
-  for (int p = 0; p < PASSES; ++p) {
+  auto pass = [&](auto which) __attribute__((always_inline)) {
+    constexpr int p = which();
 #pragma unroll
     for (int a = 0; a < PF; ++a)
 #pragma unroll
@@ -405,14 +469,16 @@ __device__ __forceinline__ void mm_body(const DenseJob& j, const DenseEpi& e, co
     }
     asm volatile("" ::: "memory");
     __builtin_amdgcn_wave_barrier();
-  }
+  };
+  pass(std::integral_constant<int, 0>{});
+  if constexpr (PASSES > 1) pass(std::integral_constant<int, 1>{});
 }
 
-template <typename T, int BM, int BN, int WM, int WN, int S, bool A_COL, bool B_COL, bool PAIR, int KIND>
+template <typename T, int BM, int BN, int WM, int WN, int S, int SB, bool A_COL, bool B_COL, bool PAIR, int KIND>
 __global__ __launch_bounds__(WM* WN * 64, 2) void k_dense_mm(DenseJob j, DenseEpi e, MmSlices sl) {
-  constexpr int STAGE = kMmStage<BM, BN>;
+  constexpr int STAGE = kMmStage<BM, BN, SB>;
   __shared__ __attribute__((aligned(1024))) uint16_t s0[STAGE], s1[STAGE], s2[S > 2 ? STAGE : 1], s3[S > 3 ? STAGE : 1];
-  mm_body<T, BM, BN, WM, WN, S, A_COL, B_COL, PAIR, KIND>(j, e, sl, blockIdx.x, s0, s1, s2, s3);
+  mm_body<T, BM, BN, WM, WN, S, SB, A_COL, B_COL, PAIR, KIND>(j, e, sl, blockIdx.x, s0, s1, s2, s3);
 }
 
 // A small backward pass's two products, dx on the first `first` workgroups and dw on the others:
@@ -420,12 +486,12 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void k_dense_mm(DenseJob j, DenseEp
 template <typename T, int S>
 __global__ __launch_bounds__(256, 2) void k_dense_mm_two(DenseJob jx, DenseEpi ex, MmSlices sx, int first, DenseJob jw,
                                                          DenseEpi ew, MmSlices sw) {
-  constexpr int STAGE = kMmStage<64, 64>;
+  constexpr int STAGE = kMmStage<64, 64, 128>;
   __shared__ __attribute__((aligned(1024))) uint16_t s0[STAGE], s1[STAGE], s2[STAGE], s3[S > 3 ? STAGE : 1];
   if ((int)blockIdx.x < first)
-    mm_body<T, 64, 64, 2, 2, S, false, true, false, DENSE_STORE>(jx, ex, sx, blockIdx.x, s0, s1, s2, s3);
+    mm_body<T, 64, 64, 2, 2, S, 128, false, true, false, DENSE_STORE>(jx, ex, sx, blockIdx.x, s0, s1, s2, s3);
   else
-    mm_body<T, 64, 64, 2, 2, S, true, true, false, DENSE_STORE>(jw, ew, sw, blockIdx.x - first, s0, s1, s2, s3);
+    mm_body<T, 64, 64, 2, 2, S, 128, true, true, false, DENSE_STORE>(jw, ew, sw, blockIdx.x - first, s0, s1, s2, s3);
 }
 
 // The slices' sums in ascending order, then the epilogue; eight columns per thread.
@@ -457,13 +523,13 @@ static unsigned mm_grid(const DenseJob& j, const MmSlices& sl, int bm, int bn) {
   return (unsigned)((items + 7) / 8 * 8);
 }
 
-template <typename T, int BM, int BN, int WM, int WN, int S>
+template <typename T, int BM, int BN, int WM, int WN, int S, int SB = 128>
 static void mm_go(const DenseJob& j, const DenseEpi& e, const MmSlices& sl, hipStream_t st) {
   const dim3 grid(mm_grid(j, sl, BM, BN)), block(WM * WN * 64);
-  if (j.pair) k_dense_mm<T, BM, BN, WM, WN, S, false, false, true, DENSE_GATED><<<grid, block, 0, st>>>(j, e, sl);
-  else if (e.kind == DENSE_LINEAR) k_dense_mm<T, BM, BN, WM, WN, S, false, false, false, DENSE_LINEAR><<<grid, block, 0, st>>>(j, e, sl);
-  else if (!j.a_col) k_dense_mm<T, BM, BN, WM, WN, S, false, true, false, DENSE_STORE><<<grid, block, 0, st>>>(j, e, sl);
-  else k_dense_mm<T, BM, BN, WM, WN, S, true, true, false, DENSE_STORE><<<grid, block, 0, st>>>(j, e, sl);
+  if (j.pair) k_dense_mm<T, BM, BN, WM, WN, S, SB, false, false, true, DENSE_GATED><<<grid, block, 0, st>>>(j, e, sl);
+  else if (e.kind == DENSE_LINEAR) k_dense_mm<T, BM, BN, WM, WN, S, SB, false, false, false, DENSE_LINEAR><<<grid, block, 0, st>>>(j, e, sl);
+  else if (!j.a_col) k_dense_mm<T, BM, BN, WM, WN, S, SB, false, true, false, DENSE_STORE><<<grid, block, 0, st>>>(j, e, sl);
+  else k_dense_mm<T, BM, BN, WM, WN, S, SB, true, true, false, DENSE_STORE><<<grid, block, 0, st>>>(j, e, sl);
 }
 
 // Tile and slice count of one product, by estimated time.  A tile's constants are what its
@@ -491,7 +557,7 @@ static MmPlan mm_plan(bool bf16, int M, int N, int K, int segs, int batch, bool 
   constexpr int CUS = 256;
   MmPlan best{{}, 1, pair ? 2 : batch, (N + 7) / 8 * 8};
   double least = 0;
-  const int steps = ceil_div(K, kStepBytes / (bf16 ? 2 : 4)) * segs;
+  const int steps = ceil_div(K, bf16 ? 64 : 32) * segs;  // of 128 bytes
   for (int t = 0; t < (bf16 ? 4 : 1); ++t) {
     const MmTileCost& c = bf16 ? kTilesBf16[t] : kTilesF32[t];
     const int64_t tiles = (int64_t)ceil_div(M, c.bm) * ceil_div(N, pair ? c.bn / 2 : c.bn) * batch;
@@ -537,7 +603,7 @@ hipError_t launch_dense(const DenseJob& j, const DenseEpi& e, bool bf16, float* 
   if (!bf16) {
     mm_go<float, 64, 64, 2, 2, 3>(j, e, sl, st);
   } else if (bn == 256) {
-    mm_go<uint16_t, 256, 256, 2, 4, 2>(j, e, sl, st);
+    mm_go<uint16_t, 256, 256, 2, 4, 4, 64>(j, e, sl, st);
   } else if (bm == 256) {
     mm_go<uint16_t, 256, 128, 4, 2, 3>(j, e, sl, st);
   } else if (bm == 128) {

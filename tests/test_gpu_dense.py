@@ -212,6 +212,88 @@ def test_linear_backward(size, dtype, grad):
             assert torch.equal(o[keep], (dx, dw, db)[keep])
 
 
+# Sizes that end inside the largest tiles and fill the device, together with those above on every
+# tile shape and with the contraction cut into slices; the 64-bit products run on the GPU.
+LARGE = [(3800, 4072, 4000), (8200, 520, 4100), (4104, 1096, 4112), (1030, 2056, 2100), (520, 4096, 520), (100, 7168, 1000)]
+
+
+def close(name, got, dtype, ref, tol):
+    got = (got.view(torch.bfloat16) if dtype == "bf16" else got).double()
+    over = (got - ref).abs() - tol
+    assert bool(torch.isfinite(got).all()) and bool((over <= 0).all()), \
+        f"{name}: {float((got - ref).abs().max()):.3e} off, {float(over.max()):.3e} over"
+
+
+@pytest.mark.parametrize("dtype", ("bf16", "f32"))
+@pytest.mark.parametrize("size", LARGE, ids=small)
+def test_large_gated(size, dtype):
+    T, K, N = size
+    gen = torch.Generator().manual_seed(T)
+    x, w1, w3 = (rand(gen, *s, dtype=dtype, std=v).to(DEV) for s, v in (((T, K), 1), ((N, K), 0.05), ((N, K), 0.05)))
+    s = B.dense_shape(T, K, N, dtype=dtype, act="silu")
+    h, g, u = (out((T, N), dtype) for _ in range(3))
+    B.gated_forward(x, w1, w3, h, s, ws_for(s, B.MOE_CALL_GATED_FORWARD), g=g, u=u)
+    x, w1, w3 = x.double(), w1.double(), w3.double()
+    rg, ru = x @ w1.T, x @ w3.T
+    eg, eu = 2 * fsum(x, w1, K), 2 * fsum(x, w3, K)
+    a, _ = act64(rg, "silu")
+    r = U[dtype]
+    close("g", g, dtype, rg, r * rg.abs() + eg)
+    close("u", u, dtype, ru, r * ru.abs() + eu)
+    close("h", h, dtype, a * ru, r * (a * ru).abs() + SLOPE * eg * ru.abs() + a.abs() * eu + SLOPE * eg * eu
+          + 2.0 ** -20 * (1 + rg.abs()) * rg.abs() * ru.abs())
+
+
+@pytest.mark.parametrize("dtype,grad", (("bf16", "bf16"), ("bf16", "f32"), ("f32", "f32")))
+@pytest.mark.parametrize("size", LARGE, ids=small)
+def test_large_gated_backward(size, dtype, grad):
+    T, K, N = size
+    gen = torch.Generator().manual_seed(T + 1)
+    x, dh, w1, w3, g, u = (rand(gen, *s, dtype=dtype, std=v).to(DEV) for s, v in (
+        ((T, K), 1), ((T, N), 1), ((N, K), 0.05), ((N, K), 0.05), ((T, N), 1.7), ((T, N), 1.7)))
+    s = B.dense_shape(T, K, N, dtype=dtype, act="gelu", grad_dtype=grad)
+    dx, dw1, dw3 = out((T, K), dtype), out((N, K), grad), out((N, K), grad)
+    B.gated_backward(dh, x, w1, w3, g, u, dx, dw1, dw3, s, ws_for(s, B.MOE_CALL_GATED_BACKWARD))
+    x, dh, w1, w3, g, u = (t.double() for t in (x, dh, w1, w3, g, u))
+    a, slope = act64(g, "gelu")
+    dg, du = dh * u * slope, dh * a
+    fe = 2.0 ** -18 * (1 + g.abs())
+    eg, eu = fe * (dh * u).abs(), fe * (dh * g).abs()
+    r, rw = U[dtype], U[grad]
+    ref = dg @ w1 + du @ w3
+    close("dx", dx, dtype, ref, r * ref.abs() + (r * dg.abs() + eg) @ w1.abs() + (r * du.abs() + eu) @ w3.abs()
+          + 2 * (fsum(dg, w1.T, 2 * N) + fsum(du, w3.T, 2 * N)))
+    for name, got, d, e in (("dw1", dw1, dg, eg), ("dw3", dw3, du, eu)):
+        ref = d.T @ x
+        close(name, got, grad, ref, rw * ref.abs() + (rw * d.abs() + e).T @ x.abs() + 2 * fsum(d.T, x.T, 3 * T))
+
+
+@pytest.mark.parametrize("dtype", ("bf16", "f32"))
+@pytest.mark.parametrize("size", LARGE, ids=small)
+def test_large_linear(size, dtype):
+    T, K, N = size
+    gen = torch.Generator().manual_seed(T + 2)
+    x, w, bias, res, dy = (rand(gen, *s, dtype=dtype, std=v).to(DEV) for s, v in (
+        ((T, K), 1), ((N, K), 0.05), ((N,), 1), ((T, N), 1), ((T, N), 1)))
+    s = B.dense_shape(T, K, N, dtype=dtype, act="gelu_tanh")
+    y, z = out((T, N), dtype), out((T, N), dtype)
+    B.linear_forward(x, w, bias, res, y, s, ws_for(s, B.MOE_CALL_LINEAR_FORWARD), z=z)
+    dx, dw, db = out((T, K), dtype), out((N, K), dtype), out((N,), dtype)
+    n = B.dense_shape(T, K, N, dtype=dtype)
+    B.linear_backward(dy, x, w, None, dx, dw, db, n, ws_for(n, B.MOE_CALL_LINEAR_BACKWARD))
+    x, w, bias, res, dy = (t.double() for t in (x, w, bias, res, dy))
+    rz = x @ w.T + bias
+    ez = 2 * fsum(x, w, K) + U32 * rz.abs()
+    a, _ = act64(rz, "gelu_tanh")
+    r = U[dtype]
+    close("z", z, dtype, rz, r * rz.abs() + 2 * ez)
+    close("y", y, dtype, a + res, r * (a + res).abs() + SLOPE * ez + 2.0 ** -20 * (1 + rz.abs()) * rz.abs()
+          + 2 * U32 * (a + res).abs())
+    close("dx", dx, dtype, dy @ w, r * (dy @ w).abs() + 2 * fsum(dy, w.T, N))
+    close("dw", dw, dtype, dy.T @ x, r * (dy.T @ x).abs() + 2 * fsum(dy.T, x.T, T))
+    close("dbias", db, dtype, dy.sum(0), r * dy.sum(0).abs() + (T + 8) * U32 * dy.abs().sum(0))
+
+
 NORM_SIZES = [(1, 1), (1, 8), (2, 7), (3, 64), (5, 1021), (64, 512), (33, 2048), (31, 2056), (300, 1000), (9, 4096),
               (70, 7168), (5, 8200), (3, 20001), (2, 40000), (4100, 129)]
 
