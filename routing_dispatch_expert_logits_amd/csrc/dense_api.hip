@@ -195,6 +195,7 @@ moe_status gradients(const DenseDims& d, const DenseWs& w, const void* d0, const
   ex.kind = DENSE_STORE;
   ex.out_f32 = !d.bf16;
   ex.out[0] = dx;
+  ex.ldo = ew.ldo = d.K;
   jw.M = d.N; jw.N = d.K; jw.K = d.T;
   jw.segs = terms; jw.batch = d1 ? 2 : 1;
   jw.a_col = jw.b_col = true;
@@ -302,6 +303,7 @@ moe_status moe_gated_forward(const void* x, const void* w1, const void* w3, void
   DenseEpi e{};
   e.kind = DENSE_GATED;
   e.act = d.act;
+  e.ldo = d.N;
   e.out[0] = h; e.save[0] = g; e.save[1] = u;
   return forward(d, w, x, w1, w3, e, ws, (hipStream_t)stream);
 }
@@ -357,6 +359,7 @@ moe_status moe_linear_forward(const void* x, const void* w, const void* bias, co
   DenseEpi e{};
   e.kind = DENSE_LINEAR;
   e.act = d.act;
+  e.ldo = d.N;
   e.bias = bias; e.residual = residual;
   e.out[0] = y; e.save[0] = z;
   return forward(d, p, x, w, nullptr, e, ws, (hipStream_t)stream);

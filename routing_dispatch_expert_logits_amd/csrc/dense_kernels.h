@@ -35,6 +35,7 @@ struct DenseEpi {
   const void* residual;  // [M x N], nullable
   void* out[2];
   void* save[2];         // z, or g and u; nullable
+  int64_t ldo;           // row length of outputs, residual and saved values
 };
 
 // bf16: element type of the operands and of what the epilogue reads and writes (else fp32).

@@ -98,7 +98,7 @@ template <typename T, int KIND, int ACT>
 __device__ __forceinline__ void mm_out8(const DenseEpi& e, int z, int m, int n, int N, float* a, const float* b,
                                         const Raw8<T>& res) {
   constexpr bool FAST = sizeof(T) == 2;
-  const int64_t idx = (int64_t)m * N + n;
+  const int64_t idx = (int64_t)m * e.ldo + n;
   const int left = N - n;
   float y[8];
   if constexpr (KIND == DENSE_STORE) {
@@ -128,7 +128,7 @@ __device__ __forceinline__ void mm_out8(const DenseEpi& e, int z, int m, int n, 
 template <typename T, int KIND>
 __device__ __forceinline__ void load_residual(const DenseEpi& e, int m, int n, int M, int N, Raw8<T>* res) {
   if (KIND == DENSE_LINEAR && e.residual)
-    res->load(static_cast<const T*>(e.residual) + (int64_t)min(m, M - 1) * N + n, m < M ? N - n : 0);
+    res->load(static_cast<const T*>(e.residual) + (int64_t)min(m, M - 1) * e.ldo + n, m < M ? N - n : 0);
 }
 
 // f(std::integral_constant<int, act>) for the activation of a launch.
@@ -535,7 +535,7 @@ static void mm_go(const DenseJob& j, const DenseEpi& e, const MmSlices& sl, hipS
 // Tile and slice count of one product, by estimated time.  A tile's constants are what its
 // kernel takes per contraction step and per workgroup beside the steps, on a CU that works
 // through several (at_once of them together) or has just one, measured with operands that
-// come from memory (MI355X).  bf16: 4096^3 takes 109 us on 256 x 256 tiles, 116 on 256 x 128,
+// come from memory (MI355X).  bf16: 4096^3 takes 104 us on 256 x 256 tiles, 116 on 256 x 128,
 // 133 on 128 x 128 and 193 on 64 x 64; 2048^3, an eighth of the work with a quarter of the
 // tiles, 54, 27, 21 and 27; 512 x 2048 x 2048 52, 26, 16 and 10.  fp32 is bound by its matrix
 // instructions on 64 x 64 tiles already (4096^3: 967 us, 142 TFLOP/s; 128 x 128 the same).
@@ -544,7 +544,7 @@ struct MmTileCost {
   double step, fixed;              // us, several workgroups after or beside each other
   double step_alone, fixed_alone;  // us, one
 };
-constexpr MmTileCost kTilesBf16[] = {{256, 256, 1.62, 7.0, 1.62, 7.0},
+constexpr MmTileCost kTilesBf16[] = {{256, 256, 1.50, 8.0, 1.50, 8.0},
                                      {256, 128, 0.88, 4.5, 0.80, 4.5},
                                      {128, 128, 0.50, 3.0, 0.47, 3.0},
                                      {64, 64, 0.165, 1.3, 0.19, 2.5}};
@@ -552,25 +552,44 @@ constexpr MmTileCost kTilesF32[] = {{64, 64, 0.42, 1.0, 0.50, 2.5}};
 struct MmPlan {
   MmTileCost tile;
   int slices, planes, ldp;
+  double us;
+  int cut;   // 256 x 256 tiles for this many output columns, and a launch of its own for the rest; 0: none
 };
-static MmPlan mm_plan(bool bf16, int M, int N, int K, int segs, int batch, bool pair) {
+static MmPlan mm_plan(bool bf16, int M, int N, int K, int segs, int batch, bool pair, bool whole = false) {
   constexpr int CUS = 256;
-  MmPlan best{{}, 1, pair ? 2 : batch, (N + 7) / 8 * 8};
-  double least = 0;
+  MmPlan best{{}, 1, pair ? 2 : batch, (N + 7) / 8 * 8, 0.0, 0};
   const int steps = ceil_div(K, bf16 ? 64 : 32) * segs;  // of 128 bytes
   for (int t = 0; t < (bf16 ? 4 : 1); ++t) {
     const MmTileCost& c = bf16 ? kTilesBf16[t] : kTilesF32[t];
     const int64_t tiles = (int64_t)ceil_div(M, c.bm) * ceil_div(N, pair ? c.bn / 2 : c.bn) * batch;
-    for (int s = 1; s <= 32 && s <= ceil_div(steps, 4); s += s < 4 ? 1 : s / 2) {
+    for (int s = 1; s <= (whole ? 1 : 32) && s <= ceil_div(steps, 4); s += s < 4 ? 1 : s / 2) {
       const int64_t rounds = (tiles * s + CUS - 1) / CUS;
       double us = rounds == 1 ? ceil_div(steps, s) * c.step_alone + c.fixed_alone
                               : rounds * (ceil_div(steps, s) * c.step + c.fixed);
       // the slices' sums are written and read again, and joined by a launch of their own
       if (s > 1) us += 3.0 + (double)s * best.planes * M * N * 8 / 5e6;
-      if (!best.tile.bm || us < least) {
-        least = us;
+      if (!best.tile.bm || us < best.us) {
+        best.us = us;
         best.tile = c;
         best.slices = s;
+      }
+    }
+  }
+  // Whole rounds of 256 x 256 tiles and smaller ones for the columns that would start another:
+  // 8192 x 2048 x 7168 has 896 such tiles, three and a half rounds of 256.
+  const MmTileCost& c = kTilesBf16[0];
+  const int on = pair ? c.bn / 2 : c.bn, tn = ceil_div(N, on);
+  const int64_t column = (int64_t)ceil_div(M, c.bm) * batch;  // tiles of one tile column
+  if (bf16 && !whole && column * tn > CUS) {
+    const int64_t rounds = column * tn / CUS, n = rounds * CUS / column;
+    if (n >= 1 && n < tn) {
+      const MmPlan rest = mm_plan(bf16, M, N - (int)n * on, K, segs, batch, pair, true);
+      const double us = rounds * (steps * c.step + c.fixed) + 3.0 + rest.us;
+      if (us < best.us) {
+        best.us = us;
+        best.tile = c;
+        best.slices = 1;
+        best.cut = (int)n * on;
       }
     }
   }
@@ -596,8 +615,9 @@ static MmSlices slices_of(const MmPlan& p, float* part) {
   return MmSlices{p.slices > 1 ? part : nullptr, p.slices, p.planes, p.ldp};
 }
 
-hipError_t launch_dense(const DenseJob& j, const DenseEpi& e, bool bf16, float* part, hipStream_t st) {
-  const MmPlan p = plan_of(j, bf16);
+// One launch, and one more where there are slices to join.
+static hipError_t launch_planned(const DenseJob& j, const DenseEpi& e, const MmPlan& p, bool bf16, float* part,
+                                 hipStream_t st) {
   const MmSlices sl = slices_of(p, part);
   const int bm = p.tile.bm, bn = p.tile.bn;
   if (!bf16) {
@@ -615,6 +635,31 @@ hipError_t launch_dense(const DenseJob& j, const DenseEpi& e, bool bf16, float* 
   if (bf16) mm_join<uint16_t>(j, e, sl, st);
   else mm_join<float>(j, e, sl, st);
   return hipGetLastError();
+}
+
+hipError_t launch_dense(const DenseJob& j, const DenseEpi& e, bool bf16, float* part, hipStream_t st) {
+  const MmPlan p = plan_of(j, bf16);
+  if (!p.cut) return launch_planned(j, e, p, bf16, part, st);
+  DenseJob left = j, right = j;
+  DenseEpi er = e;
+  const int es = bf16 ? 2 : 4, oes = e.kind == DENSE_STORE && e.out_f32 ? 4 : es;
+  left.N = p.cut;
+  right.N = j.N - p.cut;
+  for (auto& z : right.B)
+    for (auto& b : z)
+      if (b) b = static_cast<const char*>(b) + (j.b_col ? (int64_t)p.cut : p.cut * j.ldb) * es;
+  auto on = [&](auto* v, int size) {
+    return v ? static_cast<decltype(v)>(const_cast<char*>(static_cast<const char*>(v) + (int64_t)p.cut * size)) : v;
+  };
+  er.bias = on(e.bias, es);
+  er.residual = on(e.residual, es);
+  for (int i = 0; i < 2; ++i) {
+    er.out[i] = on(e.out[i], oes);
+    er.save[i] = on(e.save[i], es);
+  }
+  if (hipError_t r = launch_planned(left, e, p, bf16, nullptr, st); r != hipSuccess) return r;
+  return launch_planned(right, er, mm_plan(bf16, right.M, right.N, right.K, right.segs, right.batch, right.pair, true),
+                        bf16, nullptr, st);
 }
 
 hipError_t launch_dense_two(const DenseJob& jx, const DenseEpi& ex, const DenseJob& jw, const DenseEpi& ew, bool bf16,
