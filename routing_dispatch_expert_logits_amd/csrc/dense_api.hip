@@ -91,12 +91,9 @@ moe_status check_ws(Buffers& b, const void* ws, size_t ws_bytes, size_t need) {
 
 // ---- workspaces
 
-// The products read rows of whole 16-byte chunks; operands with other widths are copied to
+// The bf16 products read rows of whole 16-byte chunks; operands with other widths are copied to
 // such rows first.
-int64_t padded(const DenseDims& d, int cols) {
-  const int64_t c = 16 / d.es;
-  return (cols + c - 1) / c * c;
-}
+int64_t padded(const DenseDims& d, int cols) { return d.bf16 ? ((int64_t)cols + 7) / 8 * 8 : cols; }
 
 // Backward: the gradient before the activation as operand of the products (three bf16 terms of
 // each value, lo elements apart, where fp32 weight gradients are asked for), and the row
@@ -151,7 +148,7 @@ moe_status in_rows(const DenseDims& d, const DenseWs& w, const void** x, const v
   one(0, x, d.T, w.x);
   one(1, w0, d.N, w.w[0]);
   one(2, w1, d.N, w.w[1]);
-  MOE_HIP(launch_pad_rows(p, d.bf16, d.K, w.ldk, st));
+  MOE_HIP(launch_pad_rows(p, d.K, w.ldk, st));
   return MOE_OK;
 }
 

@@ -134,30 +134,27 @@ hipError_t launch_act_grad(const void* dh, const void* g, const void* u, int act
   return launch_col_sum(part, (int)grid.y, N, N, sum, nullptr, sum_f32, st);
 }
 
-// Eight elements of a padded row per thread (fp32 rows may end in half of them).
-template <typename T>
+// Eight elements of a padded row per thread.
 __global__ __launch_bounds__(256) void k_pad_rows(PadRows p, int cols, int ld) {
-  const T* src = static_cast<const T*>(p.src[blockIdx.y]);
-  T* dst = static_cast<T*>(p.dst[blockIdx.y]);
+  const uint16_t* src = static_cast<const uint16_t*>(p.src[blockIdx.y]);
+  uint16_t* dst = static_cast<uint16_t*>(p.dst[blockIdx.y]);
   if (!src) return;
-  const int per = ceil_div(ld, 8);
+  const int per = ld / 8;
   const int64_t total = p.rows[blockIdx.y] * per;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
     const int64_t r = i / per;
     const int c = (int)(i - r * per) * 8;
     float v[8];
     load8(src + r * cols + c, cols - c, v);
-    store8(dst + r * ld + c, ld - c, v);
+    store8(dst + i * 8, v);
   }
 }
 
-hipError_t launch_pad_rows(const PadRows& p, bool bf16, int cols, int64_t ld, hipStream_t st) {
+hipError_t launch_pad_rows(const PadRows& p, int cols, int64_t ld, hipStream_t st) {
   int64_t most = 1;
   for (int64_t r : p.rows) most = r > most ? r : most;
-  const int64_t want = (most * ((ld + 7) / 8) + 255) / 256;
-  const dim3 grid((unsigned)(want < 8192 ? want : 8192), 3);
-  if (bf16) k_pad_rows<uint16_t><<<grid, 256, 0, st>>>(p, cols, (int)ld);
-  else k_pad_rows<float><<<grid, 256, 0, st>>>(p, cols, (int)ld);
+  const int64_t want = (most * (ld / 8) + 255) / 256;
+  k_pad_rows<<<dim3((unsigned)(want < 8192 ? want : 8192), 3), 256, 0, st>>>(p, cols, (int)ld);
   return hipGetLastError();
 }
 

@@ -39,7 +39,7 @@ struct DenseEpi {
 };
 
 // bf16: element type of the operands and of what the epilogue reads and writes (else fp32).
-// lda and ldb are whole 16-byte chunks, row operands zero from the contraction length on.
+// bf16: lda and ldb are whole 16-byte chunks, row operands zero from the contraction length on.
 //
 // Forward products of at most kDecodeRows rows read each weight once, straight into operands,
 // and take rows of any length.
@@ -69,14 +69,14 @@ hipError_t launch_act_grad(const void* dh, const void* g, const void* u, int act
 // nullable), in a fixed order; in fp32 or bf16.
 hipError_t launch_col_sum(const float* part, int P, int N, int64_t stride, void* out0, void* out1, bool out_f32,
                           hipStream_t st);
-// dst[r][0 .. ld) = src[r][0 .. cols) and zeros for up to three operands of the same width (src
-// NULL: none) in one launch; ld the next whole number of 16-byte chunks.
+// dst[r][0 .. ld) = src[r][0 .. cols) and zeros for up to three bf16 operands of the same width
+// (src NULL: none) in one launch; ld: cols rounded up to 8.
 struct PadRows {
   const void* src[3];
   void* dst[3];
   int64_t rows[3];
 };
-hipError_t launch_pad_rows(const PadRows& p, bool bf16, int cols, int64_t ld, hipStream_t st);
+hipError_t launch_pad_rows(const PadRows& p, int cols, int64_t ld, hipStream_t st);
 hipError_t launch_fill_zero(void* p, size_t bytes, hipStream_t st);
 
 hipError_t launch_norm_forward(const void* x, const void* w, const void* b, void* y, float* mean, float* rstd,

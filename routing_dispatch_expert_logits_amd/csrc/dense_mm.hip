@@ -19,8 +19,9 @@ __device__ __forceinline__ const char* uniform(const char* p) {
   return reinterpret_cast<const char*>(((uint64_t)(uint32_t)uniform((int)(a >> 32)) << 32) | (uint32_t)uniform((int)a));
 }
 
-// A tile of R rows (m or n) by one contraction step in LDS, filled by 16-byte buffer loads
-// straight into LDS (1 KB per instruction, lane i to byte 16 i) and read as MFMA operands in
+// A tile of R rows (m or n) by one contraction step in LDS, filled by buffer loads straight into
+// LDS (DB = 16 bytes per lane, lane i to byte DB i of the instruction's part; 4 for fp32 rows
+// that are no whole number of 16-byte chunks) and read as MFMA operands in
 // pieces of 64 bytes of contraction, of which a step has one or two (SB = 64 or 128): lane l
 // holds row l % 16, the (l / 16)-th 16 bytes of the piece's contraction elements.
 // For bf16 that is one instruction's operand; for fp32 the i-th of four instructions takes
@@ -35,32 +36,36 @@ __device__ __forceinline__ const char* uniform(const char* p) {
 // of row k sits at u ^ f(k) with f(k) = (k & 3) | (k >> 1 & 4), which spreads the 16 rows one
 // instruction touches over all banks.  fp32 column operands are read a dword per element, 16
 // lanes to a 64-byte unit of one row; unit u of row k sits at u ^ (k >> 2 & 3).
-template <typename T, int R, bool COL, int SB>
+template <typename T, int R, bool COL, int SB, int DB>
 struct MmTile {
   static constexpr int ES = sizeof(T);
   static constexpr int HALFS = R * SB / 2;       // 16-bit words of the tile
-  static constexpr int INSTR = R * SB / 1024;    // fill instructions
-  static constexpr int CPR = R * ES / 16;        // column operand: 16-byte chunks per LDS row
-  static constexpr int UC = ES;                  // and chunks per unit (16 elements)
-  static constexpr int RC = SB / 16, RPI = 64 / RC;  // row operand: chunks per LDS row, rows per instruction
+  static constexpr int INSTR = R * SB / (64 * DB);  // fill instructions
+  static constexpr int PER = 16 / DB;               // lanes of a 16-byte chunk
+  static constexpr int CPR = R * ES / 16;           // column operand: chunks per LDS row
+  static constexpr int UC = ES;                     // and chunks per unit (16 elements)
+  static constexpr int RC = SB / 16;                // row operand: chunks per LDS row
   static __device__ __forceinline__ int swz(int r) { return SB == 128 ? r & 7 : (r >> 1) & 3; }
-  // Row operand: the chunk of its row that a lane fills.
-  static __device__ __forceinline__ int chunk(int lane) { return (lane % RC) ^ swz(lane / RC); }
+  // Row operand: the row that a lane of fill instruction q fills, and its first element there.
+  static __device__ __forceinline__ int row(int q, int lane) { return (q * 64 + lane) / (RC * PER); }
+  static __device__ __forceinline__ int element(int q, int lane) {
+    return ((((lane / PER) % RC) ^ swz(row(q, lane))) * PER + lane % PER) * (DB / ES);
+  }
   static __device__ __forceinline__ int f(int k) {
     return (ES == 2 ? (k & 3) | ((k >> 1) & 4) : (k >> 2) & 3) & (R / 16 - 1);
   }
 
-  // Byte offset of lane's 16 bytes of fill instruction q, from the tile's first row at
+  // Byte offset of lane's DB bytes of fill instruction q, from the tile's first row at
   // contraction 0 (row operand; rows >= valid are out of range) or from the tile's first
   // element of the step's first contraction row (column operand).
   static __device__ __forceinline__ uint32_t src(int q, int lane, int64_t ld, int valid) {
     if constexpr (COL) {
-      const int k = q * (64 / CPR) + lane / CPR, s = lane % CPR;
+      const int at = q * 64 + lane, k = at / (CPR * PER), s = at / PER % CPR;
       const int chunk = ((s / UC) ^ f(k)) * UC + s % UC;
-      return (uint32_t)(k * ld * ES + chunk * 16);
+      return (uint32_t)(k * ld * ES + chunk * 16 + lane % PER * DB);
     } else {
-      const int r = q * RPI + lane / RC;
-      return r < valid ? (uint32_t)(r * ld * ES + (chunk(lane) << 4)) : kOutOfRange;
+      const int r = row(q, lane);
+      return r < valid ? (uint32_t)((r * ld + element(q, lane)) * ES) : kOutOfRange;
     }
   }
 
@@ -189,11 +194,11 @@ constexpr int mm_waitcnt(int n) { return (n & 0xF) | ((n >> 4) << 14) | (0x7 << 
 // one reading a step's operands while the other multiplies, a barrier after each turn.
 template <int BM, int BN, int SB>
 constexpr int kMmStage = (BM + BN) * SB / 2;  // 16-bit words of a stage
-template <typename T, int BM, int BN, int WM, int WN, int S, int SB, bool A_COL, bool B_COL, bool PAIR, int KIND>
+template <typename T, int BM, int BN, int WM, int WN, int S, int SB, int DB, bool A_COL, bool B_COL, bool PAIR, int KIND>
 __device__ __forceinline__ void mm_body(const DenseJob& j, const DenseEpi& e, const MmSlices& sl, int block,
                                         uint16_t* s0, uint16_t* s1, uint16_t* s2, uint16_t* s3) {
-  using TA = MmTile<T, BM, A_COL, SB>;
-  using TB = MmTile<T, BN, B_COL, SB>;
+  using TA = MmTile<T, BM, A_COL, SB, DB>;
+  using TB = MmTile<T, BN, B_COL, SB, DB>;
   constexpr int ES = sizeof(T), BK = SB / ES;
   constexpr int W = WM * WN, TM = BM / WM, TN = BN / WN, FM = TM / 16, FN = TN / 16;
   constexpr int QA = TA::INSTR / W, QB = TB::INSTR / W;
@@ -219,7 +224,6 @@ __device__ __forceinline__ void mm_body(const DenseJob& j, const DenseEpi& e, co
 #pragma unroll
   for (int q = 0; q < QB; ++q)
     vb[q] = TB::src((PAIR ? wave % (W / 2) : wave) * QB + q, lane, j.ldb, j.N - n0);
-  const int kchunk = TA::chunk(lane) * (16 / ES);  // row operands: this lane's first element in a step
   // of the next step to load: where the tile starts and how many bytes from there are the
   // operand's (whole rows of it, none past its last one)
   const char *pa, *pb;
@@ -250,17 +254,20 @@ __device__ __forceinline__ void mm_body(const DenseJob& j, const DenseEpi& e, co
       segment();
     }
     const int rows = min(BK, left);
-    auto one = [&](const char* p, int n, bool col, const uint32_t* v, int Q, int dst)
+    auto one = [&](const char* p, int n, bool col, const uint32_t* v, int Q, int q0, int dst)
         __attribute__((always_inline)) {
       const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
           const_cast<char*>(p), 0, uniform(live ? n : 0), 0x00020000);
 #pragma unroll
-      for (int q = 0; q < Q; ++q)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_dst)(st + (dst + q * 512)), 16,
-                                                 col || kchunk < rows ? v[q] : kOutOfRange, 0, 0, 0);
+      for (int q = 0; q < Q; ++q) {
+        const uint32_t off = col || TA::element(q0 + q, lane) < rows ? v[q] : kOutOfRange;
+        const lds_dst to = (lds_dst)(st + (dst + (q0 + q) * 32 * DB));
+        if constexpr (DB == 16) __builtin_amdgcn_raw_ptr_buffer_load_lds(r, to, 16, off, 0, 0, 0);
+        else __builtin_amdgcn_raw_ptr_buffer_load_lds(r, to, 4, off, 0, 0, 0);
+      }
     };
-    one(pa, A_COL ? (rows * (int)j.lda - m0) * ES : na, A_COL, va, QA, wave * QA * 512);
-    one(pb, B_COL ? (rows * (int)j.ldb - n0) * ES : nb, B_COL, vb, QB, TA::HALFS + wave * QB * 512);
+    one(pa, A_COL ? (rows * (int)j.lda - m0) * ES : na, A_COL, va, QA, wave * QA, 0);
+    one(pb, B_COL ? (rows * (int)j.ldb - n0) * ES : nb, B_COL, vb, QB, wave * QB, TA::HALFS);
     advance(1);
   };
 
@@ -450,7 +457,7 @@ __device__ __forceinline__ void mm_body(const DenseJob& j, const DenseEpi& e, co
       with_act<KIND>(e.act, [&](auto act) __attribute__((always_inline)) {
         // a residual's rows are all on their way before the first is used: taken one iteration
         // at a time their latency is most of the epilogue (8192 x 2048 x 7168: 40 us of 273)
-        constexpr int U = KIND == DENSE_LINEAR ? PM / RPI : 1;
+        constexpr int U = KIND == DENSE_LINEAR && PM > RPI ? PM / RPI : 1;
         Raw8<T> res[U];
 #pragma unroll
         for (int i = 0; i < U; ++i) load_residual<T, KIND>(e, mp + i * RPI, n, j.M, j.N, &res[i]);
@@ -458,7 +465,7 @@ __device__ __forceinline__ void mm_body(const DenseJob& j, const DenseEpi& e, co
 #pragma unroll
           for (int i = 0; i < U; ++i) {
             const int r = r0 + i * RPI + lr, m = mp + r - lr;
-            if (m >= j.M || n >= j.N) continue;
+            if (m >= j.M || n >= j.N || (RPI > PM && r >= PM)) continue;
             f32x4 v[2] = {chunk(r, 2 * lc), chunk(r, 2 * lc + 1)}, u[2] = {v[0], v[1]};
             if (PAIR) u[0] = chunk(r, CH / 2 + 2 * lc), u[1] = chunk(r, CH / 2 + 2 * lc + 1);
             mm_out8<T, KIND, act()>(e, z, m, n, j.N, reinterpret_cast<float*>(v), reinterpret_cast<const float*>(u),
@@ -474,24 +481,25 @@ __device__ __forceinline__ void mm_body(const DenseJob& j, const DenseEpi& e, co
   if constexpr (PASSES > 1) pass(std::integral_constant<int, 1>{});
 }
 
-template <typename T, int BM, int BN, int WM, int WN, int S, int SB, bool A_COL, bool B_COL, bool PAIR, int KIND>
+template <typename T, int BM, int BN, int WM, int WN, int S, int SB, int DB, bool A_COL, bool B_COL, bool PAIR,
+          int KIND>
 __global__ __launch_bounds__(WM* WN * 64, 2) void k_dense_mm(DenseJob j, DenseEpi e, MmSlices sl) {
   constexpr int STAGE = kMmStage<BM, BN, SB>;
   __shared__ __attribute__((aligned(1024))) uint16_t s0[STAGE], s1[STAGE], s2[S > 2 ? STAGE : 1], s3[S > 3 ? STAGE : 1];
-  mm_body<T, BM, BN, WM, WN, S, SB, A_COL, B_COL, PAIR, KIND>(j, e, sl, blockIdx.x, s0, s1, s2, s3);
+  mm_body<T, BM, BN, WM, WN, S, SB, DB, A_COL, B_COL, PAIR, KIND>(j, e, sl, blockIdx.x, s0, s1, s2, s3);
 }
 
 // A small backward pass's two products, dx on the first `first` workgroups and dw on the others:
 // neither fills the device, and a launch of its own costs each about 5 us.
-template <typename T, int S>
+template <typename T, int BN, int WM, int WN, int S, int DB>
 __global__ __launch_bounds__(256, 2) void k_dense_mm_two(DenseJob jx, DenseEpi ex, MmSlices sx, int first, DenseJob jw,
                                                          DenseEpi ew, MmSlices sw) {
-  constexpr int STAGE = kMmStage<64, 64, 128>;
+  constexpr int STAGE = kMmStage<64, BN, 128>;
   __shared__ __attribute__((aligned(1024))) uint16_t s0[STAGE], s1[STAGE], s2[STAGE], s3[S > 3 ? STAGE : 1];
   if ((int)blockIdx.x < first)
-    mm_body<T, 64, 64, 2, 2, S, 128, false, true, false, DENSE_STORE>(jx, ex, sx, blockIdx.x, s0, s1, s2, s3);
+    mm_body<T, 64, BN, WM, WN, S, 128, DB, false, true, false, DENSE_STORE>(jx, ex, sx, blockIdx.x, s0, s1, s2, s3);
   else
-    mm_body<T, 64, 64, 2, 2, S, 128, true, true, false, DENSE_STORE>(jw, ew, sw, blockIdx.x - first, s0, s1, s2, s3);
+    mm_body<T, 64, BN, WM, WN, S, 128, DB, true, true, false, DENSE_STORE>(jw, ew, sw, blockIdx.x - first, s0, s1, s2, s3);
 }
 
 // The slices' sums in ascending order, then the epilogue; eight columns per thread.
@@ -523,13 +531,13 @@ static unsigned mm_grid(const DenseJob& j, const MmSlices& sl, int bm, int bn) {
   return (unsigned)((items + 7) / 8 * 8);
 }
 
-template <typename T, int BM, int BN, int WM, int WN, int S, int SB = 128>
+template <typename T, int BM, int BN, int WM, int WN, int S, int SB = 128, int DB = 16>
 static void mm_go(const DenseJob& j, const DenseEpi& e, const MmSlices& sl, hipStream_t st) {
   const dim3 grid(mm_grid(j, sl, BM, BN)), block(WM * WN * 64);
-  if (j.pair) k_dense_mm<T, BM, BN, WM, WN, S, SB, false, false, true, DENSE_GATED><<<grid, block, 0, st>>>(j, e, sl);
-  else if (e.kind == DENSE_LINEAR) k_dense_mm<T, BM, BN, WM, WN, S, SB, false, false, false, DENSE_LINEAR><<<grid, block, 0, st>>>(j, e, sl);
-  else if (!j.a_col) k_dense_mm<T, BM, BN, WM, WN, S, SB, false, true, false, DENSE_STORE><<<grid, block, 0, st>>>(j, e, sl);
-  else k_dense_mm<T, BM, BN, WM, WN, S, SB, true, true, false, DENSE_STORE><<<grid, block, 0, st>>>(j, e, sl);
+  if (j.pair) k_dense_mm<T, BM, BN, WM, WN, S, SB, DB, false, false, true, DENSE_GATED><<<grid, block, 0, st>>>(j, e, sl);
+  else if (e.kind == DENSE_LINEAR) k_dense_mm<T, BM, BN, WM, WN, S, SB, DB, false, false, false, DENSE_LINEAR><<<grid, block, 0, st>>>(j, e, sl);
+  else if (!j.a_col) k_dense_mm<T, BM, BN, WM, WN, S, SB, DB, false, true, false, DENSE_STORE><<<grid, block, 0, st>>>(j, e, sl);
+  else k_dense_mm<T, BM, BN, WM, WN, S, SB, DB, true, true, false, DENSE_STORE><<<grid, block, 0, st>>>(j, e, sl);
 }
 
 // Tile and slice count of one product, by estimated time.  A tile's constants are what its
@@ -548,7 +556,7 @@ constexpr MmTileCost kTilesBf16[] = {{256, 256, 1.50, 8.0, 1.50, 8.0},
                                      {256, 128, 0.88, 4.5, 0.80, 4.5},
                                      {128, 128, 0.50, 3.0, 0.47, 3.0},
                                      {64, 64, 0.165, 1.3, 0.19, 2.5}};
-constexpr MmTileCost kTilesF32[] = {{64, 64, 0.42, 1.0, 0.50, 2.5}};
+constexpr MmTileCost kTilesF32[] = {{64, 64, 0.42, 1.0, 0.57, 2.5}, {64, 32, 0.22, 0.8, 0.35, 2.5}};
 struct MmPlan {
   MmTileCost tile;
   int slices, planes, ldp;
@@ -559,7 +567,7 @@ static MmPlan mm_plan(bool bf16, int M, int N, int K, int segs, int batch, bool 
   constexpr int CUS = 256;
   MmPlan best{{}, 1, pair ? 2 : batch, (N + 7) / 8 * 8, 0.0, 0};
   const int steps = ceil_div(K, bf16 ? 64 : 32) * segs;  // of 128 bytes
-  for (int t = 0; t < (bf16 ? 4 : 1); ++t) {
+  for (int t = 0; t < (bf16 ? 4 : 2); ++t) {
     const MmTileCost& c = bf16 ? kTilesBf16[t] : kTilesF32[t];
     const int64_t tiles = (int64_t)ceil_div(M, c.bm) * ceil_div(N, pair ? c.bn / 2 : c.bn) * batch;
     for (int s = 1; s <= (whole ? 1 : 32) && s <= ceil_div(steps, 4); s += s < 4 ? 1 : s / 2) {
@@ -615,13 +623,19 @@ static MmSlices slices_of(const MmPlan& p, float* part) {
   return MmSlices{p.slices > 1 ? part : nullptr, p.slices, p.planes, p.ldp};
 }
 
+// fp32 operands whose rows are whole 16-byte chunks.
+static bool whole_chunks(const DenseJob& j) { return j.lda % 4 == 0 && j.ldb % 4 == 0; }
+
 // One launch, and one more where there are slices to join.
 static hipError_t launch_planned(const DenseJob& j, const DenseEpi& e, const MmPlan& p, bool bf16, float* part,
                                  hipStream_t st) {
   const MmSlices sl = slices_of(p, part);
   const int bm = p.tile.bm, bn = p.tile.bn;
   if (!bf16) {
-    mm_go<float, 64, 64, 2, 2, 3>(j, e, sl, st);
+    if (bn == 64 && whole_chunks(j)) mm_go<float, 64, 64, 2, 2, 3>(j, e, sl, st);
+    else if (bn == 64) mm_go<float, 64, 64, 2, 2, 3, 128, 4>(j, e, sl, st);
+    else if (whole_chunks(j)) mm_go<float, 64, 32, 4, 1, 3>(j, e, sl, st);
+    else mm_go<float, 64, 32, 4, 1, 3, 128, 4>(j, e, sl, st);
   } else if (bn == 256) {
     mm_go<uint16_t, 256, 256, 2, 4, 4, 64>(j, e, sl, st);
   } else if (bm == 256) {
@@ -665,14 +679,20 @@ hipError_t launch_dense(const DenseJob& j, const DenseEpi& e, bool bf16, float* 
 hipError_t launch_dense_two(const DenseJob& jx, const DenseEpi& ex, const DenseJob& jw, const DenseEpi& ew, bool bf16,
                             float* part_x, float* part_w, hipStream_t st) {
   const MmPlan px = plan_of(jx, bf16), pw = plan_of(jw, bf16);
-  if (px.tile.bm != 64 || pw.tile.bm != 64) {
+  if (px.tile.bn > 64 || pw.tile.bn > 64 || px.tile.bn != pw.tile.bn) {
     if (hipError_t r = launch_dense(jx, ex, bf16, part_x, st); r != hipSuccess) return r;
     return launch_dense(jw, ew, bf16, part_w, st);
   }
   const MmSlices sx = slices_of(px, part_x), sw = slices_of(pw, part_w);
-  const unsigned first = mm_grid(jx, sx, 64, 64), all = first + mm_grid(jw, sw, 64, 64);
-  if (bf16) k_dense_mm_two<uint16_t, 4><<<all, 256, 0, st>>>(jx, ex, sx, (int)first, jw, ew, sw);
-  else k_dense_mm_two<float, 3><<<all, 256, 0, st>>>(jx, ex, sx, (int)first, jw, ew, sw);
+  const int bn = px.tile.bn;
+  const unsigned first = mm_grid(jx, sx, 64, bn), all = first + mm_grid(jw, sw, 64, bn);
+  const bool whole = whole_chunks(jx) && whole_chunks(jw);
+  auto go = [&](auto kernel) { kernel<<<all, 256, 0, st>>>(jx, ex, sx, (int)first, jw, ew, sw); };
+  if (bf16) go(k_dense_mm_two<uint16_t, 64, 2, 2, 4, 16>);
+  else if (bn == 64 && whole) go(k_dense_mm_two<float, 64, 2, 2, 3, 16>);
+  else if (bn == 64) go(k_dense_mm_two<float, 64, 2, 2, 3, 4>);
+  else if (whole) go(k_dense_mm_two<float, 32, 4, 1, 3, 16>);
+  else go(k_dense_mm_two<float, 32, 4, 1, 3, 4>);
   if (hipError_t r = hipGetLastError(); r != hipSuccess) return r;
   if (px.slices > 1) {
     if (bf16) mm_join<uint16_t>(jx, ex, sx, st);
