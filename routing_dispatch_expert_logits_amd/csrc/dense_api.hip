@@ -275,9 +275,8 @@ moe_status moe_layer_norm_backward(const void* dy, const void* x, const void* w,
     if (db) MOE_HIP(launch_fill_zero(db, d.H * d.ges, st));
     return MOE_OK;
   }
-  float* part = dw || db ? static_cast<float*>(ws) : nullptr;
-  MOE_HIP(launch_norm_backward(dy, x, w, mean, rstd, dx, part, d.T, d.H, d.bf16, st));
-  if (part) MOE_HIP(launch_col_sum(part, norm_row_blocks(d.T, d.H), d.H, 2 * d.H, dw, db, d.grad_f32, st));
+  MOE_HIP(launch_norm_backward(dy, x, w, mean, rstd, dx, dw, db, d.grad_f32, static_cast<float*>(ws), d.T, d.H, d.bf16,
+                               st));
   return MOE_OK;
 }
 

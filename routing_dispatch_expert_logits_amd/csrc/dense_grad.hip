@@ -9,13 +9,12 @@ namespace moe {
 constexpr int kGradCols = 256;  // columns per workgroup: 32 lanes of 8
 constexpr int kGradSub = 8;     // rows in flight per workgroup
 
-// Row blocks: enough workgroups for the device, at least 32 rows each so that the partial
-// sums stay a small part of what is read.
+// Row blocks of a pass that sums columns: one for up to 32 rows (whose sums then need no second
+// launch), else 2048 workgroups or 8 rows each.
 int grad_row_blocks(int T, int N) {
-  const int cb = ceil_div(N, kGradCols);
-  const int want = ceil_div(2048, cb);
-  const int most = ceil_div(T, 32);
-  return want < most ? (want > 0 ? want : 1) : (most > 0 ? most : 1);
+  if (T <= 32) return 1;
+  const int cb = ceil_div(N, kGradCols), want = ceil_div(2048, cb), most = ceil_div(T, kGradSub);
+  return want < most ? want : most;
 }
 
 // One pass over dh, g (and u): d0 = dh u act'(g), d1 = dh act(g) in fp32, rounded on store.
@@ -119,7 +118,8 @@ hipError_t launch_col_sum(const float* part, int P, int N, int64_t stride, void*
 hipError_t launch_act_grad(const void* dh, const void* g, const void* u, int act, bool bf16, int T, int N,
                            void* d0, void* d1, int terms, int64_t lo, int64_t ld, float* part, void* sum, bool sum_f32,
                            hipStream_t st) {
-  const dim3 grid(ceil_div(N, kGradCols), grad_row_blocks(T, N));
+  const int single = ceil_div(T, kGradSub);  // without sums, a row per thread while the grid lasts
+  const dim3 grid(ceil_div(N, kGradCols), sum ? grad_row_blocks(T, N) : single < 32768 ? single : 32768);
   if (!sum) part = nullptr;
   auto go = [&](auto* t) {
     using E = std::remove_pointer_t<decltype(t)>;

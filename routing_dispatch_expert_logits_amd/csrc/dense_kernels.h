@@ -81,10 +81,10 @@ hipError_t launch_fill_zero(void* p, size_t bytes, hipStream_t st);
 
 hipError_t launch_norm_forward(const void* x, const void* w, const void* b, void* y, float* mean, float* rstd,
                                int T, int H, float eps, bool bf16, hipStream_t st);
-// part: norm_row_blocks(T, H) rows of 2 H fp32 column sums (dy n, then dy).
+// dx, dw and db each nullable; part: norm_row_blocks(T, H) rows of 2 H fp32 column sums.
 int norm_row_blocks(int T, int H);
 hipError_t launch_norm_backward(const void* dy, const void* x, const void* w, const float* mean,
-                                const float* rstd, void* dx, float* part, int T, int H, bool bf16,
-                                hipStream_t st);
+                                const float* rstd, void* dx, void* dw, void* db, bool grad_f32, float* part, int T,
+                                int H, bool bf16, hipStream_t st);
 
 }  // namespace moe

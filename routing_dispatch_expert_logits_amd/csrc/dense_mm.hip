@@ -511,6 +511,7 @@ __global__ __launch_bounds__(256) void k_dense_join(int M, int N, int batch, Den
     const int64_t row = i / n8;
     const int n = (int)(i - row * n8) * 8, z = (int)(row / M), m = (int)(row - (int64_t)z * M);
     float a[8] = {}, b[8] = {};
+#pragma unroll 4
     for (int s = 0; s < sl.slices; ++s) {
       const f32x4* p = sl.at(s, z, m, n, M);
       for (int k = 0; k < 8; ++k) a[k] += p[k >> 2][k & 3];
@@ -563,12 +564,14 @@ struct MmPlan {
   double us;
   int cut;   // 256 x 256 tiles for this many output columns, and a launch of its own for the rest; 0: none
 };
-static MmPlan mm_plan(bool bf16, int M, int N, int K, int segs, int batch, bool pair, bool whole = false) {
+static MmPlan mm_plan(bool bf16, int M, int N, int K, int segs, int batch, bool pair, bool whole = false,
+                      int widest = 256) {
   constexpr int CUS = 256;
   MmPlan best{{}, 1, pair ? 2 : batch, (N + 7) / 8 * 8, 0.0, 0};
   const int steps = ceil_div(K, bf16 ? 64 : 32) * segs;  // of 128 bytes
   for (int t = 0; t < (bf16 ? 4 : 2); ++t) {
     const MmTileCost& c = bf16 ? kTilesBf16[t] : kTilesF32[t];
+    if (c.bm > widest) continue;
     const int64_t tiles = (int64_t)ceil_div(M, c.bm) * ceil_div(N, pair ? c.bn / 2 : c.bn) * batch;
     for (int s = 1; s <= (whole ? 1 : 32) && s <= ceil_div(steps, 4); s += s < 4 ? 1 : s / 2) {
       const int64_t rounds = (tiles * s + CUS - 1) / CUS;
@@ -588,7 +591,7 @@ static MmPlan mm_plan(bool bf16, int M, int N, int K, int segs, int batch, bool 
   const MmTileCost& c = kTilesBf16[0];
   const int on = pair ? c.bn / 2 : c.bn, tn = ceil_div(N, on);
   const int64_t column = (int64_t)ceil_div(M, c.bm) * batch;  // tiles of one tile column
-  if (bf16 && !whole && column * tn > CUS) {
+  if (bf16 && !whole && widest == 256 && column * tn > CUS) {
     const int64_t rounds = column * tn / CUS, n = rounds * CUS / column;
     if (n >= 1 && n < tn) {
       const MmPlan rest = mm_plan(bf16, M, N - (int)n * on, K, segs, batch, pair, true);
@@ -678,8 +681,12 @@ hipError_t launch_dense(const DenseJob& j, const DenseEpi& e, bool bf16, float* 
 
 hipError_t launch_dense_two(const DenseJob& jx, const DenseEpi& ex, const DenseJob& jw, const DenseEpi& ew, bool bf16,
                             float* part_x, float* part_w, hipStream_t st) {
-  const MmPlan px = plan_of(jx, bf16), pw = plan_of(jw, bf16);
-  if (px.tile.bn > 64 || pw.tile.bn > 64 || px.tile.bn != pw.tile.bn) {
+  MmPlan px = plan_of(jx, bf16), pw = plan_of(jw, bf16);
+  // together on 64-row tiles where that is less than each on its best: they overlap, and a launch is saved
+  const double apart = px.us + pw.us + 3.0;
+  px = mm_plan(bf16, jx.M, jx.N, jx.K, jx.segs, jx.batch, false, false, 64);
+  pw = mm_plan(bf16, jw.M, jw.N, jw.K, jw.segs, jw.batch, false, false, 64);
+  if (0.8 * (px.us + pw.us) > apart || px.tile.bn != pw.tile.bn) {
     if (hipError_t r = launch_dense(jx, ex, bf16, part_x, st); r != hipSuccess) return r;
     return launch_dense(jw, ew, bf16, part_w, st);
   }

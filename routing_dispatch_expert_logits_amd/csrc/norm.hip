@@ -160,7 +160,8 @@ template <typename T, int NCH, int RB, int MAXT>
 __global__ __launch_bounds__(MAXT) void k_norm_backward(const T* __restrict__ dy, const T* __restrict__ x,
                                                         const T* __restrict__ w, const float* __restrict__ mean,
                                                         const float* __restrict__ rstd, T* __restrict__ dx,
-                                                        float* __restrict__ part, int rows, int per, int H) {
+                                                        float* __restrict__ part, int rows, int per, int H, void* __restrict__ dw,
+                                                        void* __restrict__ db, bool grad_f32) {
   __shared__ float s[2][16][2 * RB];
   const int r0 = (int)blockIdx.x * per, r1 = min(rows, r0 + per);
   const int wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
@@ -247,12 +248,21 @@ __global__ __launch_bounds__(MAXT) void k_norm_backward(const T* __restrict__ dy
       }
     }
   }
-  if (part) {
-    float* p = part + (int64_t)blockIdx.x * 2 * H;
+  if (!part) return;
+  float* p = part + (int64_t)blockIdx.x * 2 * H;
 #pragma unroll
-    for (int i = 0; i < NCH; ++i) {
-      store8(p + col[i], H - col[i], sw[i]);
-      store8(p + H + col[i], H - col[i], sb[i]);
+  for (int i = 0; i < NCH; ++i) {
+    const int c = col[i], n = H - c;
+    auto out = [&](void* o, const float* v) {
+      if (o && grad_f32) store8(static_cast<float*>(o) + c, n, v);
+      else if (o) store8(static_cast<uint16_t*>(o) + c, n, v);
+    };
+    if (gridDim.x == 1) {  // all rows are here: these are the gradients
+      out(dw, sw[i]);
+      out(db, sb[i]);
+    } else {
+      store8(p + c, n, sw[i]);
+      store8(p + H + c, n, sb[i]);
     }
   }
 }
@@ -314,21 +324,27 @@ static void backward_shape(int H, int* nch, int* threads) {
   *nch = chunks <= 1024 ? 1 : 4;
   *threads = ceil_div(ceil_div(chunks, *nch), 64) * 64;
 }
+static bool one_pass(int H, bool bf16) {
+  int nch, threads;
+  backward_shape(H, &nch, &threads);
+  return nch == 1 || (bf16 && threads <= 512);  // fp32 rows of four chunks a thread would not fit the registers
+}
 // Consecutive rows of one workgroup: the column sums of a block cost 4 H bytes twice over, a
 // row of it 2 H bytes or more three times, so at least 8 rows where there are that many, and
-// no more blocks than the device holds at a time.
+// no more blocks than the device holds at a time; up to 16 rows in
+// one block, which needs no second launch.
 static int rows_per_block(int T, int H) {
   int nch, threads;
   backward_shape(H, &nch, &threads);
   const int blocks = 256 * (threads >= 512 ? 1 : 512 / threads);
-  const int per = ceil_div(T, blocks), least = T < 4096 ? 4 : 8;
+  const int per = ceil_div(T, blocks), least = T <= 16 && H <= 8192 ? 16 : T < 4096 ? 4 : 8;
   return per > least ? per : least;
 }
 int norm_row_blocks(int T, int H) { return ceil_div(T, rows_per_block(T, H)); }
 
 template <typename T>
 static void norm_backward(const void* dy_, const void* x_, const void* w_, const float* mean, const float* rstd,
-                          void* dx_, float* part, int rows, int H, hipStream_t st) {
+                          void* dx_, float* part, int rows, int H, void* dw, void* db, bool grad_f32, hipStream_t st) {
   const T *dy = static_cast<const T*>(dy_), *x = static_cast<const T*>(x_), *w = static_cast<const T*>(w_);
   T* dx = static_cast<T*>(dx_);
   const int per = rows_per_block(rows, H);
@@ -336,16 +352,16 @@ static void norm_backward(const void* dy_, const void* x_, const void* w_, const
   backward_shape(H, &nch, &threads);
   const int grid = ceil_div(rows, per);
   if (nch == 1 && threads <= 256) {
-    k_norm_backward<T, 1, 4, 256><<<grid, threads, 0, st>>>(dy, x, w, mean, rstd, dx, part, rows, per, H);
+    k_norm_backward<T, 1, 4, 256><<<grid, threads, 0, st>>>(dy, x, w, mean, rstd, dx, part, rows, per, H, dw, db, grad_f32);
     return;
   }
   if (nch == 1) {
-    k_norm_backward<T, 1, sizeof(T) == 2 ? 2 : 1, 1024><<<grid, threads, 0, st>>>(dy, x, w, mean, rstd, dx, part, rows, per, H);
+    k_norm_backward<T, 1, sizeof(T) == 2 ? 2 : 1, 1024><<<grid, threads, 0, st>>>(dy, x, w, mean, rstd, dx, part, rows, per, H, dw, db, grad_f32);
     return;
   }
-  if constexpr (sizeof(T) == 2) {  // fp32 would not fit the registers
-    if (threads <= 512) {
-      k_norm_backward<T, 4, 1, 512><<<grid, threads, 0, st>>>(dy, x, w, mean, rstd, dx, part, rows, per, H);
+  if constexpr (sizeof(T) == 2) {
+    if (one_pass(H, true)) {
+      k_norm_backward<T, 4, 1, 512><<<grid, threads, 0, st>>>(dy, x, w, mean, rstd, dx, part, rows, per, H, dw, db, grad_f32);
       return;
     }
   }
@@ -355,11 +371,15 @@ static void norm_backward(const void* dy_, const void* x_, const void* w_, const
 }
 
 hipError_t launch_norm_backward(const void* dy, const void* x, const void* w, const float* mean,
-                                const float* rstd, void* dx, float* part, int T, int H, bool bf16,
-                                hipStream_t st) {
-  if (bf16) norm_backward<uint16_t>(dy, x, w, mean, rstd, dx, part, T, H, st);
-  else norm_backward<float>(dy, x, w, mean, rstd, dx, part, T, H, st);
-  return hipGetLastError();
+                                const float* rstd, void* dx, void* dw, void* db, bool grad_f32, float* part, int T,
+                                int H, bool bf16, hipStream_t st) {
+  if (!dw && !db) part = nullptr;
+  if (bf16) norm_backward<uint16_t>(dy, x, w, mean, rstd, dx, part, T, H, dw, db, grad_f32, st);
+  else norm_backward<float>(dy, x, w, mean, rstd, dx, part, T, H, dw, db, grad_f32, st);
+  const hipError_t r = hipGetLastError();
+  const int blocks = norm_row_blocks(T, H);
+  if (r != hipSuccess || !part || (blocks == 1 && one_pass(H, bf16))) return r;
+  return launch_col_sum(part, blocks, H, 2 * (int64_t)H, dw, db, grad_f32, st);
 }
 
 }  // namespace moe
