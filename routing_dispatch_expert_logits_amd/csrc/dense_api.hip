@@ -125,9 +125,9 @@ DenseWs dense_ws(const DenseDims& d, bool gated, bool backward) {
   }
   if (d.T > 0 && !decode) {
     const int z = gated ? 2 : 1;
-    w.slices = c.take(backward ? dense_part_bytes(d.bf16, d.T, d.K, d.N, z, 1, false)
-                               : dense_part_bytes(d.bf16, d.T, d.N, d.K, 1, 1, gated));
-    w.slices_w = c.take(backward ? dense_part_bytes(d.bf16, d.N, d.K, d.T, w.terms, z, false) : 0);
+    w.slices = c.take(backward ? dense_part_bytes(d.bf16, d.T, d.K, d.N, z, 1, false, false)
+                               : dense_part_bytes(d.bf16, d.T, d.N, d.K, 1, 1, gated, false));
+    w.slices_w = c.take(backward ? dense_part_bytes(d.bf16, d.N, d.K, d.T, w.terms, z, false, true) : 0);
   }
   w.total = c.cur;
   return w;

@@ -51,6 +51,7 @@ struct MmTile {
   static __device__ __forceinline__ int element(int q, int lane) {
     return ((((lane / PER) % RC) ^ swz(row(q, lane))) * PER + lane % PER) * (DB / ES);
   }
+  static_assert(!COL || (R & (R - 1)) == 0, "units are exchanged within a power of two");
   static __device__ __forceinline__ int f(int k) {
     return (ES == 2 ? (k & 3) | ((k >> 1) & 4) : (k >> 2) & 3) & (R / 16 - 1);
   }
@@ -538,7 +539,7 @@ static void mm_go(const DenseJob& j, const DenseEpi& e, const MmSlices& sl, hipS
   if (j.pair) k_dense_mm<T, BM, BN, WM, WN, S, SB, DB, false, false, true, DENSE_GATED><<<grid, block, 0, st>>>(j, e, sl);
   else if (e.kind == DENSE_LINEAR) k_dense_mm<T, BM, BN, WM, WN, S, SB, DB, false, false, false, DENSE_LINEAR><<<grid, block, 0, st>>>(j, e, sl);
   else if (!j.a_col) k_dense_mm<T, BM, BN, WM, WN, S, SB, DB, false, true, false, DENSE_STORE><<<grid, block, 0, st>>>(j, e, sl);
-  else k_dense_mm<T, BM, BN, WM, WN, S, SB, DB, true, true, false, DENSE_STORE><<<grid, block, 0, st>>>(j, e, sl);
+  else if constexpr ((BM & (BM - 1)) == 0) k_dense_mm<T, BM, BN, WM, WN, S, SB, DB, true, true, false, DENSE_STORE><<<grid, block, 0, st>>>(j, e, sl);
 }
 
 // Tile and slice count of one product, by estimated time.  A tile's constants are what its
@@ -555,6 +556,7 @@ struct MmTileCost {
 };
 constexpr MmTileCost kTilesBf16[] = {{256, 256, 1.50, 8.0, 1.50, 8.0},
                                      {256, 128, 0.88, 4.5, 0.80, 4.5},
+                                     {192, 128, 0.68, 4.0, 0.62, 4.0},  // not for column A operands
                                      {128, 128, 0.50, 3.0, 0.47, 3.0},
                                      {64, 64, 0.165, 1.3, 0.19, 2.5}};
 constexpr MmTileCost kTilesF32[] = {{64, 64, 0.42, 1.0, 0.57, 2.5}, {64, 32, 0.22, 0.8, 0.35, 2.5}};
@@ -564,21 +566,21 @@ struct MmPlan {
   double us;
   int cut;   // 256 x 256 tiles for this many output columns, and a launch of its own for the rest; 0: none
 };
-static MmPlan mm_plan(bool bf16, int M, int N, int K, int segs, int batch, bool pair, bool whole = false,
+static MmPlan mm_plan(bool bf16, int M, int N, int K, int segs, int batch, bool pair, bool a_col, bool whole = false,
                       int widest = 256) {
   constexpr int CUS = 256;
   MmPlan best{{}, 1, pair ? 2 : batch, (N + 7) / 8 * 8, 0.0, 0};
   const int steps = ceil_div(K, bf16 ? 64 : 32) * segs;  // of 128 bytes
-  for (int t = 0; t < (bf16 ? 4 : 2); ++t) {
+  for (int t = 0; t < (bf16 ? 5 : 2); ++t) {
     const MmTileCost& c = bf16 ? kTilesBf16[t] : kTilesF32[t];
-    if (c.bm > widest) continue;
+    if (c.bm > widest || (c.bm == 192 && a_col)) continue;
     const int64_t tiles = (int64_t)ceil_div(M, c.bm) * ceil_div(N, pair ? c.bn / 2 : c.bn) * batch;
     for (int s = 1; s <= (whole ? 1 : 32) && s <= ceil_div(steps, 4); s += s < 4 ? 1 : s / 2) {
       const int64_t rounds = (tiles * s + CUS - 1) / CUS;
       double us = rounds == 1 ? ceil_div(steps, s) * c.step_alone + c.fixed_alone
                               : rounds * (ceil_div(steps, s) * c.step + c.fixed);
       // the slices' sums are written and read again, and joined by a launch of their own
-      if (s > 1) us += 3.0 + (double)s * best.planes * M * N * 8 / 5e6;
+      if (s > 1) us += 4.0 + (double)s * best.planes * M * N * 8 / 5e6;
       if (!best.tile.bm || us < best.us) {
         best.us = us;
         best.tile = c;
@@ -594,7 +596,7 @@ static MmPlan mm_plan(bool bf16, int M, int N, int K, int segs, int batch, bool 
   if (bf16 && !whole && widest == 256 && column * tn > CUS) {
     const int64_t rounds = column * tn / CUS, n = rounds * CUS / column;
     if (n >= 1 && n < tn) {
-      const MmPlan rest = mm_plan(bf16, M, N - (int)n * on, K, segs, batch, pair, true);
+      const MmPlan rest = mm_plan(bf16, M, N - (int)n * on, K, segs, batch, pair, a_col, true);
       const double us = rounds * (steps * c.step + c.fixed) + 3.0 + rest.us;
       if (us < best.us) {
         best.us = us;
@@ -607,8 +609,8 @@ static MmPlan mm_plan(bool bf16, int M, int N, int K, int segs, int batch, bool 
   return best;
 }
 
-size_t dense_part_bytes(bool bf16, int M, int N, int K, int segs, int batch, bool pair) {
-  const MmPlan p = mm_plan(bf16, M, N, K, segs, batch, pair);
+size_t dense_part_bytes(bool bf16, int M, int N, int K, int segs, int batch, bool pair, bool a_col) {
+  const MmPlan p = mm_plan(bf16, M, N, K, segs, batch, pair, a_col);
   return p.slices > 1 ? (size_t)p.slices * p.planes * M * p.ldp * 4 : 0;
 }
 
@@ -621,7 +623,7 @@ static void mm_join(const DenseJob& j, const DenseEpi& e, const MmSlices& sl, hi
   else k_dense_join<T, DENSE_STORE><<<grid, 256, 0, st>>>(j.M, j.N, j.batch, e, sl);
 }
 
-static MmPlan plan_of(const DenseJob& j, bool bf16) { return mm_plan(bf16, j.M, j.N, j.K, j.segs, j.batch, j.pair); }
+static MmPlan plan_of(const DenseJob& j, bool bf16) { return mm_plan(bf16, j.M, j.N, j.K, j.segs, j.batch, j.pair, j.a_col); }
 static MmSlices slices_of(const MmPlan& p, float* part) {
   return MmSlices{p.slices > 1 ? part : nullptr, p.slices, p.planes, p.ldp};
 }
@@ -643,6 +645,8 @@ static hipError_t launch_planned(const DenseJob& j, const DenseEpi& e, const MmP
     mm_go<uint16_t, 256, 256, 2, 4, 4, 64>(j, e, sl, st);
   } else if (bm == 256) {
     mm_go<uint16_t, 256, 128, 4, 2, 3>(j, e, sl, st);
+  } else if (bm == 192) {
+    mm_go<uint16_t, 192, 128, 4, 2, 3>(j, e, sl, st);
   } else if (bm == 128) {
     mm_go<uint16_t, 128, 128, 2, 4, 4>(j, e, sl, st);
   } else {
@@ -675,7 +679,7 @@ hipError_t launch_dense(const DenseJob& j, const DenseEpi& e, bool bf16, float* 
     er.save[i] = on(e.save[i], es);
   }
   if (hipError_t r = launch_planned(left, e, p, bf16, nullptr, st); r != hipSuccess) return r;
-  return launch_planned(right, er, mm_plan(bf16, right.M, right.N, right.K, right.segs, right.batch, right.pair, true),
+  return launch_planned(right, er, mm_plan(bf16, right.M, right.N, right.K, right.segs, right.batch, right.pair, right.a_col, true),
                         bf16, nullptr, st);
 }
 
@@ -684,8 +688,8 @@ hipError_t launch_dense_two(const DenseJob& jx, const DenseEpi& ex, const DenseJ
   MmPlan px = plan_of(jx, bf16), pw = plan_of(jw, bf16);
   // together on 64-row tiles where that is less than each on its best: they overlap, and a launch is saved
   const double apart = px.us + pw.us + 3.0;
-  px = mm_plan(bf16, jx.M, jx.N, jx.K, jx.segs, jx.batch, false, false, 64);
-  pw = mm_plan(bf16, jw.M, jw.N, jw.K, jw.segs, jw.batch, false, false, 64);
+  px = mm_plan(bf16, jx.M, jx.N, jx.K, jx.segs, jx.batch, false, false, false, 64);
+  pw = mm_plan(bf16, jw.M, jw.N, jw.K, jw.segs, jw.batch, false, true, false, 64);
   if (0.8 * (px.us + pw.us) > apart || px.tile.bn != pw.tile.bn) {
     if (hipError_t r = launch_dense(jx, ex, bf16, part_x, st); r != hipSuccess) return r;
     return launch_dense(jw, ew, bf16, part_w, st);
