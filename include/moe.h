@@ -428,8 +428,8 @@ MOE_API moe_status moe_layer_forward_noalloc(const moe_layer_weights* w, const v
  *
  * The conventions at the top of this file hold, with these differences:
  * - every size from 1 up is taken, whole tiles or not: T, K and N need no multiple of
- *   anything (rows of a width that is no multiple of 8 are copied to padded rows in the
- *   workspace first, or read element by element, which costs their bytes again);
+ *   anything (bf16 operands whose width is no multiple of 8 are copied to padded rows in the
+ *   workspace first, except in forward passes of up to 16 rows, which costs their bytes again);
  * - T = 0 is a call on no rows: a forward pass does nothing, a backward pass writes zero
  *   weight and bias gradients;
  * - outputs may not overlap inputs, other outputs or the workspace, except that y of
@@ -437,7 +437,7 @@ MOE_API moe_status moe_layer_forward_noalloc(const moe_layer_weights* w, const v
  * - results do not depend on what else runs: sums are formed in a fixed order, with no
  *   atomics, in fp32.
  *
- * Limits: T <= 2^30, K and N (H) <= 2^21, no tensor above 2^35 elements (MOE_ERR_UNSUPPORTED).
+ * Limits: T <= 2^28, K and N (H) <= 2^21, no tensor above 2^33 elements (MOE_ERR_UNSUPPORTED).
  */
 typedef enum moe_act {
   MOE_ACT_NONE = 0,      /* a */

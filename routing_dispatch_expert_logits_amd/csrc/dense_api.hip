@@ -10,7 +10,9 @@ using namespace moe;
 
 namespace {
 
-constexpr int64_t kMaxRows = 1ll << 30, kMaxWidth = 1ll << 21, kMaxElems = 1ll << 35;
+// tiles of 64 rows and 16 columns: at most 2^23 of them by the elements and 2^22 more by the
+// rows, so that every grid stays below 2^32 threads
+constexpr int64_t kMaxRows = 1ll << 28, kMaxWidth = 1ll << 21, kMaxElems = 1ll << 33;
 
 struct DenseDims {
   int T, K, N, act;
@@ -125,9 +127,9 @@ DenseWs dense_ws(const DenseDims& d, bool gated, bool backward) {
   }
   if (d.T > 0 && !decode) {
     const int z = gated ? 2 : 1;
-    w.slices = c.take(backward ? dense_part_bytes(d.bf16, d.T, d.K, d.N, z, 1, false, false)
-                               : dense_part_bytes(d.bf16, d.T, d.N, d.K, 1, 1, gated, false));
-    w.slices_w = c.take(backward ? dense_part_bytes(d.bf16, d.N, d.K, d.T, w.terms, z, false, true) : 0);
+    w.slices = c.take(backward ? dense_part_bytes(d.bf16, d.T, d.K, d.N, z, 1, false, false, true)
+                               : dense_part_bytes(d.bf16, d.T, d.N, d.K, 1, 1, gated, false, false));
+    w.slices_w = c.take(backward ? dense_part_bytes(d.bf16, d.N, d.K, d.T, w.terms, z, false, true, true) : 0);
   }
   w.total = c.cur;
   return w;

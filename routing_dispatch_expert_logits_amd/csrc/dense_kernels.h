@@ -48,7 +48,7 @@ hipError_t launch_dense_decode(const DenseJob& j, const DenseEpi& e, bool bf16, 
 //
 // Products whose tiles are too few for the device are cut along the contraction; the slices'
 // sums meet in `part`, dense_part_bytes of scratch for the same sizes.
-size_t dense_part_bytes(bool bf16, int M, int N, int K, int segs, int batch, bool pair, bool a_col);
+size_t dense_part_bytes(bool bf16, int M, int N, int K, int segs, int batch, bool pair, bool a_col, bool backward);
 hipError_t launch_dense(const DenseJob& j, const DenseEpi& e, bool bf16, float* part, hipStream_t st);
 // A backward pass's dx and dw products, in one launch where both are small; each with its scratch.
 hipError_t launch_dense_two(const DenseJob& jx, const DenseEpi& ex, const DenseJob& jw, const DenseEpi& ew, bool bf16,

@@ -205,7 +205,7 @@ __device__ __forceinline__ void mm_body(const DenseJob& j, const DenseEpi& e, co
   constexpr int QA = TA::INSTR / W, QB = TB::INSTR / W;
   constexpr int ON = PAIR ? BN / 2 : BN;   // output columns of a tile
   static_assert(QA >= 1 && QB >= 1 && !(PAIR && (B_COL || FN % 2)), "tile");
-  static_assert(S >= 2 && S <= 4, "stages");
+  static_assert(S == 3 || S == 4, "stages");
   constexpr int STAGE = kMmStage<BM, BN, SB>;
 
   const MmWhere w = mm_where(block, ceil_div(j.M, BM), ceil_div(j.N, ON), j.batch, sl.slices);
@@ -318,11 +318,7 @@ __device__ __forceinline__ void mm_body(const DenseJob& j, const DenseEpi& e, co
     asm volatile("" ::: "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
-    fill(last);
-    // with two stages the loads go first: moved among the products they would come too late
-    // (8192 x 7168 x 2 * 2048 gated, operands in memory: 381 us, else 448); deeper rings have
-    // the time, and lose 8 % by it (4096^3 on 256 x 128: 115 us, else 123)
-    if (S == 2) __builtin_amdgcn_sched_barrier(0);
+    fill(last);  // the compiler may move these loads among the products: a ring this deep has the time
     multiply(cur);
   };
 
@@ -367,7 +363,7 @@ __device__ __forceinline__ void mm_body(const DenseJob& j, const DenseEpi& e, co
   segment();
   advance(first - seg * nk);
   fill(s0);
-  if (S > 2) fill(s1);
+  fill(s1);
   if (S > 3) fill(s2);
   if constexpr (SB == 64) {
     static_assert(S == 4 && W == 8 && ES == 2, "turns");
@@ -387,13 +383,6 @@ __device__ __forceinline__ void mm_body(const DenseJob& j, const DenseEpi& e, co
     if (s + 1 < steps) turn(s1, s0);
     if (s + 2 < steps) turn(s2, s1);
     if (!late) __builtin_amdgcn_s_barrier();
-  } else if constexpr (S == 2) {
-    for (int s = 0;;) {
-      step(s0, s1);
-      if (++s >= steps) break;
-      step(s1, s0);
-      if (++s >= steps) break;
-    }
   } else {
     // whole rounds of the ring, then the rest of one: with exits inside the round the compiler
     // merges their states and waits for the newest loads at the loop's head
@@ -486,7 +475,7 @@ template <typename T, int BM, int BN, int WM, int WN, int S, int SB, int DB, boo
           int KIND>
 __global__ __launch_bounds__(WM* WN * 64, 2) void k_dense_mm(DenseJob j, DenseEpi e, MmSlices sl) {
   constexpr int STAGE = kMmStage<BM, BN, SB>;
-  __shared__ __attribute__((aligned(1024))) uint16_t s0[STAGE], s1[STAGE], s2[S > 2 ? STAGE : 1], s3[S > 3 ? STAGE : 1];
+  __shared__ __attribute__((aligned(1024))) uint16_t s0[STAGE], s1[STAGE], s2[STAGE], s3[S > 3 ? STAGE : 1];
   mm_body<T, BM, BN, WM, WN, S, SB, DB, A_COL, B_COL, PAIR, KIND>(j, e, sl, blockIdx.x, s0, s1, s2, s3);
 }
 
@@ -544,7 +533,7 @@ static void mm_go(const DenseJob& j, const DenseEpi& e, const MmSlices& sl, hipS
 
 // Tile and slice count of one product, by estimated time.  A tile's constants are what its
 // kernel takes per contraction step and per workgroup beside the steps, on a CU that works
-// through several (at_once of them together) or has just one, measured with operands that
+// through several or has just one, measured with operands that
 // come from memory (MI355X).  bf16: 4096^3 takes 104 us on 256 x 256 tiles, 116 on 256 x 128,
 // 133 on 128 x 128 and 193 on 64 x 64; 2048^3, an eighth of the work with a quarter of the
 // tiles, 54, 27, 21 and 27; 512 x 2048 x 2048 52, 26, 16 and 10.  fp32 is bound by its matrix
@@ -609,9 +598,16 @@ static MmPlan mm_plan(bool bf16, int M, int N, int K, int segs, int batch, bool 
   return best;
 }
 
-size_t dense_part_bytes(bool bf16, int M, int N, int K, int segs, int batch, bool pair, bool a_col) {
-  const MmPlan p = mm_plan(bf16, M, N, K, segs, batch, pair, a_col);
+static size_t part_bytes(const MmPlan& p, int M) {
   return p.slices > 1 ? (size_t)p.slices * p.planes * M * p.ldp * 4 : 0;
+}
+// A backward pass's product may run on its own or together with the other one, on 64-row tiles
+// with slices of their own.
+size_t dense_part_bytes(bool bf16, int M, int N, int K, int segs, int batch, bool pair, bool a_col, bool backward) {
+  const size_t own = part_bytes(mm_plan(bf16, M, N, K, segs, batch, pair, a_col), M);
+  if (!backward) return own;
+  const size_t both = part_bytes(mm_plan(bf16, M, N, K, segs, batch, pair, a_col, false, 64), M);
+  return own > both ? own : both;
 }
 
 template <typename T>
@@ -687,7 +683,7 @@ hipError_t launch_dense_two(const DenseJob& jx, const DenseEpi& ex, const DenseJ
                             float* part_x, float* part_w, hipStream_t st) {
   MmPlan px = plan_of(jx, bf16), pw = plan_of(jw, bf16);
   // together on 64-row tiles where that is less than each on its best: they overlap, and a launch is saved
-  const double apart = px.us + pw.us + 3.0;
+  const double apart = px.us + pw.us + 3.0;  // and a launch
   px = mm_plan(bf16, jx.M, jx.N, jx.K, jx.segs, jx.batch, false, false, false, 64);
   pw = mm_plan(bf16, jw.M, jw.N, jw.K, jw.segs, jw.batch, false, true, false, 64);
   if (0.8 * (px.us + pw.us) > apart || px.tile.bn != pw.tile.bn) {

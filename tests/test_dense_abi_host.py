@@ -76,8 +76,8 @@ def test_dense_shapes_are_checked(call):
     for s in bad:
         assert call(s) == B.MOE_ERR_INVALID_ARG
         assert all(B.dense_workspace_bytes(s, c) == 0 for c in range(4))
-    for kw in (dict(T=(1 << 30) + 1), dict(K=(1 << 21) + 1), dict(N=(1 << 21) + 1),
-               dict(T=1 << 30, K=64), dict(K=1 << 21, N=1 << 15)):
+    for kw in (dict(T=(1 << 28) + 1), dict(K=(1 << 21) + 1), dict(N=(1 << 21) + 1),
+               dict(T=1 << 28, K=64), dict(T=1 << 28, N=33, K=8), dict(K=1 << 21, N=1 << 13)):
         assert call(with_(B.dense_shape(**ok), **kw)) == B.MOE_ERR_UNSUPPORTED
 
 
@@ -146,7 +146,7 @@ def test_norm_is_checked():
         s = with_(B.norm_shape(**ok), **kw)
         assert norm(s) == B.MOE_ERR_INVALID_ARG and norm_b(s) == B.MOE_ERR_INVALID_ARG
         assert B.norm_workspace_bytes(s) == 0
-    for kw in (dict(T=(1 << 30) + 1), dict(H=(1 << 21) + 1), dict(T=1 << 30, H=64)):
+    for kw in (dict(T=(1 << 28) + 1), dict(H=(1 << 21) + 1), dict(T=1 << 28, H=64)):
         assert norm(with_(B.norm_shape(**ok), **kw)) == B.MOE_ERR_UNSUPPORTED
     s = B.norm_shape(**ok)
     for n in ("x", "w", "y"):

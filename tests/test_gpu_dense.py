@@ -7,6 +7,7 @@ activations' own error: the bf16 kernels form them from the hardware's exp2 and 
 function, together below F = 2^-20 (1 + |a|) of |a|, and four times that for a slope.
 """
 import math
+import random
 
 import pytest
 import torch
@@ -67,8 +68,9 @@ def f64(t, dtype):
 
 
 def ws_for(s, call=None):
+    """Exactly the bytes asked for, between guard bands, NaN where they are read unwritten."""
     n = B.norm_workspace_bytes(s) if call is None else B.dense_workspace_bytes(s, call)
-    return torch.full((max(n, 16),), 0xFF, dtype=torch.uint8, device=DEV)   # NaN where it is read unwritten
+    return gu.empty((n,), "u8").fill_(0xFF) if n else None
 
 
 def check(name, got, ref, tol):
@@ -137,18 +139,18 @@ def test_gated_backward(size, dtype, grad):
     fe = 2.0 ** -18 * (1 + g.abs())
     eg, eu = fe * (dh * u).abs(), fe * (dh * g).abs()
     r = U[dtype]
-    check("dx", f64(dx, dtype), dg @ w1 + du @ w3,
-          r * (dg @ w1 + du @ w3).abs() + (r * dg.abs() + eg) @ w1.abs() + (r * du.abs() + eu) @ w3.abs()
-          + 2 * (fsum(dg, w1.T, 2 * N) + fsum(du, w3.T, 2 * N)))
-    rw = U[grad]                # three bf16 terms hold an fp32 value
-    for name, got, d, e in (("dw1", dw1, dg, eg), ("dw3", dw3, du, eu)):
-        check(name, f64(got, grad), d.T @ x,
-              U[grad] * (d.T @ x).abs() + (rw * d.abs() + e).T @ x.abs() + 2 * fsum(d.T, x.T, 3 * T))
-    # each gradient asked for alone is the same
+    # each gradient asked for alone too
     dx2, p, q = out((T, K), dtype), out((N, K), grad), out((N, K), grad)
     B.gated_backward(*args, dx2, None, None, s, ws)
     B.gated_backward(*args, None, p, q, s, ws)
-    assert torch.equal(dx, dx2) and torch.equal(dw1, p) and torch.equal(dw3, q)
+    for got in (dx, dx2):
+        check("dx", f64(got, dtype), dg @ w1 + du @ w3,
+              r * (dg @ w1 + du @ w3).abs() + (r * dg.abs() + eg) @ w1.abs() + (r * du.abs() + eu) @ w3.abs()
+              + 2 * (fsum(dg, w1.T, 2 * N) + fsum(du, w3.T, 2 * N)))
+    rw = U[grad]                # three bf16 terms hold an fp32 value
+    for name, got, d, e in (("dw1", dw1, dg, eg), ("dw3", dw3, du, eu), ("dw1", p, dg, eg), ("dw3", q, du, eu)):
+        check(name, f64(got, grad), d.T @ x,
+              U[grad] * (d.T @ x).abs() + (rw * d.abs() + e).T @ x.abs() + 2 * fsum(d.T, x.T, 3 * T))
 
 
 @pytest.mark.parametrize("dtype", ("bf16", "f32"))
@@ -198,23 +200,35 @@ def test_linear_backward(size, dtype, grad):
         dz = dy * act64(z, act)[1]
         r = U[dtype] if act != "none" else 0.0
         e = 2.0 ** -18 * (1 + z.abs()) * dy.abs() if act != "none" else 0.0 * dy
-        check("dx", f64(dx, dtype), dz @ w,
-              U[dtype] * (dz @ w).abs() + (r * dz.abs() + e) @ w.abs() + 2 * fsum(dz, w.T, N))
         rw = U[grad]                # three bf16 terms hold an fp32 value
-        check("dw", f64(dw, grad), dz.T @ x,
-              U[grad] * (dz.T @ x).abs() + (min(r, rw) * dz.abs() + e).T @ x.abs() + 2 * fsum(dz.T, x.T, 3 * T))
-        check("dbias", f64(db, grad), dz.sum(0),
-              U[grad] * dz.sum(0).abs() + e.sum(0) + (T + 8) * U32 * dz.abs().sum(0))
-        for keep in range(3):                    # each gradient alone is the same
+        ref = ((dz @ w, U[dtype] * (dz @ w).abs() + (r * dz.abs() + e) @ w.abs() + 2 * fsum(dz, w.T, N)),
+               (dz.T @ x, U[grad] * (dz.T @ x).abs() + (min(r, rw) * dz.abs() + e).T @ x.abs()
+                + 2 * fsum(dz.T, x.T, 3 * T)),
+               (dz.sum(0), U[grad] * dz.sum(0).abs() + e.sum(0) + (T + 8) * U32 * dz.abs().sum(0)))
+        kinds = (dtype, grad, grad)
+        for name, got, kind, (want, tol) in zip(("dx", "dw", "dbias"), (dx, dw, db), kinds, ref):
+            check(name, f64(got, kind), want, tol)
+        for keep in range(3):                    # each gradient alone
             o = [out((T, K), dtype), out((N, K), grad), out((N,), grad)]
             o = [t if i == keep else None for i, t in enumerate(o)]
             B.linear_backward(dev[0], dev[1] if keep == 1 else None, dev[2] if keep == 0 else None, dz_in, *o, s, ws)
-            assert torch.equal(o[keep], (dx, dw, db)[keep])
+            check("alone", f64(o[keep], kinds[keep]), *ref[keep])
 
 
 # Sizes that end inside the largest tiles and fill the device, together with those above on every
 # tile shape and with the contraction cut into slices; the 64-bit products run on the GPU.
-LARGE = [(3800, 4072, 4000), (8200, 520, 4100), (4104, 1096, 4112), (1030, 2056, 2100), (520, 4096, 520), (100, 7168, 1000)]
+LARGE = [(3800, 4072, 4000), (8200, 520, 4100), (4104, 1096, 4112), (1030, 2056, 2100), (520, 4096, 520), (100, 7168, 1000),
+         (5000, 300, 2200)]
+
+
+def random_sizes(n):
+    """Sizes spread over their logarithms, whole tiles, whole chunks and odd ones."""
+    r = random.Random(20)
+    spread = lambda lo, hi: int(math.exp(r.uniform(math.log(lo), math.log(hi))))  # noqa: E731
+    return [(spread(1, 4000),) + tuple(max(1, spread(8, 5000) // s * s) for s in r.choices((64, 8, 1), k=2)) for _ in range(n)]
+
+
+LARGE += random_sizes(28)
 
 
 def close(name, got, dtype, ref, tol):
