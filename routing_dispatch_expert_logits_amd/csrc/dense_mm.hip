@@ -98,11 +98,11 @@ struct MmTile {
 };
 
 // Eight neighbouring output columns n .. n + 7 of row m (the first `left` of them), from the
-// fp32 sums; rows of odd widths are stored at element alignment.  ACT: the activation; res: the
-// residual's eight, where there is one.
+// fp32 sums; rows of odd widths are stored at element alignment.  ACT: the activation; bias and
+// res: the bias' and the residual's eight, where there are such.
 template <typename T, int KIND, int ACT>
 __device__ __forceinline__ void mm_out8(const DenseEpi& e, int z, int m, int n, int N, float* a, const float* b,
-                                        const Raw8<T>& res) {
+                                        const Raw8<T>& bias, const Raw8<T>& res) {
   constexpr bool FAST = sizeof(T) == 2;
   const int64_t idx = (int64_t)m * e.ldo + n;
   const int left = N - n;
@@ -112,8 +112,7 @@ __device__ __forceinline__ void mm_out8(const DenseEpi& e, int z, int m, int n, 
     else store8(static_cast<T*>(e.out[z]) + idx, left, a);
   } else if constexpr (KIND == DENSE_LINEAR) {
     if (e.bias) {
-      load8(static_cast<const T*>(e.bias) + n, left, y);
-      for (int i = 0; i < 8; ++i) a[i] += y[i];
+      for (int i = 0; i < 8; ++i) a[i] += bias.get(i);
     }
     if (e.save[0]) store8(static_cast<T*>(e.save[0]) + idx, left, a);
     for (int i = 0; i < 8; ++i) a[i] = act_value<FAST>(a[i], ACT);
@@ -131,6 +130,10 @@ __device__ __forceinline__ void mm_out8(const DenseEpi& e, int z, int m, int n, 
   }
 }
 
+template <typename T, int KIND>
+__device__ __forceinline__ void load_bias(const DenseEpi& e, int n, int N, Raw8<T>* bias) {
+  if (KIND == DENSE_LINEAR && e.bias) bias->load(static_cast<const T*>(e.bias) + n, N - n);
+}
 template <typename T, int KIND>
 __device__ __forceinline__ void load_residual(const DenseEpi& e, int m, int n, int M, int N, Raw8<T>* res) {
   if (KIND == DENSE_LINEAR && e.residual)
@@ -399,14 +402,12 @@ __device__ __forceinline__ void mm_body(const DenseJob& j, const DenseEpi& e, co
   }
   __builtin_amdgcn_s_waitcnt(mm_waitcnt(0));
 
-  // Epilogue through LDS, the stages being free now: a wave's sums go to a 16 KB region of its
-  // own (in passes where they are more), rows of TN columns whose 16-byte chunks are rotated
+  // Epilogue through LDS, the stages being free now: a wave's sums go to a region of its own
+  // (in two passes where they are more than the stages hold), rows of TN columns whose 16-byte chunks are rotated
   // by row, and come back eight columns of a row per lane: whole cache lines per store, and one
   // copy of the epilogue's code in a loop, where straight from the accumulators it would be
   // FM * FN copies (which cost 12 us of a 120 us product, 4096^3, in instruction fetches and
   // scattered stores).
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
   constexpr int PASSES = TM * TN * 4 * W > S * STAGE * 2 ? 2 : 1, PM = TM / PASSES, PF = FM / PASSES;
   constexpr int CH = TN / 4;                       // chunks per row
   constexpr int OC = PAIR ? TN / 2 : TN;           // output columns of the wave
@@ -416,6 +417,20 @@ __device__ __forceinline__ void mm_body(const DenseJob& j, const DenseEpi& e, co
   uint16_t* stage = wave < PER ? s0 : wave < 2 * PER ? s1 : wave < 3 * PER ? s2 : s3;
   float* reg = reinterpret_cast<float*>(stage) + (wave % PER) * (PM * TN);
   const int nw = n0 + wn * OC, lr = lane / LPR, lc = lane % LPR;
+  const int mw = m0 + wm * TM + lr, n = nw + 8 * lc;
+  // A residual's rows are all on their way before the first is used: taken one iteration
+  // at a time their latency is most of the epilogue (8192 x 2048 x 7168: 40 us of 273).
+  constexpr int U = KIND == DENSE_LINEAR && PM > RPI ? PM / RPI : 1;
+  Raw8<T> res[PASSES][U], bias;
+  if (!sl.part) {
+    load_bias<T, KIND>(e, n, j.N, &bias);
+#pragma unroll
+    for (int p = 0; p < PASSES; ++p)
+#pragma unroll
+      for (int i = 0; i < U; ++i) load_residual<T, KIND>(e, mw + p * PM + i * RPI, n, j.M, j.N, &res[p][i]);
+  }
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
   auto pass = [&](auto which) __attribute__((always_inline)) {
     constexpr int p = which();
 #pragma unroll
@@ -426,7 +441,7 @@ __device__ __forceinline__ void mm_body(const DenseJob& j, const DenseEpi& e, co
                                   (((4 * b + (lane >> 4)) ^ (lane & (CH - 1) & 15)) << 2)) = acc[p * PF + a][b];
     asm volatile("" ::: "memory");  // the region is this wave's, and its LDS operations stay in order
     __builtin_amdgcn_wave_barrier();
-    const int mp = m0 + wm * TM + p * PM + lr, n = nw + 8 * lc;
+    const int mp = mw + p * PM;
     auto chunk = [&](int r, int c) __attribute__((always_inline)) {
       return *reinterpret_cast<const f32x4*>(reg + r * TN + ((c ^ (r & (CH - 1) & 15)) << 2));
     };
@@ -445,12 +460,6 @@ __device__ __forceinline__ void mm_body(const DenseJob& j, const DenseEpi& e, co
       }
     } else {
       with_act<KIND>(e.act, [&](auto act) __attribute__((always_inline)) {
-        // a residual's rows are all on their way before the first is used: taken one iteration
-        // at a time their latency is most of the epilogue (8192 x 2048 x 7168: 40 us of 273)
-        constexpr int U = KIND == DENSE_LINEAR && PM > RPI ? PM / RPI : 1;
-        Raw8<T> res[U];
-#pragma unroll
-        for (int i = 0; i < U; ++i) load_residual<T, KIND>(e, mp + i * RPI, n, j.M, j.N, &res[i]);
         for (int r0 = 0; r0 < PM; r0 += U * RPI) {
 #pragma unroll
           for (int i = 0; i < U; ++i) {
@@ -459,7 +468,7 @@ __device__ __forceinline__ void mm_body(const DenseJob& j, const DenseEpi& e, co
             f32x4 v[2] = {chunk(r, 2 * lc), chunk(r, 2 * lc + 1)}, u[2] = {v[0], v[1]};
             if (PAIR) u[0] = chunk(r, CH / 2 + 2 * lc), u[1] = chunk(r, CH / 2 + 2 * lc + 1);
             mm_out8<T, KIND, act()>(e, z, m, n, j.N, reinterpret_cast<float*>(v), reinterpret_cast<const float*>(u),
-                                    res[i]);
+                                    bias, res[p][i]);
           }
         }
       });
@@ -510,9 +519,10 @@ __global__ __launch_bounds__(256) void k_dense_join(int M, int N, int batch, Den
         for (int k = 0; k < 8; ++k) b[k] += p[k >> 2][k & 3];
       }
     }
-    Raw8<T> res;
+    Raw8<T> res, bias;
+    load_bias<T, KIND>(e, n, N, &bias);
     load_residual<T, KIND>(e, m, n, M, N, &res);
-    with_act<KIND>(e.act, [&](auto act) __attribute__((always_inline)) { mm_out8<T, KIND, act()>(e, z, m, n, N, a, b, res); });
+    with_act<KIND>(e.act, [&](auto act) __attribute__((always_inline)) { mm_out8<T, KIND, act()>(e, z, m, n, N, a, b, bias, res); });
   }
 }
 
