@@ -455,10 +455,11 @@ typedef struct moe_dense_shape {
   int32_t act;         /* moe_act */
   int32_t grad_dtype;  /* moe_dtype of weight and bias gradients: dtype, or MOE_F32.  With
                         * MOE_F32 in a bf16 layer the gradient before the activation enters
-                        * the weight gradients' products as three bf16 terms that hold its
-                        * fp32 value exactly, which triples those products' work wherever
-                        * there is an activation to go through; with MOE_BF16 as its rounded
-                        * value. */
+                        * the weight gradients' products as the bf16 terms that hold its fp32
+                        * value exactly, which multiplies those products' work: one term in a
+                        * linear layer with MOE_ACT_NONE or MOE_ACT_RELU, two in a gated
+                        * product with these, three with the others.  With MOE_BF16 it enters
+                        * them as its rounded value. */
   int32_t reserved;    /* 0 */
 } moe_dense_shape;
 

@@ -97,7 +97,7 @@ moe_status check_ws(Buffers& b, const void* ws, size_t ws_bytes, size_t need) {
 // such rows first.
 int64_t padded(const DenseDims& d, int cols) { return d.bf16 ? ((int64_t)cols + 7) / 8 * 8 : cols; }
 
-// Backward: the gradient before the activation as operand of the products (three bf16 terms of
+// Backward: the gradient before the activation as operand of the products (in bf16 terms of
 // each value, lo elements apart, where fp32 weight gradients are asked for), and the row
 // blocks' column sums.  slices, slices_w: the products' contraction
 // slices (dw's in slices_w).  x, w[2]: padded copies (0 bytes where the operand is read in place).
@@ -106,6 +106,13 @@ struct DenseWs {
   int terms;
   int64_t lo, ldk, ldn;
 };
+// bf16 terms that hold the fp32 gradient before the activation exactly: with a slope of 0 or 1
+// it is dy itself, or in a gated product one of two bf16 numbers (16 significant bits).
+int grad_terms(int act, bool gated) {
+  const bool slope01 = act == MOE_ACT_NONE || act == MOE_ACT_RELU;
+  return slope01 ? (gated ? 2 : 1) : 3;
+}
+
 DenseWs dense_ws(const DenseDims& d, bool gated, bool backward) {
   Carve c; DenseWs w{};
   w.ldk = padded(d, d.K);
@@ -118,7 +125,7 @@ DenseWs dense_ws(const DenseDims& d, bool gated, bool backward) {
   w.w[1] = c.take(pad_k && gated ? (size_t)d.N * w.ldk * d.es : 0);
   if (backward) {
     const bool through = gated || d.act != MOE_ACT_NONE;
-    w.terms = through && d.bf16 && d.grad_f32 ? 3 : 1;
+    w.terms = d.bf16 && d.grad_f32 ? grad_terms(d.act, gated) : 1;
     w.lo = (int64_t)(align_up((size_t)d.T * w.ldn * d.es) / d.es);
     const size_t bytes = through || w.ldn != d.N ? (size_t)w.lo * d.es * w.terms : 0;
     w.d0 = c.take(bytes);
@@ -180,12 +187,14 @@ moe_status forward(const DenseDims& d, const DenseWs& w, const void* x, const vo
 
 // dx = d0 w0 (+ d1 w1), the contraction over N, across the weights' rows, and dw_z = (sum of
 // d_z's terms)^T x, the contraction over the tokens, across both operands' rows.  dx or dw0
-// may be NULL.
+// may be NULL.  sum: column sums still to be joined.
 moe_status gradients(const DenseDims& d, const DenseWs& w, const void* d0, const void* d1, int terms, const void* x,
-                     const void* w0, const void* w1, void* dx, void* dw0, void* dw1, void* ws, hipStream_t st) {
+                     const void* w0, const void* w1, void* dx, void* dw0, void* dw1, const ColSum& sum, void* ws,
+                     hipStream_t st) {
   MOE_TRY(in_rows(d, w, dw0 ? &x : nullptr, dx ? &w0 : nullptr, dx ? &w1 : nullptr, ws, st));
-  DenseJob jx{}, jw{};
-  DenseEpi ex{}, ew{};
+  DenseProduct px{}, pw{};
+  DenseJob &jx = px.j, &jw = pw.j;
+  DenseEpi &ex = px.e, &ew = pw.e;
   jx.M = d.T; jx.N = d.K; jx.K = d.N;
   jx.segs = d1 ? 2 : 1; jx.batch = 1;
   jx.b_col = true;
@@ -208,10 +217,9 @@ moe_status gradients(const DenseDims& d, const DenseWs& w, const void* d0, const
   ew.kind = DENSE_STORE;
   ew.out_f32 = d.grad_f32;
   ew.out[0] = dw0; ew.out[1] = dw1;
-  float *px = at<float>(ws, w.slices), *pw = at<float>(ws, w.slices_w);
-  if (dx && dw0) MOE_HIP(launch_dense_two(jx, ex, jw, ew, d.bf16, px, pw, st));
-  else if (dx) MOE_HIP(launch_dense(jx, ex, d.bf16, px, st));
-  else MOE_HIP(launch_dense(jw, ew, d.bf16, pw, st));
+  px.part = at<float>(ws, w.slices);
+  pw.part = at<float>(ws, w.slices_w);
+  MOE_HIP(launch_dense_grads(dx ? &px : nullptr, dw0 ? &pw : nullptr, sum, d.bf16, st));
   return MOE_OK;
 }
 
@@ -335,8 +343,8 @@ moe_status moe_gated_backward(const void* dh, const void* x, const void* w1, con
   const int terms = dw1 ? w.terms : 1;
   void *d0 = at<void>(ws, w.d0), *d1 = at<void>(ws, w.d1);
   MOE_HIP(launch_act_grad(dh, g, u, d.act, d.bf16, d.T, d.N, d0, d1, terms, w.lo, w.ldn, nullptr, nullptr,
-                          false, st));
-  return gradients(d, w, d0, d1, terms, x, w1, w3, dx, dw1, dw3, ws, st);
+                          false, nullptr, st));
+  return gradients(d, w, d0, d1, terms, x, w1, w3, dx, dw1, dw3, ColSum{}, ws, st);
 }
 
 moe_status moe_linear_forward(const void* x, const void* w, const void* bias, const void* residual, void* y,
@@ -391,11 +399,15 @@ moe_status moe_linear_backward(const void* dy, const void* x, const void* w, con
   const bool operand = (through || p.ldn != d.N) && (dx || dw);
   void* d0 = operand ? at<void>(ws, p.d0) : nullptr;
   const int terms = dw ? p.terms : 1;
+  ColSum sum{};
   if (operand || dbias)
     MOE_HIP(launch_act_grad(dy, through ? z : nullptr, nullptr, d.act, d.bf16, d.T, d.N, d0, nullptr, terms, p.lo,
-                            p.ldn, at<float>(ws, p.part), dbias, d.grad_f32, st));
-  if (!dx && !dw) return MOE_OK;
-  return gradients(d, p, operand ? d0 : dy, nullptr, terms, x, w, nullptr, dx, dw, nullptr, ws, st);
+                            p.ldn, at<float>(ws, p.part), dbias, d.grad_f32, &sum, st));
+  if (!dx && !dw) {
+    MOE_HIP(launch_col_sum(sum, st));
+    return MOE_OK;
+  }
+  return gradients(d, p, operand ? d0 : dy, nullptr, terms, x, w, nullptr, dx, dw, nullptr, sum, ws, st);
 }
 
 }  // extern "C"

@@ -2,6 +2,7 @@
 #pragma once
 
 #include "moe.h"
+#include "dense_kernels.h"
 #include "moe_device.h"
 
 namespace moe {
@@ -178,5 +179,32 @@ struct Raw8 {
     else return __uint_as_float(v[i]);
   }
 };
+
+// COLS columns of waiting column sums by 16 COLS threads: 16 groups of the P rows (each in
+// ascending order, four loads at a time), then the groups.  half: 0 for out0, 1 for out1.
+template <int COLS>
+__device__ __forceinline__ void col_sum(const ColSum& c, int block, int half, float (*s)[COLS]) {
+  void* out = half ? c.out1 : c.out0;
+  if (!out) return;
+  const int tid = threadIdx.x % COLS, q = threadIdx.x / COLS, n = block * COLS + tid;
+  const float* src = c.part + (int64_t)half * c.N + min(n, c.N - 1);
+  float v = 0.f;
+  int p = q;
+  for (; p + 48 < c.P; p += 64) {
+    const float a = src[p * c.stride], b = src[(p + 16) * c.stride], d = src[(p + 32) * c.stride],
+                e = src[(p + 48) * c.stride];
+    v = (((v + a) + b) + d) + e;
+  }
+  for (; p < c.P; p += 16) v += src[p * c.stride];
+  s[q][tid] = v;
+  __syncthreads();
+  if (q == 0 && n < c.N) {
+    v = 0.f;
+#pragma unroll
+    for (int g = 0; g < 16; ++g) v += s[g][tid];
+    if (c.out_f32) static_cast<float*>(out)[n] = v;
+    else static_cast<uint16_t*>(out)[n] = f32_to_bf16(v);
+  }
+}
 
 }  // namespace moe

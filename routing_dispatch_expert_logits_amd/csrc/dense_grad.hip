@@ -17,6 +17,12 @@ int grad_row_blocks(int T, int N) {
   return want < most ? want : most;
 }
 
+// What its rounding to bf16 leaves of v: nothing of an infinity, whose first term says it all.
+__device__ __forceinline__ float after_bf16(float v) {
+  const float b = bf16_to_f32(f32_to_bf16(v));
+  return __builtin_isinf(b) ? 0.f : v - b;
+}
+
 // One pass over dh, g (and u): d0 = dh u act'(g), d1 = dh act(g) in fp32, rounded on store.
 // Workgroup (column block, row block); a thread owns 8 columns and every kGradSub-th row of
 // its block; the column sums of d0 go through LDS in row-lane order.
@@ -54,11 +60,11 @@ __global__ __launch_bounds__(256) void k_act_grad(const T* __restrict__ dh, cons
       if constexpr (sizeof(T) == 2) {
         for (int q = 1; q < terms; ++q) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) v0[i] -= bf16_to_f32(f32_to_bf16(v0[i]));
+          for (int i = 0; i < 8; ++i) v0[i] = after_bf16(v0[i]);
           store8(d0 + q * lo + out, np, v0);
           if (GATED) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v1[i] -= bf16_to_f32(f32_to_bf16(v1[i]));
+            for (int i = 0; i < 8; ++i) v1[i] = after_bf16(v1[i]);
             store8(d1 + q * lo + out, np, v1);
           }
         }
@@ -82,42 +88,19 @@ __global__ __launch_bounds__(256) void k_act_grad(const T* __restrict__ dh, cons
   }
 }
 
-// Column n of the partial sums: 16 groups of the P rows (each in ascending order, four loads at
-// a time), then the groups.
-__global__ __launch_bounds__(1024) void k_col_sum(const float* __restrict__ part, int P, int N, int64_t stride,
-                                                  void* __restrict__ out0, void* __restrict__ out1, bool out_f32) {
+__global__ __launch_bounds__(1024) void k_col_sum(ColSum c) {
   __shared__ float s[16][64];
-  void* out = blockIdx.y ? out1 : out0;
-  if (!out) return;
-  const int n = (int)blockIdx.x * 64 + (threadIdx.x & 63), q = threadIdx.x >> 6;
-  const float* src = part + (int64_t)blockIdx.y * N + min(n, N - 1);
-  float v = 0.f;
-  int p = q;
-  for (; p + 48 < P; p += 64) {
-    const float a = src[p * stride], b = src[(p + 16) * stride], c = src[(p + 32) * stride], d = src[(p + 48) * stride];
-    v = (((v + a) + b) + c) + d;
-  }
-  for (; p < P; p += 16) v += src[p * stride];
-  s[q][threadIdx.x & 63] = v;
-  __syncthreads();
-  if (q == 0 && n < N) {
-    v = 0.f;
-#pragma unroll
-    for (int g = 0; g < 16; ++g) v += s[g][threadIdx.x];
-    if (out_f32) static_cast<float*>(out)[n] = v;
-    else static_cast<uint16_t*>(out)[n] = f32_to_bf16(v);
-  }
+  col_sum(c, blockIdx.x, blockIdx.y, s);
 }
 
-hipError_t launch_col_sum(const float* part, int P, int N, int64_t stride, void* out0, void* out1, bool out_f32,
-                          hipStream_t st) {
-  k_col_sum<<<dim3(ceil_div(N, 64), out1 ? 2 : 1), 1024, 0, st>>>(part, P, N, stride, out0, out1, out_f32);
+hipError_t launch_col_sum(const ColSum& c, hipStream_t st) {
+  if (c.P) k_col_sum<<<dim3(ceil_div(c.N, 64), c.out1 ? 2 : 1), 1024, 0, st>>>(c);
   return hipGetLastError();
 }
 
 hipError_t launch_act_grad(const void* dh, const void* g, const void* u, int act, bool bf16, int T, int N,
                            void* d0, void* d1, int terms, int64_t lo, int64_t ld, float* part, void* sum, bool sum_f32,
-                           hipStream_t st) {
+                           ColSum* later, hipStream_t st) {
   const int single = ceil_div(T, kGradSub);  // without sums, a row per thread while the grid lasts
   const dim3 grid(ceil_div(N, kGradCols), sum ? grad_row_blocks(T, N) : single < 32768 ? single : 32768);
   if (!sum) part = nullptr;
@@ -130,8 +113,8 @@ hipError_t launch_act_grad(const void* dh, const void* g, const void* u, int act
   };
   if (bf16) go(static_cast<uint16_t*>(nullptr));
   else go(static_cast<float*>(nullptr));
-  if (const hipError_t r = hipGetLastError(); r != hipSuccess || !sum || grid.y == 1) return r;
-  return launch_col_sum(part, (int)grid.y, N, N, sum, nullptr, sum_f32, st);
+  if (sum && grid.y > 1) *later = ColSum{part, (int)grid.y, N, N, sum, nullptr, sum_f32};
+  return hipGetLastError();
 }
 
 // Eight elements of a padded row per thread.

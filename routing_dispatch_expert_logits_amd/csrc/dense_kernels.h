@@ -38,6 +38,17 @@ struct DenseEpi {
   int64_t ldo;           // row length of outputs, residual and saved values
 };
 
+// Column sums by row blocks, not joined yet: out0[n] = sum_p part[p * stride + n] and out1[n] =
+// sum_p part[p * stride + N + n] for p < P, n < N (each output nullable), in a fixed order; in
+// fp32 or bf16.  P == 0: none.
+struct ColSum {
+  const float* part;
+  int P, N;
+  int64_t stride;
+  void *out0, *out1;
+  bool out_f32;
+};
+
 // bf16: element type of the operands and of what the epilogue reads and writes (else fp32).
 // bf16: lda and ldb are whole 16-byte chunks, row operands zero from the contraction length on.
 //
@@ -50,25 +61,28 @@ hipError_t launch_dense_decode(const DenseJob& j, const DenseEpi& e, bool bf16, 
 // sums meet in `part`, dense_part_bytes of scratch for the same sizes.
 size_t dense_part_bytes(bool bf16, int M, int N, int K, int segs, int batch, bool pair, bool a_col, bool backward);
 hipError_t launch_dense(const DenseJob& j, const DenseEpi& e, bool bf16, float* part, hipStream_t st);
-// A backward pass's dx and dw products, in one launch where both are small; each with its scratch.
-hipError_t launch_dense_two(const DenseJob& jx, const DenseEpi& ex, const DenseJob& jw, const DenseEpi& ew, bool bf16,
-                            float* part_x, float* part_w, hipStream_t st);
+// A backward pass's dx and dw products (either NULL), in one launch where both are small; each
+// with its scratch.  Their slices and the column sums that wait meet in one last launch.
+struct DenseProduct {
+  DenseJob j;
+  DenseEpi e;
+  float* part;
+};
+hipError_t launch_dense_grads(const DenseProduct* dx, const DenseProduct* dw, const ColSum& sum, bool bf16,
+                              hipStream_t st);
 
 // The gradient before an activation, [T x N]:
 //   linear (dh == dy, u == NULL): d0 = dy act'(g);  gated: d0 = dh u act'(g), d1 = dh act(g).
-// d0, d1 (nullable) get them in the layer's type with rows of ld elements.  With terms = 3
-// (bf16) the second and third bf16 terms of each value follow at d + lo and d + 2 lo: the
-// three hold its 24 bits exactly.  sum (nullable) receives the column sums of the unrounded d0
-// (fp32 or bf16), by way of part: a row of N floats for each of the grad_row_blocks(T, N) row
-// blocks.
+// d0, d1 (nullable) get them in the layer's type with rows of ld elements.  With terms of 2
+// or 3 (bf16) the second and third bf16 terms of each value follow at d + lo and d + 2 lo: three
+// hold its 24 bits exactly, two a product of two bf16 numbers.  sum (nullable) receives the column sums of the unrounded d0
+// (fp32 or bf16): at once where there is one row block, else *later says what is to be joined
+// (part: a row of N floats for each of the grad_row_blocks(T, N) row blocks).
 int grad_row_blocks(int T, int N);
 hipError_t launch_act_grad(const void* dh, const void* g, const void* u, int act, bool bf16, int T, int N,
                            void* d0, void* d1, int terms, int64_t lo, int64_t ld, float* part, void* sum, bool sum_f32,
-                           hipStream_t st);
-// out0[n] = sum_p part[p * stride + n], out1[n] = sum_p part[p * stride + N + n] for n < N (each
-// nullable), in a fixed order; in fp32 or bf16.
-hipError_t launch_col_sum(const float* part, int P, int N, int64_t stride, void* out0, void* out1, bool out_f32,
-                          hipStream_t st);
+                           ColSum* later, hipStream_t st);
+hipError_t launch_col_sum(const ColSum& sum, hipStream_t st);
 // dst[r][0 .. ld) = src[r][0 .. cols) and zeros for up to three bf16 operands of the same width
 // (src NULL: none) in one launch; ld: cols rounded up to 8.
 struct PadRows {

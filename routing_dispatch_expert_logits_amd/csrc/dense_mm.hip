@@ -501,29 +501,48 @@ __global__ __launch_bounds__(256, 2) void k_dense_mm_two(DenseJob jx, DenseEpi e
     mm_body<T, 64, BN, WM, WN, S, 128, DB, true, true, false, DENSE_STORE>(jw, ew, sw, blockIdx.x - first, s0, s1, s2, s3);
 }
 
-// The slices' sums in ascending order, then the epilogue; eight columns per thread.
+// A product's slices' sums in ascending order, then the epilogue; eight columns per thread of
+// workgroup `block` of `blocks`.
+struct MmJoin {
+  int M, N, batch, blocks;
+  DenseEpi e;
+  MmSlices sl;
+};
 template <typename T, int KIND>
-__global__ __launch_bounds__(256) void k_dense_join(int M, int N, int batch, DenseEpi e, MmSlices sl) {
-  const int n8 = sl.ldp / 8;
-  const int64_t total = (int64_t)batch * M * n8;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+__device__ __forceinline__ void join(const MmJoin& j, int block) {
+  const int n8 = j.sl.ldp / 8;
+  const int64_t total = (int64_t)j.batch * j.M * n8;
+  for (int64_t i = (int64_t)block * 256 + threadIdx.x; i < total; i += (int64_t)j.blocks * 256) {
     const int64_t row = i / n8;
-    const int n = (int)(i - row * n8) * 8, z = (int)(row / M), m = (int)(row - (int64_t)z * M);
+    const int n = (int)(i - row * n8) * 8, z = (int)(row / j.M), m = (int)(row - (int64_t)z * j.M);
     float a[8] = {}, b[8] = {};
 #pragma unroll 4
-    for (int s = 0; s < sl.slices; ++s) {
-      const f32x4* p = sl.at(s, z, m, n, M);
+    for (int s = 0; s < j.sl.slices; ++s) {
+      const f32x4* p = j.sl.at(s, z, m, n, j.M);
       for (int k = 0; k < 8; ++k) a[k] += p[k >> 2][k & 3];
       if (KIND == DENSE_GATED) {
-        p = sl.at(s, 1, m, n, M);
+        p = j.sl.at(s, 1, m, n, j.M);
         for (int k = 0; k < 8; ++k) b[k] += p[k >> 2][k & 3];
       }
     }
     Raw8<T> res, bias;
-    load_bias<T, KIND>(e, n, N, &bias);
-    load_residual<T, KIND>(e, m, n, M, N, &res);
-    with_act<KIND>(e.act, [&](auto act) __attribute__((always_inline)) { mm_out8<T, KIND, act()>(e, z, m, n, N, a, b, bias, res); });
+    load_bias<T, KIND>(j.e, n, j.N, &bias);
+    load_residual<T, KIND>(j.e, m, n, j.M, j.N, &res);
+    with_act<KIND>(j.e.act, [&](auto act) __attribute__((always_inline)) { mm_out8<T, KIND, act()>(j.e, z, m, n, j.N, a, b, bias, res); });
   }
+}
+template <typename T, int KIND>
+__global__ __launch_bounds__(256) void k_dense_join(MmJoin j) { join<T, KIND>(j, blockIdx.x); }
+
+// What a backward pass has left to join, in one launch: the slices of dx, of dw, and column
+// sums.  A launch of its own costs each about 4 us, as much as most of them take.
+template <typename T>
+__global__ __launch_bounds__(256) void k_dense_tail(MmJoin x, MmJoin w, ColSum sum) {
+  __shared__ float s[16][16];
+  const int block = blockIdx.x;
+  if (block < x.blocks) join<T, DENSE_STORE>(x, block);
+  else if (block < x.blocks + w.blocks) join<T, DENSE_STORE>(w, block - x.blocks);
+  else col_sum(sum, block - x.blocks - w.blocks, 0, s);
 }
 
 // Workgroups of a product: its tiles' slices, a whole number for each of the 8 XCDs.
@@ -620,15 +639,6 @@ size_t dense_part_bytes(bool bf16, int M, int N, int K, int segs, int batch, boo
   return own > both ? own : both;
 }
 
-template <typename T>
-static void mm_join(const DenseJob& j, const DenseEpi& e, const MmSlices& sl, hipStream_t st) {
-  const int64_t want = ((int64_t)j.batch * j.M * (sl.ldp / 8) + 255) / 256;
-  const unsigned grid = (unsigned)(want < 4096 ? want : 4096);
-  if (j.pair) k_dense_join<T, DENSE_GATED><<<grid, 256, 0, st>>>(j.M, j.N, j.batch, e, sl);
-  else if (e.kind == DENSE_LINEAR) k_dense_join<T, DENSE_LINEAR><<<grid, 256, 0, st>>>(j.M, j.N, j.batch, e, sl);
-  else k_dense_join<T, DENSE_STORE><<<grid, 256, 0, st>>>(j.M, j.N, j.batch, e, sl);
-}
-
 static MmPlan plan_of(const DenseJob& j, bool bf16) { return mm_plan(bf16, j.M, j.N, j.K, j.segs, j.batch, j.pair, j.a_col); }
 static MmSlices slices_of(const MmPlan& p, float* part) {
   return MmSlices{p.slices > 1 ? part : nullptr, p.slices, p.planes, p.ldp};
@@ -637,7 +647,14 @@ static MmSlices slices_of(const MmPlan& p, float* part) {
 // fp32 operands whose rows are whole 16-byte chunks.
 static bool whole_chunks(const DenseJob& j) { return j.lda % 4 == 0 && j.ldb % 4 == 0; }
 
-// One launch, and one more where there are slices to join.
+static MmJoin join_of(const DenseJob& j, const DenseEpi& e, const MmPlan& p, float* part) {
+  MmJoin w{j.M, j.N, j.batch, 0, e, slices_of(p, part)};
+  const int64_t want = ((int64_t)j.batch * j.M * (p.ldp / 8) + 255) / 256;
+  if (p.slices > 1) w.blocks = (int)(want < 4096 ? want : 4096);
+  return w;
+}
+
+// One launch; its slices are still to be joined.
 static hipError_t launch_planned(const DenseJob& j, const DenseEpi& e, const MmPlan& p, bool bf16, float* part,
                                  hipStream_t st) {
   const MmSlices sl = slices_of(p, part);
@@ -658,14 +675,12 @@ static hipError_t launch_planned(const DenseJob& j, const DenseEpi& e, const MmP
   } else {
     mm_go<uint16_t, 64, 64, 2, 2, 4>(j, e, sl, st);
   }
-  if (hipError_t r = hipGetLastError(); r != hipSuccess || p.slices == 1) return r;
-  if (bf16) mm_join<uint16_t>(j, e, sl, st);
-  else mm_join<float>(j, e, sl, st);
   return hipGetLastError();
 }
 
-hipError_t launch_dense(const DenseJob& j, const DenseEpi& e, bool bf16, float* part, hipStream_t st) {
-  const MmPlan p = plan_of(j, bf16);
+// The product by its plan, in one or two launches; its slices are still to be joined.
+static hipError_t launch_sliced(const DenseJob& j, const DenseEpi& e, const MmPlan& p, bool bf16, float* part,
+                                hipStream_t st) {
   if (!p.cut) return launch_planned(j, e, p, bf16, part, st);
   DenseJob left = j, right = j;
   DenseEpi er = e;
@@ -689,36 +704,59 @@ hipError_t launch_dense(const DenseJob& j, const DenseEpi& e, bool bf16, float* 
                         bf16, nullptr, st);
 }
 
-hipError_t launch_dense_two(const DenseJob& jx, const DenseEpi& ex, const DenseJob& jw, const DenseEpi& ew, bool bf16,
-                            float* part_x, float* part_w, hipStream_t st) {
-  MmPlan px = plan_of(jx, bf16), pw = plan_of(jw, bf16);
-  // together on 64-row tiles where that is less than each on its best: they overlap, and a launch is saved
-  const double apart = px.us + pw.us + 3.0;  // and a launch
-  px = mm_plan(bf16, jx.M, jx.N, jx.K, jx.segs, jx.batch, false, false, false, 64);
-  pw = mm_plan(bf16, jw.M, jw.N, jw.K, jw.segs, jw.batch, false, true, false, 64);
-  if (0.8 * (px.us + pw.us) > apart || px.tile.bn != pw.tile.bn) {
-    if (hipError_t r = launch_dense(jx, ex, bf16, part_x, st); r != hipSuccess) return r;
-    return launch_dense(jw, ew, bf16, part_w, st);
+// The forward products; the epilogue where the slices meet.
+hipError_t launch_dense(const DenseJob& j, const DenseEpi& e, bool bf16, float* part, hipStream_t st) {
+  const MmPlan p = plan_of(j, bf16);
+  if (hipError_t r = launch_sliced(j, e, p, bf16, part, st); r != hipSuccess || p.slices == 1) return r;
+  const MmJoin w = join_of(j, e, p, part);
+  auto go = [&](auto kernel) { kernel<<<w.blocks, 256, 0, st>>>(w); };
+  if (j.pair && bf16) go(k_dense_join<uint16_t, DENSE_GATED>);
+  else if (j.pair) go(k_dense_join<float, DENSE_GATED>);
+  else if (bf16) go(k_dense_join<uint16_t, DENSE_LINEAR>);
+  else go(k_dense_join<float, DENSE_LINEAR>);
+  return hipGetLastError();
+}
+
+hipError_t launch_dense_grads(const DenseProduct* dx, const DenseProduct* dw, const ColSum& sum, bool bf16,
+                              hipStream_t st) {
+  MmPlan px{}, pw{};
+  if (dx) px = plan_of(dx->j, bf16);
+  if (dw) pw = plan_of(dw->j, bf16);
+  bool together = false;
+  if (dx && dw) {
+    // on 64-row tiles where that is less than each on its best: they overlap, and a launch is saved
+    const MmPlan sx = mm_plan(bf16, dx->j.M, dx->j.N, dx->j.K, dx->j.segs, dx->j.batch, false, false, false, 64);
+    const MmPlan sw = mm_plan(bf16, dw->j.M, dw->j.N, dw->j.K, dw->j.segs, dw->j.batch, false, true, false, 64);
+    together = 0.8 * (sx.us + sw.us) <= px.us + pw.us + 3.0 && sx.tile.bn == sw.tile.bn;
+    if (together) px = sx, pw = sw;
   }
-  const MmSlices sx = slices_of(px, part_x), sw = slices_of(pw, part_w);
-  const int bn = px.tile.bn;
-  const unsigned first = mm_grid(jx, sx, 64, bn), all = first + mm_grid(jw, sw, 64, bn);
-  const bool whole = whole_chunks(jx) && whole_chunks(jw);
-  auto go = [&](auto kernel) { kernel<<<all, 256, 0, st>>>(jx, ex, sx, (int)first, jw, ew, sw); };
-  if (bf16) go(k_dense_mm_two<uint16_t, 64, 2, 2, 4, 16>);
-  else if (bn == 64 && whole) go(k_dense_mm_two<float, 64, 2, 2, 3, 16>);
-  else if (bn == 64) go(k_dense_mm_two<float, 64, 2, 2, 3, 4>);
-  else if (whole) go(k_dense_mm_two<float, 32, 4, 1, 3, 16>);
-  else go(k_dense_mm_two<float, 32, 4, 1, 3, 4>);
-  if (hipError_t r = hipGetLastError(); r != hipSuccess) return r;
-  if (px.slices > 1) {
-    if (bf16) mm_join<uint16_t>(jx, ex, sx, st);
-    else mm_join<float>(jx, ex, sx, st);
+  // with no slices to join the sums are joined while the pass that wrote them has them in cache
+  const MmJoin x = dx ? join_of(dx->j, dx->e, px, dx->part) : MmJoin{}, w = dw ? join_of(dw->j, dw->e, pw, dw->part) : MmJoin{};
+  const bool tail = x.blocks + w.blocks > 0;
+  if (!tail)
+    if (hipError_t r = launch_col_sum(sum, st); r != hipSuccess) return r;
+  if (together) {
+    const MmSlices sx = slices_of(px, dx->part), sw = slices_of(pw, dw->part);
+    const int bn = px.tile.bn;
+    const unsigned first = mm_grid(dx->j, sx, 64, bn), all = first + mm_grid(dw->j, sw, 64, bn);
+    const bool whole = whole_chunks(dx->j) && whole_chunks(dw->j);
+    auto go = [&](auto kernel) { kernel<<<all, 256, 0, st>>>(dx->j, dx->e, sx, (int)first, dw->j, dw->e, sw); };
+    if (bf16) go(k_dense_mm_two<uint16_t, 64, 2, 2, 4, 16>);
+    else if (bn == 64 && whole) go(k_dense_mm_two<float, 64, 2, 2, 3, 16>);
+    else if (bn == 64) go(k_dense_mm_two<float, 64, 2, 2, 3, 4>);
+    else if (whole) go(k_dense_mm_two<float, 32, 4, 1, 3, 16>);
+    else go(k_dense_mm_two<float, 32, 4, 1, 3, 4>);
+    if (hipError_t r = hipGetLastError(); r != hipSuccess) return r;
+  } else {
+    if (dx)
+      if (hipError_t r = launch_sliced(dx->j, dx->e, px, bf16, dx->part, st); r != hipSuccess) return r;
+    if (dw)
+      if (hipError_t r = launch_sliced(dw->j, dw->e, pw, bf16, dw->part, st); r != hipSuccess) return r;
   }
-  if (pw.slices > 1) {
-    if (bf16) mm_join<uint16_t>(jw, ew, sw, st);
-    else mm_join<float>(jw, ew, sw, st);
-  }
+  if (!tail) return hipSuccess;
+  const unsigned blocks = x.blocks + w.blocks + (sum.P ? ceil_div(sum.N, 16) : 0);
+  if (bf16) k_dense_tail<uint16_t><<<blocks, 256, 0, st>>>(x, w, sum);
+  else k_dense_tail<float><<<blocks, 256, 0, st>>>(x, w, sum);
   return hipGetLastError();
 }
 

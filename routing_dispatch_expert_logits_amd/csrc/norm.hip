@@ -379,7 +379,7 @@ hipError_t launch_norm_backward(const void* dy, const void* x, const void* w, co
   const hipError_t r = hipGetLastError();
   const int blocks = norm_row_blocks(T, H);
   if (r != hipSuccess || !part || (blocks == 1 && one_pass(H, bf16))) return r;
-  return launch_col_sum(part, blocks, H, 2 * (int64_t)H, dw, db, grad_f32, st);
+  return launch_col_sum(ColSum{part, blocks, H, 2 * (int64_t)H, dw, db, grad_f32}, st);
 }
 
 }  // namespace moe

@@ -215,6 +215,49 @@ def test_linear_backward(size, dtype, grad):
             check("alone", f64(o[keep], kinds[keep]), *ref[keep])
 
 
+@pytest.mark.parametrize("act", ("none", "relu"))
+@pytest.mark.parametrize("size", ((1, 64, 64), (130, 515, 260), (700, 72, 129)), ids=small)
+def test_f32_gradients_of_a_slope_of_one(size, act):
+    """With slopes of 0 and 1 the gradient before the activation is one bf16 number or a product
+    of two, which the operands of the products hold exactly: only the fp32 sums are off."""
+    T, K, N = size
+    gen = torch.Generator().manual_seed(sum(size) + 4)
+    dy, x, g, u = rand(gen, T, N), rand(gen, T, K), rand(gen, T, N), rand(gen, T, N)
+    s = B.dense_shape(T, K, N, act=act, grad_dtype="f32")
+    dev = [framed(t) for t in (dy, x, g, u)]
+    w = framed(rand(gen, N, K))
+    dw, dw1, dw3 = (out((N, K), "f32") for _ in range(3))
+    B.linear_backward(dev[0], dev[1], None, dev[2] if act != "none" else None, None, dw, None, s,
+                      ws_for(s, B.MOE_CALL_LINEAR_BACKWARD))
+    B.gated_backward(dev[0], dev[1], w, w, dev[2], dev[3], None, dw1, dw3, s, ws_for(s, B.MOE_CALL_GATED_BACKWARD))
+    dy, x, g, u = (t.double() for t in (dy, x, g, u))
+    a, slope = act64(g, act)
+    for name, got, d in (("dw", dw, dy * slope), ("dw1", dw1, dy * u * slope), ("dw3", dw3, dy * a)):
+        check(name, f64(got, "f32"), d.T @ x, U32 * (d.T @ x).abs() + 2 * fsum(d.T, x.T, 2 * T))
+
+
+@pytest.mark.parametrize("act", ACTS)
+def test_infinite_gradients_stay_infinite(act):
+    """An infinite gradient row gives infinite weight gradients of its own row and no others, in
+    fp32 as in bf16: the terms of an fp32 gradient do not make it NaN."""
+    T, K, N = 3, 40, 24
+    gen = torch.Generator().manual_seed(7)
+    dy, x, g, u = rand(gen, T, N), rand(gen, T, K).abs() + 0.5, rand(gen, T, N).abs() + 0.5, rand(gen, T, N).abs() + 0.5
+    w = rand(gen, N, K).to(DEV)
+    dy[1, 5] = float("inf")
+    for grad in ("bf16", "f32"):
+        s = B.dense_shape(T, K, N, act=act, grad_dtype=grad)
+        dev = [t.to(DEV) for t in (dy, x, g, u)]
+        dw, dw1, dw3, db = (out(sh, grad) for sh in ((N, K), (N, K), (N, K), (N,)))
+        B.linear_backward(dev[0], dev[1], None, dev[2] if act != "none" else None, None, dw, db, s,
+                          ws_for(s, B.MOE_CALL_LINEAR_BACKWARD))
+        B.gated_backward(dev[0], dev[1], w, w, dev[2], dev[3], None, dw1, dw3, s, ws_for(s, B.MOE_CALL_GATED_BACKWARD))
+        for name, got in (("dw", dw), ("dbias", db), ("dw1", dw1), ("dw3", dw3)):
+            got = f64(got, grad)
+            assert bool((got[5] == float("inf")).all()), name
+            assert bool(torch.isfinite(torch.cat((got[:5], got[6:]))).all()), name
+
+
 # Sizes that end inside the largest tiles and fill the device, together with those above on every
 # tile shape and with the contraction cut into slices; the 64-bit products run on the GPU.
 LARGE = [(3800, 4072, 4000), (8200, 520, 4100), (4104, 1096, 4112), (1030, 2056, 2100), (520, 4096, 520), (100, 7168, 1000),
