@@ -73,9 +73,11 @@ __device__ __forceinline__ float act_value_slope(float a, int act, float* slope)
       return a * p;
     }
     case MOE_ACT_GELU_TANH: {
-      // e^(-2q) overflows to inf for very negative a: p = 0, and p (1 - p) = 0
+      // e^(-2q) overflows to inf for very negative a: p = 0, and p (1 - p) = 0 from |a| = 16 on,
+      // whose factors are held there lest a square overflows and 0 times it is NaN
       const float p = recip<FAST>(1.f + exp_of<FAST>(-kTanhC * (a + kTanhA * a * a * a)));
-      *slope = p + a * p * (1.f - p) * kTanhC * (1.f + 3.f * kTanhA * a * a);
+      const float b = fminf(fmaxf(a, -16.f), 16.f);
+      *slope = p + b * p * (1.f - p) * kTanhC * (1.f + 3.f * kTanhA * b * b);
       return a * p;
     }
     default: *slope = 1.f; return a;

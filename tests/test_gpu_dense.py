@@ -258,6 +258,28 @@ def test_infinite_gradients_stay_infinite(act):
             assert bool(torch.isfinite(torch.cat((got[:5], got[6:]))).all()), name
 
 
+@pytest.mark.parametrize("dtype", ("bf16", "f32"))
+@pytest.mark.parametrize("act", ACTS)
+def test_activations_of_the_largest_values(act, dtype):
+    """act and act' of finite pre-activations up to the type's largest: themselves and 1, or 0."""
+    z = torch.tensor([20.0, 1e5, 1e13, 1e20, 3e38], dtype=TYPES[dtype])
+    z = torch.cat((z, -z, -z[:2])).view(1, -1)
+    N = z.numel()
+    s = B.dense_shape(1, N, N, dtype=dtype, act=act)
+    eye = torch.eye(N, dtype=TYPES[dtype]).to(DEV)
+    y, db = out((1, N), dtype), out((N,), dtype)
+    B.linear_forward(z.to(DEV), eye, None, None, y, s, ws_for(s, B.MOE_CALL_LINEAR_FORWARD))
+    B.linear_backward(torch.full_like(z, 2.0).to(DEV), None, None, z.to(DEV) if act != "none" else None, None, None, db, s,
+                      ws_for(s, B.MOE_CALL_LINEAR_BACKWARD))
+    up = (z.double() > 0) | (act == "none")
+    # |act(-20)| and |act'(-20)| are below 20 e^(-20), and so far are act(20) and act'(20) from 20
+    # and 1; e^(-20), the sum, the reciprocal and the product round in fp32 (2^-18 for all of them)
+    far = 20 * math.exp(-20.0) * (1 + 2.0 ** -18)
+    want = torch.where(up, z.double(), 0.0)
+    check("y", f64(y, dtype), want, 2 * U32 * want.abs() + far)
+    check("dbias", f64(db, dtype), torch.where(up, 2.0, 0.0).double()[0], 2 * far + 2 * U32)
+
+
 # Sizes that end inside the largest tiles and fill the device, together with those above on every
 # tile shape and with the contraction cut into slices; the 64-bit products run on the GPU.
 LARGE = [(3800, 4072, 4000), (8200, 520, 4100), (4104, 1096, 4112), (1030, 2056, 2100), (520, 4096, 520), (100, 7168, 1000),
