@@ -1,5 +1,7 @@
 // Dense forward products of up to 16 rows (decoding steps): the weights are read once, straight
-// from memory into matrix-core operands.
+// from memory into matrix-core operands, which bounds them.  Measured (MI355X, bf16): 8 rows by
+// two 2048 x 7168 weights 12.9 us, 4.6 TB/s; 1 row by one of 7168 x 2048 8.1 us, 3.6 TB/s with
+// its launch.
 #include "dense_device.h"
 #include "dense_kernels.h"
 

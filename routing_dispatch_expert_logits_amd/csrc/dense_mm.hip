@@ -186,6 +186,11 @@ struct MmSlices {
 // [15:14]), no LDS operation (bits [11:8]), exports as they are.
 constexpr int mm_waitcnt(int n) { return (n & 0xF) | ((n >> 4) << 14) | (0x7 << 4); }
 
+// Bound by the matrix cores where the device is full: 8192^3 in bf16 takes 819 us forward, 787 for
+// dx and 772 for dw (1.34, 1.40 and 1.43 PFLOP/s on 256 x 256 tiles; the library's products of
+// the three layouts run at 1.43, 1.34 and 1.18), 4096^3 in fp32 950 us (145 of the library's
+// 154 TFLOP/s).  Smaller products are bound by their tiles' prologues, epilogues and last round.
+//
 // BM x BN tile by WM x WN waves, S LDS stages: up to S - 1 steps' loads are in flight while one
 // stage is multiplied.  With PAIR the tile's first BN / 2 rows of B come from the first weight
 // and the rest from the second, for the same BN / 2 output columns.

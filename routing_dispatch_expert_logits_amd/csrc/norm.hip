@@ -1,5 +1,10 @@
-// Layer norm, forward and backward.  Both are bound by memory: a row is read once, kept in
-// registers while its sums are formed, and written once.
+// Layer norm, forward and backward: y = (x - mean) rstd w + b; with n = (x - mean) rstd and
+// e = dy w, dx = rstd (e - mean(e) - n mean(e n)), dw = sum_t dy n, db = sum_t dy.  Both are
+// bound by memory: a row is read once, kept in registers while its sums are formed, and written
+// once.  Measured (MI355X, 8192 x 7168, bf16): forward 55 us, 4.27 TB/s; backward with all three
+// gradients 81 us, 4.33 TB/s; a copy of 2 GiB runs at 4.9 TB/s.  One row of 4096 takes 6.5 us, a
+// launch; 2049 x 1021 fp32 backward 13.5 us, two launches and their latencies (25 MB, 5 us at
+// that rate).
 #include "dense_device.h"
 #include "dense_kernels.h"
 
