@@ -587,27 +587,33 @@ struct MmPlan {
   MmTileCost tile;
   int slices, planes, ldp;
   double us;
+  double items, each, join;  // workgroups with work, the time of one among others, and the slices' join
   int cut;   // 256 x 256 tiles for this many output columns, and a launch of its own for the rest; 0: none
 };
+// whole: no slices; only: tiles of 64 rows and this many columns.
 static MmPlan mm_plan(bool bf16, int M, int N, int K, int segs, int batch, bool pair, bool a_col, bool whole = false,
-                      int widest = 256) {
+                      int only = 0) {
   constexpr int CUS = 256;
-  MmPlan best{{}, 1, pair ? 2 : batch, (N + 7) / 8 * 8, 0.0, 0};
+  MmPlan best{{}, 1, pair ? 2 : batch, (N + 7) / 8 * 8, 0.0, 0.0, 0.0, 0.0, 0};
   const int steps = ceil_div(K, bf16 ? 64 : 32) * segs;  // of 128 bytes
   for (int t = 0; t < (bf16 ? 5 : 2); ++t) {
     const MmTileCost& c = bf16 ? kTilesBf16[t] : kTilesF32[t];
-    if (c.bm > widest || (c.bm == 192 && a_col)) continue;
+    if ((only && (c.bm != 64 || c.bn != only)) || (c.bm == 192 && a_col)) continue;
     const int64_t tiles = (int64_t)ceil_div(M, c.bm) * ceil_div(N, pair ? c.bn / 2 : c.bn) * batch;
     for (int s = 1; s <= (whole ? 1 : 32) && s <= ceil_div(steps, 4); s += s < 4 ? 1 : s / 2) {
       const int64_t rounds = (tiles * s + CUS - 1) / CUS;
       double us = rounds == 1 ? ceil_div(steps, s) * c.step_alone + c.fixed_alone
                               : rounds * (ceil_div(steps, s) * c.step + c.fixed);
       // the slices' sums are written and read again, and joined by a launch of their own
-      if (s > 1) us += 4.0 + (double)s * best.planes * M * N * 8 / 5e6;
+      const double join = s > 1 ? 4.0 + (double)s * best.planes * M * N * 8 / 5e6 : 0.0;
+      us += join;
       if (!best.tile.bm || us < best.us) {
         best.us = us;
         best.tile = c;
         best.slices = s;
+        best.items = (double)tiles * s;
+        best.each = ceil_div(steps, s) * c.step + c.fixed;
+        best.join = join;
       }
     }
   }
@@ -616,7 +622,7 @@ static MmPlan mm_plan(bool bf16, int M, int N, int K, int segs, int batch, bool 
   const MmTileCost& c = kTilesBf16[0];
   const int on = pair ? c.bn / 2 : c.bn, tn = ceil_div(N, on);
   const int64_t column = (int64_t)ceil_div(M, c.bm) * batch;  // tiles of one tile column
-  if (bf16 && !whole && widest == 256 && column * tn > CUS) {
+  if (bf16 && !whole && !only && column * tn > CUS) {
     const int64_t rounds = column * tn / CUS, n = rounds * CUS / column;
     if (n >= 1 && n < tn) {
       const MmPlan rest = mm_plan(bf16, M, N - (int)n * on, K, segs, batch, pair, a_col, true);
@@ -635,13 +641,18 @@ static MmPlan mm_plan(bool bf16, int M, int N, int K, int segs, int batch, bool 
 static size_t part_bytes(const MmPlan& p, int M) {
   return p.slices > 1 ? (size_t)p.slices * p.planes * M * p.ldp * 4 : 0;
 }
-// A backward pass's product may run on its own or together with the other one, on 64-row tiles
-// with slices of their own.
+// A backward pass's product may run on its own or together with the other one, on tiles of 64
+// rows and 64 columns (fp32: or 32), with slices of their own.  fp32, dx and dw, 64 columns
+// against 32: 128 x 1024 x 4096 31.8 and 37.6 us, 300 x 2000 x 1000 28.7 and 38.9; 32 are better
+// where few tiles of 64 would leave the CUs uneven (1000 x 1032 x 2056: 91 and 80).
+constexpr int kTogether[] = {64, 32};
 size_t dense_part_bytes(bool bf16, int M, int N, int K, int segs, int batch, bool pair, bool a_col, bool backward) {
-  const size_t own = part_bytes(mm_plan(bf16, M, N, K, segs, batch, pair, a_col), M);
-  if (!backward) return own;
-  const size_t both = part_bytes(mm_plan(bf16, M, N, K, segs, batch, pair, a_col, false, 64), M);
-  return own > both ? own : both;
+  size_t most = part_bytes(mm_plan(bf16, M, N, K, segs, batch, pair, a_col), M);
+  for (int t = 0; backward && t < (bf16 ? 1 : 2); ++t) {
+    const size_t both = part_bytes(mm_plan(bf16, M, N, K, segs, batch, pair, a_col, false, kTogether[t]), M);
+    most = most > both ? most : both;
+  }
+  return most;
 }
 
 static MmPlan plan_of(const DenseJob& j, bool bf16) { return mm_plan(bf16, j.M, j.N, j.K, j.segs, j.batch, j.pair, j.a_col); }
@@ -730,9 +741,16 @@ hipError_t launch_dense_grads(const DenseProduct* dx, const DenseProduct* dw, co
   bool together = false;
   if (dx && dw) {
     // on 64-row tiles where that is less than each on its best: they overlap, and a launch is saved
-    const MmPlan sx = mm_plan(bf16, dx->j.M, dx->j.N, dx->j.K, dx->j.segs, dx->j.batch, false, false, false, 64);
-    const MmPlan sw = mm_plan(bf16, dw->j.M, dw->j.N, dw->j.K, dw->j.segs, dw->j.batch, false, true, false, 64);
-    together = 0.8 * (sx.us + sw.us) <= px.us + pw.us + 3.0 && sx.tile.bn == sw.tile.bn;
+    MmPlan sx{}, sw{};
+    double best = 0.0;
+    for (int t = 0; t < (bf16 ? 1 : 2); ++t) {
+      const MmPlan x = mm_plan(bf16, dx->j.M, dx->j.N, dx->j.K, dx->j.segs, dx->j.batch, false, false, false, kTogether[t]);
+      const MmPlan w = mm_plan(bf16, dw->j.M, dw->j.N, dw->j.K, dw->j.segs, dw->j.batch, false, true, false, kTogether[t]);
+      // all workgroups' time over the CUs, half of the last one's, and the joins
+      const double us = (x.items * x.each + w.items * w.each) / 256 + 0.5 * (x.each > w.each ? x.each : w.each) + x.join + w.join;
+      if (t == 0 || us < best) best = us, sx = x, sw = w;
+    }
+    together = 0.8 * (sx.us + sw.us) <= px.us + pw.us + 3.0;
     if (together) px = sx, pw = sw;
   }
   // with no slices to join the sums are joined while the pass that wrote them has them in cache
