@@ -21,6 +21,7 @@ struct DenseJob {
   const void* A[2][3];
   const void* B[2][3];
   int64_t lda, ldb;
+  int b_from;   // of a column operand B: columns of its rows that lie before B (a cut's first part)
 };
 
 enum DenseEpiKind {

@@ -19,6 +19,17 @@ __device__ __forceinline__ const char* uniform(const char* p) {
   return reinterpret_cast<const char*>(((uint64_t)(uint32_t)uniform((int)(a >> 32)) << 32) | (uint32_t)uniform((int)a));
 }
 
+// What a tile may read of an operand, in bytes.  A row operand: from its first row on, whole rows and
+// none past the last.  A column operand: from column `from` of a contraction step's first row to
+// the end of the last of its `rows` rows (tests/host/dense_bounds.hip replays every launch's loads
+// against their operands).
+__host__ __device__ __forceinline__ int mm_row_bytes(int rows, int64_t ld, int es) { return rows * (int)ld * es; }
+__host__ __device__ __forceinline__ int mm_col_bytes(int rows, int64_t ld, int from, int es) {
+  return (rows * (int)ld - from) * es;
+}
+// The column of a column operand B's rows at which the tile at output column n0 starts.
+__host__ __device__ __forceinline__ int mm_b_column(const DenseJob& j, int n0) { return j.b_from + n0; }
+
 // A tile of R rows (m or n) by one contraction step in LDS, filled by buffer loads straight into
 // LDS (DB = 16 bytes per lane, lane i to byte DB i of the instruction's part; 4 for fp32 rows
 // that are no whole number of 16-byte chunks) and read as MFMA operands in
@@ -45,21 +56,21 @@ struct MmTile {
   static constexpr int CPR = R * ES / 16;           // column operand: chunks per LDS row
   static constexpr int UC = ES;                     // and chunks per unit (16 elements)
   static constexpr int RC = SB / 16;                // row operand: chunks per LDS row
-  static __device__ __forceinline__ int swz(int r) { return SB == 128 ? r & 7 : (r >> 1) & 3; }
+  static __host__ __device__ __forceinline__ int swz(int r) { return SB == 128 ? r & 7 : (r >> 1) & 3; }
   // Row operand: the row that a lane of fill instruction q fills, and its first element there.
-  static __device__ __forceinline__ int row(int q, int lane) { return (q * 64 + lane) / (RC * PER); }
-  static __device__ __forceinline__ int element(int q, int lane) {
+  static __host__ __device__ __forceinline__ int row(int q, int lane) { return (q * 64 + lane) / (RC * PER); }
+  static __host__ __device__ __forceinline__ int element(int q, int lane) {
     return ((((lane / PER) % RC) ^ swz(row(q, lane))) * PER + lane % PER) * (DB / ES);
   }
   static_assert(!COL || (R & (R - 1)) == 0, "units are exchanged within a power of two");
-  static __device__ __forceinline__ int f(int k) {
+  static __host__ __device__ __forceinline__ int f(int k) {
     return (ES == 2 ? (k & 3) | ((k >> 1) & 4) : (k >> 2) & 3) & (R / 16 - 1);
   }
 
   // Byte offset of lane's DB bytes of fill instruction q, from the tile's first row at
   // contraction 0 (row operand; rows >= valid are out of range) or from the tile's first
   // element of the step's first contraction row (column operand).
-  static __device__ __forceinline__ uint32_t src(int q, int lane, int64_t ld, int valid) {
+  static __host__ __device__ __forceinline__ uint32_t src(int q, int lane, int64_t ld, int valid) {
     if constexpr (COL) {
       const int at = q * 64 + lane, k = at / (CPR * PER), s = at / PER % CPR;
       const int chunk = ((s / UC) ^ f(k)) * UC + s % UC;
@@ -241,8 +252,8 @@ __device__ __forceinline__ void mm_body(const DenseJob& j, const DenseEpi& e, co
     const void* b = PAIR ? (second ? j.B[1][0] : j.B[0][0]) : j.B[z][seg];
     pa = uniform(static_cast<const char*>(j.A[z][seg]) + (A_COL ? (int64_t)m0 : (int64_t)m0 * j.lda) * ES);
     pb = uniform(static_cast<const char*>(b) + (B_COL ? (int64_t)n0 : (int64_t)n0 * j.ldb) * ES);
-    na = min(BM, j.M - m0) * (int)j.lda * ES;
-    nb = min(ON, j.N - n0) * (int)j.ldb * ES;
+    na = mm_row_bytes(min(BM, j.M - m0), j.lda, ES);
+    nb = mm_row_bytes(min(ON, j.N - n0), j.ldb, ES);
     left = j.K;
   };
   auto advance = [&](int n) __attribute__((always_inline)) {
@@ -275,8 +286,8 @@ __device__ __forceinline__ void mm_body(const DenseJob& j, const DenseEpi& e, co
         else __builtin_amdgcn_raw_ptr_buffer_load_lds(r, to, 4, off, 0, 0, 0);
       }
     };
-    one(pa, A_COL ? (rows * (int)j.lda - m0) * ES : na, A_COL, va, QA, wave * QA, 0);
-    one(pb, B_COL ? (rows * (int)j.ldb - n0) * ES : nb, B_COL, vb, QB, wave * QB, TA::HALFS);
+    one(pa, A_COL ? mm_col_bytes(rows, j.lda, m0, ES) : na, A_COL, va, QA, wave * QA, 0);
+    one(pb, B_COL ? mm_col_bytes(rows, j.ldb, mm_b_column(j, n0), ES) : nb, B_COL, vb, QB, wave * QB, TA::HALFS);
     advance(1);
   };
 
@@ -694,15 +705,16 @@ static hipError_t launch_planned(const DenseJob& j, const DenseEpi& e, const MmP
   return hipGetLastError();
 }
 
-// The product by its plan, in one or two launches; its slices are still to be joined.
-static hipError_t launch_sliced(const DenseJob& j, const DenseEpi& e, const MmPlan& p, bool bf16, float* part,
-                                hipStream_t st) {
-  if (!p.cut) return launch_planned(j, e, p, bf16, part, st);
-  DenseJob left = j, right = j;
-  DenseEpi er = e;
+// A product cut at output column p.cut: the columns left of it in `left` (with e), the others in
+// `right` with `er`.
+static void cut_product(const DenseJob& j, const DenseEpi& e, const MmPlan& p, bool bf16, DenseJob& left,
+                        DenseJob& right, DenseEpi& er) {
+  left = right = j;
+  er = e;
   const int es = bf16 ? 2 : 4, oes = e.kind == DENSE_STORE && e.out_f32 ? 4 : es;
   left.N = p.cut;
   right.N = j.N - p.cut;
+  if (j.b_col) right.b_from = j.b_from + p.cut;
   for (auto& z : right.B)
     for (auto& b : z)
       if (b) b = static_cast<const char*>(b) + (j.b_col ? (int64_t)p.cut : p.cut * j.ldb) * es;
@@ -715,9 +727,21 @@ static hipError_t launch_sliced(const DenseJob& j, const DenseEpi& e, const MmPl
     er.out[i] = on(e.out[i], oes);
     er.save[i] = on(e.save[i], es);
   }
+}
+
+static MmPlan plan_of_rest(const DenseJob& right, bool bf16) {
+  return mm_plan(bf16, right.M, right.N, right.K, right.segs, right.batch, right.pair, right.a_col, true);
+}
+
+// The product by its plan, in one or two launches; its slices are still to be joined.
+static hipError_t launch_sliced(const DenseJob& j, const DenseEpi& e, const MmPlan& p, bool bf16, float* part,
+                                hipStream_t st) {
+  if (!p.cut) return launch_planned(j, e, p, bf16, part, st);
+  DenseJob left, right;
+  DenseEpi er;
+  cut_product(j, e, p, bf16, left, right, er);
   if (hipError_t r = launch_planned(left, e, p, bf16, nullptr, st); r != hipSuccess) return r;
-  return launch_planned(right, er, mm_plan(bf16, right.M, right.N, right.K, right.segs, right.batch, right.pair, right.a_col, true),
-                        bf16, nullptr, st);
+  return launch_planned(right, er, plan_of_rest(right, bf16), bf16, nullptr, st);
 }
 
 // The forward products; the epilogue where the slices meet.
