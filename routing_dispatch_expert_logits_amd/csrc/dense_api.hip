@@ -99,10 +99,12 @@ int64_t padded(const DenseDims& d, int cols) { return d.bf16 ? ((int64_t)cols + 
 
 // Backward: the gradient before the activation as operand of the products (in bf16 terms of
 // each value, lo elements apart, where fp32 weight gradients are asked for), and the row
-// blocks' column sums.  slices, slices_w: the products' contraction
+// blocks' column sums.  finite: x with zeros for infinities and NaN, which the terms after the first
+// are multiplied with: a zero or a term of the other sign would make NaN of what an infinite x has
+// already made infinite in the first term's product.  slices, slices_w: the products' contraction
 // slices (dw's in slices_w).  x, w[2]: padded copies (0 bytes where the operand is read in place).
 struct DenseWs {
-  size_t x, w[2], d0, d1, part, slices, slices_w, total;
+  size_t x, w[2], d0, d1, finite, part, slices, slices_w, total;
   int terms;
   int64_t lo, ldk, ldn;
 };
@@ -130,6 +132,7 @@ DenseWs dense_ws(const DenseDims& d, bool gated, bool backward) {
     const size_t bytes = through || w.ldn != d.N ? (size_t)w.lo * d.es * w.terms : 0;
     w.d0 = c.take(bytes);
     w.d1 = c.take(gated ? bytes : 0);
+    w.finite = c.take(w.terms > 1 ? (size_t)d.T * w.ldk * d.es : 0);
     w.part = c.take(gated || d.T == 0 ? 0 : (size_t)grad_row_blocks(d.T, d.N) * d.N * 4);
   }
   if (d.T > 0 && !decode) {
@@ -159,6 +162,10 @@ moe_status in_rows(const DenseDims& d, const DenseWs& w, const void** x, const v
   one(2, w1, d.N, w.w[1]);
   MOE_HIP(launch_pad_rows(p, d.K, w.ldk, st));
   return MOE_OK;
+}
+
+FiniteRows finite_x(const DenseDims& d, const DenseWs& w, int terms, const void* x, void* ws) {
+  return terms > 1 ? FiniteRows{x, at<void>(ws, w.finite), d.K, w.ldk} : FiniteRows{};
 }
 
 size_t norm_ws(const NormDims& d) {
@@ -210,7 +217,7 @@ moe_status gradients(const DenseDims& d, const DenseWs& w, const void* d0, const
   for (int q = 0; q < terms; ++q) {
     jw.A[0][q] = static_cast<const char*>(d0) + q * w.lo * d.es;
     if (d1) jw.A[1][q] = static_cast<const char*>(d1) + q * w.lo * d.es;
-    jw.B[0][q] = jw.B[1][q] = x;
+    jw.B[0][q] = jw.B[1][q] = q ? at<void>(ws, w.finite) : x;
   }
   jw.lda = w.ldn;
   jw.ldb = w.ldk;
@@ -343,7 +350,7 @@ moe_status moe_gated_backward(const void* dh, const void* x, const void* w1, con
   const int terms = dw1 ? w.terms : 1;
   void *d0 = at<void>(ws, w.d0), *d1 = at<void>(ws, w.d1);
   MOE_HIP(launch_act_grad(dh, g, u, d.act, d.bf16, d.T, d.N, d0, d1, terms, w.lo, w.ldn, nullptr, nullptr,
-                          false, nullptr, st));
+                          false, nullptr, finite_x(d, w, terms, x, ws), st));
   return gradients(d, w, d0, d1, terms, x, w1, w3, dx, dw1, dw3, ColSum{}, ws, st);
 }
 
@@ -402,7 +409,7 @@ moe_status moe_linear_backward(const void* dy, const void* x, const void* w, con
   ColSum sum{};
   if (operand || dbias)
     MOE_HIP(launch_act_grad(dy, through ? z : nullptr, nullptr, d.act, d.bf16, d.T, d.N, d0, nullptr, terms, p.lo,
-                            p.ldn, at<float>(ws, p.part), dbias, d.grad_f32, &sum, st));
+                            p.ldn, at<float>(ws, p.part), dbias, d.grad_f32, &sum, finite_x(d, p, terms, x, ws), st));
   if (!dx && !dw) {
     MOE_HIP(launch_col_sum(sum, st));
     return MOE_OK;

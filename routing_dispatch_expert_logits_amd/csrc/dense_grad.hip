@@ -23,18 +23,37 @@ __device__ __forceinline__ float after_bf16(float v) {
   return __builtin_isinf(b) ? 0.f : v - b;
 }
 
+// The finite rows, eight elements of a row in dst per thread.
+__device__ __forceinline__ void finite_rows(const FiniteRows& f, int rows) {
+  const uint16_t* src = static_cast<const uint16_t*>(f.src);
+  uint16_t* dst = static_cast<uint16_t*>(f.dst);
+  const int per = (int)(f.ld / 8);
+  const int64_t total = (int64_t)rows * per, step = (int64_t)gridDim.x * gridDim.y * blockDim.x;
+  for (int64_t i = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * blockDim.x + threadIdx.x; i < total; i += step) {
+    const int64_t r = i / per;
+    const int c = (int)(i - r * per) * 8;
+    float v[8];
+    load8(src + r * f.cols + c, f.cols - c, v);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = fabsf(v[k]) < __builtin_inff() ? v[k] : 0.f;  // not so for NaN
+    store8(dst + i * 8, v);
+  }
+}
+
 // Bound by memory in bf16 (4096 x 8192 gated, 3 reads and 2 writes of 64 MB: 61 us, 5.5 TB/s), by
 // the exponentials of fp32 GELU otherwise (545 x 5664: 13 us, 37 MB).
 // One pass over dh, g (and u): d0 = dh u act'(g), d1 = dh act(g) in fp32, rounded on store.
 // Workgroup (column block, row block); a thread owns 8 columns and every kGradSub-th row of
-// its block; the column sums of d0 go through LDS in row-lane order.
+// its block; the column sums of d0 go through LDS in row-lane order.  A second plane of workgroups
+// (blockIdx.z) makes the finite rows, in the same launch.
 template <typename T, bool GATED>
 __global__ __launch_bounds__(256) void k_act_grad(const T* __restrict__ dh, const T* __restrict__ g,
                                                   const T* __restrict__ u, int act, int rows, int N,
                                                   T* __restrict__ d0, T* __restrict__ d1, int terms, int64_t lo,
                                                   int64_t ld, float* __restrict__ part, void* __restrict__ out,
-                                                  bool out_f32) {
+                                                  bool out_f32, FiniteRows finite) {
   constexpr bool FAST = sizeof(T) == 2;
+  if (sizeof(T) == 2 && blockIdx.z) return finite_rows(finite, rows);
   const int tid = threadIdx.x, cl = tid & 31, sub = tid >> 5;
   const int c0 = (int)blockIdx.x * kGradCols + cl * 8;
   const int per = ceil_div(rows, (int)gridDim.y);
@@ -102,16 +121,17 @@ hipError_t launch_col_sum(const ColSum& c, hipStream_t st) {
 
 hipError_t launch_act_grad(const void* dh, const void* g, const void* u, int act, bool bf16, int T, int N,
                            void* d0, void* d1, int terms, int64_t lo, int64_t ld, float* part, void* sum, bool sum_f32,
-                           ColSum* later, hipStream_t st) {
+                           ColSum* later, const FiniteRows& finite, hipStream_t st) {
   const int single = ceil_div(T, kGradSub);  // without sums, a row per thread while the grid lasts
-  const dim3 grid(ceil_div(N, kGradCols), sum ? grad_row_blocks(T, N) : single < 32768 ? single : 32768);
+  const dim3 grid(ceil_div(N, kGradCols), sum ? grad_row_blocks(T, N) : single < 32768 ? single : 32768,
+                  finite.src ? 2 : 1);
   if (!sum) part = nullptr;
   auto go = [&](auto* t) {
     using E = std::remove_pointer_t<decltype(t)>;
     const E *a = static_cast<const E*>(dh), *b = static_cast<const E*>(g), *c = static_cast<const E*>(u);
     E *p0 = static_cast<E*>(d0), *p1 = static_cast<E*>(d1);
-    if (u) k_act_grad<E, true><<<grid, 256, 0, st>>>(a, b, c, act, T, N, p0, p1, terms, lo, ld, part, sum, sum_f32);
-    else k_act_grad<E, false><<<grid, 256, 0, st>>>(a, b, c, act, T, N, p0, p1, terms, lo, ld, part, sum, sum_f32);
+    if (u) k_act_grad<E, true><<<grid, 256, 0, st>>>(a, b, c, act, T, N, p0, p1, terms, lo, ld, part, sum, sum_f32, finite);
+    else k_act_grad<E, false><<<grid, 256, 0, st>>>(a, b, c, act, T, N, p0, p1, terms, lo, ld, part, sum, sum_f32, finite);
   };
   if (bf16) go(static_cast<uint16_t*>(nullptr));
   else go(static_cast<float*>(nullptr));

@@ -76,13 +76,21 @@ hipError_t launch_dense_grads(const DenseProduct* dx, const DenseProduct* dw, co
 //   linear (dh == dy, u == NULL): d0 = dy act'(g);  gated: d0 = dh u act'(g), d1 = dh act(g).
 // d0, d1 (nullable) get them in the layer's type with rows of ld elements.  With terms of 2
 // or 3 (bf16) the second and third bf16 terms of each value follow at d + lo and d + 2 lo: three
-// hold its 24 bits exactly, two a product of two bf16 numbers.  sum (nullable) receives the column sums of the unrounded d0
-// (fp32 or bf16): at once where there is one row block, else *later says what is to be joined
+// hold its 24 bits exactly, two a product of two bf16 numbers.  sum (nullable) receives the column
+// sums of the unrounded d0 (fp32 or bf16): at once where there is one row block, else *later says what is to be joined
 // (part: a row of N floats for each of the grad_row_blocks(T, N) row blocks).
+// finite (bf16; src NULL: none): the T rows of src with zeros in place of infinities and NaN, in rows of
+// ld elements, zeros behind the first cols: what the terms after the first are multiplied with.
+struct FiniteRows {
+  const void* src;
+  void* dst;
+  int cols;
+  int64_t ld;
+};
 int grad_row_blocks(int T, int N);
 hipError_t launch_act_grad(const void* dh, const void* g, const void* u, int act, bool bf16, int T, int N,
                            void* d0, void* d1, int terms, int64_t lo, int64_t ld, float* part, void* sum, bool sum_f32,
-                           ColSum* later, hipStream_t st);
+                           ColSum* later, const FiniteRows& finite, hipStream_t st);
 hipError_t launch_col_sum(const ColSum& sum, hipStream_t st);
 // dst[r][0 .. ld) = src[r][0 .. cols) and zeros for up to three bf16 operands of the same width
 // (src NULL: none) in one launch; ld: cols rounded up to 8.

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from routing_dispatch_expert_logits_amd import binding as B
-from tests.test_gpu_dense import DEV, U, f64, out, ws_for
+from tests.test_gpu_dense import DEV, U, act64, f64, out, rand, ws_for
 
 pytestmark = pytest.mark.gpu
 
@@ -51,3 +51,36 @@ def test_gelu_tail(rows):
     tol = U["bf16"] * slope.abs() + rel * (small + bell.abs()) + torch.where(neg, 0.0, 2.0 ** -23)
     over = (dx - slope).abs() - 2 * tol        # rounded twice: before the product with w, and after
     assert bool((over <= 0).all()), (float(over.max()), z[over.argmax()])
+
+
+def same_kind(name, got, ref):
+    """NaN, infinities of either sign and finite numbers where ref has them."""
+    assert torch.equal(got.isnan(), ref.isnan()), f"{name}: NaN in {int(got.isnan().sum())} of {got.numel()}, expected {int(ref.isnan().sum())}"
+    inf = ref.isinf()
+    assert torch.equal(got.isinf(), inf) and torch.equal(got[inf], ref[inf]), name
+
+
+@pytest.mark.parametrize("dtype,grad", (("bf16", "bf16"), ("bf16", "f32"), ("f32", "f32")))
+@pytest.mark.parametrize("act", ("silu", "gelu", "gelu_tanh", "relu", "none"))
+@pytest.mark.parametrize("size", ((3, 40, 24), (70, 41, 130), (300, 1000, 264)), ids=lambda s: "x".join(map(str, s)))
+def test_infinite_inputs_give_infinite_weight_gradients(size, act, dtype, grad):
+    """dw = sum_t dz x is infinite where one x of the column is, and NaN where x is or where infinities
+    of both signs meet; the terms that hold a dz in fp32 have other signs and zeros among them."""
+    T, K, N = size
+    gen = torch.Generator().manual_seed(T + K)
+    dy, x, g, u, w = (rand(gen, *s, dtype=dtype) for s in ((T, N), (T, K), (T, N), (T, N), (N, K)))
+    g = g.abs() + 0.25                                  # no slope and no value is 0
+    x[1, 3], x[2, 5], x[0, 7], x[2, 7], x[1, 9] = (float(v) for v in ("inf", "-inf", "inf", "inf", "nan"))
+    s = B.dense_shape(T, K, N, dtype=dtype, act=act, grad_dtype=grad)
+    dev = [t.to(DEV) for t in (dy, x, g, u, w)]
+    dw, dw1, dw3 = (out((N, K), grad) for _ in range(3))
+    B.linear_backward(dev[0], dev[1], None, dev[2] if act != "none" else None, None, dw, None, s,
+                      ws_for(s, B.MOE_CALL_LINEAR_BACKWARD))
+    dx = out((T, K), dtype)
+    B.gated_backward(dev[0], dev[1], dev[4], dev[4], dev[2], dev[3], dx, dw1, dw3, s, ws_for(s, B.MOE_CALL_GATED_BACKWARD))
+    dy, x, g, u, w = (t.double() for t in (dy, x, g, u, w))
+    a, slope = act64(g, act)
+    for name, got, d in (("dw", dw, dy * slope), ("dw1", dw1, dy * u * slope), ("dw3", dw3, dy * a)):
+        assert not d[:3].eq(0).any()
+        same_kind(name, f64(got, grad), d.T @ x)
+    assert torch.isfinite(f64(dx, dtype)).all()         # dx does not read x
