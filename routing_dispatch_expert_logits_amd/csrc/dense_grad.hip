@@ -17,10 +17,13 @@ int grad_row_blocks(int T, int N) {
   return want < most ? want : most;
 }
 
-// What its rounding to bf16 leaves of v: nothing of an infinity, whose first term says it all.
-__device__ __forceinline__ float after_bf16(float v) {
-  const float b = bf16_to_f32(f32_to_bf16(v));
-  return __builtin_isinf(b) ? 0.f : v - b;
+// The first bf16 term of v, v rounded but no infinity in place of a finite v, and in *rest what it
+// leaves of v: nothing of an infinity, whose first term says it all.
+__device__ __forceinline__ float first_term(float v, float* rest) {
+  const bool finite = fabsf(v) < __builtin_inff();
+  const float b = bf16_to_f32(f32_to_bf16(v)), t = finite ? copysignf(fminf(fabsf(b), 0x1.fep127f), b) : b;
+  *rest = finite ? v - t : 0.f;
+  return t;
 }
 
 // The finite rows, eight elements of a row in dst per thread.
@@ -76,18 +79,26 @@ __global__ __launch_bounds__(256) void k_act_grad(const T* __restrict__ dh, cons
         v1[i] = i < nc ? vdh[i] * a : 0.f;
         sum[i] += v0[i];
       }
-      if (d0) store8(d0 + out, np, v0);
-      if (GATED) store8(d1 + out, np, v1);
-      if constexpr (sizeof(T) == 2) {
-        for (int q = 1; q < terms; ++q) {
+      if (sizeof(T) == 4 || terms == 1) {
+        if (d0) store8(d0 + out, np, v0);
+        if (GATED) store8(d1 + out, np, v1);
+        continue;
+      }
+      float t0[8], t1[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) v0[i] = after_bf16(v0[i]);
-          store8(d0 + q * lo + out, np, v0);
-          if (GATED) {
+      for (int i = 0; i < 8; ++i) {
+        t0[i] = first_term(v0[i], &v0[i]);
+        if (GATED) t1[i] = first_term(v1[i], &v1[i]);
+      }
+      store8(d0 + out, np, t0);
+      if (GATED) store8(d1 + out, np, t1);
+      for (int q = 1; q < terms; ++q) {
+        store8(d0 + q * lo + out, np, v0);
+        if (GATED) store8(d1 + q * lo + out, np, v1);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v1[i] = after_bf16(v1[i]);
-            store8(d1 + q * lo + out, np, v1);
-          }
+        for (int i = 0; i < 8; ++i) {
+          v0[i] -= bf16_to_f32(f32_to_bf16(v0[i]));
+          if (GATED) v1[i] -= bf16_to_f32(f32_to_bf16(v1[i]));
         }
       }
     }

@@ -84,3 +84,19 @@ def test_infinite_inputs_give_infinite_weight_gradients(size, act, dtype, grad):
         assert not d[:3].eq(0).any()
         same_kind(name, f64(got, grad), d.T @ x)
     assert torch.isfinite(f64(dx, dtype)).all()         # dx does not read x
+
+
+def test_terms_of_the_largest_gradients():
+    """A gradient before the activation between the largest bf16 number and the largest fp32 one is
+    finite: 129/128 times 254/128 2^127 is 1.99988 2^127, which rounds to infinity in bf16 (from
+    1.99609 2^127 on).  With x = 2^-10 its weight gradient is exact in fp32, like dh act(g)'s."""
+    dh, g, u, x = 129 / 128, 1.0, 254 / 128 * 2.0 ** 127, 2.0 ** -10
+    s = B.dense_shape(1, 1, 1, act="none", grad_dtype="f32")
+    dev = [torch.full((1, 1), v, dtype=torch.bfloat16, device=DEV) for v in (dh, x, 1.0, 1.0, g, u)]
+    for sign in (1, -1):
+        dw1, dw3 = out((1, 1), "f32"), out((1, 1), "f32")
+        B.gated_backward(dev[0] * sign, *dev[1:], None, dw1, dw3, s, ws_for(s, B.MOE_CALL_GATED_BACKWARD))
+        assert f64(dw1, "f32").item() == sign * dh * u * x and f64(dw3, "f32").item() == sign * dh * x
+    inf = torch.full((1, 1), float("inf"), dtype=torch.bfloat16, device=DEV)
+    B.gated_backward(inf, *dev[1:], None, dw1, dw3, s, ws_for(s, B.MOE_CALL_GATED_BACKWARD))
+    assert f64(dw1, "f32").item() == f64(dw3, "f32").item() == float("inf")
