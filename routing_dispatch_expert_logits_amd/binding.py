@@ -283,11 +283,12 @@ def norm_workspace_bytes(s: MoeNormShape) -> int:
     return int(lib.moe_norm_workspace_bytes(ctypes.byref(s)))
 
 
-def _refuse(call: str, name: str, t, shape: tuple, code: int, device: int):
+def _refuse(call: str, name: str, t, shape: tuple, code: Optional[int], device: int):
+    """code: the tensor's dtype code, None where any type will do."""
     import torch
     if tuple(t.shape) != tuple(shape):
         why = f"shape {tuple(t.shape)}, expected {tuple(shape)}"
-    elif t.dtype not in _tensor_types()[code]:
+    elif code is not None and t.dtype not in _tensor_types()[code]:
         why = f"type {t.dtype}"
     elif not t.is_cuda:
         why = "not on a GPU"
@@ -305,7 +306,7 @@ def _tensor_types() -> dict:
     global _types
     if _types is None:
         import torch
-        _types = {MOE_F32: (torch.float32,), MOE_BF16: (torch.bfloat16, torch.int16), None: (torch.uint8,)}
+        _types = {MOE_F32: (torch.float32,), MOE_BF16: (torch.bfloat16, torch.int16)}
     return _types
 
 

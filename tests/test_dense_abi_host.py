@@ -177,3 +177,12 @@ def test_binding_refuses_other_tensors():
         assert e.value.status == B.MOE_ERR_INVALID_ARG
     with pytest.raises(KeyError):
         B.dense_shape(4, 16, 8, act="swish2")
+
+
+def test_binding_refuses_workspaces_for_what_they_are():
+    """A workspace may be of any type: what is wrong with it is not its type."""
+    s = B.dense_shape(33, 96, 80)
+    for dtype in (torch.float32, torch.uint8):
+        with pytest.raises(B.MoeError, match=r"ws: not on a GPU") as e:
+            B.linear_forward(at(0), at(1), None, None, at(4), s, torch.zeros(64, dtype=dtype))
+        assert e.value.status == B.MOE_ERR_INVALID_ARG

@@ -100,3 +100,12 @@ def test_terms_of_the_largest_gradients():
     inf = torch.full((1, 1), float("inf"), dtype=torch.bfloat16, device=DEV)
     B.gated_backward(inf, *dev[1:], None, dw1, dw3, s, ws_for(s, B.MOE_CALL_GATED_BACKWARD))
     assert f64(dw1, "f32").item() == f64(dw3, "f32").item() == float("inf")
+
+
+def test_binding_refuses_strided_workspaces():
+    s = B.dense_shape(4, 16, 8, act="silu")
+    x, w, y = (torch.zeros(sh, dtype=torch.bfloat16, device=DEV) for sh in ((4, 16), (8, 16), (4, 8)))
+    for dtype in (torch.float32, torch.uint8):
+        with pytest.raises(B.MoeError, match="ws: not dense row-major"):
+            B.linear_backward(y, x, w, y, torch.empty_like(x), None, None, s,
+                              torch.zeros(1 << 20, dtype=dtype, device=DEV)[::2])
