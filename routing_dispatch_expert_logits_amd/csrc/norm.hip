@@ -160,7 +160,8 @@ hipError_t launch_norm_forward(const void* x, const void* w, const void* b, void
 // Backward in one pass over dy and x.  A workgroup takes a block of consecutive rows, RB at a
 // time; a thread owns NCH chunks of 8 columns, whose dw and db sums it keeps in registers over
 // all its rows (rows in order), while the two sums of a row that dx needs meet in LDS.  The
-// next rows' loads are in flight while these are worked on.
+// next rows' loads are in flight while these are worked on.  Behind a row's end dy and w are zeros,
+// and n is made 0: a mean times rstd that overflows would enter the row's sums as 0 times infinity.
 template <typename T, int NCH, int RB, int MAXT>
 __global__ __launch_bounds__(MAXT) void k_norm_backward(const T* __restrict__ dy, const T* __restrict__ x,
                                                         const T* __restrict__ w, const float* __restrict__ mean,
@@ -171,6 +172,8 @@ __global__ __launch_bounds__(MAXT) void k_norm_backward(const T* __restrict__ dy
   const int r0 = (int)blockIdx.x * per, r1 = min(rows, r0 + per);
   const int wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
   const float inv = 1.f / (float)H;
+  // whether the wave holds columns behind the row's end
+  const bool beyond = __builtin_amdgcn_readfirstlane(8 * ((int)threadIdx.x + 64 + (NCH - 1) * (int)blockDim.x) > H);
   float vw[NCH][8], sw[NCH][8] = {}, sb[NCH][8] = {};
   int col[NCH];
 #pragma unroll
@@ -208,6 +211,11 @@ __global__ __launch_bounds__(MAXT) void k_norm_backward(const T* __restrict__ dy
           n[q][i][k] = (nx[q][i].get(k) - nm[q]) * rs[q];
           d[q][i][k] = nd[q][i].get(k);
         }
+      if (beyond)
+#pragma unroll
+        for (int i = 0; i < NCH; ++i)
+#pragma unroll
+          for (int k = 0; k < 8; ++k) n[q][i][k] = col[i] + k < H ? n[q][i][k] : 0.f;
     }
     if (r + RB < r1) load(r + RB);
 #pragma unroll
@@ -290,7 +298,7 @@ __global__ __launch_bounds__(1024) void k_norm_dx_long(const T* __restrict__ dy,
       for (int i = 0; i < 8; ++i) {
         const float e = vd[i] * vw[i];
         s1 += e;
-        s2 += e * ((vx[i] - m) * r);
+        s2 += c + i < H ? e * ((vx[i] - m) * r) : 0.f;
       }
     }
     s1 = block_sum(s1, s[0]) / H;

@@ -109,3 +109,29 @@ def test_binding_refuses_strided_workspaces():
         with pytest.raises(B.MoeError, match="ws: not dense row-major"):
             B.linear_backward(y, x, w, y, torch.empty_like(x), None, None, s,
                               torch.zeros(1 << 20, dtype=dtype, device=DEV)[::2])
+
+
+@pytest.mark.parametrize("dtype", ("bf16", "f32"))
+@pytest.mark.parametrize("H", (100, 500, 1021, 8200, 20001))
+def test_norm_gradient_of_a_far_constant_row(H, dtype):
+    """A constant row has n = 0 and dx = rstd (e - mean(e)), however far it lies: mean times rstd
+    overflows here, and the columns that fill a row up to whole chunks and waves have no part in it."""
+    far = 2.0 ** 126 / 2 ** math.ceil(math.log2(H))     # the row's sum is below 2^127
+    eps = 2.0 ** -50                                    # rstd 2^25
+    gen = torch.Generator().manual_seed(H)
+    x, w, dy = rand(gen, 3, H, dtype=dtype), rand(gen, H, dtype=dtype), rand(gen, 3, H, dtype=dtype)
+    x[1] = far
+    s = B.norm_shape(3, H, eps=eps, dtype=dtype)
+    y, dx, dw, db = out((3, H), dtype), out((3, H), dtype), out((H,), dtype), out((H,), dtype)
+    mean, rstd = out((3,), "f32"), out((3,), "f32")
+    dev = [t.to(DEV) for t in (x, w, dy)]
+    B.layer_norm_forward(dev[0], dev[1], None, y, s, mean=mean, rstd=rstd)
+    assert mean[1].item() == far and rstd[1].item() == 2.0 ** 25 and f64(y, dtype)[1].eq(0).all()
+    B.layer_norm_backward(dev[2], dev[0], dev[1], mean, rstd, dx, dw, db, s, ws_for(s))
+    e = (dy.double() * w.double())[1]
+    ref = 2.0 ** 25 * (e - e.mean())
+    # e, its mean of H terms (at most 16 + H / 64 additions deep), their difference and its product
+    tol = U[dtype] * ref.abs() + 2.0 ** 25 * 2.0 ** -24 * (4 * e.abs() + (20 + H // 64) * e.abs().mean())
+    got = f64(dx, dtype)
+    assert bool(((got[1] - ref).abs() <= tol).all()) and torch.isfinite(got).all(), float((got[1] - ref).abs().max())
+    assert torch.isfinite(f64(dw, dtype)).all()
