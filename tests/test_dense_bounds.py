@@ -15,7 +15,9 @@ HOST = os.path.join(os.path.dirname(os.path.abspath(__file__)), "host")
 # whole tiles, ragged ones, single rows; column operands that end at a page's end after a cut
 SIZES = [(1, 64, 64), (17, 72, 56), (33, 333, 77), (130, 515, 260), (256, 256, 256), (300, 64, 1000), (1000, 1032, 72),
          (1021, 1416, 2120), (3800, 4072, 4000), (515, 1001, 1777), (4096, 2048, 8192), (4096, 4096, 4096),
-         (8192, 2048, 7168), (8192, 7208, 2048), (131072, 520, 32768), (100, 7168, 1000), (300000, 8, 16)]
+         (8192, 2048, 7168), (8192, 7208, 2048), (131072, 520, 32768), (100, 7168, 1000), (300000, 8, 16),
+         # the largest row count and widths
+         (1 << 28, 1, 8), (1 << 28, 8, 32), (40, 1 << 21, 24), (40, 24, 1 << 21), (4096, 1 << 21, 40), (1 << 12, 1 << 20, 1 << 13)]
 
 
 def spread_sizes(n):

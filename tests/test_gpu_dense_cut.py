@@ -6,6 +6,7 @@ import pytest
 import torch
 
 from routing_dispatch_expert_logits_amd import binding as B
+from tests import test_gpu_dense as test_dense
 from tests.dense_sizes import CUT_BACKWARD, CUT_FORWARD
 from tests.test_gpu_dense import ACTS, DEV, SLOPE, TYPES, U, U32, act64, close, framed, fsum, out, rand, small, ws_for
 
@@ -145,3 +146,32 @@ def test_gated_past_32_bit_offsets():
         s1 += dg.T @ x[t].float()
         s3 += du.T @ x[t].float()
     assert torch.equal(dw1, s1) and torch.equal(dw3, s3)
+
+
+# the largest row count, the largest widths, and decoding rows of them
+@pytest.mark.parametrize("size", [(1 << 28, 1, 8), (40, 1 << 21, 24), (40, 24, 1 << 21), (4, 1 << 21, 24), (4, 24, 1 << 21)],
+                         ids=small)
+def test_largest_sizes(size):
+    T, K, N = size
+    gen = torch.Generator(device=DEV).manual_seed(3)
+    x, w, dy = ones(gen, T, K), ones(gen, N, K), ones(gen, T, N)
+    s = B.dense_shape(T, K, N, act="none", grad_dtype="f32")
+    y, dx = torch.empty_like(dy), torch.empty_like(x)
+    dw, db = torch.empty(N, K, device=DEV), torch.empty(N, device=DEV)
+    ws = torch.empty(max(B.dense_workspace_bytes(s, c) for c in (B.MOE_CALL_LINEAR_FORWARD, B.MOE_CALL_LINEAR_BACKWARD)),
+                     dtype=torch.uint8, device=DEV)
+    B.linear_forward(x, w, None, None, y, s, ws)
+    B.linear_backward(dy, x, w, None, dx, dw, db, s, ws)
+    sw, sb = torch.zeros(N, K, device=DEV), torch.zeros(N, device=DEV)
+    for t in rows(T, 1 << 24):
+        assert torch.equal(y[t], (x[t].float() @ w.float().T).to(y.dtype)), t
+        assert torch.equal(dx[t], (dy[t].float() @ w.float()).to(dx.dtype)), t
+        sw += dy[t].float().T @ x[t].float()
+        sb += dy[t].float().sum(0)
+    assert torch.equal(dw, sw) and torch.equal(db, sb)
+
+
+@pytest.mark.parametrize("dtype", ("bf16", "f32"))
+def test_widest_norm(dtype):
+    test_dense.test_norm_forward((3, 1 << 21), dtype)
+    test_dense.test_norm_backward((3, 1 << 21), dtype, "f32")
