@@ -43,8 +43,8 @@ __device__ __forceinline__ void finite_rows(const FiniteRows& f, int rows) {
   }
 }
 
-// Bound by memory in bf16 (4096 x 8192 gated, 3 reads and 2 writes of 64 MB: 61 us, 5.5 TB/s), by
-// the exponentials of fp32 GELU otherwise (545 x 5664: 13 us, 37 MB).
+// Bound by memory in bf16 (4096 x 8192 gated, 3 reads and 2 writes of 64 MB: 60 to 64 us, 5.2 to
+// 5.6 TB/s), by the exponentials of fp32 GELU otherwise (545 x 5664: 13 us, 37 MB).
 // One pass over dh, g (and u): d0 = dh u act'(g), d1 = dh act(g) in fp32, rounded on store.
 // Workgroup (column block, row block); a thread owns 8 columns and every kGradSub-th row of
 // its block; the column sums of d0 go through LDS in row-lane order.  A second plane of workgroups

@@ -655,7 +655,9 @@ static size_t part_bytes(const MmPlan& p, int M) {
 // A backward pass's product may run on its own or together with the other one, on tiles of 64
 // rows and 64 columns (fp32: or 32), with slices of their own.  fp32, dx and dw, 64 columns
 // against 32: 128 x 1024 x 4096 31.8 and 37.6 us, 300 x 2000 x 1000 28.7 and 38.9; 32 are better
-// where few tiles of 64 would leave the CUs uneven (1000 x 1032 x 2056: 91 and 80).
+// where few tiles of 64 would leave the CUs uneven (1000 x 1032 x 2056: 91 and 80).  Whole rounds of
+// tiles are not in this estimate, and where they decide it can miss: 3000 x 1000 x 1000 takes 125 us,
+// and 116 where each product keeps the width and slices that it would choose on its own.
 constexpr int kTogether[] = {64, 32};
 size_t dense_part_bytes(bool bf16, int M, int N, int K, int segs, int batch, bool pair, bool a_col, bool backward) {
   size_t most = part_bytes(mm_plan(bf16, M, N, K, segs, batch, pair, a_col), M);

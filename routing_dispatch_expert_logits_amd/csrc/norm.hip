@@ -2,9 +2,10 @@
 // e = dy w, dx = rstd (e - mean(e) - n mean(e n)), dw = sum_t dy n, db = sum_t dy.  Both are
 // bound by memory: a row is read once, kept in registers while its sums are formed, and written
 // once.  Measured (MI355X, 8192 x 7168, bf16): forward 55 us, 4.27 TB/s; backward with all three
-// gradients 81 us, 4.33 TB/s; a copy of 2 GiB runs at 4.9 TB/s.  One row of 4096 takes 6.5 us, a
-// launch; 2049 x 1021 fp32 backward 13.5 us, two launches and their latencies (25 MB, 5 us at
-// that rate).
+// gradients 82 us, 77 of them the pass over the rows and 5 the launch that joins its column sums; a
+// copy of 2 GiB runs at 4.9 TB/s.  One row of 4096 takes 6.7 us, a launch; 2049 x 1021 fp32
+// backward 13.5 us, two launches and their latencies (25 MB, 5 us at that rate).  Rows too wide for
+// registers are read twice or more: 2048 x 16384 fp32 backward 193 us, 2.1 TB/s.
 #include "dense_device.h"
 #include "dense_kernels.h"
 
@@ -342,10 +343,12 @@ static bool one_pass(int H, bool bf16) {
   backward_shape(H, &nch, &threads);
   return nch == 1 || (bf16 && threads <= 512);  // fp32 rows of four chunks a thread would not fit the registers
 }
-// Consecutive rows of one workgroup: the column sums of a block cost 4 H bytes twice over, a
-// row of it 2 H bytes or more three times, so at least 8 rows where there are that many, and
-// no more blocks than the device holds at a time; up to 16 rows in
-// one block, which needs no second launch.
+// Consecutive rows of one workgroup: no more blocks than the device holds at a time.  The column
+// sums of a block cost 8 H bytes twice over, a row of it 2 H bytes or more three times, so at least 8
+// rows from 4096 rows on, where the blocks fill the device all the same; below, 4, for more of them
+// at a time (8 instead of 4: 300 x 7168 bf16 18.1 and 13.3 us, 1000 x 7168 20.9 and 18.2, 2049 x 1021
+// fp32 15.2 and 13.5; 3500 x 2048 17.9 and 18.4).  Up to 16 rows in one block, which needs no second
+// launch.
 static int rows_per_block(int T, int H) {
   int nch, threads;
   backward_shape(H, &nch, &threads);
