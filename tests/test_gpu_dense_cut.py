@@ -175,3 +175,35 @@ def test_largest_sizes(size):
 def test_widest_norm(dtype):
     test_dense.test_norm_forward((3, 1 << 21), dtype)
     test_dense.test_norm_backward((3, 1 << 21), dtype, "f32")
+
+
+@pytest.mark.parametrize("dtype,H", (("bf16", 8192), ("bf16", 20000), ("f32", 8200)))
+def test_norm_gradient_past_32_bit_offsets(dtype, H):
+    """dy is zero but in the first and the last row, which then give the column sums of a call on the
+    two alone, and have its dx; the rows between have none.  dw is a sum of two products of dy and
+    n = (x - mean) rstd: at most five roundings at 2^-24 each (x - mean, n, the product, which a fused
+    multiply-add in a block of both rows leaves out, and the sum), of the terms' magnitudes."""
+    T = (1 << 31) // H + 37
+    gen = torch.Generator().manual_seed(H)
+    few = [rand(gen, 2, H, dtype=dtype).to(DEV) for _ in range(2)]
+    w = rand(gen, H, dtype=dtype).to(DEV)
+    dy, x = (torch.zeros(T, H, dtype=TYPES[dtype], device=DEV) for _ in range(2))
+    for big, two in zip((dy, x), few):
+        big[0], big[-1] = two[0], two[1]
+    grads = []
+    for d, v in ((dy, x), few):
+        rows_ = d.shape[0]
+        s = B.norm_shape(rows_, H, dtype=dtype, grad_dtype="f32")
+        mean, rstd = torch.zeros(rows_, device=DEV), torch.ones(rows_, device=DEV)
+        mean[-1], rstd[0] = 0.25, 2.0
+        o = [torch.empty_like(d), torch.empty(H, device=DEV), torch.empty(H, device=DEV)]
+        ws = torch.empty(B.norm_workspace_bytes(s), dtype=torch.uint8, device=DEV)
+        B.layer_norm_backward(d, v, w, mean, rstd, *o, s, ws)
+        grads.append(o)
+    (dx, dw, db), (dx2, dw2, db2) = grads
+    assert torch.equal(dx[0], dx2[0]) and torch.equal(dx[-1], dx2[1])
+    assert not any(bool(dx[1:-1][t].any()) for t in rows(T - 2))
+    d, n = few[0].double(), (few[1].double() - mean.double()[:, None]) * rstd.double()[:, None]
+    for got in (dw, dw2):
+        assert bool(((got.double() - (d * n).sum(0)).abs() <= 5 * U32 * (d * n).abs().sum(0)).all())
+    assert torch.equal(db, db2)
