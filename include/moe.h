@@ -86,7 +86,7 @@
 extern "C" {
 #endif
 
-#define MOE_ABI_VERSION 6
+#define MOE_ABI_VERSION 7
 
 #ifndef MOE_API
 #define MOE_API __attribute__((visibility("default")))
@@ -310,6 +310,24 @@ MOE_API moe_status moe_quantize_mxfp8(const void* src, int src_dtype, int64_t ro
 MOE_API moe_status moe_combine(const void* y_perm, const int32_t* token_row, const float* topk_w,
                        const void* shared_out, void* out, int out_dtype, int flags,
                        const moe_shape* s, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Backward pass of the combine: with dout[t] the gradient of out[t],
+ *   dy_perm[token_row[t,j]] = topk_w[t,j] dout[t],
+ *   dtopk_w[t,j] = <dout[t], y_perm[token_row[t,j]]>  (0 for a dropped assignment).
+ * The shared expert's gradient is dout.  (The gradient of the rows that moe_dispatch_permute copied, with respect
+ * to the tokens', is moe_combine of their gradients with every weight 1.)
+ *
+ * dout [T x D] (out_dtype), y_perm [T*k x D] (dtype; may be NULL without dtopk_w), token_row [T x k],
+ * topk_w [T x k] (may be NULL without dy_perm).
+ * dy_perm [T*k x D] (dtype) out, dtopk_w [T x k] fp32 out, either may be NULL (not both).  Rows of
+ * dy_perm that no assignment has (an expert capacity's rows from offsets[E] on) are left as they
+ * are.  Products and sums in fp32, in a fixed order, one rounding.  Outputs may not overlap inputs or each other
+ * (MOE_ERR_INVALID_ARG).  token_row entries are distinct (not checked); one outside 0 .. T*k - 1 is a dropped assignment.
+ */
+MOE_API moe_status moe_combine_backward(const void* dout, const void* y_perm, const int32_t* token_row,
+                                        const float* topk_w, void* dy_perm, float* dtopk_w, int out_dtype,
+                                        const moe_shape* s, void* stream);
 
 /* Weights of one layer for moe_layer_forward (device pointers, layouts as above). */
 typedef struct moe_layer_weights {
@@ -552,6 +570,138 @@ MOE_API moe_status moe_linear_forward(const void* x, const void* w, const void* 
 MOE_API moe_status moe_linear_backward(const void* dy, const void* x, const void* w, const void* z,
                                        void* dx, void* dw, void* dbias, const moe_dense_shape* s,
                                        void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Products grouped by expert
+ * --------------------------
+ * The expert products of moe_grouped_ffn as operators of their own, with their gradients: rows sorted by
+ * expert (x_perm as moe_dispatch_permute writes it), each expert's rows times that expert's weight.  Expert e's
+ * rows are offsets[e] .. offsets[e+1] - 1 of the R rows; offsets [E+1] int32 stay on the device and
+ * need not start at 0 nor end at R: rows before offsets[0] and from offsets[E] on have no part in any result, and
+ * outputs leave them as they are.  Expert layers trained with moe_route_topk, moe_dispatch_permute,
+ *   moe_grouped_gated_forward, moe_grouped_linear_forward, moe_combine
+ * have their gradients by moe_combine_backward, the two backward calls below, and moe_combine with weights of 1.
+ *
+ * The conventions of the dense operators hold: every size from 1 up (bf16 operands whose width is no
+ * multiple of 8 are copied to padded rows in the workspace first, the weights among them), R = 0 is a call on no
+ * rows, outputs may not overlap anything, sums are fp32 in a fixed order with no atomics.
+ * Precondition not checked: offsets do not decrease.  Offsets outside 0 .. R are taken as the nearer of the two, so no
+ * offsets lead to an access out of bounds.
+ *
+ * Limits: E <= 1024, R <= 2^28, K and N <= 2^21, E*K and E*N <= 2^27, no tensor above 2^33 elements
+ * (MOE_ERR_UNSUPPORTED).
+ */
+typedef struct moe_grouped_shape {
+  int64_t R;           /* rows of all experts */
+  int64_t K;           /* input width */
+  int64_t N;           /* output width */
+  int64_t E;           /* experts */
+  int32_t dtype;       /* moe_dtype of rows, weights and outputs (integer products: of outputs) */
+  int32_t act;         /* moe_act of a gated product; MOE_ACT_NONE for a linear one */
+  int32_t grad_dtype;  /* moe_dtype of weight gradients: dtype, or MOE_F32 (as in moe_dense_shape) */
+  int32_t reserved;    /* 0 */
+} moe_grouped_shape;
+
+typedef enum moe_grouped_call {
+  MOE_CALL_GROUPED_LINEAR_FORWARD = 0,
+  MOE_CALL_GROUPED_LINEAR_BACKWARD = 1,
+  MOE_CALL_GROUPED_GATED_FORWARD = 2,
+  MOE_CALL_GROUPED_GATED_BACKWARD = 3,
+  MOE_CALL_GROUPED_LINEAR_INT8 = 4,
+  MOE_CALL_GROUPED_GATED_INT8 = 5
+} moe_grouped_call;
+
+/* Workspace bytes of a grouped call on shape s (0 if the shape is invalid). Host only. */
+MOE_API size_t moe_grouped_workspace_bytes(const moe_grouped_shape* s, int call);
+
+/*
+ * y_r = x_r w[e]^T for the rows r of every expert e, rounded once from the fp32 sums.
+ * x [R x K], w [E x N x K], y [R x N] out (dtype).  Weights of experts without rows have no part in it.
+ */
+MOE_API moe_status moe_grouped_linear_forward(const void* x, const int32_t* offsets, const void* w, void* y,
+                                              const moe_grouped_shape* s, void* ws, size_t ws_bytes,
+                                              void* stream);
+
+/*
+ * dx_r = dy_r w[e],  dw[e] = sum over the rows r of e of dy_r^T x_r (zeros for an expert without rows).
+ * dx [R x K] (dtype), dw [E x N x K] (grad_dtype) out, either may be NULL (not both); x may be NULL
+ * without dw, w without dx.
+ */
+MOE_API moe_status moe_grouped_linear_backward(const void* dy, const void* x, const int32_t* offsets,
+                                               const void* w, void* dx, void* dw, const moe_grouped_shape* s,
+                                               void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * g_r = x_r w1[e]^T, u_r = x_r w3[e]^T, h = act(g) u from the fp32 sums, rounded once.
+ * x [R x K], w1 and w3 [E x N x K], h [R x N] out (dtype); g, u [R x N] (dtype) out, both or neither: the
+ * rounded projections, which a backward pass reads.
+ */
+MOE_API moe_status moe_grouped_gated_forward(const void* x, const int32_t* offsets, const void* w1,
+                                             const void* w3, void* h, void* g, void* u,
+                                             const moe_grouped_shape* s, void* ws, size_t ws_bytes,
+                                             void* stream);
+
+/*
+ * With dg = dh u act'(g) and du = dh act(g) (fp32, rounded to dtype as operands of the products; see
+ * moe_dense_shape.grad_dtype):
+ *   dx_r = dg_r w1[e] + du_r w3[e],  dw1[e] = sum dg_r^T x_r,  dw3[e] = sum du_r^T x_r.
+ * dx [R x K] (dtype), dw1 and dw3 [E x N x K] (grad_dtype) out; dx may be NULL (w1 and w3 too then), dw1 and
+ * dw3 both (x too then).
+ */
+MOE_API moe_status moe_grouped_gated_backward(const void* dh, const void* x, const int32_t* offsets,
+                                              const void* w1, const void* w3, const void* g, const void* u,
+                                              void* dx, void* dw1, void* dw3, const moe_grouped_shape* s,
+                                              void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Products in 8-bit integers
+ * --------------------------
+ * Forward products with a scale for each token (row of x) and each output channel (row of w), dense or grouped by
+ * expert: half the weight bytes of bf16 and twice its matrix rate.  Value-changing, like MXFP8 dispatch.
+ *
+ * A row x gets scale = max |x| / 127 (fp32) and codes q = x / scale rounded to the nearest integer (the
+ * exact quotient, ties to even) and clamped to -127 .. 127; a row of zeros, or one whose scale is below fp32's
+ * smallest number, has scale 0 and codes 0; a row with an infinity or NaN has scale NaN and codes 0, which makes its
+ * products NaN.  Rows of codes are moe_int8_row_bytes(cols) long, cols rounded up to 16, zeros behind the
+ * first cols (a caller that makes codes itself, in -127 .. 127, leaves zeros there too: not checked).
+ *
+ * A product is row_scale col_scale sum(q_x q_w): the sum exactly (whole numbers in 32 bits), the
+ * scales in fp32, then the activation and residual as in the bf16 and fp32 products, one rounding to s->dtype.
+ *
+ * Limits: as the dense and grouped products, and K <= 2^17, which keeps the sums in 32 bits.
+ */
+
+/* Bytes of a row of cols codes; 0 if cols is not in 1 .. 2^21.  Host only. */
+MOE_API int64_t moe_int8_row_bytes(int64_t cols);
+
+/* Codes q [rows x moe_int8_row_bytes(cols)] and scales [rows] of src [rows x cols] (src_dtype, dense). */
+MOE_API moe_status moe_quantize_int8(const void* src, int src_dtype, int64_t rows, int64_t cols, int8_t* q,
+                                     float* scale, void* stream);
+
+/*
+ * y = act(x w^T + bias) + residual.  x: codes of T rows with x_scale [T], w: codes of N rows with
+ * w_scale [N], K columns each; bias [N] (nullable), residual [T x N] (nullable, may be y), y [T x N]
+ * out (dtype).  grad_dtype of s is not used.
+ */
+MOE_API moe_status moe_linear_int8_forward(const int8_t* x, const float* x_scale, const int8_t* w,
+                                           const float* w_scale, const void* bias, const void* residual,
+                                           void* y, const moe_dense_shape* s, void* stream);
+
+/* h = act(x w1^T) * (x w3^T), codes and scales as above; h [T x N] out (dtype). */
+MOE_API moe_status moe_gated_int8_forward(const int8_t* x, const float* x_scale, const int8_t* w1,
+                                          const float* w1_scale, const int8_t* w3, const float* w3_scale,
+                                          void* h, const moe_dense_shape* s, void* stream);
+
+/* The grouped products in codes: x of R rows with x_scale [R], w of E x N rows with w_scale [E x N]. */
+MOE_API moe_status moe_grouped_linear_int8_forward(const int8_t* x, const float* x_scale,
+                                                   const int32_t* offsets, const int8_t* w,
+                                                   const float* w_scale, void* y, const moe_grouped_shape* s,
+                                                   void* ws, size_t ws_bytes, void* stream);
+MOE_API moe_status moe_grouped_gated_int8_forward(const int8_t* x, const float* x_scale,
+                                                  const int32_t* offsets, const int8_t* w1,
+                                                  const float* w1_scale, const int8_t* w3,
+                                                  const float* w3_scale, void* h, const moe_grouped_shape* s,
+                                                  void* ws, size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -21,11 +21,13 @@ MOE_COMBINE_FUSED, MOE_COMBINE_UNFUSED = 0, 1
 MOE_DISPATCH_DTYPE, MOE_DISPATCH_MXFP8 = 0, 1
 MOE_NUM_STAGE_EVENTS = 10
 NOALLOC_SCRATCH_BYTES = 64 << 20
-ABI_VERSION = 6
+ABI_VERSION = 7
 MOE_PLAN_GATE, MOE_PLAN_X_PERM = 1, 2
 MOE_ACT_NONE, MOE_ACT_RELU, MOE_ACT_SILU, MOE_ACT_GELU, MOE_ACT_GELU_TANH = range(5)
 (MOE_CALL_GATED_FORWARD, MOE_CALL_GATED_BACKWARD, MOE_CALL_LINEAR_FORWARD,
  MOE_CALL_LINEAR_BACKWARD) = range(4)
+(MOE_CALL_GROUPED_LINEAR_FORWARD, MOE_CALL_GROUPED_LINEAR_BACKWARD, MOE_CALL_GROUPED_GATED_FORWARD,
+ MOE_CALL_GROUPED_GATED_BACKWARD, MOE_CALL_GROUPED_LINEAR_INT8, MOE_CALL_GROUPED_GATED_INT8) = range(6)
 ACT_NAMES = {"none": MOE_ACT_NONE, "relu": MOE_ACT_RELU, "silu": MOE_ACT_SILU, "gelu": MOE_ACT_GELU,
              "gelu_tanh": MOE_ACT_GELU_TANH}
 
@@ -68,6 +70,11 @@ class MoeDenseShape(ctypes.Structure):
 
 class MoeNormShape(ctypes.Structure):
     _fields_ = [("T", _i64), ("H", _i64), ("eps", ctypes.c_float), ("dtype", _i32),
+                ("grad_dtype", _i32), ("reserved", _i32)]
+
+
+class MoeGroupedShape(ctypes.Structure):
+    _fields_ = [("R", _i64), ("K", _i64), ("N", _i64), ("E", _i64), ("dtype", _i32), ("act", _i32),
                 ("grad_dtype", _i32), ("reserved", _i32)]
 
 
@@ -118,10 +125,24 @@ def _load() -> ctypes.CDLL:
     lib.moe_gated_backward.argtypes = [_vp] * 9 + [P(MoeDenseShape), _vp, sz, _vp]
     lib.moe_linear_forward.argtypes = [_vp] * 6 + [P(MoeDenseShape), _vp, sz, _vp]
     lib.moe_linear_backward.argtypes = [_vp] * 7 + [P(MoeDenseShape), _vp, sz, _vp]
+    lib.moe_combine_backward.argtypes = [_vp] * 6 + [ctypes.c_int, P(MoeShape), _vp]
+    lib.moe_grouped_workspace_bytes.restype = sz
+    lib.moe_grouped_workspace_bytes.argtypes = [P(MoeGroupedShape), ctypes.c_int]
+    lib.moe_int8_row_bytes.restype = _i64
+    lib.moe_int8_row_bytes.argtypes = [_i64]
+    lib.moe_quantize_int8.argtypes = [_vp, ctypes.c_int, _i64, _i64, _vp, _vp, _vp]
+    lib.moe_linear_int8_forward.argtypes = [_vp] * 7 + [P(MoeDenseShape), _vp]
+    lib.moe_gated_int8_forward.argtypes = [_vp] * 7 + [P(MoeDenseShape), _vp]
+    for f, n in (("moe_grouped_linear_forward", 4), ("moe_grouped_linear_backward", 6), ("moe_grouped_gated_forward", 7),
+                 ("moe_grouped_gated_backward", 10), ("moe_grouped_linear_int8_forward", 6),
+                 ("moe_grouped_gated_int8_forward", 8)):
+        getattr(lib, f).argtypes = [_vp] * n + [P(MoeGroupedShape), _vp, sz, _vp]
+        getattr(lib, f).restype = ctypes.c_int
     for f in ("moe_route_topk", "moe_dispatch_permute", "moe_grouped_ffn", "moe_combine",
               "moe_layer_forward", "moe_quantize_mxfp8", "moe_layer_forward_noalloc",
               "moe_layer_norm_forward", "moe_layer_norm_backward", "moe_gated_forward",
-              "moe_gated_backward", "moe_linear_forward", "moe_linear_backward"):
+              "moe_gated_backward", "moe_linear_forward", "moe_linear_backward", "moe_combine_backward",
+              "moe_quantize_int8", "moe_linear_int8_forward", "moe_gated_int8_forward"):
         getattr(lib, f).restype = ctypes.c_int
     v = lib.moe_abi_version()
     if v != ABI_VERSION:
@@ -300,19 +321,21 @@ def _refuse(call: str, name: str, t, shape: tuple, code: Optional[int], device: 
 
 
 _types = None
+_INT8, _INT32 = "int8", "int32"   # tensors of codes, and of offsets and rows
 
 
 def _tensor_types() -> dict:
     global _types
     if _types is None:
         import torch
-        _types = {MOE_F32: (torch.float32,), MOE_BF16: (torch.bfloat16, torch.int16)}
+        _types = {MOE_F32: (torch.float32,), MOE_BF16: (torch.bfloat16, torch.int16), _INT8: (torch.int8,),
+                  _INT32: (torch.int32,)}
     return _types
 
 
-def _dense_call(call: str, fn, s, tensors: tuple, stream, ws=()):
+def _dense_call(call: str, fn, s, tensors: tuple, stream, ws=(), before: tuple = ()):
     """Check `tensors`, (name, tensor, shape, dtype code) in the call's order, and make the call; ws: () for a
-    call that takes no workspace, else (tensor,)."""
+    call that takes no workspace, else (tensor,); before: plain arguments between the tensors and the shape (s None: none)."""
     import torch
     types, device, args = _tensor_types(), -1, []
     for name, t, shape, code in tensors:
@@ -324,7 +347,9 @@ def _dense_call(call: str, fn, s, tensors: tuple, stream, ws=()):
             _refuse(call, name, t, shape, code, device)
         device = d
         args.append(t.data_ptr())
-    args.append(ctypes.byref(s))
+    args += before
+    if s is not None:
+        args.append(ctypes.byref(s))
     if ws:
         t = ws[0]
         if t is None:
@@ -393,3 +418,120 @@ def linear_backward(dy, x, w, z, dx, dw, dbias, s: MoeDenseShape, ws, stream=Non
     _dense_call("moe_linear_backward", lib.moe_linear_backward, s, (
         ("dy", dy, (T, N), dt), ("x", x, (T, K), dt), ("w", w, (N, K), dt), ("z", z, (T, N), dt),
         ("dx", dx, (T, K), dt), ("dw", dw, (N, K), gt), ("dbias", dbias, (N,), gt)), stream, (ws,))
+
+
+# ---- products grouped by expert, their gradients and the combine's
+
+
+def grouped_shape(R: int, K: int, N: int, E: int, dtype: str = "bf16", act: str = "none",
+                  grad_dtype: Optional[str] = None) -> MoeGroupedShape:
+    """R rows of E experts, K input columns, N output columns; grad_dtype: of weight gradients (default dtype)."""
+    return MoeGroupedShape(R, K, N, E, _dtype_code(dtype), ACT_NAMES[act], _dtype_code(grad_dtype or dtype), 0)
+
+
+def grouped_workspace_bytes(s: MoeGroupedShape, call: int) -> int:
+    return int(lib.moe_grouped_workspace_bytes(ctypes.byref(s), call))
+
+
+def grouped_linear_forward(x, offsets, w, y, s: MoeGroupedShape, ws, stream=None):
+    """y_r = x_r w[e]^T for the rows offsets[e] .. offsets[e + 1] - 1 of every expert e."""
+    R, K, N, E, dt = s.R, s.K, s.N, s.E, s.dtype
+    _dense_call("moe_grouped_linear_forward", lib.moe_grouped_linear_forward, s, (
+        ("x", x, (R, K), dt), ("offsets", offsets, (E + 1,), _INT32), ("w", w, (E, N, K), dt), ("y", y, (R, N), dt)),
+        stream, (ws,))
+
+
+def grouped_linear_backward(dy, x, offsets, w, dx, dw, s: MoeGroupedShape, ws, stream=None):
+    """Gradients dx (dtype) and dw (grad_dtype) of grouped_linear_forward; either may be None."""
+    R, K, N, E, dt, gt = s.R, s.K, s.N, s.E, s.dtype, s.grad_dtype
+    _dense_call("moe_grouped_linear_backward", lib.moe_grouped_linear_backward, s, (
+        ("dy", dy, (R, N), dt), ("x", x, (R, K), dt), ("offsets", offsets, (E + 1,), _INT32), ("w", w, (E, N, K), dt),
+        ("dx", dx, (R, K), dt), ("dw", dw, (E, N, K), gt)), stream, (ws,))
+
+
+def grouped_gated_forward(x, offsets, w1, w3, h, s: MoeGroupedShape, ws, g=None, u=None, stream=None):
+    """h_r = act(x_r w1[e]^T) * (x_r w3[e]^T); g and u (both or neither) receive the two projections."""
+    R, K, N, E, dt = s.R, s.K, s.N, s.E, s.dtype
+    _dense_call("moe_grouped_gated_forward", lib.moe_grouped_gated_forward, s, (
+        ("x", x, (R, K), dt), ("offsets", offsets, (E + 1,), _INT32), ("w1", w1, (E, N, K), dt),
+        ("w3", w3, (E, N, K), dt), ("h", h, (R, N), dt), ("g", g, (R, N), dt), ("u", u, (R, N), dt)), stream, (ws,))
+
+
+def grouped_gated_backward(dh, x, offsets, w1, w3, g, u, dx, dw1, dw3, s: MoeGroupedShape, ws, stream=None):
+    """Gradients dx (dtype), dw1 and dw3 (grad_dtype) of grouped_gated_forward from the g and u it kept; dx, or
+    dw1 and dw3, may be None."""
+    R, K, N, E, dt, gt = s.R, s.K, s.N, s.E, s.dtype, s.grad_dtype
+    _dense_call("moe_grouped_gated_backward", lib.moe_grouped_gated_backward, s, (
+        ("dh", dh, (R, N), dt), ("x", x, (R, K), dt), ("offsets", offsets, (E + 1,), _INT32), ("w1", w1, (E, N, K), dt),
+        ("w3", w3, (E, N, K), dt), ("g", g, (R, N), dt), ("u", u, (R, N), dt), ("dx", dx, (R, K), dt),
+        ("dw1", dw1, (E, N, K), gt), ("dw3", dw3, (E, N, K), gt)), stream, (ws,))
+
+
+def combine_backward(dout, y_perm, token_row, topk_w, dy_perm, dtopk_w, out_dtype: int, s: MoeShape, stream=None):
+    """Gradients of combine: dy_perm (dtype) of the expert rows and dtopk_w (fp32) of the routing weights, either
+    None; dout of type out_dtype."""
+    T, D, k, dt = s.T, s.L or s.H, s.k, s.dtype
+    _dense_call("moe_combine_backward", lib.moe_combine_backward, s, (
+        ("dout", dout, (T, D), int(out_dtype)), ("y_perm", y_perm, (T * k, D), dt), ("token_row", token_row, (T, k), _INT32),
+        ("topk_w", topk_w, (T, k), MOE_F32), ("dy_perm", dy_perm, (T * k, D), dt), ("dtopk_w", dtopk_w, (T, k), MOE_F32)),
+        stream, before=(int(out_dtype),))
+
+
+# ---- products in 8-bit integers with a scale for each token and channel
+
+
+def int8_row_bytes(cols: int) -> int:
+    """Length of a row of `cols` codes."""
+    return int(lib.moe_int8_row_bytes(cols))
+
+
+def quantize_int8(src, q, scale, stream=None):
+    """Codes q [.., int8_row_bytes(cols)] and scales [..] of the rows of src [.., cols] (bf16 or fp32)."""
+    import torch
+    code = MOE_F32 if src.dtype == torch.float32 else MOE_BF16
+    cols = src.shape[-1] if src.dim() else 0
+    rows = src.numel() // cols if cols else 0
+    lead = tuple(src.shape[:-1])
+    _dense_call("moe_quantize_int8", _quantize(code, rows, cols), None, (
+        ("src", src, tuple(src.shape), code), ("q", q, lead + (int8_row_bytes(cols),), _INT8),
+        ("scale", scale, lead, MOE_F32)), stream)
+
+
+def _quantize(code: int, rows: int, cols: int):
+    return lambda src, q, scale, stream: lib.moe_quantize_int8(src, code, rows, cols, q, scale, stream)
+
+
+def linear_int8_forward(x, x_scale, w, w_scale, bias, residual, y, s: MoeDenseShape, stream=None):
+    """y = act(x w^T + bias) + residual from codes x [T, int8_row_bytes(K)] and w [N, int8_row_bytes(K)] with their
+    scales (residual may be y itself)."""
+    T, N, dt, ld = s.T, s.N, s.dtype, int8_row_bytes(s.K)
+    _dense_call("moe_linear_int8_forward", lib.moe_linear_int8_forward, s, (
+        ("x", x, (T, ld), _INT8), ("x_scale", x_scale, (T,), MOE_F32), ("w", w, (N, ld), _INT8),
+        ("w_scale", w_scale, (N,), MOE_F32), ("bias", bias, (N,), dt), ("residual", residual, (T, N), dt),
+        ("y", y, (T, N), dt)), stream)
+
+
+def gated_int8_forward(x, x_scale, w1, w1_scale, w3, w3_scale, h, s: MoeDenseShape, stream=None):
+    """h = act(x w1^T) * (x w3^T) from codes and scales."""
+    T, N, dt, ld = s.T, s.N, s.dtype, int8_row_bytes(s.K)
+    _dense_call("moe_gated_int8_forward", lib.moe_gated_int8_forward, s, (
+        ("x", x, (T, ld), _INT8), ("x_scale", x_scale, (T,), MOE_F32), ("w1", w1, (N, ld), _INT8),
+        ("w1_scale", w1_scale, (N,), MOE_F32), ("w3", w3, (N, ld), _INT8), ("w3_scale", w3_scale, (N,), MOE_F32),
+        ("h", h, (T, N), dt)), stream)
+
+
+def grouped_linear_int8_forward(x, x_scale, offsets, w, w_scale, y, s: MoeGroupedShape, ws, stream=None):
+    """grouped_linear_forward from codes w [E, N, int8_row_bytes(K)] with w_scale [E, N]."""
+    R, N, E, dt, ld = s.R, s.N, s.E, s.dtype, int8_row_bytes(s.K)
+    _dense_call("moe_grouped_linear_int8_forward", lib.moe_grouped_linear_int8_forward, s, (
+        ("x", x, (R, ld), _INT8), ("x_scale", x_scale, (R,), MOE_F32), ("offsets", offsets, (E + 1,), _INT32),
+        ("w", w, (E, N, ld), _INT8), ("w_scale", w_scale, (E, N), MOE_F32), ("y", y, (R, N), dt)), stream, (ws,))
+
+
+def grouped_gated_int8_forward(x, x_scale, offsets, w1, w1_scale, w3, w3_scale, h, s: MoeGroupedShape, ws, stream=None):
+    """grouped_gated_forward from codes and scales."""
+    R, N, E, dt, ld = s.R, s.N, s.E, s.dtype, int8_row_bytes(s.K)
+    _dense_call("moe_grouped_gated_int8_forward", lib.moe_grouped_gated_int8_forward, s, (
+        ("x", x, (R, ld), _INT8), ("x_scale", x_scale, (R,), MOE_F32), ("offsets", offsets, (E + 1,), _INT32),
+        ("w1", w1, (E, N, ld), _INT8), ("w1_scale", w1_scale, (E, N), MOE_F32), ("w3", w3, (E, N, ld), _INT8),
+        ("w3_scale", w3_scale, (E, N), MOE_F32), ("h", h, (R, N), dt)), stream, (ws,))

@@ -2,29 +2,18 @@
 // launch sequence of each call.  No call allocates, synchronises or reads device memory.
 #include <cmath>
 
+#include "dense_host.h"
 #include "dense_kernels.h"
-#include "moe.h"
-#include "moe_host.h"
 
 using namespace moe;
 
 namespace {
-
-// tiles of 64 rows and 16 columns: at most 2^23 of them by the elements and 2^22 more by the
-// rows, so that every grid stays below 2^32 threads
-constexpr int64_t kMaxRows = 1ll << 28, kMaxWidth = 1ll << 21, kMaxElems = 1ll << 33;
 
 struct DenseDims {
   int T, K, N, act;
   bool bf16, grad_f32;
   size_t es, ges;   // element bytes of the layer, of the weight gradients
 };
-
-moe_status check_types(int dtype, int grad_dtype) {
-  if (dtype != MOE_F32 && dtype != MOE_BF16) return MOE_ERR_INVALID_ARG;
-  if (grad_dtype != dtype && grad_dtype != MOE_F32) return MOE_ERR_INVALID_ARG;
-  return MOE_OK;
-}
 
 moe_status check_dense(const moe_dense_shape* s, DenseDims& d) {
   if (!s || s->T < 0 || s->K < 1 || s->N < 1 || s->reserved != 0) return MOE_ERR_INVALID_ARG;
@@ -60,37 +49,6 @@ moe_status check_norm(const moe_norm_shape* s, NormDims& d) {
   return MOE_OK;
 }
 
-// The buffers of one call: every one given is 16-byte aligned, and no output overlaps
-// another buffer.
-struct Buffers {
-  struct One { uintptr_t lo, hi; bool out; } v[12];
-  int n = 0;
-  bool ok = true;
-  void add(const void* p, size_t bytes, bool out, bool required) {
-    if (!p) { ok = ok && !required; return; }
-    ok = ok && al16(p);
-    const uintptr_t a = reinterpret_cast<uintptr_t>(p);
-    v[n++] = One{a, a + bytes, out};
-  }
-  void in(const void* p, size_t bytes, bool required = true) { add(p, bytes, false, required); }
-  void out(const void* p, size_t bytes, bool required = true) { add(p, bytes, true, required); }
-  moe_status status() const {
-    if (!ok) return MOE_ERR_INVALID_ARG;
-    for (int a = 0; a < n; ++a)
-      for (int b = a + 1; b < n; ++b)
-        if ((v[a].out || v[b].out) && v[a].lo < v[b].hi && v[b].lo < v[a].hi) return MOE_ERR_INVALID_ARG;
-    return MOE_OK;
-  }
-};
-
-moe_status check_ws(Buffers& b, const void* ws, size_t ws_bytes, size_t need) {
-  if (b.status() != MOE_OK) return MOE_ERR_INVALID_ARG;
-  if (need == 0) return MOE_OK;
-  if (!ws || ws_bytes < need) return MOE_ERR_WORKSPACE;
-  b.out(ws, need);
-  return b.status();
-}
-
 // ---- workspaces
 
 // The bf16 products read rows of whole 16-byte chunks; operands with other widths are copied to
@@ -108,13 +66,6 @@ struct DenseWs {
   int terms;
   int64_t lo, ldk, ldn;
 };
-// bf16 terms that hold the fp32 gradient before the activation exactly: with a slope of 0 or 1
-// it is dy itself, or in a gated product one of two bf16 numbers (16 significant bits).
-int grad_terms(int act, bool gated) {
-  const bool slope01 = act == MOE_ACT_NONE || act == MOE_ACT_RELU;
-  return slope01 ? (gated ? 2 : 1) : 3;
-}
-
 DenseWs dense_ws(const DenseDims& d, bool gated, bool backward) {
   Carve c; DenseWs w{};
   w.ldk = padded(d, d.K);
@@ -171,11 +122,6 @@ FiniteRows finite_x(const DenseDims& d, const DenseWs& w, int terms, const void*
 size_t norm_ws(const NormDims& d) {
   return d.T == 0 ? 0 : align_up((size_t)norm_row_blocks(d.T, d.H) * 2 * d.H * 4);
 }
-
-#define MOE_TRY(call)                                         \
-  do {                                                        \
-    if (const moe_status r = (call); r != MOE_OK) return r;   \
-  } while (0)
 
 // z = x w0^T (and x w1^T) with epilogue e.
 moe_status forward(const DenseDims& d, const DenseWs& w, const void* x, const void* w0, const void* w1,

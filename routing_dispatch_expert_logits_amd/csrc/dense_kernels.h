@@ -37,6 +37,8 @@ struct DenseEpi {
   void* out[2];
   void* save[2];         // z, or g and u; nullable
   int64_t ldo;           // row length of outputs, residual and saved values
+  const float* row_scale;     // integer products: a factor for each row and for each column
+  const float* col_scale[2];
 };
 
 // Column sums by row blocks, not joined yet: out0[n] = sum_p part[p * stride + n] and out1[n] =

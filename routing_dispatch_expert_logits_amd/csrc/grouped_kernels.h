@@ -1,0 +1,42 @@
+// Internal launchers of the products grouped by expert, the 8-bit integer products and the combine's
+// gradients (not part of the C ABI).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "dense_kernels.h"
+
+namespace moe {
+
+// Rows sorted by expert: those of expert e are [offsets[e], offsets[e + 1]) of R, read on the device and
+// clamped to what there is, so that no offsets reach past the rows.
+struct Groups {
+  const int32_t* offsets;
+  int E, R;
+};
+
+// Element types of a grouped product's operands.
+enum GroupedType { GROUPED_F32 = 0, GROUPED_BF16 = 1, GROUPED_INT8 = 2 };
+
+// Rows by their expert's weight: job j of one expert (M unused), whose weights are w_stride elements apart and whose
+// row operands and outputs are those of its rows; j.b_col: the gradient's product, across the weights' rows.
+// table: grouped_table_bytes of scratch.  out_bf16: what an integer product's epilogue writes.
+size_t grouped_table_bytes(GroupedType t, int R, int E, int N, int K, int segs, bool pair, bool b_col);
+hipError_t launch_grouped(const DenseJob& j, const DenseEpi& e, GroupedType t, bool out_bf16, const Groups& g,
+                          int64_t w_stride, void* table, hipStream_t st);
+// Weight gradients: for every expert out[z][e] = sum of its rows' A_z x B_z, M x N (j.K unused), zeros without rows.
+hipError_t launch_grouped_dw(const DenseJob& j, const DenseEpi& e, GroupedType t, const Groups& g, hipStream_t st);
+
+// Integer products of dense rows; row operands of whole 16-byte chunks, zero from the contraction length on.
+hipError_t launch_int8(const DenseJob& j, const DenseEpi& e, bool out_bf16, hipStream_t st);
+// Codes and scales of rows; ld: row length of q.
+hipError_t launch_quantize_int8(const void* src, bool bf16, int64_t rows, int cols, int64_t ld, int8_t* q, float* scale,
+                                hipStream_t st);
+
+// dy_perm[token_row[t, j]] = topk_w[t, j] dout[t] and dtopk_w[t, j] = <dout[t], y_perm[token_row[t, j]]>, either NULL.
+hipError_t launch_combine_grad(const void* dout, bool dout_f32, const void* y_perm, const int32_t* token_row,
+                               const float* topk_w, int D, bool bf16, int T, int k, void* dy_perm, float* dtopk_w,
+                               hipStream_t st);
+
+}  // namespace moe

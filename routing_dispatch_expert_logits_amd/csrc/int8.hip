@@ -1,0 +1,112 @@
+// Products in 8-bit integers with a scale for each row and each output column, and the rows' codes.
+//
+//   scale = max |x| / 127 (fp32),  q = x / scale rounded to the nearest integer, ties to even,
+//   y = row_scale col_scale sum q_x q_w
+//
+// The sums are whole numbers in 32 bits, so exact in any order, while the contraction is no longer than
+// 2^17 (127^2 2^17 < 2^31).
+#include "dense_tile.h"
+#include "grouped_kernels.h"
+
+namespace moe {
+
+template <typename O, int BM, int BN, int WM, int WN, int S, int SB, bool PAIR, int KIND>
+__global__ __launch_bounds__(WM* WN * 64, 2) void k_int8_mm(DenseJob j, DenseEpi e) {
+  constexpr int STAGE = kMmStage<BM, BN, SB>;
+  __shared__ __attribute__((aligned(1024))) uint16_t s0[STAGE], s1[STAGE], s2[STAGE], s3[S > 3 ? STAGE : 1];
+  const MmWhere w = mm_where(blockIdx.x, ceil_div(j.M, BM), ceil_div(j.N, PAIR ? BN / 2 : BN), 1, 1);
+  mm_body<int8_t, O, BM, BN, WM, WN, S, SB, 16, false, false, PAIR, KIND>(
+      j, e, MmSlices{nullptr, 1, 1, 0}, w, MmPart{j.M, j.K, 0, 0, 0, 0, 0}, s0, s1, s2, s3);
+}
+
+template <typename O, int BM, int BN, int WM, int WN, int S, int SB = 128>
+static void go(const DenseJob& j, const DenseEpi& e, hipStream_t st) {
+  const int64_t items = (int64_t)ceil_div(j.M, BM) * ceil_div(j.N, j.pair ? BN / 2 : BN);
+  const dim3 grid((unsigned)((items + 7) / 8 * 8)), block(WM * WN * 64);
+  if (j.pair) k_int8_mm<O, BM, BN, WM, WN, S, SB, true, DENSE_GATED><<<grid, block, 0, st>>>(j, e);
+  else k_int8_mm<O, BM, BN, WM, WN, S, SB, false, DENSE_LINEAR><<<grid, block, 0, st>>>(j, e);
+}
+
+hipError_t launch_int8(const DenseJob& j, const DenseEpi& e, bool out_bf16, hipStream_t st) {
+  if (out_bf16) go<uint16_t, 64, 64, 2, 2, 4>(j, e, st);
+  else go<float, 64, 64, 2, 2, 4>(j, e, st);
+  return hipGetLastError();
+}
+
+// ---- codes of rows
+
+// The largest magnitude's bits: for finite numbers their order is the magnitudes', infinities and NaN are above.
+__device__ __forceinline__ uint32_t magnitude(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+
+// A row's scale and what turns its elements into codes: x / s as x up inv, with up a power of two that keeps
+// the smallest scales' reciprocals finite (s up is exact, as x up is: |x| <= 127.5 s or it is clamped).
+struct Int8Scale {
+  float scale, up, s, inv;
+  __device__ __forceinline__ explicit Int8Scale(uint32_t most) {
+    const bool finite = most < 0x7f800000u;
+    scale = finite ? __uint_as_float(most) / 127.f : __builtin_nanf("");
+    up = scale < 0x1p-100f ? 0x1p100f : 1.f;
+    s = scale * up;
+    inv = scale > 0.f ? 1.f / s : 0.f;   // 0 for rows of zeros and for rows that are not finite: codes 0
+  }
+  // rint(x / scale) from the exact quotient: n is off only where x inv is within its rounding (2^-16)
+  // of a tie, and the remainder x - n s, which an fma has exactly, says on which side of it x / s is.
+  __device__ __forceinline__ int code(float x) const {
+    if (inv == 0.f) return 0;
+    x *= up;
+    float n = rintf(x * inv);
+    const float r = fmaf(-n, s, x), half = 0.5f * s;
+    if (fabsf(r) >= half) {
+      const bool odd = (int)n & 1;
+      if (fabsf(r) > half || odd) n += r > 0.f ? 1.f : -1.f;
+    }
+    return (int)fminf(fmaxf(n, -127.f), 127.f);
+  }
+};
+
+__device__ __forceinline__ uint2 codes8(const Int8Scale& s, const float* f) {
+  uint32_t c[2] = {0, 0};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) c[i >> 2] |= (uint32_t)(s.code(f[i]) & 0xff) << (8 * (i & 3));
+  return make_uint2(c[0], c[1]);
+}
+
+// One row per workgroup, eight elements of it per thread at a time; read once for the largest magnitude and once more
+// for the codes.
+template <typename ST>
+__global__ __launch_bounds__(256) void k_quantize_int8(const ST* __restrict__ src, int64_t rows, int cols, int64_t ld,
+                                                       int8_t* __restrict__ q, float* __restrict__ scale) {
+  __shared__ uint32_t part[4];
+  const int n8 = (int)(ld / 8);
+  for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
+    const ST* x = src + r * cols;
+    uint32_t most = 0;
+    for (int i = threadIdx.x; i < n8; i += 256) {
+      float f[8];
+      load8(x + 8 * i, cols - 8 * i, f);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) most = max(most, magnitude(f[k]));
+    }
+    most = wave_max_u32(most);
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = most;
+    __syncthreads();
+    const Int8Scale s(max(max(part[0], part[1]), max(part[2], part[3])));
+    __syncthreads();
+    if (threadIdx.x == 0) scale[r] = s.scale;
+    for (int i = threadIdx.x; i < n8; i += 256) {
+      float f[8];
+      load8(x + 8 * i, cols - 8 * i, f);
+      reinterpret_cast<uint2*>(q + r * ld)[i] = codes8(s, f);
+    }
+  }
+}
+
+hipError_t launch_quantize_int8(const void* src, bool bf16, int64_t rows, int cols, int64_t ld, int8_t* q, float* scale,
+                                hipStream_t st) {
+  const unsigned grid = (unsigned)(rows < (1 << 20) ? rows : 1 << 20);
+  if (bf16) k_quantize_int8<uint16_t><<<grid, 256, 0, st>>>(static_cast<const uint16_t*>(src), rows, cols, ld, q, scale);
+  else k_quantize_int8<float><<<grid, 256, 0, st>>>(static_cast<const float*>(src), rows, cols, ld, q, scale);
+  return hipGetLastError();
+}
+
+}  // namespace moe

@@ -6,8 +6,8 @@
 #include <cstddef>
 #include <cstdint>
 
-#include "moe.h"
-#include "moe_host.h"
+#include "dense_host.h"
+#include "grouped_kernels.h"
 #include "moe_kernels.h"
 
 using namespace moe;
@@ -437,6 +437,27 @@ moe_status moe_combine(const void* y_perm, const int32_t* token_row, const float
   MOE_HIP(launch_unpermute(y_perm, row16, token_row, d.R, nullptr, ytok, st));
   MOE_HIP(launch_weighted_reduce(ytok, row16, d.bf16, token_row, topk_w, shared_out, d.T, d.k, out,
                                  of32, st));
+  return MOE_OK;
+}
+
+moe_status moe_combine_backward(const void* dout, const void* y_perm, const int32_t* token_row, const float* topk_w,
+                                void* dy_perm, float* dtopk_w, int out_dtype, const moe_shape* s, void* stream) {
+  Dims d;
+  MOE_TRY(check_shape(s, d));
+  if (out_dtype != MOE_F32 && out_dtype != MOE_BF16) return MOE_ERR_INVALID_ARG;
+  if (!dy_perm && !dtopk_w) return MOE_ERR_INVALID_ARG;
+  const bool df32 = out_dtype == MOE_F32;
+  const size_t rows = (size_t)d.R * d.D * d.es;
+  Buffers b;
+  b.in(dout, (size_t)d.T * d.D * (df32 ? 4 : 2));
+  b.in(y_perm, rows, dtopk_w != nullptr);
+  b.in(token_row, (size_t)d.R * 4);
+  b.in(topk_w, (size_t)d.R * 4, dy_perm != nullptr);
+  b.out(dy_perm, rows, false);
+  b.out(dtopk_w, (size_t)d.R * 4, false);
+  MOE_TRY(b.status());
+  MOE_HIP(launch_combine_grad(dout, df32, y_perm, token_row, topk_w, d.D, d.bf16, d.T, d.k, dy_perm, dtopk_w,
+                              static_cast<hipStream_t>(stream)));
   return MOE_OK;
 }
 

@@ -1,0 +1,716 @@
+"""Products grouped by expert, 8-bit integer products and the combine's gradients on the GPU against
+their definitions in 64 bits.
+
+Tolerances count roundings, as in tests/test_gpu_dense.py: u = 2^-8 (bf16) or 2^-24 (fp32) relative for each
+value rounded to the layer's type, (n + 8) 2^-24 sum |a b| for an fp32 sum of n products in any order, F =
+2^-20 (1 + |a|) |a| for an activation.  The sums of integer products are exact.
+"""
+import math
+import random
+
+import numpy as np
+import pytest
+import torch
+
+from routing_dispatch_expert_logits_amd import binding as B
+from tests import gpu_util as gu
+from tests.test_gpu_dense import ACTS, SLOPE, TYPES, U, U32, act64, check, f64, framed, fsum, out, rand
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda:0"
+
+
+def ws_for(s, call):
+    """Exactly the bytes asked for, between guard bands, NaN where they are read unwritten."""
+    n = B.grouped_workspace_bytes(s, call)
+    return gu.empty((n,), "u8").fill_(0xFF) if n else None
+
+
+def offsets_of(counts, first=0):
+    off = torch.tensor([first] + list(counts), dtype=torch.int32).cumsum(0).to(torch.int32)
+    return off
+
+
+def groups(off):
+    ends = off.tolist()
+    return [(e, slice(a, b)) for e, (a, b) in enumerate(zip(ends, ends[1:])) if b > a]
+
+
+def skewed(E, R, seed):
+    g = torch.Generator().manual_seed(seed)
+    p = torch.arange(1, E + 1, dtype=torch.float64) ** -0.7
+    return torch.bincount(torch.multinomial(p[torch.randperm(E, generator=g)], R, replacement=True, generator=g),
+                          minlength=E).tolist()
+
+
+# row counts of the experts, rows before the first and behind the last one, K, N
+CASES = [([0], 0, 4, 64, 64), ([1], 0, 0, 64, 64), ([0, 0, 3], 0, 0, 257, 131), ([5, 0, 3], 2, 4, 8, 8), ([2, 1], 0, 0, 3, 1),
+         ([1] * 8 + [0] * 88, 0, 0, 136, 72), ([64, 1, 0, 130, 63], 0, 0, 128, 96), ([16, 17, 15, 33, 0, 1], 3, 0, 1024, 200),
+         ([257], 0, 7, 72, 264), ([300, 0, 0, 2, 259], 1, 1, 200, 136), (skewed(40, 900, 1), 0, 33, 333, 77),
+         (skewed(200, 130, 2), 5, 5, 520, 48), ([128, 256, 64, 384], 0, 0, 256, 256)]
+
+
+def case_id(c):
+    return f"{len(c[0])}experts-{sum(c[0])}rows-{c[3]}x{c[4]}" if isinstance(c, tuple) else None
+
+
+def sizes(c):
+    counts, first, behind, K, N = c
+    off = offsets_of(counts, first)
+    return off, int(off[-1]) + behind, K, N, len(counts)
+
+
+def rows_left(t, off, kind):
+    """The rows of no expert were not written."""
+    raw = t.detach().contiguous().view(torch.uint8).cpu().numpy().reshape(t.shape[0], -1)
+    assert (raw[:int(off[0])] == gu.POISON).all() and (raw[int(off[-1]):] == gu.POISON).all(), kind
+
+
+def by_groups(off, a, w, n):
+    """[rows of a] w[e]^T and the bound of its fp32 sums of n products; zeros in the rows of no expert."""
+    y, tol = (torch.zeros(a.shape[0], w.shape[1], dtype=torch.float64) for _ in range(2))
+    for e, r in groups(off):
+        y[r], tol[r] = a[r] @ w[e].T, fsum(a[r], w[e], n)
+    return y, tol
+
+
+def bad_rows(x, off):
+    """NaN in the rows of no expert: they have no part in anything."""
+    x = x.clone()
+    x[:int(off[0])] = float("nan")
+    x[int(off[-1]):] = float("nan")
+    return x
+
+
+def live(off):
+    return slice(int(off[0]), int(off[-1]))
+
+
+@pytest.mark.parametrize("dtype", ("bf16", "f32"))
+@pytest.mark.parametrize("case", CASES, ids=case_id)
+def test_linear(case, dtype):
+    off, R, K, N, E = sizes(case)
+    gen = torch.Generator().manual_seed(R + K)
+    x, dy = bad_rows(rand(gen, R, K, dtype=dtype), off), bad_rows(rand(gen, R, N, dtype=dtype), off)
+    w = rand(gen, E, N, K, dtype=dtype, std=K ** -0.5)
+    dev, doff = [framed(t) for t in (x, w, dy)], off.to(DEV)
+    s = B.grouped_shape(R, K, N, E, dtype=dtype)
+    y = out((R, N), dtype)
+    B.grouped_linear_forward(dev[0], doff, dev[1], y, s, ws_for(s, B.MOE_CALL_GROUPED_LINEAR_FORWARD))
+    rows_left(y, off, "y")
+    xd, wd, dd = (t.double() for t in (x, w, dy))
+    ref, tol = by_groups(off, xd, wd, K)
+    check("y", f64(y, dtype)[live(off)], ref[live(off)], (U[dtype] * ref.abs() + 2 * tol)[live(off)])
+    for grad in (("bf16", "f32") if dtype == "bf16" else ("f32",)):
+        s = B.grouped_shape(R, K, N, E, dtype=dtype, grad_dtype=grad)
+        ws = ws_for(s, B.MOE_CALL_GROUPED_LINEAR_BACKWARD)
+        dx, dw, dx2, dw2 = out((R, K), dtype), out((E, N, K), grad), out((R, K), dtype), out((E, N, K), grad)
+        B.grouped_linear_backward(dev[2], dev[0], doff, dev[1], dx, dw, s, ws)
+        B.grouped_linear_backward(dev[2], None, doff, dev[1], dx2, None, s, ws)
+        B.grouped_linear_backward(dev[2], dev[0], doff, None, None, dw2, s, ws)
+        assert torch.equal(dx, dx2) and torch.equal(dw, dw2)
+        rows_left(dx, off, "dx")
+        ref, tol = by_groups(off, dd, wd.transpose(1, 2), N)
+        check("dx", f64(dx, dtype)[live(off)], ref[live(off)], (U[dtype] * ref.abs() + 2 * tol)[live(off)])
+        got = f64(dw, grad)
+        for e in range(E):
+            r = slice(int(off[e]), int(off[e + 1]))
+            want = dd[r].T @ xd[r]
+            check(f"dw[{e}]", got[e], want, U[grad] * want.abs() + 2 * fsum(dd[r].T, xd[r].T, r.stop - r.start))
+
+
+@pytest.mark.parametrize("dtype", ("bf16", "f32"))
+@pytest.mark.parametrize("case", CASES, ids=case_id)
+def test_gated(case, dtype):
+    off, R, K, N, E = sizes(case)
+    gen = torch.Generator().manual_seed(R + K + 1)
+    act = ACTS[(R + K + N) % 5]
+    x, w1, w3 = rand(gen, R, K, dtype=dtype), rand(gen, E, N, K, dtype=dtype, std=K ** -0.5), rand(gen, E, N, K, dtype=dtype, std=0.1)
+    x = bad_rows(x, off)
+    dev, doff = [framed(t) for t in (x, w1, w3)], off.to(DEV)
+    s = B.grouped_shape(R, K, N, E, dtype=dtype, act=act)
+    ws = ws_for(s, B.MOE_CALL_GROUPED_GATED_FORWARD)
+    h, g, u, h2 = (out((R, N), dtype) for _ in range(4))
+    B.grouped_gated_forward(dev[0], doff, dev[1], dev[2], h, s, ws, g=g, u=u)
+    B.grouped_gated_forward(dev[0], doff, dev[1], dev[2], h2, s, ws)
+    assert torch.equal(h, h2)
+    for n, t in (("h", h), ("g", g), ("u", u)):
+        rows_left(t, off, n)
+    xd, w1d, w3d = (t.double() for t in (x, w1, w3))
+    v = live(off)
+    (rg, eg), (ru, eu) = ((a[v], b[v]) for a, b in (by_groups(off, xd, w1d, K), by_groups(off, xd, w3d, K)))
+    a, _ = act64(rg, act)
+    check("g", f64(g, dtype)[v], rg, U[dtype] * rg.abs() + 2 * eg)
+    check("u", f64(u, dtype)[v], ru, U[dtype] * ru.abs() + 2 * eu)
+    check("h", f64(h, dtype)[v], a * ru, U[dtype] * (a * ru).abs() + 2 * (SLOPE * eg * ru.abs() + a.abs() * eu + SLOPE * eg * eu)
+          + 2.0 ** -20 * (1 + rg.abs()) * rg.abs() * ru.abs())
+
+
+@pytest.mark.parametrize("dtype,grad", (("bf16", "bf16"), ("bf16", "f32"), ("f32", "f32")))
+@pytest.mark.parametrize("case", CASES, ids=case_id)
+def test_gated_backward(case, dtype, grad):
+    off, R, K, N, E = sizes(case)
+    gen = torch.Generator().manual_seed(R + K + 2)
+    act = ACTS[(R + K + N + 2) % 5]
+    x, dh = (bad_rows(rand(gen, R, n, dtype=dtype), off) for n in (K, N))
+    g, u = (bad_rows(rand(gen, R, N, dtype=dtype, std=1.7), off) for _ in range(2))
+    w1, w3 = rand(gen, E, N, K, dtype=dtype, std=0.1), rand(gen, E, N, K, dtype=dtype, std=0.1)
+    dev, doff = [framed(t) for t in (dh, x, w1, w3, g, u)], off.to(DEV)
+    s = B.grouped_shape(R, K, N, E, dtype=dtype, act=act, grad_dtype=grad)
+    ws = ws_for(s, B.MOE_CALL_GROUPED_GATED_BACKWARD)
+    dx, dw1, dw3 = out((R, K), dtype), out((E, N, K), grad), out((E, N, K), grad)
+    dx2, p, q = out((R, K), dtype), out((E, N, K), grad), out((E, N, K), grad)
+    B.grouped_gated_backward(dev[0], dev[1], doff, *dev[2:], dx, dw1, dw3, s, ws)
+    B.grouped_gated_backward(dev[0], None, doff, *dev[2:], dx2, None, None, s, ws)
+    B.grouped_gated_backward(dev[0], dev[1], doff, None, None, *dev[4:], None, p, q, s, ws)
+    assert torch.equal(dx, dx2)
+    rows_left(dx, off, "dx")
+    x, dh, w1, w3, g, u = (t.double() for t in (x, dh, w1, w3, g, u))
+    a, slope = act64(g, act)
+    dg, du = dh * u * slope, dh * a
+    fe = 2.0 ** -18 * (1 + g.abs())
+    eg, eu = fe * (dh * u).abs(), fe * (dh * g).abs()
+    r, v = U[dtype], live(off)
+    (x1, t1), (x3, t3) = by_groups(off, dg, w1.transpose(1, 2), 2 * N), by_groups(off, du, w3.transpose(1, 2), 2 * N)
+    o1, _ = by_groups(off, r * dg.abs() + eg, w1.abs().transpose(1, 2), 0)
+    o3, _ = by_groups(off, r * du.abs() + eu, w3.abs().transpose(1, 2), 0)
+    check("dx", f64(dx, dtype)[v], (x1 + x3)[v], (r * (x1 + x3).abs() + o1 + o3 + 2 * (t1 + t3))[v])
+    rw = U[grad]                # three bf16 terms hold an fp32 value
+    for name, got, d, e in (("dw1", dw1, dg, eg), ("dw3", dw3, du, eu), ("dw1", p, dg, eg), ("dw3", q, du, eu)):
+        got = f64(got, grad)
+        for i in range(E):
+            k = slice(int(off[i]), int(off[i + 1]))
+            want = d[k].T @ x[k]
+            check(f"{name}[{i}]", got[i], want, U[grad] * want.abs() + (rw * d[k].abs() + e[k]).T @ x[k].abs()
+                  + 2 * fsum(d[k].T, x[k].T, 3 * (k.stop - k.start)))
+
+
+# Sizes on the larger tiles; the 64-bit products run on the GPU.
+def spread_cases(n):
+    r = random.Random(31)
+    log = lambda lo, hi: int(math.exp(r.uniform(math.log(lo), math.log(hi))))  # noqa: E731
+    cases = []
+    for i in range(n):
+        E, R = log(1, 300), log(1, 9000)
+        K, N = (max(1, log(8, 2600) // s * s) for s in r.choices((64, 8, 1), k=2))
+        E = min(E, int(6e7 / (K * N)) + 1)
+        counts = skewed(E, R, i) if i % 3 else [max(1, R // E)] * E
+        cases.append((counts, r.choice((0, 0, 7)), r.choice((0, 0, 100)), K, N))
+    return cases
+
+
+LARGE = [(skewed(32, 8200, 3), 0, 0, 1024, 768), ([2100, 0, 4000, 300], 0, 9, 520, 1096), (skewed(128, 4096, 4), 0, 0, 768, 520),
+         (skewed(16, 4096, 5), 0, 0, 2048, 1032), (skewed(300, 700, 6), 2, 0, 1024, 1024), ([6000], 0, 0, 256, 640),
+         (skewed(8, 2000, 7), 0, 0, 1001, 517)] + spread_cases(18)
+
+
+def close(name, got, dtype, ref, tol):
+    got = (got.view(torch.bfloat16) if dtype == "bf16" else got).double()
+    over = (got - ref).abs() - tol
+    assert bool(torch.isfinite(got).all()) and bool((over <= 0).all()), \
+        f"{name}: {float((got - ref).abs().max()):.3e} off, {float(over.max()):.3e} over"
+
+
+@pytest.mark.parametrize("dtype", ("bf16", "f32"))
+@pytest.mark.parametrize("case", LARGE, ids=case_id)
+def test_large(case, dtype):
+    off, R, K, N, E = sizes(case)
+    gen = torch.Generator().manual_seed(R + N)
+    doff = off.to(DEV)
+    x, dy, g, u = (bad_rows(rand(gen, R, n, dtype=dtype), off).to(DEV) for n in (K, N, N, N))
+    w, w3 = (rand(gen, E, N, K, dtype=dtype, std=0.05).to(DEV) for _ in range(2))
+    sl, sg = (B.grouped_shape(R, K, N, E, dtype=dtype, act=a) for a in ("none", "silu"))
+    y, h, gg, uu = (out((R, N), dtype) for _ in range(4))
+    dx, dxg = out((R, K), dtype), out((R, K), dtype)
+    dw, dw1, dw3 = (out((E, N, K), dtype) for _ in range(3))
+    B.grouped_linear_forward(x, doff, w, y, sl, ws_for(sl, B.MOE_CALL_GROUPED_LINEAR_FORWARD))
+    B.grouped_gated_forward(x, doff, w, w3, h, sg, ws_for(sg, B.MOE_CALL_GROUPED_GATED_FORWARD), g=gg, u=uu)
+    B.grouped_linear_backward(dy, x, doff, w, dx, dw, sl, ws_for(sl, B.MOE_CALL_GROUPED_LINEAR_BACKWARD))
+    B.grouped_gated_backward(dy, x, doff, w, w3, g, u, dxg, dw1, dw3, sg, ws_for(sg, B.MOE_CALL_GROUPED_GATED_BACKWARD))
+    for n, t in (("y", y), ("h", h), ("g", gg), ("u", uu), ("dx", dx), ("dx gated", dxg)):
+        rows_left(t, off, n)
+    r = U[dtype]
+    for e in range(E):
+        k = slice(int(off[e]), int(off[e + 1]))
+        X, D, G, V, W, W3 = (t.double() for t in (x[k], dy[k], g[k], u[k], w[e], w3[e]))
+        a, slope = act64(G, "silu")
+        dg, du = D * V * slope, D * a
+        fe = 2.0 ** -18 * (1 + G.abs())
+        eg, eu = fe * (D * V).abs(), fe * (D * G).abs()
+        if k.stop > k.start:
+            ref, ru = X @ W.T, X @ W3.T
+            t, tu = 2 * fsum(X, W, K), 2 * fsum(X, W3, K)
+            close("y", y[k], dtype, ref, r * ref.abs() + t)
+            close("g", gg[k], dtype, ref, r * ref.abs() + t)
+            close("u", uu[k], dtype, ru, r * ru.abs() + tu)
+            b, _ = act64(ref, "silu")
+            close("h", h[k], dtype, b * ru, r * (b * ru).abs() + SLOPE * t * ru.abs() + b.abs() * tu + SLOPE * t * tu
+                  + 2.0 ** -20 * (1 + ref.abs()) * ref.abs() * ru.abs())
+            ref = D @ W
+            close("dx", dx[k], dtype, ref, r * ref.abs() + 2 * fsum(D, W.T, N))
+            ref = dg @ W + du @ W3
+            close("dx gated", dxg[k], dtype, ref, r * ref.abs() + (r * dg.abs() + eg) @ W.abs() + (r * du.abs() + eu) @ W3.abs()
+                  + 2 * (fsum(dg, W.T, 2 * N) + fsum(du, W3.T, 2 * N)))
+        n = k.stop - k.start
+        ref = D.T @ X
+        close("dw", dw[e], dtype, ref, r * ref.abs() + 2 * fsum(D.T, X.T, n))
+        for name, got, d, err in (("dw1", dw1, dg, eg), ("dw3", dw3, du, eu)):
+            ref = d.T @ X
+            close(name, got[e], dtype, ref, r * ref.abs() + (r * d.abs() + err).T @ X.abs() + 2 * fsum(d.T, X.T, n))
+
+
+def test_offsets_outside_the_rows_are_held_to_them():
+    """Offsets below 0 and above R are taken as 0 and R."""
+    R, K, N, E = 40, 72, 136, 3
+    gen = torch.Generator().manual_seed(1)
+    x, w, dy = rand(gen, R, K).to(DEV), rand(gen, E, N, K).to(DEV), rand(gen, R, N).to(DEV)
+    s = B.grouped_shape(R, K, N, E)
+    got = []
+    for off in ([-7, 11, 30, 999], [0, 11, 30, 40]):
+        o = torch.tensor(off, dtype=torch.int32, device=DEV)
+        y, dx, dw = out((R, N), "bf16"), out((R, K), "bf16"), out((E, N, K), "bf16")
+        B.grouped_linear_forward(x, o, w, y, s, ws_for(s, B.MOE_CALL_GROUPED_LINEAR_FORWARD))
+        B.grouped_linear_backward(dy, x, o, w, dx, dw, s, ws_for(s, B.MOE_CALL_GROUPED_LINEAR_BACKWARD))
+        got.append((y, dx, dw))
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+
+
+def test_bad_values_stay_with_their_expert_and_row():
+    """NaN and infinities of one row reach that row's outputs and its expert's weight gradient."""
+    counts, K, N = [70, 0, 30, 64], 136, 72
+    off = offsets_of(counts)
+    R, E = int(off[-1]), len(counts)
+    gen = torch.Generator().manual_seed(9)
+    x, w, dy = rand(gen, R, K), rand(gen, E, N, K), rand(gen, R, N)
+    bad = x.clone()
+    bad[75, 5], bad[99, 135] = float("nan"), float("inf")
+    s = B.grouped_shape(R, K, N, E)
+    res = []
+    for v in (x, bad):
+        y, dw = out((R, N), "bf16"), out((E, N, K), "bf16")
+        B.grouped_linear_forward(framed(v), off.to(DEV), framed(w), y, s, ws_for(s, B.MOE_CALL_GROUPED_LINEAR_FORWARD))
+        B.grouped_linear_backward(framed(dy), framed(v), off.to(DEV), None, None, dw, s, ws_for(s, B.MOE_CALL_GROUPED_LINEAR_BACKWARD))
+        res.append((f64(y, "bf16"), f64(dw, "bf16")))
+    rows = [r for r in range(R) if r not in (75, 99)]
+    assert torch.equal(res[0][0][rows], res[1][0][rows])
+    assert not torch.isfinite(res[1][0][75]).any() and not torch.isfinite(res[1][0][99]).all()
+    assert torch.equal(res[0][1][[0, 1, 3]], res[1][1][[0, 1, 3]])
+    assert not torch.isfinite(res[1][1][2][:, 5]).any()
+
+
+def test_no_rows():
+    for dtype in ("bf16", "f32"):
+        E, K, N = 5, 40, 24
+        w = torch.zeros(E, N, K, dtype=TYPES[dtype], device=DEV)
+        x, d = (torch.empty(0, n, dtype=TYPES[dtype], device=DEV) for n in (K, N))
+        off = torch.zeros(E + 1, dtype=torch.int32, device=DEV)
+        s, sg = B.grouped_shape(0, K, N, E, dtype=dtype), B.grouped_shape(0, K, N, E, dtype=dtype, act="gelu")
+        B.grouped_linear_forward(x, off, w, d, s, ws_for(s, B.MOE_CALL_GROUPED_LINEAR_FORWARD))
+        dw, dw1, dw3 = (out((E, N, K), dtype) for _ in range(3))
+        B.grouped_linear_backward(d, x, off, w, torch.empty_like(x), dw, s, ws_for(s, B.MOE_CALL_GROUPED_LINEAR_BACKWARD))
+        B.grouped_gated_backward(d, x, off, w, w, d, d, torch.empty_like(x), dw1, dw3, sg,
+                                 ws_for(sg, B.MOE_CALL_GROUPED_GATED_BACKWARD))
+        assert all(f64(t, dtype).eq(0).all() for t in (dw, dw1, dw3))
+
+
+# ---- 8-bit integers
+
+def codes64(x):
+    """Codes and scales by their definition, the quotient in 64 bits."""
+    a = x.double().abs().amax(1)
+    scale = (a / 127).float()
+    ok = torch.isfinite(a) & (scale > 0)
+    q = torch.round(x.double() / torch.where(ok, scale, torch.ones_like(scale)).double()[:, None]).clamp(-127, 127)
+    q = torch.where(ok[:, None], q, torch.zeros_like(q))
+    return q.to(torch.int8), torch.where(torch.isfinite(a), scale, torch.full_like(scale, float("nan")))
+
+
+def quantised(x, dtype):
+    rows, cols = x.shape
+    ld = B.int8_row_bytes(cols)
+    q, scale = gu.empty((rows, ld), "u8").view(torch.int8), out((rows,), "f32")
+    B.quantize_int8(framed(x), q, scale)
+    return q, scale
+
+
+@pytest.mark.parametrize("dtype", ("bf16", "f32"))
+@pytest.mark.parametrize("size", ((1, 1), (3, 17), (1, 4096), (5, 16), (70, 1000), (33, 2049), (4, 8200), (2, 40000), (1000, 333)),
+                         ids=str)
+def test_quantize(size, dtype):
+    """Codes and scales are the definition's, bit for bit, and rows end in zeros."""
+    gen = torch.Generator().manual_seed(sum(size))
+    rows, cols = size
+    x = rand(gen, rows, cols, dtype="f32") * torch.exp2(torch.randint(-130, 120, (rows, 1), generator=gen).float())
+    x = x.to(TYPES[dtype])
+    q, scale = quantised(x, dtype)
+    wq, ws = codes64(x)
+    assert torch.equal(scale.cpu(), ws)
+    assert torch.equal(q.cpu()[:, :cols], wq)
+    assert not q.cpu()[:, cols:].any()
+
+
+def test_quantize_ties_and_borders():
+    """Quotients at and next to ties: scales that are powers of two, and values half a step away from a
+    code in fp32's last places."""
+    x = []
+    for p in (-140, -126, -100, -20, 0, 30, 119):
+        s = 2.0 ** p
+        k = torch.arange(-126, 127).double() + 0.5
+        near = torch.cat([k * s, torch.tensor([127.0 * s])]).float()
+        x.append(near)
+    for amax in (1.0, 3.3, 250.0, 1e-30, 7e-37, 2e37):
+        s = np.float32(np.float32(amax) / np.float32(127))
+        k = np.arange(-126, 127) + 0.5
+        mid = (k * np.float64(s)).astype(np.float32)
+        for v in (mid, np.nextafter(mid, np.float32(np.inf)), np.nextafter(mid, np.float32(-np.inf))):
+            x.append(torch.cat([torch.from_numpy(v), torch.tensor([amax])]))
+    x = torch.stack([t.float() for t in x])
+    q, scale = quantised(x, "f32")
+    wq, ws = codes64(x)
+    assert torch.equal(scale.cpu(), ws)
+    assert torch.equal(q.cpu()[:, :x.shape[1]], wq)
+
+
+def test_quantize_zeros_and_bad_rows():
+    x = torch.randn(6, 40, generator=torch.Generator().manual_seed(3))
+    x[0] = 0
+    x[1, 39] = float("inf")
+    x[2, 0] = float("nan")
+    x[3] = 0
+    x[3, 7] = 2.0 ** -149          # its scale is below fp32's smallest number
+    x[4] = x[4].sign() * torch.tensor([190 * 2.0 ** -149])
+    for dtype in ("f32", "bf16"):
+        v = x.to(TYPES[dtype])
+        q, scale = quantised(v, dtype)
+        wq, ws = codes64(v)
+        assert torch.equal(q.cpu()[:, :40], wq)
+        assert torch.equal(torch.nan_to_num(scale.cpu(), nan=-1.0), torch.nan_to_num(ws, nan=-1.0))
+        assert scale.cpu()[1:3].isnan().all() and not q.cpu()[:4].any()
+
+
+def random_codes(gen, *shape):
+    """Codes in rows of whole chunks, zeros behind, and scales."""
+    ld = B.int8_row_bytes(shape[-1])
+    q = torch.zeros(*shape[:-1], ld, dtype=torch.int8)
+    q[..., :shape[-1]] = torch.randint(-127, 128, shape, generator=gen, dtype=torch.int8)
+    return q, torch.rand(*shape[:-1], generator=gen) * 0.01 + 1e-4
+
+
+def framed_codes(q):
+    """Codes with others right before and behind them."""
+    pad = 4096
+    buf = torch.full((q.numel() + 2 * pad,), 77, dtype=torch.int8, device=DEV)
+    view = buf[pad:pad + q.numel()].view(q.shape)
+    view.copy_(q)
+    return view
+
+
+INT8_SIZES = [(1, 64, 64), (1, 257, 131), (2, 8, 8), (3, 1, 1), (8, 7168, 96), (16, 136, 200), (17, 72, 56), (33, 333, 77),
+              (64, 64, 64), (65, 128, 129), (130, 515, 260), (257, 200, 264), (300, 64, 1000), (700, 1032, 520), (2, 1 << 17, 24)]
+
+
+@pytest.mark.parametrize("dtype", ("bf16", "f32"))
+@pytest.mark.parametrize("size", INT8_SIZES, ids=str)
+def test_int8_dense(size, dtype):
+    T, K, N = size
+    gen = torch.Generator().manual_seed(sum(size))
+    (x, sx), (w, sw), (w3, sw3) = random_codes(gen, T, K), random_codes(gen, N, K), random_codes(gen, N, K)
+    if K == 1 << 17:
+        x[:], w[:] = 127, -127           # the largest sum
+    bias, res = rand(gen, N, dtype=dtype), rand(gen, T, N, dtype=dtype)
+    q = [framed_codes(t) for t in (x, w, w3)]
+    sc = [framed(t) for t in (sx, sw, sw3)]
+    z = (x.double() @ w.double().T) * sx.double()[:, None] * sw.double()
+    ez = 4 * U32 * z.abs()
+    for act, b, r in (("none", 0, 0), (ACTS[sum(size) % 5], 1, 1), ("gelu", 1, 0), ("silu", 0, 1)):
+        s = B.dense_shape(T, K, N, dtype=dtype, act=act)
+        y = out((T, N), dtype)
+        B.linear_int8_forward(q[0], sc[0], q[1], sc[1], framed(bias) if b else None, framed(res) if r else None, y, s)
+        zb = z + (bias.double() if b else 0.0)
+        a, _ = act64(zb, act)
+        ry = a + (res.double() if r else 0.0)
+        check("y", f64(y, dtype), ry, U[dtype] * ry.abs() + SLOPE * (ez + U32 * zb.abs())
+              + 2.0 ** -20 * (1 + zb.abs()) * zb.abs() + 2 * U32 * ry.abs())
+    y2 = out((T, N), dtype)
+    y2.copy_(res.to(DEV).view(y2.dtype))
+    B.linear_int8_forward(q[0], sc[0], q[1], sc[1], None, y2, y2, s)
+    assert torch.equal(y, y2)
+    s = B.dense_shape(T, K, N, dtype=dtype, act="silu")
+    h = out((T, N), dtype)
+    B.gated_int8_forward(q[0], sc[0], q[1], sc[1], q[2], sc[2], h, s)
+    u = (x.double() @ w3.double().T) * sx.double()[:, None] * sw3.double()
+    a, _ = act64(z, "silu")
+    check("h", f64(h, dtype), a * u, U[dtype] * (a * u).abs() + 8 * U32 * (z * u).abs() * SLOPE
+          + 2.0 ** -20 * (1 + z.abs()) * (z * u).abs())
+
+
+@pytest.mark.parametrize("dtype", ("bf16", "f32"))
+@pytest.mark.parametrize("case", CASES + LARGE[:7] + LARGE[9:15], ids=case_id)
+def test_int8_grouped(case, dtype):
+    off, R, K, N, E = sizes(case)
+    gen = torch.Generator().manual_seed(R + K + 5)
+    (x, sx), (w, sw), (w3, sw3) = random_codes(gen, R, K), random_codes(gen, E, N, K), random_codes(gen, E, N, K)
+    q, sc, doff = [framed_codes(t) for t in (x, w, w3)], [framed(t) for t in (sx, sw, sw3)], off.to(DEV)
+    sl, sg = (B.grouped_shape(R, K, N, E, dtype=dtype, act=a) for a in ("none", "gelu_tanh"))
+    y, h = out((R, N), dtype), out((R, N), dtype)
+    B.grouped_linear_int8_forward(q[0], sc[0], doff, q[1], sc[1], y, sl, ws_for(sl, B.MOE_CALL_GROUPED_LINEAR_INT8))
+    B.grouped_gated_int8_forward(q[0], sc[0], doff, q[1], sc[1], q[2], sc[2], h, sg, ws_for(sg, B.MOE_CALL_GROUPED_GATED_INT8))
+    rows_left(y, off, "y")
+    rows_left(h, off, "h")
+    for e, r in groups(off):
+        X, S = q[0][r].double(), sc[0][r].double()[:, None]
+        z, u = ((X @ a[e].double().T) * S * b[e].double() for a, b in ((q[1], sc[1]), (q[2], sc[2])))
+        close("y", y[r], dtype, z, (U[dtype] + 4 * U32) * z.abs())
+        a, _ = act64(z, "gelu_tanh")
+        close("h", h[r], dtype, a * u, U[dtype] * (a * u).abs() + 8 * U32 * (z * u).abs() * SLOPE
+              + 2.0 ** -20 * (1 + z.abs()) * (z * u).abs())
+
+
+def test_int8_bad_rows_make_nan_of_their_products():
+    gen = torch.Generator().manual_seed(8)
+    x, w = rand(gen, 20, 72, dtype="f32"), rand(gen, 40, 72, dtype="f32")
+    x[3, 4], x[17, 71] = float("inf"), float("nan")
+    (q, sx), (qw, sw) = quantised(x, "f32"), quantised(w, "f32")
+    y = out((20, 40), "f32")
+    B.linear_int8_forward(q, sx, qw, sw, None, None, y, B.dense_shape(20, 72, 40, dtype="f32"))
+    y = y.cpu()
+    assert y[[3, 17]].isnan().all() and torch.isfinite(y[[r for r in range(20) if r not in (3, 17)]]).all()
+
+
+# ---- the combine's gradients
+
+def routed(T, E, k, capacity, seed):
+    """token_row as the permutation writes it, and how many rows are kept."""
+    g = torch.Generator().manual_seed(seed)
+    ids = torch.rand(T, E, generator=g).topk(k, dim=1).indices
+    counts, rows = [0] * E, torch.full((T, k), -1, dtype=torch.int32)
+    for t in range(T):
+        for j in range(k):
+            e = int(ids[t, j])
+            if not capacity or counts[e] < capacity:
+                rows[t, j] = counts[e]
+                counts[e] += 1
+    start = np.concatenate([[0], np.cumsum(counts)])
+    for t in range(T):
+        for j in range(k):
+            if rows[t, j] >= 0:
+                rows[t, j] += int(start[int(ids[t, j])])
+    return rows, int(start[-1])
+
+
+@pytest.mark.parametrize("dtype,grad", (("bf16", "bf16"), ("bf16", "f32"), ("f32", "f32"), ("f32", "bf16")))
+@pytest.mark.parametrize("size", ((1, 64, 1, 1, 0), (1, 128, 12, 8, 0), (3, 192, 5, 3, 2), (70, 320, 8, 8, 0), (33, 2048, 40, 5, 3),
+                                  (9, 7168, 64, 16, 0), (5, 16384, 70, 64, 0), (300, 1024, 16, 2, 30)), ids=str)
+def test_combine_backward(size, dtype, grad):
+    T, D, E, k, cap = size
+    gen = torch.Generator().manual_seed(sum(size))
+    rows, kept = routed(T, E, k, cap, sum(size))
+    dout, y = rand(gen, T, D, dtype=grad), rand(gen, T * k, D, dtype=dtype)
+    w = torch.rand(T, k, generator=gen)
+    s = B.shape(T, D, E, k, 64, dtype=dtype, capacity=cap)
+    code = B.MOE_F32 if grad == "f32" else B.MOE_BF16
+    y[kept:] = float("nan")            # rows of no assignment
+    dev = [framed(t) for t in (dout, y)] + [rows.to(DEV), framed(w)]
+    dy, dw, dy2, dw2 = out((T * k, D), dtype), out((T, k), "f32"), out((T * k, D), dtype), out((T, k), "f32")
+    B.combine_backward(*dev, dy, dw, code, s)
+    B.combine_backward(dev[0], None, dev[2], dev[3], dy2, None, code, s)
+    B.combine_backward(dev[0], dev[1], dev[2], None, None, dw2, code, s)
+    assert torch.equal(dy, dy2) and torch.equal(dw, dw2)
+    gu.assert_poison(dy, kept)
+    got, d, yd = f64(dy, dtype), dout.double(), y.double()
+    for j in range(k):
+        t = (rows[:, j] >= 0).nonzero()[:, 0]
+        r = rows[t, j].long()
+        want = d[t] * w[t, j].double()[:, None]
+        check("dy", got[r], want, (U[dtype] + U32) * want.abs())
+        want = (d[t] * yd[r]).sum(1)
+        check("dw", dw.cpu().double()[t, j], want, (D + 8) * U32 * (d[t] * yd[r]).abs().sum(1))
+        assert not dw.cpu()[rows[:, j] < 0, j].any()
+
+
+# ---- the operators together: one routed layer's training step, and its serving in integers
+
+class Layer:
+    """Routing, permutation, expert products and combine, forward and backward, through the calls."""
+
+    def __init__(self, T, H, E, k, I, dtype, seed, act="silu", capacity=0):
+        gen = torch.Generator().manual_seed(seed)
+        self.T, self.H, self.E, self.k, self.I, self.dtype, self.act = T, H, E, k, I, dtype, act
+        t = TYPES[dtype]
+        self.p = dict(w1=rand(gen, E, I, H, dtype=dtype, std=H ** -0.5), w3=rand(gen, E, I, H, dtype=dtype, std=H ** -0.5),
+                      w2=rand(gen, E, H, I, dtype=dtype, std=I ** -0.5))
+        self.x, self.dout = rand(gen, T, H, dtype=dtype), rand(gen, T, H, dtype=dtype)
+        self.logits = torch.randn(T, E, generator=gen)
+        self.d = {n: v.to(DEV) for n, v in dict(self.p, x=self.x, dout=self.dout, logits=self.logits).items()}
+        R = T * k
+        self.s = B.shape(T, H, E, k, max(64, I // 64 * 64), dtype=dtype, capacity=capacity)
+        self.sg, self.sl = B.grouped_shape(R, H, I, E, dtype=dtype, act=act), B.grouped_shape(R, I, H, E, dtype=dtype)
+        n = max(*(B.workspace_bytes(self.s, c) for c in (B.MOE_CALL_ROUTE, B.MOE_CALL_DISPATCH)),
+                *(B.grouped_workspace_bytes(self.sl, c) for c in (0, 1)), *(B.grouped_workspace_bytes(self.sg, c) for c in (2, 3)))
+        self.ws = torch.empty(max(n, 16), dtype=torch.uint8, device=DEV)
+        e = lambda *shape, dt=t: torch.zeros(shape, dtype=dt, device=DEV)  # noqa: E731
+        i32 = torch.int32
+        self.o = dict(ids=e(T, k, dt=i32), w=e(T, k, dt=torch.float32), counts=e(E, dt=i32), offsets=e(E + 1, dt=i32),
+                      row_token=e(R, dt=i32), token_row=e(T, k, dt=i32), xp=e(R, H), h=e(R, I), g=e(R, I), u=e(R, I),
+                      yp=e(R, H), y=e(T, H), dyp=e(R, H), dtw=e(T, k, dt=torch.float32), dh=e(R, I), dxp=e(R, H), dx=e(T, H),
+                      dw1=e(E, I, H), dw3=e(E, I, H), dw2=e(E, H, I))
+        self.ones = torch.ones(T, k, device=DEV)
+        self.code = B.MOE_BF16 if dtype == "bf16" else B.MOE_F32
+
+    def run(self, stream=None):
+        d, o, ws, s, c = self.d, self.o, self.ws, self.s, self.code
+        B.route_topk(None, None, None, d["logits"], o["ids"], o["w"], o["counts"], o["offsets"], s, ws, stream=stream)
+        B.dispatch_permute(d["x"], o["ids"], o["offsets"], o["xp"], o["row_token"], o["token_row"], s, ws, stream=stream)
+        B.grouped_gated_forward(o["xp"], o["offsets"], d["w1"], d["w3"], o["h"], self.sg, ws, g=o["g"], u=o["u"], stream=stream)
+        B.grouped_linear_forward(o["h"], o["offsets"], d["w2"], o["yp"], self.sl, ws, stream=stream)
+        B.combine(o["yp"], o["token_row"], o["w"], o["y"], c, B.MOE_COMBINE_FUSED, s, None, stream=stream)
+        B.combine_backward(d["dout"], o["yp"], o["token_row"], o["w"], o["dyp"], o["dtw"], c, s, stream=stream)
+        B.grouped_linear_backward(o["dyp"], o["h"], o["offsets"], d["w2"], o["dh"], o["dw2"], self.sl, ws, stream=stream)
+        B.grouped_gated_backward(o["dh"], o["xp"], o["offsets"], d["w1"], d["w3"], o["g"], o["u"], o["dxp"], o["dw1"],
+                                 o["dw3"], self.sg, ws, stream=stream)
+        B.combine(o["dxp"], o["token_row"], self.ones, o["dx"], c, B.MOE_COMBINE_FUSED, s, None, stream=stream)
+
+    def forward64(self, x, w, **over):
+        """The layer in 64 bits with the routing that the GPU took; w [T, k]."""
+        p = {n: v.double() for n, v in self.p.items()}
+        p.update(over)
+        ids, rows = self.o["ids"].cpu().long(), self.o["token_row"].cpu()
+        y = torch.zeros(self.T, self.H, dtype=torch.float64)
+        for e in range(self.E):
+            t, j = ((ids == e) & (rows >= 0)).nonzero(as_tuple=True)
+            if len(t):
+                a, _ = act64(x[t] @ p["w1"][e].T, self.act)
+                y = y.index_add(0, t, w[t, j][:, None] * ((a * (x[t] @ p["w3"][e].T)) @ p["w2"][e].T))
+        return y
+
+
+@pytest.mark.parametrize("dtype", ("bf16", "f32"))
+@pytest.mark.parametrize("size", ((1, 64, 8, 2, 64, 0), (40, 128, 16, 3, 200, 0), (300, 256, 12, 4, 136, 0), (120, 128, 6, 2, 72, 25)),
+                         ids=str)
+def test_layer_against_64_bits(size, dtype):
+    """The run of all nine calls against autograd in 64 bits.  Up to seven values rounded to the layer's type lie
+    between an input and a gradient (x's row, g and u, h, y's row, dy, dh, the gradient), each entering through
+    factors whose effect on the gradient's norm is about that of the value itself: 9 u of the norm bounds
+    them for the quantities' 2-norms.  In fp32 the sums of up to 256 products take the place of the
+    roundings: 64 u."""
+    T, H, E, k, I, cap = size
+    b = Layer(T, H, E, k, I, dtype, 60 + T, capacity=cap)
+    b.run()
+    leaves = {n: v.double().requires_grad_() for n, v in b.p.items()}
+    x, w = b.x.double().requires_grad_(), b.o["w"].cpu().double().requires_grad_()
+    y = b.forward64(x, w, **leaves)
+    y.backward(b.dout.double())
+    bound = 9 * U["bf16"] if dtype == "bf16" else 64 * U32
+    ref = dict(y=y.detach(), dw1=leaves["w1"].grad, dw3=leaves["w3"].grad, dw2=leaves["w2"].grad, dx=x.grad, dtw=w.grad)
+    for n, r in ref.items():
+        err = float((b.o[n].cpu().double() - r).norm() / r.norm())
+        assert err <= bound, (n, err)
+
+
+def test_layer_gradients_against_differences():
+    """<gradient, v> against the central difference of the 64-bit layer along v (step 1e-4: its own error is of
+    the order 1e-8); the fp32 gradients are within 64 u of the 64-bit ones."""
+    b = Layer(23, 72, 7, 3, 104, "f32", 92, act="gelu_tanh")
+    b.run()
+    gen = torch.Generator().manual_seed(4)
+    dout = b.dout.double()
+
+    def loss(x=None, w=None, **over):
+        return float((b.forward64(b.x.double() if x is None else x, b.o["w"].cpu().double() if w is None else w, **over) * dout).sum())
+
+    for leaf, grad in (("w1", "dw1"), ("w3", "dw3"), ("w2", "dw2"), ("x", "dx"), ("w", "dtw")):
+        p = (b.x if leaf == "x" else b.o["w"].cpu() if leaf == "w" else b.p[leaf]).double()
+        v = torch.empty(p.shape, dtype=torch.float64).normal_(generator=gen)
+        h = 1e-4
+        diff = (loss(**{leaf: p + h * v}) - loss(**{leaf: p - h * v})) / (2 * h)
+        got = b.o[grad].cpu().double()
+        assert abs(float((got * v).sum()) - diff) <= 64 * U32 * float(got.norm() * v.norm()) + 1e-6 * abs(diff), leaf
+
+
+def test_layer_in_a_graph_replays_like_eager():
+    """Captured once, replayed with other routings and inputs and with eager work between: every replay
+    gives the eager calls' bits."""
+    b = Layer(130, 128, 20, 4, 264, "bf16", 18)
+    b.run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        b.run()
+    for i in range(4):
+        gen = torch.Generator().manual_seed(200 + i)
+        b.d["x"].copy_(rand(gen, 130, 128))
+        b.d["dout"].copy_(rand(gen, 130, 128))
+        b.d["logits"].copy_(torch.randn(130, 20, generator=gen) * (1 + i))
+        b.run()
+        want = {n: t.clone() for n, t in b.o.items()}
+        for t in b.o.values():
+            t.zero_()
+        b.ws.fill_(0xFF)
+        graph.replay()
+        torch.cuda.synchronize()
+        for n, t in b.o.items():
+            assert torch.equal(t, want[n]), (i, n)
+
+
+def test_two_layers_on_two_streams_at_once():
+    one, two = Layer(200, 256, 16, 4, 328, "bf16", 5), Layer(60, 128, 40, 2, 1000, "bf16", 6)
+    want = []
+    for b in (one, two):
+        b.run()
+        torch.cuda.synchronize()
+        want.append({n: t.clone() for n, t in b.o.items()})
+        for t in b.o.values():
+            t.zero_()
+    torch.cuda.synchronize()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(5):
+        one.run(stream=s1)
+        two.run(stream=s2)
+    torch.cuda.synchronize()
+    for b, w in zip((one, two), want):
+        for n, t in b.o.items():
+            assert torch.equal(t, w[n]), n
+
+
+@pytest.mark.parametrize("size", ((3, 128, 30, 4, 64), (200, 256, 12, 4, 192)), ids=str)
+def test_layer_in_integers(size):
+    """quantise, gated product, quantise, linear product, combine, against the bf16 layer in 64 bits.  A code is off by
+    at most half a step, 1/254 of its row's largest value; for rows of n normal values that largest is below 4.5
+    (n <= 256), so a row's relative error is below 4.5 / (254 sqrt 3) = 0.0102 of its norm and of a
+    random product's.  x, w1, w3, h (whose largest value is below 15 of its deviations, a product of two normal ones:
+    0.034) and w2 enter: 4 * 0.0102 + 0.034 + 0.01 for bf16's roundings bounds their sum."""
+    T, H, E, k, I = size
+    b = Layer(T, H, E, k, I, "bf16", 33)
+    b.run()
+    o, d, R = b.o, b.d, T * k
+
+    def codes(t):
+        q = torch.empty(*t.shape[:-1], B.int8_row_bytes(t.shape[-1]), dtype=torch.int8, device=DEV)
+        s = torch.empty(t.shape[:-1], device=DEV)
+        B.quantize_int8(t, q, s)
+        return q, s
+
+    (w1, s1), (w3, s3), (w2, s2) = (codes(d[n]) for n in ("w1", "w3", "w2"))
+    h, yp, y = torch.empty_like(o["h"]), torch.empty_like(o["yp"]), torch.empty_like(o["y"])
+    q, s = codes(o["xp"])
+    B.grouped_gated_int8_forward(q, s, o["offsets"], w1, s1, w3, s3, h, b.sg, ws_for(b.sg, B.MOE_CALL_GROUPED_GATED_INT8))
+    q, s = codes(h)
+    B.grouped_linear_int8_forward(q, s, o["offsets"], w2, s2, yp, b.sl, ws_for(b.sl, B.MOE_CALL_GROUPED_LINEAR_INT8))
+    B.combine(yp, o["token_row"], o["w"], y, b.code, B.MOE_COMBINE_FUSED, b.s, None)
+    ref = b.forward64(b.x.double(), o["w"].cpu().double())
+    assert float((y.cpu().double() - ref).norm() / ref.norm()) <= 4 * 0.0102 + 0.034 + 0.01
+
+
+def test_binding_refuses_other_tensors():
+    s = B.grouped_shape(4, 16, 8, 2, dtype="f32")
+    x, w, y = torch.zeros(4, 16, device=DEV), torch.zeros(2, 8, 16, device=DEV), torch.zeros(4, 8, device=DEV)
+    off = torch.zeros(3, dtype=torch.int32, device=DEV)
+    for args, why in (((x, off.long(), w, y), "type"), ((x, off[:2], w, y), "shape"), ((x, off, w[0], y), "shape"),
+                      ((x, off.cpu(), w, y), "not on a GPU"), ((x, off, w.transpose(0, 1).contiguous().transpose(0, 1), y), "row-major")):
+        with pytest.raises(B.MoeError, match=why) as e:
+            B.grouped_linear_forward(*args, s, None)
+        assert e.value.status == B.MOE_ERR_INVALID_ARG
+    with pytest.raises(B.MoeError, match="type"):
+        B.quantize_int8(x, torch.zeros(4, 16, dtype=torch.uint8, device=DEV), torch.zeros(4, device=DEV))
