@@ -227,6 +227,12 @@ constexpr int mm_waitcnt(int n) { return (n & 0xF) | ((n >> 4) << 14) | (0x7 << 
 // Steps of 128 bytes: all waves read a stage's operands and multiply at their own pace, one
 // barrier per step.  Steps of 64 bytes (8 waves, two per SIMD): the waves of a SIMD take turns,
 // one reading a step's operands while the other multiplies, a barrier after each turn.
+// Passes of the epilogue: so many that W waves' sums of `tile` bytes find room in S stages of `stage` bytes.
+constexpr int mm_passes(int stage, int S, int tile, int W) {
+  int p = 1;
+  while (stage / (tile / p) * S < W) p *= 2;
+  return p;
+}
 template <int BM, int BN, int SB>
 constexpr int kMmStage = (BM + BN) * SB / 2;  // 16-bit words of a stage
 //
@@ -412,8 +418,8 @@ __device__ __forceinline__ void mm_body(const DenseJob& j, const DenseEpi& e, co
   fill(s0);
   fill(s1);
   if (S > 3) fill(s2);
-  if constexpr (SB == 64) {
-    static_assert(S == 4 && W == 8 && ES <= 2, "turns");
+  if constexpr (SB == 64 && W == 8) {
+    static_assert(S == 4 && ES <= 2, "turns");
     __builtin_amdgcn_s_waitcnt(mm_waitcnt(2 * (QA + QB)));
     asm volatile("" ::: "memory");
     __builtin_amdgcn_s_barrier();
@@ -447,12 +453,12 @@ __device__ __forceinline__ void mm_body(const DenseJob& j, const DenseEpi& e, co
   __builtin_amdgcn_s_waitcnt(mm_waitcnt(0));
 
   // Epilogue through LDS, the stages being free now: a wave's sums go to a region of its own
-  // (in two passes where they are more than the stages hold), rows of TN columns whose 16-byte chunks are rotated
+  // (in passes where they are more than the stages hold), rows of TN columns whose 16-byte chunks are rotated
   // by row, and come back eight columns of a row per lane: whole cache lines per store, and one
   // copy of the epilogue's code in a loop, where straight from the accumulators it would be
   // FM * FN copies (which cost 12 us of a 120 us product, 4096^3, in instruction fetches and
   // scattered stores).
-  constexpr int PASSES = TM * TN * 4 * W > S * STAGE * 2 ? 2 : 1, PM = TM / PASSES, PF = FM / PASSES;
+  constexpr int PASSES = mm_passes(STAGE * 2, S, TM * TN * 4, W), PM = TM / PASSES, PF = FM / PASSES;
   constexpr int CH = TN / 4;                       // chunks per row
   constexpr int OC = PAIR ? TN / 2 : TN;           // output columns of the wave
   constexpr int LPR = OC / 8, RPI = 64 / LPR;      // lanes per row, rows per iteration
@@ -541,6 +547,7 @@ __device__ __forceinline__ void mm_body(const DenseJob& j, const DenseEpi& e, co
   };
   pass(std::integral_constant<int, 0>{});
   if constexpr (PASSES > 1) pass(std::integral_constant<int, 1>{});
+  if constexpr (PASSES > 2) pass(std::integral_constant<int, 2>{}), pass(std::integral_constant<int, 3>{});
 }
 
 }  // namespace moe

@@ -61,6 +61,8 @@ GroupedWs grouped_ws(const GroupedDims& d, bool gated, bool backward, bool int8)
   const GroupedType t = int8 ? GROUPED_INT8 : d.bf16 ? GROUPED_BF16 : GROUPED_F32;
   w.ldk = int8 ? code_bytes(d.K) : padded(d.bf16, d.K);
   w.ldn = padded(d.bf16, d.N);
+  const bool decode = !backward && d.R <= kGroupedDecodeRows;
+  if (decode && !int8) w.ldk = d.K;  // its kernel takes rows of any length
   const bool pad_k = !int8 && w.ldk != d.K;
   w.x = c.take(pad_k ? (size_t)d.R * w.ldk * d.es : 0);
   for (int i = 0; i < (gated ? 2 : 1); ++i) w.w[i] = c.take(pad_k ? (size_t)d.E * d.N * w.ldk * d.es : 0);
@@ -72,9 +74,9 @@ GroupedWs grouped_ws(const GroupedDims& d, bool gated, bool backward, bool int8)
     w.d1 = c.take(gated ? bytes : 0);
     w.finite = c.take(w.terms > 1 ? (size_t)d.R * w.ldk * d.es : 0);
   }
-  w.table = c.take(d.R == 0 ? 0
-                   : backward ? grouped_table_bytes(t, d.R, d.E, d.K, d.N, gated ? 2 : 1, false, true)
-                              : grouped_table_bytes(t, d.R, d.E, d.N, d.K, 1, gated, false));
+  w.table = c.take(d.R == 0 || decode ? 0
+                   : backward ? grouped_table_bytes(t, d.R, d.E, d.K, d.N, gated ? 2 : 1, false)
+                              : grouped_table_bytes(t, d.R, d.E, d.N, d.K, 1, gated));
   w.total = c.cur;
   return w;
 }
@@ -111,7 +113,10 @@ moe_status forward(const GroupedDims& d, const GroupedWs& w, GroupedType t, cons
   e.act = d.act;
   e.ldo = d.N;
   e.out_f32 = !d.bf16;
-  MOE_HIP(launch_grouped(j, e, t, d.bf16, Groups{offsets, d.E, d.R}, (int64_t)d.N * w.ldk, at<void>(ws, w.table), st));
+  const Groups g{offsets, d.E, d.R};
+  const int64_t w_stride = (int64_t)d.N * w.ldk;
+  MOE_HIP(d.R <= kGroupedDecodeRows ? launch_grouped_decode(j, e, t, d.bf16, g, w_stride, st)
+                                    : launch_grouped(j, e, t, d.bf16, g, w_stride, at<void>(ws, w.table), st));
   return MOE_OK;
 }
 
@@ -333,7 +338,9 @@ static moe_status int8_forward(const int8_t* x, const float* x_scale, const int8
   e.bias = bias; e.residual = residual;
   e.out[0] = y;
   e.row_scale = x_scale; e.col_scale[0] = w0_scale; e.col_scale[1] = w1_scale;
-  MOE_HIP(launch_int8(j, e, s->dtype == MOE_BF16, (hipStream_t)stream));
+  const hipStream_t st = (hipStream_t)stream;
+  const bool bf16 = s->dtype == MOE_BF16;
+  MOE_HIP(T <= (size_t)kInt8DecodeRows ? launch_grouped_decode(j, e, GROUPED_INT8, bf16, Groups{}, 0, st) : launch_int8(j, e, bf16, st));
   return MOE_OK;
 }
 

@@ -16,15 +16,26 @@ struct Groups {
   int E, R;
 };
 
+// Expert e's rows: first, end.
+__device__ __forceinline__ int2 group_rows(const Groups& g, int e) {
+  const int lo = min(max(g.offsets[e], 0), g.R);
+  return make_int2(lo, min(max(g.offsets[e + 1], lo), g.R));
+}
+
 // Element types of a grouped product's operands.
 enum GroupedType { GROUPED_F32 = 0, GROUPED_BF16 = 1, GROUPED_INT8 = 2 };
 
 // Rows by their expert's weight: job j of one expert (M unused), whose weights are w_stride elements apart and whose
 // row operands and outputs are those of its rows; j.b_col: the gradient's product, across the weights' rows.
 // table: grouped_table_bytes of scratch.  out_bf16: what an integer product's epilogue writes.
-size_t grouped_table_bytes(GroupedType t, int R, int E, int N, int K, int segs, bool pair, bool b_col);
+size_t grouped_table_bytes(GroupedType t, int R, int E, int N, int K, int segs, bool pair);
 hipError_t launch_grouped(const DenseJob& j, const DenseEpi& e, GroupedType t, bool out_bf16, const Groups& g,
                           int64_t w_stride, void* table, hipStream_t st);
+// Forward products of few rows, whose operands may have rows of any length (codes: whole 16-byte chunks): no
+// table.  g.E == 0: dense rows, j.M of them (integers).
+constexpr int kGroupedDecodeRows = 64, kInt8DecodeRows = 16;
+hipError_t launch_grouped_decode(const DenseJob& j, const DenseEpi& e, GroupedType t, bool out_bf16, const Groups& g,
+                                 int64_t w_stride, hipStream_t st);
 // Weight gradients: for every expert out[z][e] = sum of its rows' A_z x B_z, M x N (j.K unused), zeros without rows.
 hipError_t launch_grouped_dw(const DenseJob& j, const DenseEpi& e, GroupedType t, const Groups& g, hipStream_t st);
 

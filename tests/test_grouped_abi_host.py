@@ -46,7 +46,7 @@ CALL = {f: i for i, f in enumerate(GROUPED)}
 
 
 def shape(call, **kw):
-    a = dict(R=33, K=96, N=80, E=5, act="silu" if call in GATED else "none")
+    a = dict(R=333, K=96, N=80, E=5, act="silu" if call in GATED else "none")
     a.update(kw)
     return B.grouped_shape(**a)
 
@@ -114,6 +114,13 @@ def test_workspaces_are_checked(call):
         assert call(s, ws_bytes=need - 1) == B.MOE_ERR_WORKSPACE
         assert call(s, ws=None) == B.MOE_ERR_WORKSPACE
         assert call(s, ws=at(30) + 8) == B.MOE_ERR_INVALID_ARG
+
+
+def test_few_rows_forward_need_no_workspace():
+    """Decoding steps read weights of any width in place and make no table."""
+    for call in (LF, GF, LI, GI):
+        for s in (shape(call, R=64), shape(call, R=1, K=97, N=83)):
+            assert B.grouped_workspace_bytes(s, CALL[call]) == 0
 
 
 def test_fp32_weight_gradients_keep_terms():
