@@ -9,6 +9,7 @@ import fails.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 from typing import Optional
 
@@ -151,6 +152,7 @@ def _load() -> ctypes.CDLL:
 
 
 lib = _load()
+import torch as _torch  # noqa: E402  (after _load, which says why it is first)
 
 
 def status_string(status: int) -> str:
@@ -336,8 +338,7 @@ def _tensor_types() -> dict:
 def _dense_call(call: str, fn, s, tensors: tuple, stream, ws=(), before: tuple = ()):
     """Check `tensors`, (name, tensor, shape, dtype code) in the call's order, and make the call; ws: () for a
     call that takes no workspace, else (tensor,); before: plain arguments between the tensors and the shape (s None: none)."""
-    import torch
-    types, device, args = _tensor_types(), -1, []
+    types, device, args = _types or _tensor_types(), -1, []
     for name, t, shape, code in tensors:
         if t is None or isinstance(t, int):
             args.append(t)
@@ -359,11 +360,12 @@ def _dense_call(call: str, fn, s, tensors: tuple, stream, ws=(), before: tuple =
             if d < 0 or not t.is_contiguous() or d != device >= 0:
                 _refuse(call, "ws", t, t.shape, None, device)
             args += (t.data_ptr(), t.numel() * t.element_size())
-    if device < 0 or device == torch.cuda.current_device():
-        args.append(_stream(stream) if stream is not None or device < 0 else torch._C._cuda_getCurrentRawStream(device))
+    # the tensors are on a GPU, so torch has initialised it
+    if device < 0 or device == _torch._C._cuda_getDevice():
+        args.append(_stream(stream) if stream is not None or device < 0 else _torch._C._cuda_getCurrentRawStream(device))
         rc = fn(*args)
     else:
-        with torch.cuda.device(device):
+        with _torch.cuda.device(device):
             rc = fn(*args, _stream(stream))
     if rc != MOE_OK:
         raise MoeError(call, rc)
@@ -481,24 +483,18 @@ def combine_backward(dout, y_perm, token_row, topk_w, dy_perm, dtopk_w, out_dtyp
 
 
 def int8_row_bytes(cols: int) -> int:
-    """Length of a row of `cols` codes."""
-    return int(lib.moe_int8_row_bytes(cols))
+    """Length of a row of `cols` codes: moe_int8_row_bytes, in whole 16-byte chunks."""
+    return (cols + 15) // 16 * 16 if 1 <= cols <= 1 << 21 else 0
 
 
 def quantize_int8(src, q, scale, stream=None):
     """Codes q [.., int8_row_bytes(cols)] and scales [..] of the rows of src [.., cols] (bf16 or fp32)."""
-    import torch
-    code = MOE_F32 if src.dtype == torch.float32 else MOE_BF16
-    cols = src.shape[-1] if src.dim() else 0
-    rows = src.numel() // cols if cols else 0
-    lead = tuple(src.shape[:-1])
-    _dense_call("moe_quantize_int8", _quantize(code, rows, cols), None, (
-        ("src", src, tuple(src.shape), code), ("q", q, lead + (int8_row_bytes(cols),), _INT8),
-        ("scale", scale, lead, MOE_F32)), stream)
-
-
-def _quantize(code: int, rows: int, cols: int):
-    return lambda src, q, scale, stream: lib.moe_quantize_int8(src, code, rows, cols, q, scale, stream)
+    code, shape = MOE_F32 if src.dtype == _torch.float32 else MOE_BF16, src.shape
+    *lead, cols = shape if len(shape) else (0,)
+    rows = math.prod(lead)
+    _dense_call("moe_quantize_int8", lambda a, b, c, st: lib.moe_quantize_int8(a, code, rows, cols, b, c, st), None, (
+        ("src", src, shape, code), ("q", q, (*lead, int8_row_bytes(cols)), _INT8), ("scale", scale, tuple(lead), MOE_F32)),
+        stream)
 
 
 def linear_int8_forward(x, x_scale, w, w_scale, bias, residual, y, s: MoeDenseShape, stream=None):

@@ -40,16 +40,16 @@ struct Bytes16 {
 };
 
 // A strip is 16 of an expert's weight rows (with PAIR 8 of each projection).  A workgroup of 8 waves has 8 / SPLIT
-// strips of one expert that has rows; SPLIT waves share a strip's contraction, up to 8 chunks of loads in flight each,
+// strips of one expert that has rows; SPLIT waves share a strip's contraction, U chunks of loads in flight each,
 // and their sums meet in LDS in wave order.  Rows beyond an expert's first 16 meet the same weights again.
 // blockIdx.y: the expert, or, where there are fewer rows than experts, the row that an expert's rows begin with.
-template <typename T, typename O, int KIND, int SPLIT>
+template <typename T, typename O, int KIND, int SPLIT, int U>
 __global__ __launch_bounds__(512) void k_grouped_decode(DenseJob j, DenseEpi e, Groups groups, int64_t w_stride) {
   using C = Bytes16<T>;
   constexpr bool PAIR = KIND == DENSE_GATED, INT8 = sizeof(T) == 1;
   using Acc = std::conditional_t<INT8, i32x4, f32x4>;
   using A = std::conditional_t<INT8, int, float>;
-  constexpr int W = 8, U = 8, ON = PAIR ? 8 : 16, STRIPS = W / SPLIT, WIDE = STRIPS * ON;
+  constexpr int W = 8, ON = PAIR ? 8 : 16, STRIPS = W / SPLIT, WIDE = STRIPS * ON;
   __shared__ A s[W][16][17];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
   int expert = 0, lo = 0, hi = j.M;
@@ -147,12 +147,12 @@ __global__ __launch_bounds__(512) void k_grouped_decode(DenseJob j, DenseEpi e, 
   }
 }
 
-template <typename T, typename O, int SPLIT>
+template <typename T, typename O, int SPLIT, int U = 8>
 static void go(const DenseJob& j, const DenseEpi& e, const Groups& g, int64_t w_stride, int strips, int experts, hipStream_t st) {
   const dim3 grid(ceil_div(strips, 8 / SPLIT), experts);
-  if (j.pair) k_grouped_decode<T, O, DENSE_GATED, SPLIT><<<grid, 512, 0, st>>>(j, e, g, w_stride);
-  else if (e.kind == DENSE_STORE) k_grouped_decode<T, O, DENSE_STORE, SPLIT><<<grid, 512, 0, st>>>(j, e, g, w_stride);
-  else if constexpr (sizeof(T) == 1) k_grouped_decode<T, O, DENSE_LINEAR, SPLIT><<<grid, 512, 0, st>>>(j, e, g, w_stride);
+  if (j.pair) k_grouped_decode<T, O, DENSE_GATED, SPLIT, U><<<grid, 512, 0, st>>>(j, e, g, w_stride);
+  else if (e.kind == DENSE_STORE) k_grouped_decode<T, O, DENSE_STORE, SPLIT, U><<<grid, 512, 0, st>>>(j, e, g, w_stride);
+  else if constexpr (sizeof(T) == 1) k_grouped_decode<T, O, DENSE_LINEAR, SPLIT, U><<<grid, 512, 0, st>>>(j, e, g, w_stride);
 }
 
 // Waves that share a strip: as many as fill the device (4096 waves), while each keeps 4 chunks, half of its loads in
@@ -167,7 +167,8 @@ static void go(const DenseJob& j, const DenseEpi& e, const Groups& g, int64_t w_
   if (split == 1) go<T, O, 1>(j, e, g, w_stride, strips, experts, st);
   else if (split == 2) go<T, O, 2>(j, e, g, w_stride, strips, experts, st);
   else if (split == 4) go<T, O, 4>(j, e, g, w_stride, strips, experts, st);
-  else go<T, O, 8>(j, e, g, w_stride, strips, experts, st);
+  else if (chunks <= 64 || strips * experts > 512) go<T, O, 8>(j, e, g, w_stride, strips, experts, st);
+  else go<T, O, 8, 16>(j, e, g, w_stride, strips, experts, st);
 }
 
 hipError_t launch_grouped_decode(const DenseJob& j, const DenseEpi& e, GroupedType t, bool out_bf16, const Groups& g,

@@ -84,7 +84,7 @@ struct GroupedTile {
 };
 constexpr GroupedTile kTiles[] = {{256, 256, 256, 1.75, 11.5, 1.75, 11.5},
                                   {128, 256, 512, 2.2, 7.0, 1.3, 6.0},
-                                  {64, 64, 512, 0.4, 1.8, 0.19, 2.5}};
+                                  {64, 64, 512, 0.42, 3.0, 0.19, 2.5}};
 
 static double rounds_us(const GroupedTile& c, double items, double steps) {
   if (items <= 256) return steps * c.step_alone + c.fixed_alone;

@@ -79,11 +79,52 @@ __device__ __forceinline__ uint2 codes8(const Int8Scale& s, const float* f) {
   return make_uint2(c[0], c[1]);
 }
 
-// One row per workgroup, eight elements of it per thread at a time; read once for the largest magnitude and once more
-// for the codes.
-template <typename ST>
+// Bound by memory.  A row of up to 16384 elements stays in registers between its largest magnitude and its codes: NV
+// pieces of eight elements per lane of one wave (WAVES 1, four rows a workgroup) or of four.
+template <typename ST, int WAVES, int NV>
 __global__ __launch_bounds__(256) void k_quantize_int8(const ST* __restrict__ src, int64_t rows, int cols, int64_t ld,
                                                        int8_t* __restrict__ q, float* __restrict__ scale) {
+  constexpr int LANES = 64 * WAVES, ROWS = 4 / WAVES;
+  __shared__ uint32_t part[2][4];
+  const int at = threadIdx.x % LANES, n8 = (int)(ld / 8);
+  int turn = 0;
+  for (int64_t r = (int64_t)blockIdx.x * ROWS + threadIdx.x / LANES; r < rows; r += (int64_t)gridDim.x * ROWS, turn ^= 1) {
+    const ST* x = src + r * cols;
+    Raw8<ST> v[NV];
+#pragma unroll
+    for (int h = 0; h < NV; ++h) {
+      const int i = at + h * LANES;
+      v[h].load(x + 8 * min(i, n8 - 1), i < n8 ? cols - 8 * i : 0);
+    }
+    uint32_t most = 0;
+#pragma unroll
+    for (int h = 0; h < NV; ++h)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) most = max(most, magnitude(v[h].get(k)));
+    most = wave_max_u32(most);
+    if constexpr (WAVES > 1) {
+      if ((threadIdx.x & 63) == 0) part[turn][threadIdx.x >> 6] = most;
+      __syncthreads();   // the next row's maxima go to the other four places
+      most = max(max(part[turn][0], part[turn][1]), max(part[turn][2], part[turn][3]));
+    }
+    const Int8Scale s(most);
+    if (at == 0) scale[r] = s.scale;
+#pragma unroll
+    for (int h = 0; h < NV; ++h) {
+      const int i = at + h * LANES;
+      if (i >= n8) continue;
+      float f[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) f[k] = v[h].get(k);
+      reinterpret_cast<uint2*>(q + r * ld)[i] = codes8(s, f);
+    }
+  }
+}
+
+// Longer rows are read twice.
+template <typename ST>
+__global__ __launch_bounds__(256) void k_quantize_int8_long(const ST* __restrict__ src, int64_t rows, int cols, int64_t ld,
+                                                            int8_t* __restrict__ q, float* __restrict__ scale) {
   __shared__ uint32_t part[4];
   const int n8 = (int)(ld / 8);
   for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
@@ -109,11 +150,26 @@ __global__ __launch_bounds__(256) void k_quantize_int8(const ST* __restrict__ sr
   }
 }
 
+template <typename ST>
+static void quantize(const ST* src, int64_t rows, int cols, int64_t ld, int8_t* q, float* scale, hipStream_t st) {
+  const int n8 = (int)(ld / 8);
+  auto go = [&](auto kernel, int per) {
+    const int64_t want = (rows + per - 1) / per;
+    kernel<<<(unsigned)(want < (1 << 20) ? want : 1 << 20), 256, 0, st>>>(src, rows, cols, ld, q, scale);
+  };
+  if (n8 <= 64) go(k_quantize_int8<ST, 1, 1>, 4);
+  else if (n8 <= 128) go(k_quantize_int8<ST, 1, 2>, 4);
+  else if (n8 <= 256) go(k_quantize_int8<ST, 1, 4>, 4);
+  else if (n8 <= 512) go(k_quantize_int8<ST, 4, 2>, 1);
+  else if (n8 <= 1024) go(k_quantize_int8<ST, 4, 4>, 1);
+  else if (n8 <= 2048) go(k_quantize_int8<ST, 4, 8>, 1);
+  else go(k_quantize_int8_long<ST>, 1);
+}
+
 hipError_t launch_quantize_int8(const void* src, bool bf16, int64_t rows, int cols, int64_t ld, int8_t* q, float* scale,
                                 hipStream_t st) {
-  const unsigned grid = (unsigned)(rows < (1 << 20) ? rows : 1 << 20);
-  if (bf16) k_quantize_int8<uint16_t><<<grid, 256, 0, st>>>(static_cast<const uint16_t*>(src), rows, cols, ld, q, scale);
-  else k_quantize_int8<float><<<grid, 256, 0, st>>>(static_cast<const float*>(src), rows, cols, ld, q, scale);
+  if (bf16) quantize(static_cast<const uint16_t*>(src), rows, cols, ld, q, scale, st);
+  else quantize(static_cast<const float*>(src), rows, cols, ld, q, scale, st);
   return hipGetLastError();
 }
 

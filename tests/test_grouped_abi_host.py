@@ -140,8 +140,9 @@ def test_no_rows_launch_nothing_forward():
 
 
 def test_int8_sizes():
-    assert [B.int8_row_bytes(n) for n in (1, 16, 17, 1 << 21)] == [16, 16, 32, 1 << 21]
-    assert [B.int8_row_bytes(n) for n in (0, -5, (1 << 21) + 1)] == [0, 0, 0]
+    for f in (B.int8_row_bytes, L.moe_int8_row_bytes):
+        assert [f(n) for n in (1, 16, 17, 1 << 21)] == [16, 16, 32, 1 << 21]
+        assert [f(n) for n in (0, -5, (1 << 21) + 1)] == [0, 0, 0]
     # the sums of longer contractions would not fit 32 bits
     assert DL(B.dense_shape(2, (1 << 17) + 1, 8)) == B.MOE_ERR_UNSUPPORTED
     assert LI(shape(LI, K=(1 << 17) + 1, N=8)) == B.MOE_ERR_UNSUPPORTED
