@@ -127,36 +127,30 @@ moe_status gradients(const GroupedDims& d, const GroupedWs& w, const void* d0, c
   MOE_TRY(in_rows(d, w, dw0 ? &x : nullptr, dx ? &w0 : nullptr, dx ? &w1 : nullptr, ws, st));
   const GroupedType t = d.bf16 ? GROUPED_BF16 : GROUPED_F32;
   const Groups g{offsets, d.E, d.R};
-  DenseEpi e{};
-  e.kind = DENSE_STORE;
-  e.ldo = d.K;
-  if (dx) {
-    DenseJob j{};
-    j.N = d.K; j.K = d.N;
-    j.segs = d1 ? 2 : 1; j.batch = 1;
-    j.b_col = true;
-    j.A[0][0] = d0; j.A[0][1] = d1; j.lda = w.ldn;
-    j.B[0][0] = w0; j.B[0][1] = w1; j.ldb = w.ldk;
-    e.out_f32 = !d.bf16;
-    e.out[0] = dx;
-    MOE_HIP(launch_grouped(j, e, t, d.bf16, g, (int64_t)d.N * w.ldk, at<void>(ws, w.table), st));
+  GroupedProduct px{}, pw{};
+  DenseJob &jx = px.j, &jw = pw.j;
+  px.e.kind = pw.e.kind = DENSE_STORE;
+  px.e.ldo = pw.e.ldo = d.K;
+  jx.N = d.K; jx.K = d.N;
+  jx.segs = d1 ? 2 : 1; jx.batch = 1;
+  jx.b_col = true;
+  jx.A[0][0] = d0; jx.A[0][1] = d1; jx.lda = w.ldn;
+  jx.B[0][0] = w0; jx.B[0][1] = w1; jx.ldb = w.ldk;
+  px.e.out_f32 = !d.bf16;
+  px.e.out[0] = dx;
+  jw.M = d.N; jw.N = d.K;
+  jw.segs = terms; jw.batch = d1 ? 2 : 1;
+  jw.a_col = jw.b_col = true;
+  for (int q = 0; q < terms; ++q) {
+    jw.A[0][q] = static_cast<const char*>(d0) + q * w.lo * d.es;
+    if (d1) jw.A[1][q] = static_cast<const char*>(d1) + q * w.lo * d.es;
+    jw.B[0][q] = jw.B[1][q] = q ? at<void>(ws, w.finite) : x;
   }
-  if (dw0) {
-    DenseJob j{};
-    j.M = d.N; j.N = d.K;
-    j.segs = terms; j.batch = d1 ? 2 : 1;
-    j.a_col = j.b_col = true;
-    for (int q = 0; q < terms; ++q) {
-      j.A[0][q] = static_cast<const char*>(d0) + q * w.lo * d.es;
-      if (d1) j.A[1][q] = static_cast<const char*>(d1) + q * w.lo * d.es;
-      j.B[0][q] = j.B[1][q] = q ? at<void>(ws, w.finite) : x;
-    }
-    j.lda = w.ldn;
-    j.ldb = w.ldk;
-    e.out_f32 = d.grad_f32;
-    e.out[0] = dw0; e.out[1] = dw1;
-    MOE_HIP(launch_grouped_dw(j, e, t, g, st));
-  }
+  jw.lda = w.ldn;
+  jw.ldb = w.ldk;
+  pw.e.out_f32 = d.grad_f32;
+  pw.e.out[0] = dw0; pw.e.out[1] = dw1;
+  MOE_HIP(launch_grouped_grads(dx ? &px : nullptr, dw0 ? &pw : nullptr, t, g, (int64_t)d.N * w.ldk, at<void>(ws, w.table), st));
   return MOE_OK;
 }
 

@@ -27,17 +27,23 @@ enum GroupedType { GROUPED_F32 = 0, GROUPED_BF16 = 1, GROUPED_INT8 = 2 };
 
 // Rows by their expert's weight: job j of one expert (M unused), whose weights are w_stride elements apart and whose
 // row operands and outputs are those of its rows; j.b_col: the gradient's product, across the weights' rows.
-// table: grouped_table_bytes of scratch.  out_bf16: what an integer product's epilogue writes.
+// scratch: grouped_table_bytes.  out_bf16: what an integer product's epilogue writes.
 size_t grouped_table_bytes(GroupedType t, int R, int E, int N, int K, int segs, bool pair);
 hipError_t launch_grouped(const DenseJob& j, const DenseEpi& e, GroupedType t, bool out_bf16, const Groups& g,
-                          int64_t w_stride, void* table, hipStream_t st);
+                          int64_t w_stride, void* scratch, hipStream_t st);
 // Forward products of few rows, whose operands may have rows of any length (codes: whole 16-byte chunks): no
 // table.  g.E == 0: dense rows, j.M of them (integers).
 constexpr int kGroupedDecodeRows = 64, kInt8DecodeRows = 16;
 hipError_t launch_grouped_decode(const DenseJob& j, const DenseEpi& e, GroupedType t, bool out_bf16, const Groups& g,
                                  int64_t w_stride, hipStream_t st);
-// Weight gradients: for every expert out[z][e] = sum of its rows' A_z x B_z, M x N (j.K unused), zeros without rows.
-hipError_t launch_grouped_dw(const DenseJob& j, const DenseEpi& e, GroupedType t, const Groups& g, hipStream_t st);
+// A backward pass's products, either NULL: dx as launch_grouped's with b_col, and for every expert dw's out[z][e] = sum of its
+// rows' A_z x B_z, M x N (j.K unused), zeros without rows.
+struct GroupedProduct {
+  DenseJob j;
+  DenseEpi e;
+};
+hipError_t launch_grouped_grads(const GroupedProduct* dx, const GroupedProduct* dw, GroupedType t, const Groups& g,
+                                int64_t w_stride, void* scratch, hipStream_t st);
 
 // Integer products of dense rows; row operands of whole 16-byte chunks, zero from the contraction length on.
 hipError_t launch_int8(const DenseJob& j, const DenseEpi& e, bool out_bf16, hipStream_t st);

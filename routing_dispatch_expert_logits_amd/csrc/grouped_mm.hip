@@ -36,16 +36,65 @@ __global__ __launch_bounds__(kTableThreads) void k_group_tiles(Groups g, int bm,
   }
 }
 
+// The same without a table: how many m-tiles there are, and where one of them is.  Each wave sums the tile counts of
+// its lanes' experts.  It costs a workgroup about a microsecond, where the table's launch costs a call 4.6.
+struct TileFinder {
+  const Groups g;
+  int bm, per, before, total;   // a lane's experts, tiles before them, of all
+  __device__ __forceinline__ int tiles(int e) const {
+    if (e >= g.E) return 0;
+    const int2 r = group_rows(g, e);
+    return ceil_div(r.y - r.x, bm);
+  }
+  __device__ __forceinline__ TileFinder(const Groups& groups, int rows) : g(groups), bm(rows) {
+    const int lane = threadIdx.x & 63;
+    per = ceil_div(g.E, 64);
+    int mine = 0;
+    for (int i = 0; i < per; ++i) mine += tiles(lane * per + i);
+    const int upto = wave_inclusive_scan(mine, lane);
+    before = upto - mine;
+    total = __builtin_amdgcn_readlane(upto, 63);
+  }
+  // {first row, rows of the expert from there on, expert} of m-tile t < total.
+  __device__ __forceinline__ int4 at(int t) const {
+    const int lane = threadIdx.x & 63;
+    int4 found = make_int4(0, 0, 0, 0);
+    bool here = false;
+    for (int i = 0, b = before; i < per; ++i) {
+      const int e = lane * per + i, n = tiles(e);
+      if (t >= b && t < b + n) {
+        const int2 r = group_rows(g, e);
+        found = make_int4(r.x + (t - b) * bm, r.y - (r.x + (t - b) * bm), e, 0);
+        here = true;
+      }
+      b += n;
+    }
+    const int who = __builtin_ctzll(__ballot(here));
+    return make_int4(__builtin_amdgcn_readlane(found.x, who), __builtin_amdgcn_readlane(found.y, who),
+                     __builtin_amdgcn_readlane(found.z, who), 0);
+  }
+};
+
+// The tile of workgroup `block`: rows of one expert by columns of its weight.  table: the m-tiles, or NULL.
 template <typename T, typename O, int BM, int BN, int WM, int WN, int S, int SB, int DB, bool B_COL, bool PAIR, int KIND>
-__global__ __launch_bounds__(WM* WN * 64, 2) void k_grouped_mm(DenseJob j, DenseEpi e, const int4* __restrict__ table,
-                                                               int64_t w_stride) {
-  constexpr int STAGE = kMmStage<BM, BN, SB>;
-  __shared__ __attribute__((aligned(1024))) uint16_t s0[STAGE], s1[STAGE], s2[STAGE], s3[S > 3 ? STAGE : 1];
-  const int total = uniform(table[0].x);
-  if (total == 0) return;
-  MmWhere w = mm_where(blockIdx.x, total, ceil_div(j.N, PAIR ? BN / 2 : BN), 1, 1);
-  if (!w.ok) return;
-  const int4 tile = table[1 + w.mt];
+__device__ __forceinline__ void rows_tile(const DenseJob& j, const DenseEpi& e, const Groups& g, const int4* table,
+                                          int64_t w_stride, int block, uint16_t* s0, uint16_t* s1, uint16_t* s2, uint16_t* s3) {
+  const int tn = ceil_div(j.N, PAIR ? BN / 2 : BN);
+  MmWhere w;
+  int4 tile;
+  if (table) {
+    const int total = uniform(table[0].x);
+    if (total == 0) return;
+    w = mm_where(block, total, tn, 1, 1);
+    if (!w.ok) return;
+    tile = table[1 + w.mt];
+  } else {
+    const TileFinder f(g, BM);
+    if (f.total == 0) return;
+    w = mm_where(block, f.total, tn, 1, 1);
+    if (!w.ok) return;
+    tile = f.at(w.mt);
+  }
   const int64_t row = uniform(tile.x), expert = uniform(tile.z);
   w.mt = 0;
   const MmPart at{uniform(tile.y), j.K, row * j.lda, expert * w_stride, row * e.ldo, row, expert * j.N};
@@ -53,11 +102,11 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void k_grouped_mm(DenseJob j, Dense
                                                                            s2, s3);
 }
 
+// The same of the weight gradients: columns of one expert's gradient by columns of its rows.
 template <typename T, int BM, int BN, int WM, int WN, int S, int SB, int DB>
-__global__ __launch_bounds__(WM* WN * 64, 2) void k_grouped_dw(DenseJob j, DenseEpi e, Groups g) {
-  constexpr int STAGE = kMmStage<BM, BN, SB>;
-  __shared__ __attribute__((aligned(1024))) uint16_t s0[STAGE], s1[STAGE], s2[STAGE], s3[S > 3 ? STAGE : 1];
-  MmWhere w = mm_where(blockIdx.x, ceil_div(j.M, BM), ceil_div(j.N, BN), g.E * j.batch, 1);
+__device__ __forceinline__ void dw_tile(const DenseJob& j, const DenseEpi& e, const Groups& g, int block, uint16_t* s0,
+                                        uint16_t* s1, uint16_t* s2, uint16_t* s3) {
+  MmWhere w = mm_where(block, ceil_div(j.M, BM), ceil_div(j.N, BN), g.E * j.batch, 1);
   if (!w.ok) return;
   const int expert = uniform(w.z / j.batch);
   w.z -= expert * j.batch;
@@ -66,6 +115,36 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void k_grouped_dw(DenseJob j, Dense
   const MmPart at{j.M, uniform(r.y - r.x), row * j.lda, row * j.ldb, (int64_t)expert * j.M * e.ldo, 0, 0};
   mm_body<T, T, BM, BN, WM, WN, S, SB, DB, true, true, false, DENSE_STORE>(j, e, MmSlices{nullptr, 1, 1, 0}, w, at, s0, s1,
                                                                            s2, s3);
+}
+
+template <typename T, typename O, int BM, int BN, int WM, int WN, int S, int SB, int DB, bool B_COL, bool PAIR, int KIND>
+__global__ __launch_bounds__(WM* WN * 64, 2) void k_grouped_mm(DenseJob j, DenseEpi e, Groups g,
+                                                               const int4* __restrict__ table, int64_t w_stride) {
+  constexpr int STAGE = kMmStage<BM, BN, SB>;
+  __shared__ __attribute__((aligned(1024))) uint16_t s0[STAGE], s1[STAGE], s2[STAGE], s3[S > 3 ? STAGE : 1];
+  rows_tile<T, O, BM, BN, WM, WN, S, SB, DB, B_COL, PAIR, KIND>(j, e, g, table, w_stride, blockIdx.x, s0, s1, s2, s3);
+}
+
+template <typename T, int BM, int BN, int WM, int WN, int S, int SB, int DB>
+__global__ __launch_bounds__(WM* WN * 64, 2) void k_grouped_dw(DenseJob j, DenseEpi e, Groups g) {
+  constexpr int STAGE = kMmStage<BM, BN, SB>;
+  __shared__ __attribute__((aligned(1024))) uint16_t s0[STAGE], s1[STAGE], s2[STAGE], s3[S > 3 ? STAGE : 1];
+  dw_tile<T, BM, BN, WM, WN, S, SB, DB>(j, e, g, blockIdx.x, s0, s1, s2, s3);
+}
+
+// A backward pass's two products on 64 x 64 tiles in one launch: small ones leave the device half empty on their own.
+// The first `first` workgroups are dx's (dx_first) or the weight gradients', whichever's contraction is longer.
+template <typename T, int S, int DB>
+__global__ __launch_bounds__(256, 2) void k_grouped_two(DenseJob jx, DenseEpi ex, int64_t w_stride, DenseJob jw, DenseEpi ew,
+                                                        int first, bool dx_first, Groups g, const int4* __restrict__ table) {
+  constexpr int STAGE = kMmStage<64, 64, 128>;
+  __shared__ __attribute__((aligned(1024))) uint16_t s0[STAGE], s1[STAGE], s2[STAGE], s3[S > 3 ? STAGE : 1];
+  const bool early = (int)blockIdx.x < first;
+  const int block = early ? blockIdx.x : blockIdx.x - first;
+  if (early == dx_first)
+    rows_tile<T, T, 64, 64, 2, 2, S, 128, DB, true, false, DENSE_STORE>(jx, ex, g, table, w_stride, block, s0, s1, s2, s3);
+  else
+    dw_tile<T, 64, 64, 2, 2, S, 128, DB>(jw, ew, g, block, s0, s1, s2, s3);
 }
 
 // m-tiles of bm rows that R rows of E experts can take at most.
@@ -111,71 +190,111 @@ size_t grouped_table_bytes(GroupedType t, int R, int E, int N, int K, int segs, 
   return 16 * (size_t)(1 + most_tiles(R, E, tile_of(t, R, E, N, K, segs, pair).bm));
 }
 
-template <typename T, typename O, int BM, int BN, int WM, int WN, int S, int SB = 128, int DB = 16>
-static void go(const DenseJob& j, const DenseEpi& e, const int4* t, int64_t tiles, int64_t w_stride, hipStream_t st) {
-  const int64_t items = tiles * ceil_div(j.N, j.pair ? BN / 2 : BN);
-  const dim3 grid((unsigned)((items + 7) / 8 * 8)), block(WM * WN * 64);
-  if (j.pair) k_grouped_mm<T, O, BM, BN, WM, WN, S, SB, DB, false, true, DENSE_GATED><<<grid, block, 0, st>>>(j, e, t, w_stride);
-  else if constexpr (sizeof(T) == 1) k_grouped_mm<T, O, BM, BN, WM, WN, S, SB, DB, false, false, DENSE_STORE><<<grid, block, 0, st>>>(j, e, t, w_stride);
-  else if (j.b_col) k_grouped_mm<T, O, BM, BN, WM, WN, S, SB, DB, true, false, DENSE_STORE><<<grid, block, 0, st>>>(j, e, t, w_stride);
-  else k_grouped_mm<T, O, BM, BN, WM, WN, S, SB, DB, false, false, DENSE_STORE><<<grid, block, 0, st>>>(j, e, t, w_stride);
+static unsigned whole_eights(int64_t items) { return (unsigned)((items + 7) / 8 * 8); }
+
+// The workgroups of a product by rows, and its m-tiles: in the table, unless so few workgroups would read it (two rounds
+// of the device) that each had better look for itself (*table NULL then).
+struct RowsGrid {
+  GroupedTile c;
+  unsigned blocks;
+};
+static hipError_t rows_grid(const DenseJob& j, GroupedType t, const Groups& g, RowsGrid* r, const int4** table, void* scratch,
+                            hipStream_t st) {
+  r->c = tile_of(t, g.R, g.E, j.N, j.K, j.segs, j.pair);
+  const int64_t tiles = most_tiles(g.R, g.E, r->c.bm), items = tiles * ceil_div(j.N, j.pair ? r->c.bn / 2 : r->c.bn);
+  r->blocks = whole_eights(items);
+  *table = nullptr;
+  if (items <= 2 * r->c.at_once) return hipSuccess;
+  *table = static_cast<int4*>(scratch);
+  const int64_t blocks = (tiles + kTableThreads - 1) / kTableThreads;
+  k_group_tiles<<<(unsigned)(blocks < 64 ? blocks : 64), kTableThreads, 0, st>>>(g, r->c.bm, (int)tiles, static_cast<int4*>(scratch));
+  return hipGetLastError();
 }
 
+template <typename T, typename O, int BM, int BN, int WM, int WN, int S, int SB = 128, int DB = 16>
+static void go(const DenseJob& j, const DenseEpi& e, const Groups& g, const int4* t, unsigned grid, int64_t w_stride, hipStream_t st) {
+  const int block = WM * WN * 64;
+  if (j.pair) k_grouped_mm<T, O, BM, BN, WM, WN, S, SB, DB, false, true, DENSE_GATED><<<grid, block, 0, st>>>(j, e, g, t, w_stride);
+  else if constexpr (sizeof(T) == 1) k_grouped_mm<T, O, BM, BN, WM, WN, S, SB, DB, false, false, DENSE_STORE><<<grid, block, 0, st>>>(j, e, g, t, w_stride);
+  else if (j.b_col) k_grouped_mm<T, O, BM, BN, WM, WN, S, SB, DB, true, false, DENSE_STORE><<<grid, block, 0, st>>>(j, e, g, t, w_stride);
+  else k_grouped_mm<T, O, BM, BN, WM, WN, S, SB, DB, false, false, DENSE_STORE><<<grid, block, 0, st>>>(j, e, g, t, w_stride);
+}
 template <typename T, typename O>
-static void go_tile(const GroupedTile& c, const DenseJob& j, const DenseEpi& e, const int4* t, int64_t tiles,
-                    int64_t w_stride, hipStream_t st) {
-  if (c.bm == 256) go<T, O, 256, 256, 2, 4, 4, 64>(j, e, t, tiles, w_stride, st);
-  else if (c.bm == 128) go<T, O, 128, 256, 2, 2, 3, 64>(j, e, t, tiles, w_stride, st);
-  else go<T, O, 64, 64, 2, 2, 4>(j, e, t, tiles, w_stride, st);
+static void go_tile(const DenseJob& j, const DenseEpi& e, const Groups& g, const int4* t, const RowsGrid& r, int64_t w_stride,
+                    hipStream_t st) {
+  if (r.c.bm == 256) go<T, O, 256, 256, 2, 4, 4, 64>(j, e, g, t, r.blocks, w_stride, st);
+  else if (r.c.bm == 128) go<T, O, 128, 256, 2, 2, 3, 64>(j, e, g, t, r.blocks, w_stride, st);
+  else go<T, O, 64, 64, 2, 2, 4>(j, e, g, t, r.blocks, w_stride, st);
 }
 
 static bool whole_chunks(const DenseJob& j) { return j.lda % 4 == 0 && j.ldb % 4 == 0; }
 
 hipError_t launch_grouped(const DenseJob& j, const DenseEpi& e, GroupedType t, bool out_bf16, const Groups& g,
-                          int64_t w_stride, void* table, hipStream_t st) {
-  const GroupedTile c = tile_of(t, g.R, g.E, j.N, j.K, j.segs, j.pair);
-  const int bm = c.bm;
-  const int64_t tiles = most_tiles(g.R, g.E, bm);
-  int4* tab = static_cast<int4*>(table);
-  const int64_t blocks = (tiles + kTableThreads - 1) / kTableThreads;
-  k_group_tiles<<<(unsigned)(blocks < 64 ? blocks : 64), kTableThreads, 0, st>>>(g, bm, (int)tiles, tab);
-  if (hipError_t r = hipGetLastError(); r != hipSuccess) return r;
+                          int64_t w_stride, void* scratch, hipStream_t st) {
+  RowsGrid r;
+  const int4* tab;
+  if (hipError_t s = rows_grid(j, t, g, &r, &tab, scratch, st); s != hipSuccess) return s;
   if (t == GROUPED_F32) {
-    if (whole_chunks(j)) go<float, float, 64, 64, 2, 2, 3>(j, e, tab, tiles, w_stride, st);
-    else go<float, float, 64, 64, 2, 2, 3, 128, 4>(j, e, tab, tiles, w_stride, st);
+    if (whole_chunks(j)) go<float, float, 64, 64, 2, 2, 3>(j, e, g, tab, r.blocks, w_stride, st);
+    else go<float, float, 64, 64, 2, 2, 3, 128, 4>(j, e, g, tab, r.blocks, w_stride, st);
   } else if (t == GROUPED_BF16) {
-    go_tile<uint16_t, uint16_t>(c, j, e, tab, tiles, w_stride, st);
+    go_tile<uint16_t, uint16_t>(j, e, g, tab, r, w_stride, st);
   } else if (out_bf16) {
-    go_tile<int8_t, uint16_t>(c, j, e, tab, tiles, w_stride, st);
+    go_tile<int8_t, uint16_t>(j, e, g, tab, r, w_stride, st);
   } else {
-    go_tile<int8_t, float>(c, j, e, tab, tiles, w_stride, st);
+    go_tile<int8_t, float>(j, e, g, tab, r, w_stride, st);
   }
   return hipGetLastError();
 }
 
-template <typename T, int BM, int BN, int WM, int WN, int S, int SB = 128, int DB = 16>
-static void go_dw(const DenseJob& j, const DenseEpi& e, const Groups& g, hipStream_t st) {
-  const int64_t items = (int64_t)ceil_div(j.M, BM) * ceil_div(j.N, BN) * g.E * j.batch;
-  k_grouped_dw<T, BM, BN, WM, WN, S, SB, DB><<<(unsigned)((items + 7) / 8 * 8), WM * WN * 64, 0, st>>>(j, e, g);
+// Tile of the weight gradients: as many rows for every expert.
+static const GroupedTile& dw_tile_of(const DenseJob& j, GroupedType t, const Groups& g) {
+  if (t == GROUPED_F32) return kTiles[2];
+  const double steps = (g.R / (double)g.E / 64 + 0.5) * j.segs;
+  const GroupedTile* best = nullptr;
+  double least = 0;
+  for (const GroupedTile& c : kTiles) {
+    const double us = rounds_us(c, (double)g.E * j.batch * ceil_div(j.M, c.bm) * ceil_div(j.N, c.bn), steps);
+    if (!best || us < least) best = &c, least = us;
+  }
+  return *best;
+}
+static unsigned dw_blocks(const DenseJob& j, const GroupedTile& c, const Groups& g) {
+  return whole_eights((int64_t)ceil_div(j.M, c.bm) * ceil_div(j.N, c.bn) * g.E * j.batch);
 }
 
-hipError_t launch_grouped_dw(const DenseJob& j, const DenseEpi& e, GroupedType t, const Groups& g, hipStream_t st) {
-  if (t == GROUPED_BF16) {
-    // as many rows for every expert; the epilogue only stores
-    const double steps = (g.R / (double)g.E / 64 + 0.5) * j.segs;
-    int best = 0;
-    double least = 0;
-    for (int i = 0; i < 3; ++i) {
-      const GroupedTile& c = kTiles[i];
-      const double us = rounds_us(c, (double)g.E * j.batch * ceil_div(j.M, c.bm) * ceil_div(j.N, c.bn), steps);
-      if (i == 0 || us < least) best = i, least = us;
-    }
-    if (best == 0) go_dw<uint16_t, 256, 256, 2, 4, 4, 64>(j, e, g, st);
-    else if (best == 1) go_dw<uint16_t, 128, 256, 2, 2, 3, 64>(j, e, g, st);
-    else go_dw<uint16_t, 64, 64, 2, 2, 4>(j, e, g, st);
+static hipError_t launch_dw(const DenseJob& j, const DenseEpi& e, GroupedType t, const Groups& g, const GroupedTile& c, hipStream_t st) {
+  const unsigned grid = dw_blocks(j, c, g);
+  if (t == GROUPED_F32) {
+    if (whole_chunks(j)) k_grouped_dw<float, 64, 64, 2, 2, 3, 128, 16><<<grid, 256, 0, st>>>(j, e, g);
+    else k_grouped_dw<float, 64, 64, 2, 2, 3, 128, 4><<<grid, 256, 0, st>>>(j, e, g);
+  } else if (c.bm == 256) {
+    k_grouped_dw<uint16_t, 256, 256, 2, 4, 4, 64, 16><<<grid, 512, 0, st>>>(j, e, g);
+  } else if (c.bm == 128) {
+    k_grouped_dw<uint16_t, 128, 256, 2, 2, 3, 64, 16><<<grid, 256, 0, st>>>(j, e, g);
+  } else {
+    k_grouped_dw<uint16_t, 64, 64, 2, 2, 4, 128, 16><<<grid, 256, 0, st>>>(j, e, g);
   }
-  else if (whole_chunks(j)) go_dw<float, 64, 64, 2, 2, 3>(j, e, g, st);
-  else go_dw<float, 64, 64, 2, 2, 3, 128, 4>(j, e, g, st);
+  return hipGetLastError();
+}
+
+hipError_t launch_grouped_grads(const GroupedProduct* dx, const GroupedProduct* dw, GroupedType t, const Groups& g,
+                                int64_t w_stride, void* scratch, hipStream_t st) {
+  if (!dw) return launch_grouped(dx->j, dx->e, t, t == GROUPED_BF16, g, w_stride, scratch, st);
+  const GroupedTile& c = dw_tile_of(dw->j, t, g);
+  if (!dx || c.bm != 64 || tile_of(t, g.R, g.E, dx->j.N, dx->j.K, dx->j.segs, false).bm != 64) {
+    if (hipError_t r = launch_dw(dw->j, dw->e, t, g, c, st); r != hipSuccess || !dx) return r;
+    return launch_grouped(dx->j, dx->e, t, t == GROUPED_BF16, g, w_stride, scratch, st);
+  }
+  RowsGrid r;
+  const int4* tab;
+  if (hipError_t s = rows_grid(dx->j, t, g, &r, &tab, scratch, st); s != hipSuccess) return s;
+  const bool dx_first = (int64_t)dx->j.K * dx->j.segs >= (int64_t)g.R / g.E * dw->j.segs;
+  const unsigned blocks = dw_blocks(dw->j, c, g), first = dx_first ? r.blocks : blocks, all = r.blocks + blocks;
+  auto go = [&](auto kernel) { kernel<<<all, 256, 0, st>>>(dx->j, dx->e, w_stride, dw->j, dw->e, (int)first, dx_first, g, tab); };
+  if (t == GROUPED_BF16) go(k_grouped_two<uint16_t, 4, 16>);
+  else if (whole_chunks(dx->j) && whole_chunks(dw->j)) go(k_grouped_two<float, 3, 16>);
+  else go(k_grouped_two<float, 3, 4>);
   return hipGetLastError();
 }
 
