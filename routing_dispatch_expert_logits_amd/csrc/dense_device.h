@@ -120,21 +120,25 @@ __device__ __forceinline__ void load8(const T* p, float* f) {
     }
   }
 }
-template <typename T>
+// PAST: past the caches.
+typedef uint32_t u32x4_of2 __attribute__((ext_vector_type(4), aligned(2)));
+template <bool PAST = false, typename T>
 __device__ __forceinline__ void store8(T* p, const float* f) {
   if constexpr (sizeof(T) == 2) {
     Bytes16of2 b;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       b.v[i] = f32_to_bf16(f[2 * i]) | (static_cast<uint32_t>(f32_to_bf16(f[2 * i + 1])) << 16);
-    *reinterpret_cast<Bytes16of2*>(p) = b;
+    if constexpr (PAST) __builtin_nontemporal_store(u32x4_of2{b.v[0], b.v[1], b.v[2], b.v[3]}, reinterpret_cast<u32x4_of2*>(p));
+    else *reinterpret_cast<Bytes16of2*>(p) = b;
   } else {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       Bytes16of4 b;
 #pragma unroll
       for (int i = 0; i < 4; ++i) b.v[i] = __float_as_uint(f[4 * h + i]);
-      reinterpret_cast<Bytes16of4*>(p)[h] = b;
+      if constexpr (PAST) __builtin_nontemporal_store(u32x4_of2{b.v[0], b.v[1], b.v[2], b.v[3]}, reinterpret_cast<u32x4_of2*>(p) + h);
+      else reinterpret_cast<Bytes16of4*>(p)[h] = b;
     }
   }
 }
@@ -145,9 +149,9 @@ __device__ __forceinline__ void load8(const T* p, int n, float* f) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) f[i] = i < n ? load1(p + i) : 0.f;
 }
-template <typename T>
+template <bool PAST = false, typename T>
 __device__ __forceinline__ void store8(T* p, int n, const float* f) {
-  if (n >= 8) return store8(p, f);
+  if (n >= 8) return store8<PAST>(p, f);
 #pragma unroll
   for (int i = 0; i < 8; ++i)
     if (i < n) store1(p + i, f[i]);

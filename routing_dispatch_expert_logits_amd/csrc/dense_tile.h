@@ -114,9 +114,9 @@ struct MmTile {
 };
 
 // Eight neighbouring output columns n .. n + 7 of row m (the first `left` of them), from the
-// fp32 sums; rows of odd widths are stored at element alignment.  ACT: the activation; bias and
+// fp32 sums; rows of odd widths are stored at element alignment.  ACT: the activation; PAST: past the caches; bias and
 // res: the bias' and the residual's eight, where there are such; o: the first element of row 0.
-template <typename T, int KIND, int ACT>
+template <typename T, int KIND, int ACT, bool PAST = false>
 __device__ __forceinline__ void mm_out8(const DenseEpi& e, int z, int64_t o, int m, int n, int N, float* a,
                                         const float* b, const Raw8<T>& bias, const Raw8<T>& res) {
   constexpr bool FAST = sizeof(T) == 2;
@@ -124,25 +124,25 @@ __device__ __forceinline__ void mm_out8(const DenseEpi& e, int z, int64_t o, int
   const int left = N - n;
   float y[8];
   if constexpr (KIND == DENSE_STORE) {
-    if (e.out_f32) store8(static_cast<float*>(e.out[z]) + idx, left, a);
-    else store8(static_cast<T*>(e.out[z]) + idx, left, a);
+    if (e.out_f32) store8<PAST>(static_cast<float*>(e.out[z]) + idx, left, a);
+    else store8<PAST>(static_cast<T*>(e.out[z]) + idx, left, a);
   } else if constexpr (KIND == DENSE_LINEAR) {
     if (e.bias) {
       for (int i = 0; i < 8; ++i) a[i] += bias.get(i);
     }
-    if (e.save[0]) store8(static_cast<T*>(e.save[0]) + idx, left, a);
+    if (e.save[0]) store8<PAST>(static_cast<T*>(e.save[0]) + idx, left, a);
     for (int i = 0; i < 8; ++i) a[i] = act_value<FAST>(a[i], ACT);
     if (e.residual) {
       for (int i = 0; i < 8; ++i) a[i] += res.get(i);
     }
-    store8(static_cast<T*>(e.out[0]) + idx, left, a);
+    store8<PAST>(static_cast<T*>(e.out[0]) + idx, left, a);
   } else {
     if (e.save[0]) {
-      store8(static_cast<T*>(e.save[0]) + idx, left, a);
-      store8(static_cast<T*>(e.save[1]) + idx, left, b);
+      store8<PAST>(static_cast<T*>(e.save[0]) + idx, left, a);
+      store8<PAST>(static_cast<T*>(e.save[1]) + idx, left, b);
     }
     for (int i = 0; i < 8; ++i) y[i] = act_value<FAST>(a[i], ACT) * b[i];
-    store8(static_cast<T*>(e.out[0]) + idx, left, y);
+    store8<PAST>(static_cast<T*>(e.out[0]) + idx, left, y);
   }
 }
 
@@ -236,10 +236,12 @@ constexpr int mm_passes(int stage, int S, int tile, int W) {
 template <int BM, int BN, int SB>
 constexpr int kMmStage = (BM + BN) * SB / 2;  // 16-bit words of a stage
 //
-// T: the operands' type; O: that of what the epilogue reads and writes.  EDGE: a wave with no row of the
-// product does not multiply (rows in groups of any number end inside most tiles).
+// T: the operands' type; O: that of what the epilogue reads and writes.  GROUPED: a wave with no row of the
+// product does not multiply (rows in groups of any number end inside most tiles), and outputs are written past the
+// caches, where the operands that other tiles read again stay (32768 rows of 128 experts, 2048 -> 768, both products of
+// a gated backward pass: 728 -> 708 us).  STREAM: so are B's loads, for weights that one tile reads.
 template <typename T, typename O, int BM, int BN, int WM, int WN, int S, int SB, int DB, bool A_COL, bool B_COL, bool PAIR,
-          int KIND, bool EDGE = false>
+          int KIND, bool GROUPED = false, bool STREAM = false>
 __device__ __forceinline__ void mm_body(const DenseJob& j, const DenseEpi& e, const MmSlices& sl, const MmWhere& w,
                                         const MmPart& at, uint16_t* s0, uint16_t* s1, uint16_t* s2, uint16_t* s3) {
   using TA = MmTile<T, BM, A_COL, SB, DB>;
@@ -289,7 +291,7 @@ __device__ __forceinline__ void mm_body(const DenseJob& j, const DenseEpi& e, co
     na -= n * SB;
     nb -= n * SB;
   };
-  // The next step's loads.  Past the last step they are issued all the same with an empty
+  // The next step's loads (cache policy 2: not to be kept).  Past the last step they are issued all the same with an empty
   // buffer (zeros, no memory read), so that the count of loads in flight is the same at every
   // wait, which the compiler's own waits need too.
   int filled = 0;
@@ -308,7 +310,10 @@ __device__ __forceinline__ void mm_body(const DenseJob& j, const DenseEpi& e, co
       for (int q = 0; q < Q; ++q) {
         const uint32_t off = col || TA::element(q0 + q, lane) < rows ? v[q] : kOutOfRange;
         const lds_dst to = (lds_dst)(st + (dst + (q0 + q) * 32 * DB));
-        if constexpr (DB == 16) __builtin_amdgcn_raw_ptr_buffer_load_lds(r, to, 16, off, 0, 0, 0);
+        if constexpr (DB == 16) {
+          if (STREAM && dst) __builtin_amdgcn_raw_ptr_buffer_load_lds(r, to, 16, off, 0, 0, 2);
+          else __builtin_amdgcn_raw_ptr_buffer_load_lds(r, to, 16, off, 0, 0, 0);
+        }
         else __builtin_amdgcn_raw_ptr_buffer_load_lds(r, to, 4, off, 0, 0, 0);
       }
     };
@@ -317,7 +322,7 @@ __device__ __forceinline__ void mm_body(const DenseJob& j, const DenseEpi& e, co
     advance(1);
   };
 
-  const bool some = !EDGE || at.M - m0 > wm * TM;   // this wave has rows
+  const bool some = !GROUPED || at.M - m0 > wm * TM;   // this wave has rows
   Acc acc[FM][FN];
 #pragma unroll
   for (int a = 0; a < FM; ++a)
@@ -328,7 +333,7 @@ __device__ __forceinline__ void mm_body(const DenseJob& j, const DenseEpi& e, co
     else return __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(b), as_bf16x8(a), c, 0, 0, 0);
   };
   auto multiply = [&](const uint16_t* st) __attribute__((always_inline)) {
-    if (EDGE && !some) return;
+    if (GROUPED && !some) return;
 #pragma unroll
     for (int h = 0; h < SB / 64; ++h) {
       u32x4 fb[FN];
@@ -536,7 +541,7 @@ __device__ __forceinline__ void mm_body(const DenseJob& j, const DenseEpi& e, co
             if (m >= at.M || n >= j.N || (RPI > PM && r >= PM)) continue;
             f32x4 v[2] = {chunk(r, 2 * lc), chunk(r, 2 * lc + 1)}, u[2] = {v[0], v[1]};
             if (PAIR) u[0] = chunk(r, CH / 2 + 2 * lc), u[1] = chunk(r, CH / 2 + 2 * lc + 1);
-            mm_out8<O, KIND, act()>(e, z, at.o, m, n, j.N, reinterpret_cast<float*>(v), reinterpret_cast<const float*>(u),
+            mm_out8<O, KIND, act(), GROUPED>(e, z, at.o, m, n, j.N, reinterpret_cast<float*>(v), reinterpret_cast<const float*>(u),
                                     bias, res[p][i]);
           }
         }

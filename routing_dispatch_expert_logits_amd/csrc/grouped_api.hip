@@ -61,7 +61,7 @@ GroupedWs grouped_ws(const GroupedDims& d, bool gated, bool backward, bool int8)
   const GroupedType t = int8 ? GROUPED_INT8 : d.bf16 ? GROUPED_BF16 : GROUPED_F32;
   w.ldk = int8 ? code_bytes(d.K) : padded(d.bf16, d.K);
   w.ldn = padded(d.bf16, d.N);
-  const bool decode = !backward && d.R <= kGroupedDecodeRows;
+  const bool decode = !backward && d.R <= kDecodeRows;
   if (decode && !int8) w.ldk = d.K;  // its kernel takes rows of any length
   const bool pad_k = !int8 && w.ldk != d.K;
   w.x = c.take(pad_k ? (size_t)d.R * w.ldk * d.es : 0);
@@ -75,8 +75,8 @@ GroupedWs grouped_ws(const GroupedDims& d, bool gated, bool backward, bool int8)
     w.finite = c.take(w.terms > 1 ? (size_t)d.R * w.ldk * d.es : 0);
   }
   w.table = c.take(d.R == 0 || decode ? 0
-                   : backward ? grouped_table_bytes(t, d.R, d.E, d.K, d.N, gated ? 2 : 1, false)
-                              : grouped_table_bytes(t, d.R, d.E, d.N, d.K, 1, gated));
+                   : backward ? grouped_table_bytes(t, d.R, d.E, d.K, d.N, gated ? 2 : 1, false, true)
+                              : grouped_table_bytes(t, d.R, d.E, d.N, d.K, 1, gated, false));
   w.total = c.cur;
   return w;
 }
@@ -115,7 +115,7 @@ moe_status forward(const GroupedDims& d, const GroupedWs& w, GroupedType t, cons
   e.out_f32 = !d.bf16;
   const Groups g{offsets, d.E, d.R};
   const int64_t w_stride = (int64_t)d.N * w.ldk;
-  MOE_HIP(d.R <= kGroupedDecodeRows ? launch_grouped_decode(j, e, t, d.bf16, g, w_stride, st)
+  MOE_HIP(d.R <= kDecodeRows ? launch_grouped_decode(j, e, t, d.bf16, g, w_stride, st)
                                     : launch_grouped(j, e, t, d.bf16, g, w_stride, at<void>(ws, w.table), st));
   return MOE_OK;
 }
@@ -334,7 +334,7 @@ static moe_status int8_forward(const int8_t* x, const float* x_scale, const int8
   e.row_scale = x_scale; e.col_scale[0] = w0_scale; e.col_scale[1] = w1_scale;
   const hipStream_t st = (hipStream_t)stream;
   const bool bf16 = s->dtype == MOE_BF16;
-  MOE_HIP(T <= (size_t)kInt8DecodeRows ? launch_grouped_decode(j, e, GROUPED_INT8, bf16, Groups{}, 0, st) : launch_int8(j, e, bf16, st));
+  MOE_HIP(T <= (size_t)kDecodeRows ? launch_grouped_decode(j, e, GROUPED_INT8, bf16, Groups{}, 0, st) : launch_int8(j, e, bf16, st));
   return MOE_OK;
 }
 

@@ -19,15 +19,8 @@ struct Bytes16 {
   __device__ __forceinline__ void load(const T* p, int n) {
     v = u32x4{0, 0, 0, 0};
     if (sizeof(T) == 1 ? n > 0 : n >= PER) {
-      if constexpr (sizeof(T) == 1) {
-        v = *reinterpret_cast<const u32x4*>(p);
-      } else if constexpr (sizeof(T) == 2) {
-        const Bytes16of2 b = *reinterpret_cast<const Bytes16of2*>(p);
-        v = u32x4{b.v[0], b.v[1], b.v[2], b.v[3]};
-      } else {
-        const Bytes16of4 b = *reinterpret_cast<const Bytes16of4*>(p);
-        v = u32x4{b.v[0], b.v[1], b.v[2], b.v[3]};
-      }
+      using Vec = std::conditional_t<sizeof(T) == 1, u32x4, u32x4_of2>;
+      v = *reinterpret_cast<const Vec*>(p);
       return;
     }
 #pragma unroll

@@ -28,12 +28,11 @@ enum GroupedType { GROUPED_F32 = 0, GROUPED_BF16 = 1, GROUPED_INT8 = 2 };
 // Rows by their expert's weight: job j of one expert (M unused), whose weights are w_stride elements apart and whose
 // row operands and outputs are those of its rows; j.b_col: the gradient's product, across the weights' rows.
 // scratch: grouped_table_bytes.  out_bf16: what an integer product's epilogue writes.
-size_t grouped_table_bytes(GroupedType t, int R, int E, int N, int K, int segs, bool pair);
+size_t grouped_table_bytes(GroupedType t, int R, int E, int N, int K, int segs, bool pair, bool b_col);
 hipError_t launch_grouped(const DenseJob& j, const DenseEpi& e, GroupedType t, bool out_bf16, const Groups& g,
                           int64_t w_stride, void* scratch, hipStream_t st);
-// Forward products of few rows, whose operands may have rows of any length (codes: whole 16-byte chunks): no
-// table.  g.E == 0: dense rows, j.M of them (integers).
-constexpr int kGroupedDecodeRows = 64, kInt8DecodeRows = 16;
+// Forward products of at most kDecodeRows rows, whose operands may have rows of any length (codes: whole 16-byte
+// chunks): no table.  (32 rows of 8 experts, 2048 -> 768 gated: 13.0 us, 12.1 by launch_grouped; 64 of 54 of 128: 87.9 and 76.2.)  g.E == 0: dense rows, j.M of them (integers).
 hipError_t launch_grouped_decode(const DenseJob& j, const DenseEpi& e, GroupedType t, bool out_bf16, const Groups& g,
                                  int64_t w_stride, hipStream_t st);
 // A backward pass's products, either NULL: dx as launch_grouped's with b_col, and for every expert dw's out[z][e] = sum of its

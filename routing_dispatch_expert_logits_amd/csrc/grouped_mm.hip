@@ -76,7 +76,8 @@ struct TileFinder {
 };
 
 // The tile of workgroup `block`: rows of one expert by columns of its weight.  table: the m-tiles, or NULL.
-template <typename T, typename O, int BM, int BN, int WM, int WN, int S, int SB, int DB, bool B_COL, bool PAIR, int KIND>
+template <typename T, typename O, int BM, int BN, int WM, int WN, int S, int SB, int DB, bool B_COL, bool PAIR, int KIND,
+          bool STREAM>
 __device__ __forceinline__ void rows_tile(const DenseJob& j, const DenseEpi& e, const Groups& g, const int4* table,
                                           int64_t w_stride, int block, uint16_t* s0, uint16_t* s1, uint16_t* s2, uint16_t* s3) {
   const int tn = ceil_div(j.N, PAIR ? BN / 2 : BN);
@@ -98,7 +99,7 @@ __device__ __forceinline__ void rows_tile(const DenseJob& j, const DenseEpi& e, 
   const int64_t row = uniform(tile.x), expert = uniform(tile.z);
   w.mt = 0;
   const MmPart at{uniform(tile.y), j.K, row * j.lda, expert * w_stride, row * e.ldo, row, expert * j.N};
-  mm_body<T, O, BM, BN, WM, WN, S, SB, DB, false, B_COL, PAIR, KIND, true>(j, e, MmSlices{nullptr, 1, 1, 0}, w, at, s0, s1,
+  mm_body<T, O, BM, BN, WM, WN, S, SB, DB, false, B_COL, PAIR, KIND, true, STREAM>(j, e, MmSlices{nullptr, 1, 1, 0}, w, at, s0, s1,
                                                                            s2, s3);
 }
 
@@ -113,16 +114,17 @@ __device__ __forceinline__ void dw_tile(const DenseJob& j, const DenseEpi& e, co
   const int2 r = group_rows(g, expert);
   const int64_t row = uniform(r.x);
   const MmPart at{j.M, uniform(r.y - r.x), row * j.lda, row * j.ldb, (int64_t)expert * j.M * e.ldo, 0, 0};
-  mm_body<T, T, BM, BN, WM, WN, S, SB, DB, true, true, false, DENSE_STORE>(j, e, MmSlices{nullptr, 1, 1, 0}, w, at, s0, s1,
+  mm_body<T, T, BM, BN, WM, WN, S, SB, DB, true, true, false, DENSE_STORE, true>(j, e, MmSlices{nullptr, 1, 1, 0}, w, at, s0, s1,
                                                                            s2, s3);
 }
 
-template <typename T, typename O, int BM, int BN, int WM, int WN, int S, int SB, int DB, bool B_COL, bool PAIR, int KIND>
+template <typename T, typename O, int BM, int BN, int WM, int WN, int S, int SB, int DB, bool B_COL, bool PAIR, int KIND,
+          bool STREAM>
 __global__ __launch_bounds__(WM* WN * 64, 2) void k_grouped_mm(DenseJob j, DenseEpi e, Groups g,
                                                                const int4* __restrict__ table, int64_t w_stride) {
   constexpr int STAGE = kMmStage<BM, BN, SB>;
   __shared__ __attribute__((aligned(1024))) uint16_t s0[STAGE], s1[STAGE], s2[STAGE], s3[S > 3 ? STAGE : 1];
-  rows_tile<T, O, BM, BN, WM, WN, S, SB, DB, B_COL, PAIR, KIND>(j, e, g, table, w_stride, blockIdx.x, s0, s1, s2, s3);
+  rows_tile<T, O, BM, BN, WM, WN, S, SB, DB, B_COL, PAIR, KIND, STREAM>(j, e, g, table, w_stride, blockIdx.x, s0, s1, s2, s3);
 }
 
 template <typename T, int BM, int BN, int WM, int WN, int S, int SB, int DB>
@@ -142,7 +144,7 @@ __global__ __launch_bounds__(256, 2) void k_grouped_two(DenseJob jx, DenseEpi ex
   const bool early = (int)blockIdx.x < first;
   const int block = early ? blockIdx.x : blockIdx.x - first;
   if (early == dx_first)
-    rows_tile<T, T, 64, 64, 2, 2, S, 128, DB, true, false, DENSE_STORE>(jx, ex, g, table, w_stride, block, s0, s1, s2, s3);
+    rows_tile<T, T, 64, 64, 2, 2, S, 128, DB, true, false, DENSE_STORE, false>(jx, ex, g, table, w_stride, block, s0, s1, s2, s3);
   else
     dw_tile<T, 64, 64, 2, 2, S, 128, DB>(jw, ew, g, block, s0, s1, s2, s3);
 }
@@ -165,6 +167,11 @@ constexpr GroupedTile kTiles[] = {{256, 256, 256, 1.75, 11.5, 1.75, 11.5},
                                   {128, 256, 512, 2.2, 7.0, 1.3, 6.0},
                                   {64, 64, 512, 0.42, 3.0, 0.19, 2.5}};
 
+// Rows so few that an expert's mostly fit one tile: each weight is read once, in whole lines, and past the caches (2048
+// rows of 896 experts, 1024 -> 4096: 1191 us, 1299 on 64 x 64, which kept them; in integers 640, 763 and on 128 x 256 685).
+constexpr GroupedTile kStreamTile = {64, 128, 512, 0, 0, 0, 0};
+constexpr int kStreamRows = 16;   // an expert's, on average
+
 static double rounds_us(const GroupedTile& c, double items, double steps) {
   if (items <= 256) return steps * c.step_alone + c.fixed_alone;
   const double rounds = items / c.at_once;
@@ -172,8 +179,9 @@ static double rounds_us(const GroupedTile& c, double items, double steps) {
 }
 
 // R rows of E experts by their N columns: half a tile's rows are empty in an expert's last one, on average.
-static GroupedTile tile_of(GroupedType t, int R, int E, int N, int K, int segs, bool pair) {
+static GroupedTile tile_of(GroupedType t, int R, int E, int N, int K, int segs, bool pair, bool b_col) {
   if (t == GROUPED_F32) return kTiles[2];
+  if (!b_col && R <= (int64_t)kStreamRows * E && (int64_t)(R < E ? R : E) * ceil_div(N, pair ? 64 : 128) >= 512) return kStreamTile;
   const double experts = R < E ? R : E, steps = ceil_div(K, t == GROUPED_INT8 ? 128 : 64) * segs;
   const GroupedTile* best = nullptr;
   double least = 0;
@@ -186,8 +194,8 @@ static GroupedTile tile_of(GroupedType t, int R, int E, int N, int K, int segs, 
   return *best;
 }
 
-size_t grouped_table_bytes(GroupedType t, int R, int E, int N, int K, int segs, bool pair) {
-  return 16 * (size_t)(1 + most_tiles(R, E, tile_of(t, R, E, N, K, segs, pair).bm));
+size_t grouped_table_bytes(GroupedType t, int R, int E, int N, int K, int segs, bool pair, bool b_col) {
+  return 16 * (size_t)(1 + most_tiles(R, E, tile_of(t, R, E, N, K, segs, pair, b_col).bm));
 }
 
 static unsigned whole_eights(int64_t items) { return (unsigned)((items + 7) / 8 * 8); }
@@ -200,7 +208,7 @@ struct RowsGrid {
 };
 static hipError_t rows_grid(const DenseJob& j, GroupedType t, const Groups& g, RowsGrid* r, const int4** table, void* scratch,
                             hipStream_t st) {
-  r->c = tile_of(t, g.R, g.E, j.N, j.K, j.segs, j.pair);
+  r->c = tile_of(t, g.R, g.E, j.N, j.K, j.segs, j.pair, j.b_col);
   const int64_t tiles = most_tiles(g.R, g.E, r->c.bm), items = tiles * ceil_div(j.N, j.pair ? r->c.bn / 2 : r->c.bn);
   r->blocks = whole_eights(items);
   *table = nullptr;
@@ -211,19 +219,20 @@ static hipError_t rows_grid(const DenseJob& j, GroupedType t, const Groups& g, R
   return hipGetLastError();
 }
 
-template <typename T, typename O, int BM, int BN, int WM, int WN, int S, int SB = 128, int DB = 16>
+template <typename T, typename O, int BM, int BN, int WM, int WN, int S, int SB = 128, int DB = 16, bool STREAM = false>
 static void go(const DenseJob& j, const DenseEpi& e, const Groups& g, const int4* t, unsigned grid, int64_t w_stride, hipStream_t st) {
   const int block = WM * WN * 64;
-  if (j.pair) k_grouped_mm<T, O, BM, BN, WM, WN, S, SB, DB, false, true, DENSE_GATED><<<grid, block, 0, st>>>(j, e, g, t, w_stride);
-  else if constexpr (sizeof(T) == 1) k_grouped_mm<T, O, BM, BN, WM, WN, S, SB, DB, false, false, DENSE_STORE><<<grid, block, 0, st>>>(j, e, g, t, w_stride);
-  else if (j.b_col) k_grouped_mm<T, O, BM, BN, WM, WN, S, SB, DB, true, false, DENSE_STORE><<<grid, block, 0, st>>>(j, e, g, t, w_stride);
-  else k_grouped_mm<T, O, BM, BN, WM, WN, S, SB, DB, false, false, DENSE_STORE><<<grid, block, 0, st>>>(j, e, g, t, w_stride);
+  if (j.pair) k_grouped_mm<T, O, BM, BN, WM, WN, S, SB, DB, false, true, DENSE_GATED, STREAM><<<grid, block, 0, st>>>(j, e, g, t, w_stride);
+  else if constexpr (sizeof(T) == 1) k_grouped_mm<T, O, BM, BN, WM, WN, S, SB, DB, false, false, DENSE_STORE, STREAM><<<grid, block, 0, st>>>(j, e, g, t, w_stride);
+  else if (!STREAM && j.b_col) k_grouped_mm<T, O, BM, BN, WM, WN, S, SB, DB, !STREAM, false, DENSE_STORE, STREAM><<<grid, block, 0, st>>>(j, e, g, t, w_stride);
+  else k_grouped_mm<T, O, BM, BN, WM, WN, S, SB, DB, false, false, DENSE_STORE, STREAM><<<grid, block, 0, st>>>(j, e, g, t, w_stride);
 }
 template <typename T, typename O>
 static void go_tile(const DenseJob& j, const DenseEpi& e, const Groups& g, const int4* t, const RowsGrid& r, int64_t w_stride,
                     hipStream_t st) {
   if (r.c.bm == 256) go<T, O, 256, 256, 2, 4, 4, 64>(j, e, g, t, r.blocks, w_stride, st);
   else if (r.c.bm == 128) go<T, O, 128, 256, 2, 2, 3, 64>(j, e, g, t, r.blocks, w_stride, st);
+  else if (r.c.bn == kStreamTile.bn) go<T, O, 64, 128, 1, 4, 3, 128, 16, true>(j, e, g, t, r.blocks, w_stride, st);
   else go<T, O, 64, 64, 2, 2, 4>(j, e, g, t, r.blocks, w_stride, st);
 }
 
@@ -282,7 +291,7 @@ hipError_t launch_grouped_grads(const GroupedProduct* dx, const GroupedProduct* 
                                 int64_t w_stride, void* scratch, hipStream_t st) {
   if (!dw) return launch_grouped(dx->j, dx->e, t, t == GROUPED_BF16, g, w_stride, scratch, st);
   const GroupedTile& c = dw_tile_of(dw->j, t, g);
-  if (!dx || c.bm != 64 || tile_of(t, g.R, g.E, dx->j.N, dx->j.K, dx->j.segs, false).bm != 64) {
+  if (!dx || c.bm != 64 || tile_of(t, g.R, g.E, dx->j.N, dx->j.K, dx->j.segs, false, true).bm != 64) {
     if (hipError_t r = launch_dw(dw->j, dw->e, t, g, c, st); r != hipSuccess || !dx) return r;
     return launch_grouped(dx->j, dx->e, t, t == GROUPED_BF16, g, w_stride, scratch, st);
   }

@@ -119,7 +119,7 @@ def test_workspaces_are_checked(call):
 def test_few_rows_forward_need_no_workspace():
     """Decoding steps read weights of any width in place and make no table."""
     for call in (LF, GF, LI, GI):
-        for s in (shape(call, R=64), shape(call, R=1, K=97, N=83)):
+        for s in (shape(call, R=16), shape(call, R=1, K=97, N=83)):
             assert B.grouped_workspace_bytes(s, CALL[call]) == 0
 
 
