@@ -473,6 +473,8 @@ def combine_backward(dout, y_perm, token_row, topk_w, dy_perm, dtopk_w, out_dtyp
     """Gradients of combine: dy_perm (dtype) of the expert rows and dtopk_w (fp32) of the routing weights, either
     None; dout of type out_dtype."""
     T, D, k, dt = s.T, s.L or s.H, s.k, s.dtype
+    if out_dtype not in (MOE_F32, MOE_BF16):
+        raise MoeError("moe_combine_backward (out_dtype)", MOE_ERR_INVALID_ARG)
     _dense_call("moe_combine_backward", lib.moe_combine_backward, s, (
         ("dout", dout, (T, D), int(out_dtype)), ("y_perm", y_perm, (T * k, D), dt), ("token_row", token_row, (T, k), _INT32),
         ("topk_w", topk_w, (T, k), MOE_F32), ("dy_perm", dy_perm, (T * k, D), dt), ("dtopk_w", dtopk_w, (T, k), MOE_F32)),

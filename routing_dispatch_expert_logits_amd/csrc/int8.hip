@@ -15,7 +15,7 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void k_int8_mm(DenseJob j, DenseEpi
   constexpr int STAGE = kMmStage<BM, BN, SB>;
   __shared__ __attribute__((aligned(1024))) uint16_t s0[STAGE], s1[STAGE], s2[STAGE], s3[S > 3 ? STAGE : 1];
   const MmWhere w = mm_where(blockIdx.x, ceil_div(j.M, BM), ceil_div(j.N, PAIR ? BN / 2 : BN), 1, 1);
-  mm_body<int8_t, O, BM, BN, WM, WN, S, SB, 16, false, false, PAIR, KIND>(
+  mm_body<int8_t, O, BM, BN, WM, WN, S, SB, 16, false, false, PAIR, KIND, true>(
       j, e, MmSlices{nullptr, 1, 1, 0}, w, MmPart{j.M, j.K, 0, 0, 0, 0, 0}, s0, s1, s2, s3);
 }
 
@@ -27,13 +27,29 @@ static void go(const DenseJob& j, const DenseEpi& e, hipStream_t st) {
   else k_int8_mm<O, BM, BN, WM, WN, S, SB, false, DENSE_LINEAR><<<grid, block, 0, st>>>(j, e);
 }
 
+// Tile by estimated time, from what a kernel takes per round of `at_once` workgroups: us per contraction step of 128
+// bytes and besides, measured (MI355X).  8192 x 8192 x 8192 / 8192 x 2048 x 7168 with a residual / 2048 x 4096 x 4096 /
+// 512 x 4096 x 4096 take 453 / 157 / 52 / 47 us on 256 x 256 (2.43 POP/s; the library's largest is 2.13), 532 / 177 / 39 / 33 on
+// 256 x 128, 812 / 272 / 58 / 17 on 64 x 64.
+struct Int8Tile {
+  int bm, bn, at_once;
+  double step, fixed;
+};
+constexpr Int8Tile kInt8Tiles[] = {{256, 256, 256, 1.7, 10.0}, {256, 128, 256, 1.0, 6.0}, {64, 64, 512, 0.42, 3.0}};
+
 hipError_t launch_int8(const DenseJob& j, const DenseEpi& e, bool out_bf16, hipStream_t st) {
-  // Two workgroups of 128 x 256 on a CU while their tiles make a round of it, else 64 x 64 (8192 x 2048 x 7168 with bias
-  // and residual: 175 us, 236 on 64 x 64; 17 x 7168 x 2048: ).
-  const bool large = (int64_t)ceil_div(j.M, 128) * ceil_div(j.N, j.pair ? 128 : 256) >= 128;
+  int best = 0;
+  double least = 0;
+  for (int i = 0; i < 3; ++i) {
+    const Int8Tile& c = kInt8Tiles[i];
+    const int64_t items = (int64_t)ceil_div(j.M, c.bm) * ceil_div(j.N, j.pair ? c.bn / 2 : c.bn);
+    const double us = (double)((items + c.at_once - 1) / c.at_once) * (ceil_div(j.K, 128) * c.step + c.fixed);
+    if (i == 0 || us < least) best = i, least = us;
+  }
   auto by_type = [&](auto* t) {
     using O = std::remove_pointer_t<decltype(t)>;
-    if (large) go<O, 128, 256, 2, 2, 3, 64>(j, e, st);
+    if (best == 0) go<O, 256, 256, 2, 4, 4, 64>(j, e, st);
+    else if (best == 1) go<O, 256, 128, 4, 2, 3>(j, e, st);
     else go<O, 64, 64, 2, 2, 4>(j, e, st);
   };
   if (out_bf16) by_type(static_cast<uint16_t*>(nullptr));
