@@ -162,20 +162,21 @@ static int64_t most_tiles(int R, int E, int bm) { return R / bm + (R < E ? R : E
 struct GroupedTile {
   int bm, bn, at_once;
   double step, fixed, step_alone, fixed_alone;
+  double fixed_dw;   // besides, where no residual and no activation is met and no tile is looked up: weight gradients
 };
-constexpr GroupedTile kTiles[] = {{256, 256, 256, 1.75, 11.5, 1.75, 11.5},
-                                  {128, 256, 512, 2.2, 7.0, 1.3, 6.0},
-                                  {64, 64, 512, 0.42, 3.0, 0.19, 2.5}};
+constexpr GroupedTile kTiles[] = {{256, 256, 256, 1.75, 11.5, 1.75, 11.5, 5.6},
+                                  {128, 256, 512, 2.2, 7.0, 1.3, 6.0, 5.0},
+                                  {64, 64, 512, 0.42, 3.0, 0.19, 2.5, 3.0}};
 
 // Rows so few that an expert's mostly fit one tile: each weight is read once, in whole lines, and past the caches (2048
 // rows of 896 experts, 1024 -> 4096: 1191 us, 1299 on 64 x 64, which kept them; in integers 640, 763 and on 128 x 256 685).
-constexpr GroupedTile kStreamTile = {64, 128, 512, 0, 0, 0, 0};
+constexpr GroupedTile kStreamTile = {64, 128, 512};
 constexpr int kStreamRows = 16;   // an expert's, on average
 
-static double rounds_us(const GroupedTile& c, double items, double steps) {
+static double rounds_us(const GroupedTile& c, double items, double steps, double fixed) {
   if (items <= 256) return steps * c.step_alone + c.fixed_alone;
   const double rounds = items / c.at_once;
-  return (rounds < 1 ? 1 : rounds + 0.5) * (steps * c.step + c.fixed);
+  return (rounds < 1 ? 1 : rounds + 0.5) * (steps * c.step + fixed);
 }
 
 // R rows of E experts by their N columns: half a tile's rows are empty in an expert's last one, on average.
@@ -188,7 +189,7 @@ static GroupedTile tile_of(GroupedType t, int R, int E, int N, int K, int segs, 
   for (const GroupedTile& c : kTiles) {
     double m = R / (double)c.bm + 0.5 * experts;
     if (m < experts) m = experts;
-    const double us = rounds_us(c, m * ceil_div(N, pair ? c.bn / 2 : c.bn), steps);
+    const double us = rounds_us(c, m * ceil_div(N, pair ? c.bn / 2 : c.bn), steps, c.fixed);
     if (!best || us < least) best = &c, least = us;
   }
   return *best;
@@ -256,14 +257,15 @@ hipError_t launch_grouped(const DenseJob& j, const DenseEpi& e, GroupedType t, b
   return hipGetLastError();
 }
 
-// Tile of the weight gradients: as many rows for every expert.
+// Tile of the weight gradients: as many rows for every expert (32768 rows of 128, 2048 -> 768 gated: 331 us on 256 x 256, 365
+// on 128 x 256).
 static const GroupedTile& dw_tile_of(const DenseJob& j, GroupedType t, const Groups& g) {
   if (t == GROUPED_F32) return kTiles[2];
   const double steps = (g.R / (double)g.E / 64 + 0.5) * j.segs;
   const GroupedTile* best = nullptr;
   double least = 0;
   for (const GroupedTile& c : kTiles) {
-    const double us = rounds_us(c, (double)g.E * j.batch * ceil_div(j.M, c.bm) * ceil_div(j.N, c.bn), steps);
+    const double us = rounds_us(c, (double)g.E * j.batch * ceil_div(j.M, c.bm) * ceil_div(j.N, c.bn), steps, c.fixed_dw);
     if (!best || us < least) best = &c, least = us;
   }
   return *best;

@@ -203,6 +203,8 @@ def spread_cases(n):
 LARGE = [(skewed(32, 8200, 3), 0, 0, 1024, 768), ([2100, 0, 4000, 300], 0, 9, 520, 1096), (skewed(128, 4096, 4), 0, 0, 768, 520),
          (skewed(16, 4096, 5), 0, 0, 2048, 1032), (skewed(300, 700, 6), 2, 0, 1024, 1024), ([6000], 0, 0, 256, 640),
          (skewed(8, 2000, 7), 0, 0, 1001, 517)] + spread_cases(18)
+# the tallest tiles of every product: long contractions of many rows
+LARGE += [([1900, 300, 1950], 0, 0, 4104, 1544), (skewed(4, 8200, 8), 3, 5, 2048, 2056)]
 
 
 def close(name, got, dtype, ref, tol):
@@ -446,8 +448,30 @@ def test_int8_dense(size, dtype):
           + 2.0 ** -20 * (1 + z.abs()) * (z * u).abs())
 
 
+# whole rounds of the largest tiles, and ragged ones on each
 @pytest.mark.parametrize("dtype", ("bf16", "f32"))
-@pytest.mark.parametrize("case", CASES + LARGE[:7] + LARGE[9:15], ids=case_id)
+@pytest.mark.parametrize("size", [(4104, 1096, 4112), (2050, 4096, 4104), (8200, 520, 4100), (1030, 2056, 2100), (5000, 300, 2200)], ids=str)
+def test_int8_dense_large(size, dtype):
+    T, K, N = size
+    gen = torch.Generator().manual_seed(T)
+    q, sc = zip(*(tuple(t.to(DEV) for t in random_codes(gen, n, K)) for n in (T, N, N)))
+    bias, res = rand(gen, N, dtype=dtype).to(DEV), rand(gen, T, N, dtype=dtype).to(DEV)
+    z, u = ((q[0].double() @ q[i].double().T) * sc[0].double()[:, None] * sc[i].double() for i in (1, 2))
+    y, h = out((T, N), dtype), out((T, N), dtype)
+    s = B.dense_shape(T, K, N, dtype=dtype, act="gelu")
+    B.linear_int8_forward(q[0], sc[0], q[1], sc[1], bias, res, y, s)
+    B.gated_int8_forward(q[0], sc[0], q[1], sc[1], q[2], sc[2], h, s)
+    zb = z + bias.double()
+    ry = act64(zb, "gelu")[0] + res.double()
+    close("y", y, dtype, ry, U[dtype] * ry.abs() + SLOPE * (4 * U32 * z.abs() + U32 * zb.abs())
+          + 2.0 ** -20 * (1 + zb.abs()) * zb.abs() + 2 * U32 * ry.abs())
+    a = act64(z, "gelu")[0]
+    close("h", h, dtype, a * u, U[dtype] * (a * u).abs() + 8 * U32 * (z * u).abs() * SLOPE
+          + 2.0 ** -20 * (1 + z.abs()) * (z * u).abs())
+
+
+@pytest.mark.parametrize("dtype", ("bf16", "f32"))
+@pytest.mark.parametrize("case", CASES + LARGE[:7] + LARGE[9:15] + LARGE[-2:], ids=case_id)
 def test_int8_grouped(case, dtype):
     off, R, K, N, E = sizes(case)
     gen = torch.Generator().manual_seed(R + K + 5)
@@ -714,3 +738,45 @@ def test_binding_refuses_other_tensors():
         assert e.value.status == B.MOE_ERR_INVALID_ARG
     with pytest.raises(B.MoeError, match="type"):
         B.quantize_int8(x, torch.zeros(4, 16, dtype=torch.uint8, device=DEV), torch.zeros(4, device=DEV))
+
+
+def test_rows_past_32_bit_offsets():
+    """Tensors of more than 2^31 elements: the last rows are computed like the first, in the products, in codes and in
+    the combine's gradients."""
+    R, K, N = 300001, 8192, 8
+    x = torch.empty(R, K, dtype=torch.bfloat16, device=DEV)
+    x[:] = torch.linspace(-2, 3, K, device=DEV).bfloat16()
+    x[-1] = torch.linspace(1, -5, K, device=DEV).bfloat16()
+    gen = torch.Generator().manual_seed(12)
+    w = rand(gen, 2, N, K).to(DEV)
+    off = torch.tensor([0, R - 1, R], dtype=torch.int32, device=DEV)
+    few, foff = torch.cat([x[:1], x[-1:]]), torch.tensor([0, 1, 2], dtype=torch.int32, device=DEV)
+    y, fy = (torch.empty(n, N, dtype=torch.bfloat16, device=DEV) for n in (R, 2))
+    s, fs = B.grouped_shape(R, K, N, 2), B.grouped_shape(2, K, N, 2)
+    B.grouped_linear_forward(x, off, w, y, s, ws_for(s, B.MOE_CALL_GROUPED_LINEAR_FORWARD))
+    B.grouped_linear_forward(few, foff, w, fy, fs, None)
+    # sums of 8192 products in two orders, |x| <= 5: both within this of the exact ones
+    tol = 2.0 ** -8 * fy.double().abs() + 2 * fsum(few.double(), w.double().abs().amax(0), K)
+    for i, r in enumerate((0, -1)):
+        assert bool(((y[r].double() - fy[i].double()).abs() <= tol[i]).all())
+    assert torch.equal(y[0], y[R // 2]) and torch.equal(y[0], y[R - 2])
+    dx, fdx = torch.empty_like(x), torch.empty_like(few)
+    B.grouped_linear_backward(y, None, off, w, dx, None, s, ws_for(s, B.MOE_CALL_GROUPED_LINEAR_BACKWARD))
+    B.grouped_linear_backward(torch.stack((y[0], y[-1])), None, foff, w, fdx, None, fs, ws_for(fs, B.MOE_CALL_GROUPED_LINEAR_BACKWARD))
+    assert torch.equal(dx[0], fdx[0]) and torch.equal(dx[-1], fdx[1]) and torch.equal(dx[R // 2], fdx[0])
+    del dx
+    q, scale = torch.empty(R, K, dtype=torch.int8, device=DEV), torch.empty(R, device=DEV)
+    fq, fscale = torch.empty(2, K, dtype=torch.int8, device=DEV), torch.empty(2, device=DEV)
+    B.quantize_int8(x, q, scale)
+    B.quantize_int8(few, fq, fscale)
+    assert torch.equal(q[0], fq[0]) and torch.equal(q[-1], fq[1]) and torch.equal(q[R // 2], fq[0])
+    assert torch.equal(scale[[0, -1]], fscale)
+    del q
+    T = R - 1
+    rows = torch.arange(T, dtype=torch.int32, device=DEV).flip(0)[:, None].contiguous()
+    c = B.shape(T, K, 1, 1, 64)
+    dw, dy, wt = torch.empty(T, 1, device=DEV), torch.empty(T, K, dtype=torch.bfloat16, device=DEV), torch.full((T, 1), 0.5, device=DEV)
+    B.combine_backward(x[1:], x[:-1], rows, wt, dy, dw, B.MOE_BF16, c)
+    assert torch.equal(dy[0], x[-1] * 0.5) and torch.equal(dy[-1], x[1] * 0.5)
+    want = (x[-1].double() * x[0].double()).sum()
+    assert abs(float(dw[-1, 0] - want)) <= (K + 8) * U32 * float((x[-1].double() * x[0].double()).abs().sum())
