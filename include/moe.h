@@ -583,8 +583,9 @@ MOE_API moe_status moe_linear_backward(const void* dy, const void* x, const void
  * have their gradients by moe_combine_backward, the two backward calls below, and moe_combine with weights of 1.
  *
  * The conventions of the dense operators hold: every size from 1 up (bf16 operands whose width is no
- * multiple of 8 are copied to padded rows in the workspace first, the weights among them), R = 0 is a call on no
- * rows, outputs may not overlap anything, sums are fp32 in a fixed order with no atomics.
+ * multiple of 8 are copied to padded rows in the workspace first, the weights among them, except in forward passes of
+ * up to 16 rows; integer products need no copies), R = 0 is a call on no rows, outputs may not overlap anything, sums are
+ * fp32 in a fixed order with no atomics.
  * Precondition not checked: offsets do not decrease.  Offsets outside 0 .. R are taken as the nearer of the two, so no
  * offsets lead to an access out of bounds.
  *

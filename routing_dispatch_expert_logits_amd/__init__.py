@@ -1,5 +1,6 @@
 """Routed-expert MoE layer forward on one AMD Instinct MI355X (gfx950), and the dense operators
-around it (layer norm, gated product, linear projection) with their gradients.
+around it (layer norm, gated product, linear projection) with their gradients, the expert products
+and the combine with theirs, and forward products in 8-bit integers.
 
 The work runs in hand-written HIP kernels behind the C ABI of libmoe.so
 (include/moe.h); ``binding`` is the thin ctypes layer over it with the same
