@@ -114,7 +114,8 @@ struct MmTile {
 };
 
 // Eight neighbouring output columns n .. n + 7 of row m (the first `left` of them), from the
-// fp32 sums; rows of odd widths are stored at element alignment.  ACT: the activation; PAST: past the caches; bias and
+// fp32 sums; rows of odd widths are stored at element alignment.  ACT: the activation; PAST: past the caches, where
+// rows are whole 16-byte chunks (parts of a line would be read and written again); bias and
 // res: the bias' and the residual's eight, where there are such; o: the first element of row 0.
 template <typename T, int KIND, int ACT, bool PAST = false>
 __device__ __forceinline__ void mm_out8(const DenseEpi& e, int z, int64_t o, int m, int n, int N, float* a,
@@ -122,27 +123,31 @@ __device__ __forceinline__ void mm_out8(const DenseEpi& e, int z, int64_t o, int
   constexpr bool FAST = sizeof(T) == 2;
   const int64_t idx = o + (int64_t)m * e.ldo + n;
   const int left = N - n;
+  auto store8 = [past = PAST && e.ldo % 8 == 0](auto* p, int n, const float* f) __attribute__((always_inline)) {
+    if (past) moe::store8<true>(p, n, f);
+    else moe::store8<false>(p, n, f);
+  };
   float y[8];
   if constexpr (KIND == DENSE_STORE) {
-    if (e.out_f32) store8<PAST>(static_cast<float*>(e.out[z]) + idx, left, a);
-    else store8<PAST>(static_cast<T*>(e.out[z]) + idx, left, a);
+    if (e.out_f32) store8(static_cast<float*>(e.out[z]) + idx, left, a);
+    else store8(static_cast<T*>(e.out[z]) + idx, left, a);
   } else if constexpr (KIND == DENSE_LINEAR) {
     if (e.bias) {
       for (int i = 0; i < 8; ++i) a[i] += bias.get(i);
     }
-    if (e.save[0]) store8<PAST>(static_cast<T*>(e.save[0]) + idx, left, a);
+    if (e.save[0]) store8(static_cast<T*>(e.save[0]) + idx, left, a);
     for (int i = 0; i < 8; ++i) a[i] = act_value<FAST>(a[i], ACT);
     if (e.residual) {
       for (int i = 0; i < 8; ++i) a[i] += res.get(i);
     }
-    store8<PAST>(static_cast<T*>(e.out[0]) + idx, left, a);
+    store8(static_cast<T*>(e.out[0]) + idx, left, a);
   } else {
     if (e.save[0]) {
-      store8<PAST>(static_cast<T*>(e.save[0]) + idx, left, a);
-      store8<PAST>(static_cast<T*>(e.save[1]) + idx, left, b);
+      store8(static_cast<T*>(e.save[0]) + idx, left, a);
+      store8(static_cast<T*>(e.save[1]) + idx, left, b);
     }
     for (int i = 0; i < 8; ++i) y[i] = act_value<FAST>(a[i], ACT) * b[i];
-    store8<PAST>(static_cast<T*>(e.out[0]) + idx, left, y);
+    store8(static_cast<T*>(e.out[0]) + idx, left, y);
   }
 }
 
@@ -239,15 +244,17 @@ constexpr int kMmStage = (BM + BN) * SB / 2;  // 16-bit words of a stage
 // T: the operands' type; O: that of what the epilogue reads and writes.  GROUPED: a wave with no row of the
 // product does not multiply (rows in groups of any number end inside most tiles), and outputs are written past the
 // caches, where the operands that other tiles read again stay (32768 rows of 128 experts, 2048 -> 768, both products of
-// a gated backward pass: 728 -> 708 us).  STREAM: so are B's loads, for weights that one tile reads.
+// a gated backward pass: 728 -> 708 us).  STREAM: so are B's loads, for weights that one tile reads.  HEIGHT: rows that the
+// waves share, where A's tile in LDS is filled by whole instructions of every wave and has more (the rest reads 0); the
+// 16-row blocks without rows are not multiplied then.
 template <typename T, typename O, int BM, int BN, int WM, int WN, int S, int SB, int DB, bool A_COL, bool B_COL, bool PAIR,
-          int KIND, bool GROUPED = false, bool STREAM = false>
+          int KIND, bool GROUPED = false, bool STREAM = false, int HEIGHT = BM>
 __device__ __forceinline__ void mm_body(const DenseJob& j, const DenseEpi& e, const MmSlices& sl, const MmWhere& w,
                                         const MmPart& at, uint16_t* s0, uint16_t* s1, uint16_t* s2, uint16_t* s3) {
   using TA = MmTile<T, BM, A_COL, SB, DB>;
   using TB = MmTile<T, BN, B_COL, SB, DB>;
   constexpr int ES = sizeof(T), BK = SB / ES;
-  constexpr int W = WM * WN, TM = BM / WM, TN = BN / WN, FM = TM / 16, FN = TN / 16;
+  constexpr int W = WM * WN, TM = HEIGHT / WM, TN = BN / WN, FM = TM / 16, FN = TN / 16;
   constexpr int QA = TA::INSTR / W, QB = TB::INSTR / W;
   constexpr int ON = PAIR ? BN / 2 : BN;   // output columns of a tile
   static_assert(QA >= 1 && QB >= 1 && !(PAIR && (B_COL || FN % 2)), "tile");
@@ -257,7 +264,7 @@ __device__ __forceinline__ void mm_body(const DenseJob& j, const DenseEpi& e, co
   using Acc = std::conditional_t<INT8, i32x4, f32x4>;
 
   if (!w.ok) return;
-  const int m0 = uniform(w.mt * BM), n0 = uniform(w.nt * ON), z = uniform(w.z);
+  const int m0 = uniform(w.mt * HEIGHT), n0 = uniform(w.nt * ON), z = uniform(w.z);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / WN, wn = wave % WN;
   const int nk = ceil_div(at.K, BK), slice = uniform(w.slice);
@@ -267,7 +274,7 @@ __device__ __forceinline__ void mm_body(const DenseJob& j, const DenseEpi& e, co
   // fill: this wave's instructions are wave * Q .. + Q of each tile
   uint32_t va[QA], vb[QB];
 #pragma unroll
-  for (int q = 0; q < QA; ++q) va[q] = TA::src(wave * QA + q, lane, j.lda, at.M - m0);
+  for (int q = 0; q < QA; ++q) va[q] = TA::src(wave * QA + q, lane, j.lda, HEIGHT == BM ? at.M - m0 : min(HEIGHT, at.M - m0));
   const bool second = PAIR && wave >= W / 2;
 #pragma unroll
   for (int q = 0; q < QB; ++q)
@@ -280,7 +287,7 @@ __device__ __forceinline__ void mm_body(const DenseJob& j, const DenseEpi& e, co
     const void* b = PAIR ? (second ? j.B[1][0] : j.B[0][0]) : j.B[z][seg];
     pa = uniform(static_cast<const char*>(j.A[z][seg]) + (at.a + (A_COL ? (int64_t)m0 : (int64_t)m0 * j.lda)) * ES);
     pb = uniform(static_cast<const char*>(b) + (at.b + (B_COL ? (int64_t)n0 : (int64_t)n0 * j.ldb)) * ES);
-    na = mm_row_bytes(min(BM, at.M - m0), j.lda, ES);
+    na = mm_row_bytes(min(HEIGHT, at.M - m0), j.lda, ES);
     nb = mm_row_bytes(min(ON, j.N - n0), j.ldb, ES);
     left = at.K;
   };
@@ -322,7 +329,7 @@ __device__ __forceinline__ void mm_body(const DenseJob& j, const DenseEpi& e, co
     advance(1);
   };
 
-  const bool some = !GROUPED || at.M - m0 > wm * TM;   // this wave has rows
+  const int mine = at.M - m0 - wm * TM;   // rows of this wave, in tiles of rows that no other expert has
   Acc acc[FM][FN];
 #pragma unroll
   for (int a = 0; a < FM; ++a)
@@ -332,8 +339,9 @@ __device__ __forceinline__ void mm_body(const DenseJob& j, const DenseEpi& e, co
     if constexpr (INT8) return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, b), __builtin_bit_cast(i32x4, a), c, 0, 0, 0);
     else return __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(b), as_bf16x8(a), c, 0, 0, 0);
   };
+  static_assert(HEIGHT == BM || (SB == 64 && W == 8), "only turns leave blocks out");
   auto multiply = [&](const uint16_t* st) __attribute__((always_inline)) {
-    if (GROUPED && !some) return;
+    if (GROUPED && mine <= 0) return;
 #pragma unroll
     for (int h = 0; h < SB / 64; ++h) {
       u32x4 fb[FN];
@@ -402,13 +410,15 @@ __device__ __forceinline__ void mm_body(const DenseJob& j, const DenseEpi& e, co
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
     __builtin_amdgcn_sched_barrier(0);
-    if (some) {
+    if (!GROUPED || mine > 0) {
       __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-      for (int a = 0; a < FM; ++a)
+      for (int a = 0; a < FM; ++a) {
+        if (HEIGHT != BM && 16 * a >= mine) continue;
 #pragma unroll
         for (int b = 0; b < FN; ++b)
           acc[a][b] = mfma(fb[b], fa[a], acc[a][b]);
+      }
       __builtin_amdgcn_s_setprio(0);
     }
     __builtin_amdgcn_sched_barrier(0);

@@ -82,27 +82,27 @@ GroupedWs grouped_ws(const GroupedDims& d, bool gated, bool backward, bool int8)
 }
 
 // x and the weights (each nullable) at row length w.ldk: in place, or copied to the workspace.
-moe_status in_rows(const GroupedDims& d, const GroupedWs& w, const void** x, const void** w0, const void** w1, void* ws,
-                   hipStream_t st) {
+moe_status in_rows(const GroupedDims& d, const GroupedWs& w, const Groups& g, const void** x, const void** w0, const void** w1,
+                   void* ws, hipStream_t st) {
   if (w.ldk == d.K) return MOE_OK;
-  PadRows p{};
-  auto one = [&](int i, const void** v, int64_t rows, size_t off) {
-    if (!v || !*v) return;
-    p.src[i] = *v;
-    p.dst[i] = at<void>(ws, off);
-    p.rows[i] = rows;
-    *v = p.dst[i];
-  };
-  one(0, x, d.R, w.x);
-  one(1, w0, (int64_t)d.E * d.N, w.w[0]);
-  one(2, w1, (int64_t)d.E * d.N, w.w[1]);
-  MOE_HIP(launch_pad_rows(p, d.K, w.ldk, st));
+  if (x) {
+    const PadRows p{{*x}, {at<void>(ws, w.x)}, {d.R}};
+    MOE_HIP(launch_pad_rows(p, d.K, w.ldk, st));
+    *x = p.dst[0];
+  }
+  if (w0) {
+    void *p0 = at<void>(ws, w.w[0]), *p1 = at<void>(ws, w.w[1]);
+    MOE_HIP(launch_pad_weights(*w0, *w1, p0, p1, g, d.N, d.K, w.ldk, st));
+    *w0 = p0;
+    if (*w1) *w1 = p1;
+  }
   return MOE_OK;
 }
 
 moe_status forward(const GroupedDims& d, const GroupedWs& w, GroupedType t, const void* x, const int32_t* offsets,
                    const void* w0, const void* w1, DenseEpi e, void* ws, hipStream_t st) {
-  if (t != GROUPED_INT8) MOE_TRY(in_rows(d, w, &x, &w0, &w1, ws, st));
+  const Groups g{offsets, d.E, d.R};
+  if (t != GROUPED_INT8) MOE_TRY(in_rows(d, w, g, &x, &w0, &w1, ws, st));
   DenseJob j{};
   j.N = d.N; j.K = d.K;
   j.segs = 1; j.batch = 1;
@@ -113,7 +113,6 @@ moe_status forward(const GroupedDims& d, const GroupedWs& w, GroupedType t, cons
   e.act = d.act;
   e.ldo = d.N;
   e.out_f32 = !d.bf16;
-  const Groups g{offsets, d.E, d.R};
   const int64_t w_stride = (int64_t)d.N * w.ldk;
   MOE_HIP(d.R <= kDecodeRows ? launch_grouped_decode(j, e, t, d.bf16, g, w_stride, st)
                                     : launch_grouped(j, e, t, d.bf16, g, w_stride, at<void>(ws, w.table), st));
@@ -124,9 +123,9 @@ moe_status forward(const GroupedDims& d, const GroupedWs& w, GroupedType t, cons
 moe_status gradients(const GroupedDims& d, const GroupedWs& w, const void* d0, const void* d1, int terms, const void* x,
                      const int32_t* offsets, const void* w0, const void* w1, void* dx, void* dw0, void* dw1, void* ws,
                      hipStream_t st) {
-  MOE_TRY(in_rows(d, w, dw0 ? &x : nullptr, dx ? &w0 : nullptr, dx ? &w1 : nullptr, ws, st));
   const GroupedType t = d.bf16 ? GROUPED_BF16 : GROUPED_F32;
   const Groups g{offsets, d.E, d.R};
+  MOE_TRY(in_rows(d, w, g, dw0 ? &x : nullptr, dx ? &w0 : nullptr, dx ? &w1 : nullptr, ws, st));
   GroupedProduct px{}, pw{};
   DenseJob &jx = px.j, &jw = pw.j;
   px.e.kind = pw.e.kind = DENSE_STORE;

@@ -35,6 +35,10 @@ hipError_t launch_grouped(const DenseJob& j, const DenseEpi& e, GroupedType t, b
 // chunks): no table.  (32 rows of 8 experts, 2048 -> 768 gated: 13.0 us, 12.1 by launch_grouped; 64 of 54 of 128: 87.9 and 76.2.)  g.E == 0: dense rows, j.M of them (integers).
 hipError_t launch_grouped_decode(const DenseJob& j, const DenseEpi& e, GroupedType t, bool out_bf16, const Groups& g,
                                  int64_t w_stride, hipStream_t st);
+// bf16 weights [E x N x cols] (the second may be NULL) in rows of ld elements with zeros behind, ld: cols rounded up to 8;
+// those of experts without rows are left out.
+hipError_t launch_pad_weights(const void* w0, const void* w1, void* p0, void* p1, const Groups& g, int N, int cols, int64_t ld,
+                              hipStream_t st);
 // A backward pass's products, either NULL: dx as launch_grouped's with b_col, and for every expert dw's out[z][e] = sum of its
 // rows' A_z x B_z, M x N (j.K unused), zeros without rows.
 struct GroupedProduct {

@@ -1,11 +1,21 @@
 // Products grouped by expert on the matrix cores, on the tiles of dense_tile.h: each expert's rows by
 // its own weight, in one launch whatever the row counts are.
+#include <cmath>
+
 #include "dense_tile.h"
 #include "grouped_kernels.h"
 
 namespace moe {
 
-// The m-tiles of all experts in order: t[0].x of them, t[1 + i] = {first row, rows of the expert from there on, expert}.
+// Rows of each of the tiles of at most bm rows that n rows take: as many for each where blocks of 16 rows without any
+// are left out (tiles of 320), else bm.  Tile i's are i * height .. min(n, (i + 1) * height), never none.
+__host__ __device__ __forceinline__ int tile_height(int n, int bm) {
+  if (bm <= 256 || n <= bm) return bm;
+  const int t = ceil_div(n, bm);
+  return ceil_div(ceil_div(n, t), 16) * 16;
+}
+
+// The m-tiles of all experts in order: t[0].x of them, t[1 + i] = {first row, rows, expert}.
 // A workgroup sums the tile counts in LDS, then every thread looks up the experts of its tiles.
 constexpr int kTableThreads = 1024;
 static_assert(kMaxE <= kTableThreads, "an expert per thread");
@@ -31,8 +41,8 @@ __global__ __launch_bounds__(kTableThreads) void k_group_tiles(Groups g, int bm,
   for (int i = blockIdx.x * kTableThreads + tid; i < total; i += gridDim.x * kTableThreads) {
     const int e = min(upper_index(starts, g.E, i), g.E - 1);
     const int2 r = group_rows(g, e);
-    const int first = r.x + (i - starts[e]) * bm;
-    t[1 + i] = make_int4(first, r.y - first, e, 0);
+    const int h = tile_height(r.y - r.x, bm), first = r.x + (i - starts[e]) * h;
+    t[1 + i] = make_int4(first, min(h, r.y - first), e, 0);
   }
 }
 
@@ -55,7 +65,7 @@ struct TileFinder {
     before = upto - mine;
     total = __builtin_amdgcn_readlane(upto, 63);
   }
-  // {first row, rows of the expert from there on, expert} of m-tile t < total.
+  // {first row, rows, expert} of m-tile t < total.
   __device__ __forceinline__ int4 at(int t) const {
     const int lane = threadIdx.x & 63;
     int4 found = make_int4(0, 0, 0, 0);
@@ -64,7 +74,8 @@ struct TileFinder {
       const int e = lane * per + i, n = tiles(e);
       if (t >= b && t < b + n) {
         const int2 r = group_rows(g, e);
-        found = make_int4(r.x + (t - b) * bm, r.y - (r.x + (t - b) * bm), e, 0);
+        const int h = tile_height(r.y - r.x, bm), first = r.x + (t - b) * h;
+        found = make_int4(first, min(h, r.y - first), e, 0);
         here = true;
       }
       b += n;
@@ -77,7 +88,7 @@ struct TileFinder {
 
 // The tile of workgroup `block`: rows of one expert by columns of its weight.  table: the m-tiles, or NULL.
 template <typename T, typename O, int BM, int BN, int WM, int WN, int S, int SB, int DB, bool B_COL, bool PAIR, int KIND,
-          bool STREAM>
+          bool STREAM, int HEIGHT>
 __device__ __forceinline__ void rows_tile(const DenseJob& j, const DenseEpi& e, const Groups& g, const int4* table,
                                           int64_t w_stride, int block, uint16_t* s0, uint16_t* s1, uint16_t* s2, uint16_t* s3) {
   const int tn = ceil_div(j.N, PAIR ? BN / 2 : BN);
@@ -90,7 +101,7 @@ __device__ __forceinline__ void rows_tile(const DenseJob& j, const DenseEpi& e, 
     if (!w.ok) return;
     tile = table[1 + w.mt];
   } else {
-    const TileFinder f(g, BM);
+    const TileFinder f(g, HEIGHT);
     if (f.total == 0) return;
     w = mm_where(block, f.total, tn, 1, 1);
     if (!w.ok) return;
@@ -99,11 +110,22 @@ __device__ __forceinline__ void rows_tile(const DenseJob& j, const DenseEpi& e, 
   const int64_t row = uniform(tile.x), expert = uniform(tile.z);
   w.mt = 0;
   const MmPart at{uniform(tile.y), j.K, row * j.lda, expert * w_stride, row * e.ldo, row, expert * j.N};
-  mm_body<T, O, BM, BN, WM, WN, S, SB, DB, false, B_COL, PAIR, KIND, true, STREAM>(j, e, MmSlices{nullptr, 1, 1, 0}, w, at, s0, s1,
+  mm_body<T, O, BM, BN, WM, WN, S, SB, DB, false, B_COL, PAIR, KIND, true, STREAM, HEIGHT>(j, e, MmSlices{nullptr, 1, 1, 0}, w, at, s0, s1,
                                                                            s2, s3);
 }
 
-// The same of the weight gradients: columns of one expert's gradient by columns of its rows.
+// Zeros in the bytes lo .. hi of p (2-byte aligned), in 16-byte chunks but for the ends.
+__device__ __forceinline__ void zero_bytes(char* p, int64_t lo, int64_t hi) {
+  const int64_t a = reinterpret_cast<int64_t>(p) + lo, b = reinterpret_cast<int64_t>(p) + hi;
+  const int64_t a16 = min((a + 15) & ~15ll, b), b16 = max(b & ~15ll, a16), step = 16 * blockDim.x;
+  for (int64_t i = a16 + 16 * threadIdx.x; i < b16; i += step) __builtin_nontemporal_store(u32x4{0, 0, 0, 0}, reinterpret_cast<u32x4*>(i));
+  const int64_t edge = 2 * threadIdx.x;
+  if (a + edge < a16) *reinterpret_cast<uint16_t*>(a + edge) = 0;
+  if (b16 + edge < b) *reinterpret_cast<uint16_t*>(b16 + edge) = 0;
+}
+
+// The same of the weight gradients: columns of one expert's gradient by columns of its rows.  An expert without rows
+// has its gradient's bytes filled with zeros, a share by each workgroup.
 template <typename T, int BM, int BN, int WM, int WN, int S, int SB, int DB>
 __device__ __forceinline__ void dw_tile(const DenseJob& j, const DenseEpi& e, const Groups& g, int block, uint16_t* s0,
                                         uint16_t* s1, uint16_t* s2, uint16_t* s3) {
@@ -113,18 +135,24 @@ __device__ __forceinline__ void dw_tile(const DenseJob& j, const DenseEpi& e, co
   w.z -= expert * j.batch;
   const int2 r = group_rows(g, expert);
   const int64_t row = uniform(r.x);
+  if (uniform(r.y - r.x) == 0) {
+    const int tiles = ceil_div(j.M, BM) * ceil_div(j.N, BN), tile = w.mt * ceil_div(j.N, BN) + w.nt;
+    const int64_t bytes = (int64_t)j.M * e.ldo * (sizeof(T) == 4 || e.out_f32 ? 4 : 2);
+    // shares end at even bytes
+    return zero_bytes(static_cast<char*>(e.out[w.z]) + expert * bytes, bytes / 2 * tile / tiles * 2, bytes / 2 * (tile + 1) / tiles * 2);
+  }
   const MmPart at{j.M, uniform(r.y - r.x), row * j.lda, row * j.ldb, (int64_t)expert * j.M * e.ldo, 0, 0};
   mm_body<T, T, BM, BN, WM, WN, S, SB, DB, true, true, false, DENSE_STORE, true>(j, e, MmSlices{nullptr, 1, 1, 0}, w, at, s0, s1,
                                                                            s2, s3);
 }
 
 template <typename T, typename O, int BM, int BN, int WM, int WN, int S, int SB, int DB, bool B_COL, bool PAIR, int KIND,
-          bool STREAM>
+          bool STREAM, int HEIGHT>
 __global__ __launch_bounds__(WM* WN * 64, 2) void k_grouped_mm(DenseJob j, DenseEpi e, Groups g,
                                                                const int4* __restrict__ table, int64_t w_stride) {
   constexpr int STAGE = kMmStage<BM, BN, SB>;
   __shared__ __attribute__((aligned(1024))) uint16_t s0[STAGE], s1[STAGE], s2[STAGE], s3[S > 3 ? STAGE : 1];
-  rows_tile<T, O, BM, BN, WM, WN, S, SB, DB, B_COL, PAIR, KIND, STREAM>(j, e, g, table, w_stride, blockIdx.x, s0, s1, s2, s3);
+  rows_tile<T, O, BM, BN, WM, WN, S, SB, DB, B_COL, PAIR, KIND, STREAM, HEIGHT>(j, e, g, table, w_stride, blockIdx.x, s0, s1, s2, s3);
 }
 
 template <typename T, int BM, int BN, int WM, int WN, int S, int SB, int DB>
@@ -144,7 +172,7 @@ __global__ __launch_bounds__(256, 2) void k_grouped_two(DenseJob jx, DenseEpi ex
   const bool early = (int)blockIdx.x < first;
   const int block = early ? blockIdx.x : blockIdx.x - first;
   if (early == dx_first)
-    rows_tile<T, T, 64, 64, 2, 2, S, 128, DB, true, false, DENSE_STORE, false>(jx, ex, g, table, w_stride, block, s0, s1, s2, s3);
+    rows_tile<T, T, 64, 64, 2, 2, S, 128, DB, true, false, DENSE_STORE, false, 64>(jx, ex, g, table, w_stride, block, s0, s1, s2, s3);
   else
     dw_tile<T, 64, 64, 2, 2, S, 128, DB>(jw, ew, g, block, s0, s1, s2, s3);
 }
@@ -154,32 +182,44 @@ static int64_t most_tiles(int R, int E, int bm) { return R / bm + (R < E ? R : E
 
 // Tile of a grouped product by estimated time, from what a kernel takes per round of `at_once` workgroups on the
 // device: us per contraction step of 128 bytes and besides (a single round of up to 256 workgroups, one to a CU: `alone`),
-// measured (MI355X).  256 x 256 tiles in turns have the fewest bytes through a CU's L1 and are best for long
-// contractions (62580 rows of 32 experts, 7168 -> 2048 gated: 3414 us, 4167 on 128 x 256); two workgroups of
-// 128 x 256 on a CU overlap one's first loads and stores with the other's products, which is best for short
-// ones (32768 rows of 128 experts, 768 -> 2048: 182 us, 193 on 256 x 256, 272 on 64 x 64); 64 x 64 waste least on a few rows of
-// many experts (2048 rows of 896, 1024 -> 4096: 1084 us; 1130 and 1255).
+// measured (MI355X).  The tallest tile, 320 x 256 in turns (256 for weight gradients, whose operands' columns are powers of
+// two in LDS), reads each weight panel least often: 32768 rows of 128 experts, 768 -> 2048, take 149 us, where 256 x 256
+// (half of the experts have a few rows more) takes 189 and 128 x 256 180; 62580 rows of 32, 7168 -> 2048 gated, 3315, 3432 and
+// 4161.  Two workgroups of 128 x 256 on a CU overlap one's first loads and stores with the other's products, which is best
+// for the shortest contractions (270 rows of each of 128 experts, 256 -> 2048: 86 and 98, 200 rows 4 us less); 64 x 64 waste
+// least on few rows (32768 rows of 128, 768 -> 2048: 272).
 struct GroupedTile {
   int bm, bn, at_once;
   double step, fixed, step_alone, fixed_alone;
-  double fixed_dw;   // besides, where no residual and no activation is met and no tile is looked up: weight gradients
 };
-constexpr GroupedTile kTiles[] = {{256, 256, 256, 1.75, 11.5, 1.75, 11.5, 5.6},
-                                  {128, 256, 512, 2.2, 7.0, 1.3, 6.0, 5.0},
-                                  {64, 64, 512, 0.42, 3.0, 0.19, 2.5, 3.0}};
-
+constexpr GroupedTile kTiles[] = {{320, 256, 256, 2.0, 11.5, 2.0, 11.5},
+                                  {128, 256, 512, 2.2, 7.0, 1.3, 6.0},
+                                  {64, 64, 512, 0.42, 3.0, 0.19, 2.5}};
+// Besides, there is no activation to meet and no tile to look up.
+constexpr GroupedTile kTilesDw[] = {{256, 256, 256, 1.75, 5.6, 1.75, 11.5},
+                                    {128, 256, 512, 2.2, 5.0, 1.3, 6.0},
+                                    {64, 64, 512, 0.42, 3.0, 0.19, 2.5}};
 // Rows so few that an expert's mostly fit one tile: each weight is read once, in whole lines, and past the caches (2048
 // rows of 896 experts, 1024 -> 4096: 1191 us, 1299 on 64 x 64, which kept them; in integers 640, 763 and on 128 x 256 685).
 constexpr GroupedTile kStreamTile = {64, 128, 512};
 constexpr int kStreamRows = 16;   // an expert's, on average
 
-static double rounds_us(const GroupedTile& c, double items, double steps, double fixed) {
+static double rounds_us(const GroupedTile& c, double items, double steps) {
   if (items <= 256) return steps * c.step_alone + c.fixed_alone;
   const double rounds = items / c.at_once;
-  return (rounds < 1 ? 1 : rounds + 0.5) * (steps * c.step + fixed);
+  return (rounds < 1 ? 1 : rounds + 0.5) * (steps * c.step + c.fixed);
 }
 
-// R rows of E experts by their N columns: half a tile's rows are empty in an expert's last one, on average.
+// Tiles of bm rows that an expert with about `rows` takes, on average over row counts spread normally around it (by
+// their square root and a twentieth): 1 + the chances of more than one tile's, two tiles' .. rows.
+static double mean_tiles(double rows, int bm) {
+  const double spread = sqrt(rows) + 0.05 * rows;
+  double tiles = 1 + floor(fmax(0.0, rows - 4 * spread) / bm);
+  for (double i = tiles; i * bm < rows + 4 * spread; ++i) tiles += 0.5 * erfc((i * bm - rows) / (spread * 1.4142135623730951));
+  return tiles;
+}
+
+// R rows of E experts by their N columns.
 static GroupedTile tile_of(GroupedType t, int R, int E, int N, int K, int segs, bool pair, bool b_col) {
   if (t == GROUPED_F32) return kTiles[2];
   if (!b_col && R <= (int64_t)kStreamRows * E && (int64_t)(R < E ? R : E) * ceil_div(N, pair ? 64 : 128) >= 512) return kStreamTile;
@@ -187,9 +227,7 @@ static GroupedTile tile_of(GroupedType t, int R, int E, int N, int K, int segs, 
   const GroupedTile* best = nullptr;
   double least = 0;
   for (const GroupedTile& c : kTiles) {
-    double m = R / (double)c.bm + 0.5 * experts;
-    if (m < experts) m = experts;
-    const double us = rounds_us(c, m * ceil_div(N, pair ? c.bn / 2 : c.bn), steps, c.fixed);
+    const double us = rounds_us(c, experts * mean_tiles(R / experts, c.bm) * ceil_div(N, pair ? c.bn / 2 : c.bn), steps);
     if (!best || us < least) best = &c, least = us;
   }
   return *best;
@@ -197,6 +235,35 @@ static GroupedTile tile_of(GroupedType t, int R, int E, int N, int K, int segs, 
 
 size_t grouped_table_bytes(GroupedType t, int R, int E, int N, int K, int segs, bool pair, bool b_col) {
   return 16 * (size_t)(1 + most_tiles(R, E, tile_of(t, R, E, N, K, segs, pair, b_col).bm));
+}
+
+// Rows of the weights of experts that have rows, padded: eight elements of a row per thread; blockIdx.y the expert.
+__global__ __launch_bounds__(256) void k_pad_weights(const uint16_t* w0, const uint16_t* w1, uint16_t* p0, uint16_t* p1, Groups g,
+                                                     int64_t rows, int cols, int ld) {
+  const int2 r = group_rows(g, blockIdx.y);
+  if (r.x == r.y) return;
+  const int per = ld / 8;
+  const int64_t total = rows * per, in = blockIdx.y * rows * cols, out = blockIdx.y * rows * ld;
+  for (int z = 0; z < (w1 ? 2 : 1); ++z) {
+    const uint16_t* src = (z ? w1 : w0) + in;
+    uint16_t* dst = (z ? p1 : p0) + out;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+      const int64_t row = i / per;
+      const int c = (int)(i - row * per) * 8;
+      float v[8];
+      load8(src + row * cols + c, cols - c, v);
+      store8(dst + i * 8, v);
+    }
+  }
+}
+
+hipError_t launch_pad_weights(const void* w0, const void* w1, void* p0, void* p1, const Groups& g, int N, int cols, int64_t ld,
+                              hipStream_t st) {
+  const int64_t want = ((int64_t)N * (ld / 8) + 255) / 256, most = 65536 / g.E + 1;
+  k_pad_weights<<<dim3((unsigned)(want < most ? want : most), g.E), 256, 0, st>>>(
+      static_cast<const uint16_t*>(w0), static_cast<const uint16_t*>(w1), static_cast<uint16_t*>(p0), static_cast<uint16_t*>(p1), g, N,
+      cols, (int)ld);
+  return hipGetLastError();
 }
 
 static unsigned whole_eights(int64_t items) { return (unsigned)((items + 7) / 8 * 8); }
@@ -220,18 +287,18 @@ static hipError_t rows_grid(const DenseJob& j, GroupedType t, const Groups& g, R
   return hipGetLastError();
 }
 
-template <typename T, typename O, int BM, int BN, int WM, int WN, int S, int SB = 128, int DB = 16, bool STREAM = false>
+template <typename T, typename O, int BM, int BN, int WM, int WN, int S, int SB = 128, int DB = 16, bool STREAM = false, int HEIGHT = BM>
 static void go(const DenseJob& j, const DenseEpi& e, const Groups& g, const int4* t, unsigned grid, int64_t w_stride, hipStream_t st) {
   const int block = WM * WN * 64;
-  if (j.pair) k_grouped_mm<T, O, BM, BN, WM, WN, S, SB, DB, false, true, DENSE_GATED, STREAM><<<grid, block, 0, st>>>(j, e, g, t, w_stride);
-  else if constexpr (sizeof(T) == 1) k_grouped_mm<T, O, BM, BN, WM, WN, S, SB, DB, false, false, DENSE_STORE, STREAM><<<grid, block, 0, st>>>(j, e, g, t, w_stride);
-  else if (!STREAM && j.b_col) k_grouped_mm<T, O, BM, BN, WM, WN, S, SB, DB, !STREAM, false, DENSE_STORE, STREAM><<<grid, block, 0, st>>>(j, e, g, t, w_stride);
-  else k_grouped_mm<T, O, BM, BN, WM, WN, S, SB, DB, false, false, DENSE_STORE, STREAM><<<grid, block, 0, st>>>(j, e, g, t, w_stride);
+  if (j.pair) k_grouped_mm<T, O, BM, BN, WM, WN, S, SB, DB, false, true, DENSE_GATED, STREAM, HEIGHT><<<grid, block, 0, st>>>(j, e, g, t, w_stride);
+  else if constexpr (sizeof(T) == 1) k_grouped_mm<T, O, BM, BN, WM, WN, S, SB, DB, false, false, DENSE_STORE, STREAM, HEIGHT><<<grid, block, 0, st>>>(j, e, g, t, w_stride);
+  else if (!STREAM && j.b_col) k_grouped_mm<T, O, BM, BN, WM, WN, S, SB, DB, !STREAM, false, DENSE_STORE, STREAM, HEIGHT><<<grid, block, 0, st>>>(j, e, g, t, w_stride);
+  else k_grouped_mm<T, O, BM, BN, WM, WN, S, SB, DB, false, false, DENSE_STORE, STREAM, HEIGHT><<<grid, block, 0, st>>>(j, e, g, t, w_stride);
 }
 template <typename T, typename O>
 static void go_tile(const DenseJob& j, const DenseEpi& e, const Groups& g, const int4* t, const RowsGrid& r, int64_t w_stride,
                     hipStream_t st) {
-  if (r.c.bm == 256) go<T, O, 256, 256, 2, 4, 4, 64>(j, e, g, t, r.blocks, w_stride, st);
+  if (r.c.bm == 320) go<T, O, 384, 256, 2, 4, 4, 64, 16, false, 320>(j, e, g, t, r.blocks, w_stride, st);
   else if (r.c.bm == 128) go<T, O, 128, 256, 2, 2, 3, 64>(j, e, g, t, r.blocks, w_stride, st);
   else if (r.c.bn == kStreamTile.bn) go<T, O, 64, 128, 1, 4, 3, 128, 16, true>(j, e, g, t, r.blocks, w_stride, st);
   else go<T, O, 64, 64, 2, 2, 4>(j, e, g, t, r.blocks, w_stride, st);
@@ -260,12 +327,12 @@ hipError_t launch_grouped(const DenseJob& j, const DenseEpi& e, GroupedType t, b
 // Tile of the weight gradients: as many rows for every expert (32768 rows of 128, 2048 -> 768 gated: 331 us on 256 x 256, 365
 // on 128 x 256).
 static const GroupedTile& dw_tile_of(const DenseJob& j, GroupedType t, const Groups& g) {
-  if (t == GROUPED_F32) return kTiles[2];
+  if (t == GROUPED_F32) return kTilesDw[2];
   const double steps = (g.R / (double)g.E / 64 + 0.5) * j.segs;
   const GroupedTile* best = nullptr;
   double least = 0;
-  for (const GroupedTile& c : kTiles) {
-    const double us = rounds_us(c, (double)g.E * j.batch * ceil_div(j.M, c.bm) * ceil_div(j.N, c.bn), steps, c.fixed_dw);
+  for (const GroupedTile& c : kTilesDw) {
+    const double us = rounds_us(c, (double)g.E * j.batch * ceil_div(j.M, c.bm) * ceil_div(j.N, c.bn), steps);
     if (!best || us < least) best = &c, least = us;
   }
   return *best;

@@ -48,19 +48,20 @@ static int least(int a, int b) { return a < b ? a : b; }
 static int held(int v, int lo) { return v < lo ? lo : v > R ? R : v; }
 
 // Rows by weights: the first and last contraction step of each expert's first and last m-tile, first and last n-tile.
-template <typename T, int BM, int BN, int SB, int DB, bool B_COL>
+template <typename T, int BM, int BN, int SB, int DB, bool B_COL, int HEIGHT = BM>
 static void by_rows(const char* what, int contraction, int cols, int64_t lda, int64_t ldb, int64_t w_stride, int on) {
   constexpr int ES = sizeof(T), BK = SB / ES;
   using TA = MmTile<T, BM, false, SB, DB>;
   using TB = MmTile<T, BN, B_COL, SB, DB>;
   for (int e = 0; e < E; ++e) {
     const int lo = held(offsets[e], 0), hi = held(offsets[e + 1], lo);
-    for (int row = lo; row < hi; row += BM) {
-      if (row > lo && row + 2 * BM < hi) continue;
+    const int h = tile_height(hi - lo, HEIGHT);
+    for (int row = lo; row < hi; row += h) {
+      if (row > lo && row + 2 * h < hi) continue;
+      const int valid = least(h, hi - row);
       for (int k0 : {0, (contraction - 1) / BK * BK}) {
         const int rows = least(BK, contraction - k0);
-        side<TA, false, DB>(what, row * lda + k0, R * lda * ES, lda, hi - row, rows,
-                            mm_row_bytes(least(BM, hi - row), lda, ES) - k0 * ES);
+        side<TA, false, DB>(what, row * lda + k0, R * lda * ES, lda, valid, rows, mm_row_bytes(valid, lda, ES) - k0 * ES);
         for (int n0 = 0; n0 < cols; n0 += on) {
           if (n0 > 0 && n0 + 2 * on < cols) continue;
           if (B_COL)
@@ -113,12 +114,12 @@ int main(int argc, char** argv) {
       if (ldk % 4 == 0) by_rows<float, 64, 64, 128, 16, false>(what, K, N, ldk, ldk, N * ldk, on);
       else by_rows<float, 64, 64, 128, 4, false>(what, K, N, ldk, ldk, N * ldk, on);
     } else if (t == GROUPED_BF16) {
-      if (c.bm == 256) by_rows<uint16_t, 256, 256, 64, 16, false>(what, K, N, ldk, ldk, N * ldk, on);
+      if (c.bm == 320) by_rows<uint16_t, 384, 256, 64, 16, false, 320>(what, K, N, ldk, ldk, N * ldk, on);
       else if (c.bm == 128) by_rows<uint16_t, 128, 256, 64, 16, false>(what, K, N, ldk, ldk, N * ldk, on);
       else if (c.bn == 128) by_rows<uint16_t, 64, 128, 128, 16, false>(what, K, N, ldk, ldk, N * ldk, on);
       else by_rows<uint16_t, 64, 64, 128, 16, false>(what, K, N, ldk, ldk, N * ldk, on);
     } else {
-      if (c.bm == 256) by_rows<int8_t, 256, 256, 64, 16, false>(what, K, N, ldk, ldk, N * ldk, on);
+      if (c.bm == 320) by_rows<int8_t, 384, 256, 64, 16, false, 320>(what, K, N, ldk, ldk, N * ldk, on);
       else if (c.bm == 128) by_rows<int8_t, 128, 256, 64, 16, false>(what, K, N, ldk, ldk, N * ldk, on);
       else if (c.bn == 128) by_rows<int8_t, 64, 128, 128, 16, false>(what, K, N, ldk, ldk, N * ldk, on);
       else by_rows<int8_t, 64, 64, 128, 16, false>(what, K, N, ldk, ldk, N * ldk, on);
@@ -140,7 +141,7 @@ int main(int argc, char** argv) {
         by_experts<float, 64, 64, 128, 4>("dw", ldn, ldk);
       }
     } else {
-      if (x.bm == 256) by_rows<uint16_t, 256, 256, 64, 16, true>("dx", N, K, ldn, ldk, N * ldk, 256);
+      if (x.bm == 320) by_rows<uint16_t, 384, 256, 64, 16, true, 320>("dx", N, K, ldn, ldk, N * ldk, 256);
       else if (x.bm == 128) by_rows<uint16_t, 128, 256, 64, 16, true>("dx", N, K, ldn, ldk, N * ldk, 256);
       else by_rows<uint16_t, 64, 64, 128, 16, true>("dx", N, K, ldn, ldk, N * ldk, 64);
       if (w.bm == 256) by_experts<uint16_t, 256, 256, 64, 16>("dw", ldn, ldk);

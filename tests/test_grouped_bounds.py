@@ -61,9 +61,9 @@ def test_loads_stay_in_their_operands(bounds, dtype):
 
 
 def test_every_tile_height_is_reached(bounds):
-    """What the replay covers: forward products, dx and dw on 64, 128 and 256 rows."""
+    """What the replay covers: forward products and dx on 64, 128 and 320 rows, dw on 64, 128 and 256."""
     seen = [set() for _ in range(4)]
     for case in CASES + spread_cases(200):
         for s, h in zip(seen, bounds("bf16", case)):
             s.add(h)
-    assert all(s == {64, 128, 256} for s in seen), seen
+    assert all(s == {64, 128, 320} for s in seen[:3]) and seen[3] == {64, 128, 256}, seen
