@@ -114,8 +114,7 @@ struct MmTile {
 };
 
 // Eight neighbouring output columns n .. n + 7 of row m (the first `left` of them), from the
-// fp32 sums; rows of odd widths are stored at element alignment.  ACT: the activation; PAST: past the caches, where
-// rows are whole 16-byte chunks (parts of a line would be read and written again); bias and
+// fp32 sums; rows of odd widths are stored at element alignment.  ACT: the activation; PAST: past the caches; bias and
 // res: the bias' and the residual's eight, where there are such; o: the first element of row 0.
 template <typename T, int KIND, int ACT, bool PAST = false>
 __device__ __forceinline__ void mm_out8(const DenseEpi& e, int z, int64_t o, int m, int n, int N, float* a,
@@ -123,31 +122,27 @@ __device__ __forceinline__ void mm_out8(const DenseEpi& e, int z, int64_t o, int
   constexpr bool FAST = sizeof(T) == 2;
   const int64_t idx = o + (int64_t)m * e.ldo + n;
   const int left = N - n;
-  auto store8 = [past = PAST && e.ldo % 8 == 0](auto* p, int n, const float* f) __attribute__((always_inline)) {
-    if (past) moe::store8<true>(p, n, f);
-    else moe::store8<false>(p, n, f);
-  };
   float y[8];
   if constexpr (KIND == DENSE_STORE) {
-    if (e.out_f32) store8(static_cast<float*>(e.out[z]) + idx, left, a);
-    else store8(static_cast<T*>(e.out[z]) + idx, left, a);
+    if (e.out_f32) store8<PAST>(static_cast<float*>(e.out[z]) + idx, left, a);
+    else store8<PAST>(static_cast<T*>(e.out[z]) + idx, left, a);
   } else if constexpr (KIND == DENSE_LINEAR) {
     if (e.bias) {
       for (int i = 0; i < 8; ++i) a[i] += bias.get(i);
     }
-    if (e.save[0]) store8(static_cast<T*>(e.save[0]) + idx, left, a);
+    if (e.save[0]) store8<PAST>(static_cast<T*>(e.save[0]) + idx, left, a);
     for (int i = 0; i < 8; ++i) a[i] = act_value<FAST>(a[i], ACT);
     if (e.residual) {
       for (int i = 0; i < 8; ++i) a[i] += res.get(i);
     }
-    store8(static_cast<T*>(e.out[0]) + idx, left, a);
+    store8<PAST>(static_cast<T*>(e.out[0]) + idx, left, a);
   } else {
     if (e.save[0]) {
-      store8(static_cast<T*>(e.save[0]) + idx, left, a);
-      store8(static_cast<T*>(e.save[1]) + idx, left, b);
+      store8<PAST>(static_cast<T*>(e.save[0]) + idx, left, a);
+      store8<PAST>(static_cast<T*>(e.save[1]) + idx, left, b);
     }
     for (int i = 0; i < 8; ++i) y[i] = act_value<FAST>(a[i], ACT) * b[i];
-    store8(static_cast<T*>(e.out[0]) + idx, left, y);
+    store8<PAST>(static_cast<T*>(e.out[0]) + idx, left, y);
   }
 }
 

@@ -37,20 +37,64 @@ struct Int8Tile {
 };
 constexpr Int8Tile kInt8Tiles[] = {{256, 256, 256, 1.7, 10.0}, {256, 128, 256, 1.0, 6.0}, {64, 64, 512, 0.42, 3.0}};
 
-hipError_t launch_int8(const DenseJob& j, const DenseEpi& e, bool out_bf16, hipStream_t st) {
-  int best = 0;
-  double least = 0;
+struct Int8Plan {
+  int tile;   // of kInt8Tiles
+  int cut;    // 256 x 256 tiles for this many output columns, and a launch of its own for the rest; 0: none
+  double us;
+};
+static Int8Plan int8_plan(int M, int N, int K, bool pair, bool whole) {
+  Int8Plan best{};
+  const int steps = ceil_div(K, 128);
   for (int i = 0; i < 3; ++i) {
     const Int8Tile& c = kInt8Tiles[i];
-    const int64_t items = (int64_t)ceil_div(j.M, c.bm) * ceil_div(j.N, j.pair ? c.bn / 2 : c.bn);
-    const double us = (double)((items + c.at_once - 1) / c.at_once) * (ceil_div(j.K, 128) * c.step + c.fixed);
-    if (i == 0 || us < least) best = i, least = us;
+    const int64_t items = (int64_t)ceil_div(M, c.bm) * ceil_div(N, pair ? c.bn / 2 : c.bn);
+    const double us = (double)((items + c.at_once - 1) / c.at_once) * (steps * c.step + c.fixed);
+    if (i == 0 || us < best.us) best = {i, 0, us};
   }
+  // Whole rounds of 256 x 256 tiles, and smaller ones for the columns that would start another: 8192 x 2048 x 7168 has 896
+  // such tiles, three and a half rounds.
+  const Int8Tile& c = kInt8Tiles[0];
+  const int on = pair ? c.bn / 2 : c.bn, tn = ceil_div(N, on);
+  const int64_t column = ceil_div(M, c.bm), rounds = column * tn / c.at_once, n = rounds * c.at_once / column;
+  if (!whole && rounds >= 1 && n >= 1 && n < tn) {
+    const double us = rounds * (steps * c.step + c.fixed) + 3.0 + int8_plan(M, N - (int)n * on, K, pair, true).us;
+    if (us < best.us) best = {0, (int)n * on, us};
+  }
+  return best;
+}
+
+template <typename O>
+static void go(const DenseJob& j, const DenseEpi& e, int tile, hipStream_t st) {
+  if (tile == 0) go<O, 256, 256, 2, 4, 4, 64>(j, e, st);
+  else if (tile == 1) go<O, 256, 128, 4, 2, 3>(j, e, st);
+  else go<O, 64, 64, 2, 2, 4>(j, e, st);
+}
+
+// Output columns from n on.
+template <typename O>
+static void from_column(DenseJob& j, DenseEpi& e, int n) {
+  auto on = [&](auto* v) { return v ? static_cast<decltype(v)>(const_cast<O*>(static_cast<const O*>(v) + n)) : v; };
+  j.N -= n;
+  for (int z = 0; z < 2; ++z) {
+    if (j.B[z][0]) j.B[z][0] = static_cast<const int8_t*>(j.B[z][0]) + n * j.ldb;
+    if (e.col_scale[z]) e.col_scale[z] += n;
+  }
+  e.bias = on(e.bias);
+  e.residual = on(e.residual);
+  e.out[0] = on(e.out[0]);
+}
+
+hipError_t launch_int8(const DenseJob& j, const DenseEpi& e, bool out_bf16, hipStream_t st) {
+  const Int8Plan p = int8_plan(j.M, j.N, j.K, j.pair, false);
   auto by_type = [&](auto* t) {
     using O = std::remove_pointer_t<decltype(t)>;
-    if (best == 0) go<O, 256, 256, 2, 4, 4, 64>(j, e, st);
-    else if (best == 1) go<O, 256, 128, 4, 2, 3>(j, e, st);
-    else go<O, 64, 64, 2, 2, 4>(j, e, st);
+    DenseJob left = j, right = j;
+    DenseEpi er = e;
+    if (p.cut) left.N = p.cut;
+    go<O>(left, e, p.tile, st);
+    if (!p.cut) return;
+    from_column<O>(right, er, p.cut);
+    go<O>(right, er, int8_plan(right.M, right.N, right.K, right.pair, true).tile, st);
   };
   if (out_bf16) by_type(static_cast<uint16_t*>(nullptr));
   else by_type(static_cast<float*>(nullptr));

@@ -451,7 +451,7 @@ def test_int8_dense(size, dtype):
 # whole rounds of the largest tiles, and ragged ones on each
 @pytest.mark.parametrize("dtype", ("bf16", "f32"))
 @pytest.mark.parametrize("size", [(4104, 1096, 4112), (2050, 4096, 4104), (5100, 1096, 4090), (8200, 520, 4100), (1030, 2056, 2100),
-                                  (5000, 300, 2200)], ids=str)
+                                  (5000, 300, 2200), (8192, 72, 2312), (8200, 1032, 7100)], ids=str)
 def test_int8_dense_large(size, dtype):
     T, K, N = size
     gen = torch.Generator().manual_seed(T)
