@@ -110,8 +110,8 @@ __device__ __forceinline__ void rows_tile(const DenseJob& j, const DenseEpi& e, 
   const int64_t row = uniform(tile.x), expert = uniform(tile.z);
   w.mt = 0;
   const MmPart at{uniform(tile.y), j.K, row * j.lda, expert * w_stride, row * e.ldo, row, expert * j.N};
-  mm_body<T, O, BM, BN, WM, WN, S, SB, DB, false, B_COL, PAIR, KIND, true, STREAM, HEIGHT>(j, e, MmSlices{nullptr, 1, 1, 0}, w, at, s0, s1,
-                                                                           s2, s3);
+  mm_body<T, O, BM, BN, WM, WN, S, SB, DB, false, B_COL, PAIR, KIND, true, STREAM, HEIGHT>(j, e, MmSlices{nullptr, 1, 1, 0}, w, at, s0,
+                                                                                          s1, s2, s3);
 }
 
 // Zeros in the bytes lo .. hi of p (2-byte aligned), in 16-byte chunks but for the ends.
@@ -186,8 +186,8 @@ static int64_t most_tiles(int R, int E, int bm) { return R / bm + (R < E ? R : E
 // two in LDS), reads each weight panel least often: 32768 rows of 128 experts, 768 -> 2048, take 149 us, where 256 x 256
 // (half of the experts have a few rows more) takes 189 and 128 x 256 180; 62580 rows of 32, 7168 -> 2048 gated, 3315, 3432 and
 // 4161.  Two workgroups of 128 x 256 on a CU overlap one's first loads and stores with the other's products, which is best
-// for the shortest contractions (270 rows of each of 128 experts, 256 -> 2048: 86 and 98, 200 rows 4 us less); 64 x 64 waste
-// least on few rows (32768 rows of 128, 768 -> 2048: 272).
+// for the shortest contractions (1024 rows of each of 32 experts, 256 -> 2048: 61 us, 64 on the tallest; 512 -> 2048: 89 and
+// 90); 64 x 64 leave fewest CUs idle (64 rows of each of 8, 2048 -> 768 gated: 14 us, 35 on 128 x 256; the 149 us above: 272).
 struct GroupedTile {
   int bm, bn, at_once;
   double step, fixed, step_alone, fixed_alone;
@@ -211,8 +211,10 @@ static double rounds_us(const GroupedTile& c, double items, double steps) {
 }
 
 // Tiles of bm rows that an expert with about `rows` takes, on average over row counts spread normally around it (by
-// their square root and a twentieth): 1 + the chances of more than one tile's, two tiles' .. rows.
+// their square root and a twentieth): 1 + the chances of more than one tile's, two tiles' .. rows.  Of many tiles the last
+// is half empty.
 static double mean_tiles(double rows, int bm) {
+  if (rows > 8.0 * bm) return rows / bm + 0.5;
   const double spread = sqrt(rows) + 0.05 * rows;
   double tiles = 1 + floor(fmax(0.0, rows - 4 * spread) / bm);
   for (double i = tiles; i * bm < rows + 4 * spread; ++i) tiles += 0.5 * erfc((i * bm - rows) / (spread * 1.4142135623730951));
