@@ -191,7 +191,7 @@ __device__ __forceinline__ MmWhere mm_where(int block, int tm, int tn, int batch
 
 // The product that a tile belongs to: its rows and contraction length and where its operands and its
 // output start (elements), as one of those that a grouped launch covers.  row, col: its first row
-// and column among the scales of an integer product.
+// and column among the scales of an integer product; row too among those of a grouped launch's slices.
 struct MmPart {
   int M, K;
   int64_t a, b, o;
@@ -203,6 +203,7 @@ struct MmPart {
 struct MmSlices {
   float* part;   // NULL: one slice, straight to the epilogue
   int slices, planes, ldp;
+  int rows;      // of a plane, in a grouped launch: those of all its products
   __device__ __forceinline__ f32x4* at(int slice, int plane, int m, int n, int M) const {  // n: a multiple of 8
     return reinterpret_cast<f32x4*>(part + (((int64_t)slice * planes + plane) * M + m) * ldp + n);
   }
@@ -528,11 +529,11 @@ __device__ __forceinline__ void mm_body(const DenseJob& j, const DenseEpi& e, co
       for (int r = lr; r < PM; r += RPI) {
         const int m = mp + r - lr;
         if (m >= at.M || n >= j.N) continue;
-        f32x4* o = sl.at(slice, z, m, n, at.M);
+        f32x4* o = sl.at(slice, z, GROUPED ? (int)at.row + m : m, n, GROUPED ? sl.rows : at.M);
         o[0] = chunk(r, 2 * lc);
         o[1] = chunk(r, 2 * lc + 1);
         if (PAIR) {
-          o = sl.at(slice, 1, m, n, at.M);
+          o = sl.at(slice, 1, GROUPED ? (int)at.row + m : m, n, GROUPED ? sl.rows : at.M);
           o[0] = chunk(r, CH / 2 + 2 * lc);
           o[1] = chunk(r, CH / 2 + 2 * lc + 1);
         }

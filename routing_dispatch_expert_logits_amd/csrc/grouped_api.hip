@@ -49,9 +49,9 @@ int64_t code_bytes(int64_t cols) { return (cols + 15) / 16 * 16; }
 
 // x, w[2]: padded copies (0 bytes where the operand is read in place); d0, d1: the gradient before the
 // activation as operand of the products, lo elements between its terms; finite: x with zeros for infinities
-// and NaN, for the terms after the first; table: the row tiles.
+// and NaN, for the terms after the first; scratch: the row tiles and a cut contraction's sums.
 struct GroupedWs {
-  size_t x, w[2], d0, d1, finite, table, total;
+  size_t x, w[2], d0, d1, finite, scratch, total;
   int terms;
   int64_t lo, ldk, ldn;
 };
@@ -74,9 +74,9 @@ GroupedWs grouped_ws(const GroupedDims& d, bool gated, bool backward, bool int8)
     w.d1 = c.take(gated ? bytes : 0);
     w.finite = c.take(w.terms > 1 ? (size_t)d.R * w.ldk * d.es : 0);
   }
-  w.table = c.take(d.R == 0 || decode ? 0
-                   : backward ? grouped_table_bytes(t, d.R, d.E, d.K, d.N, gated ? 2 : 1, false, true)
-                              : grouped_table_bytes(t, d.R, d.E, d.N, d.K, 1, gated, false));
+  w.scratch = c.take(d.R == 0 || decode ? 0
+                   : backward ? grouped_scratch_bytes(t, d.R, d.E, d.K, d.N, gated ? 2 : 1, false, true)
+                              : grouped_scratch_bytes(t, d.R, d.E, d.N, d.K, 1, gated, false));
   w.total = c.cur;
   return w;
 }
@@ -115,7 +115,7 @@ moe_status forward(const GroupedDims& d, const GroupedWs& w, GroupedType t, cons
   e.out_f32 = !d.bf16;
   const int64_t w_stride = (int64_t)d.N * w.ldk;
   MOE_HIP(d.R <= kDecodeRows ? launch_grouped_decode(j, e, t, d.bf16, g, w_stride, st)
-                                    : launch_grouped(j, e, t, d.bf16, g, w_stride, at<void>(ws, w.table), st));
+                                    : launch_grouped(j, e, t, d.bf16, g, w_stride, at<void>(ws, w.scratch), st));
   return MOE_OK;
 }
 
@@ -149,7 +149,7 @@ moe_status gradients(const GroupedDims& d, const GroupedWs& w, const void* d0, c
   jw.ldb = w.ldk;
   pw.e.out_f32 = d.grad_f32;
   pw.e.out[0] = dw0; pw.e.out[1] = dw1;
-  MOE_HIP(launch_grouped_grads(dx ? &px : nullptr, dw0 ? &pw : nullptr, t, g, (int64_t)d.N * w.ldk, at<void>(ws, w.table), st));
+  MOE_HIP(launch_grouped_grads(dx ? &px : nullptr, dw0 ? &pw : nullptr, t, g, (int64_t)d.N * w.ldk, at<void>(ws, w.scratch), st));
   return MOE_OK;
 }
 

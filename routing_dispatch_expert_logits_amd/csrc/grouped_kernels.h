@@ -27,8 +27,8 @@ enum GroupedType { GROUPED_F32 = 0, GROUPED_BF16 = 1, GROUPED_INT8 = 2 };
 
 // Rows by their expert's weight: job j of one expert (M unused), whose weights are w_stride elements apart and whose
 // row operands and outputs are those of its rows; j.b_col: the gradient's product, across the weights' rows.
-// scratch: grouped_table_bytes.  out_bf16: what an integer product's epilogue writes.
-size_t grouped_table_bytes(GroupedType t, int R, int E, int N, int K, int segs, bool pair, bool b_col);
+// scratch: grouped_scratch_bytes, for the table of tiles and a cut contraction's sums.  out_bf16: what an integer product's epilogue writes.
+size_t grouped_scratch_bytes(GroupedType t, int R, int E, int N, int K, int segs, bool pair, bool b_col);
 hipError_t launch_grouped(const DenseJob& j, const DenseEpi& e, GroupedType t, bool out_bf16, const Groups& g,
                           int64_t w_stride, void* scratch, hipStream_t st);
 // Forward products of at most kDecodeRows rows, whose operands may have rows of any length (codes: whole 16-byte

@@ -86,32 +86,37 @@ struct TileFinder {
   }
 };
 
+// Products on these tiles may be cut along the contraction.
+template <typename T, int BM, int BN>
+constexpr bool kCuts = BM == 64 && BN == 64 && sizeof(T) != 1;
+
 // The tile of workgroup `block`: rows of one expert by columns of its weight.  table: the m-tiles, or NULL.
 template <typename T, typename O, int BM, int BN, int WM, int WN, int S, int SB, int DB, bool B_COL, bool PAIR, int KIND,
           bool STREAM, int HEIGHT>
 __device__ __forceinline__ void rows_tile(const DenseJob& j, const DenseEpi& e, const Groups& g, const int4* table,
-                                          int64_t w_stride, int block, uint16_t* s0, uint16_t* s1, uint16_t* s2, uint16_t* s3) {
+                                          int64_t w_stride, const MmSlices& cut, int block, uint16_t* s0, uint16_t* s1,
+                                          uint16_t* s2, uint16_t* s3) {
   const int tn = ceil_div(j.N, PAIR ? BN / 2 : BN);
+  const MmSlices sl = kCuts<T, BM, BN> ? cut : MmSlices{nullptr, 1, 1, 0, 0};
   MmWhere w;
   int4 tile;
   if (table) {
     const int total = uniform(table[0].x);
     if (total == 0) return;
-    w = mm_where(block, total, tn, 1, 1);
+    w = mm_where(block, total, tn, 1, sl.slices);
     if (!w.ok) return;
     tile = table[1 + w.mt];
   } else {
     const TileFinder f(g, HEIGHT);
     if (f.total == 0) return;
-    w = mm_where(block, f.total, tn, 1, 1);
+    w = mm_where(block, f.total, tn, 1, sl.slices);
     if (!w.ok) return;
     tile = f.at(w.mt);
   }
   const int64_t row = uniform(tile.x), expert = uniform(tile.z);
   w.mt = 0;
   const MmPart at{uniform(tile.y), j.K, row * j.lda, expert * w_stride, row * e.ldo, row, expert * j.N};
-  mm_body<T, O, BM, BN, WM, WN, S, SB, DB, false, B_COL, PAIR, KIND, true, STREAM, HEIGHT>(j, e, MmSlices{nullptr, 1, 1, 0}, w, at, s0,
-                                                                                          s1, s2, s3);
+  mm_body<T, O, BM, BN, WM, WN, S, SB, DB, false, B_COL, PAIR, KIND, true, STREAM, HEIGHT>(j, e, sl, w, at, s0, s1, s2, s3);
 }
 
 // Zeros in the bytes lo .. hi of p (2-byte aligned), in 16-byte chunks but for the ends.
@@ -142,17 +147,17 @@ __device__ __forceinline__ void dw_tile(const DenseJob& j, const DenseEpi& e, co
     return zero_bytes(static_cast<char*>(e.out[w.z]) + expert * bytes, bytes / 2 * tile / tiles * 2, bytes / 2 * (tile + 1) / tiles * 2);
   }
   const MmPart at{j.M, uniform(r.y - r.x), row * j.lda, row * j.ldb, (int64_t)expert * j.M * e.ldo, 0, 0};
-  mm_body<T, T, BM, BN, WM, WN, S, SB, DB, true, true, false, DENSE_STORE, true>(j, e, MmSlices{nullptr, 1, 1, 0}, w, at, s0, s1,
+  mm_body<T, T, BM, BN, WM, WN, S, SB, DB, true, true, false, DENSE_STORE, true>(j, e, MmSlices{nullptr, 1, 1, 0, 0}, w, at, s0, s1,
                                                                            s2, s3);
 }
 
 template <typename T, typename O, int BM, int BN, int WM, int WN, int S, int SB, int DB, bool B_COL, bool PAIR, int KIND,
           bool STREAM, int HEIGHT>
 __global__ __launch_bounds__(WM* WN * 64, 2) void k_grouped_mm(DenseJob j, DenseEpi e, Groups g,
-                                                               const int4* __restrict__ table, int64_t w_stride) {
+                                                               const int4* __restrict__ table, int64_t w_stride, MmSlices sl) {
   constexpr int STAGE = kMmStage<BM, BN, SB>;
   __shared__ __attribute__((aligned(1024))) uint16_t s0[STAGE], s1[STAGE], s2[STAGE], s3[S > 3 ? STAGE : 1];
-  rows_tile<T, O, BM, BN, WM, WN, S, SB, DB, B_COL, PAIR, KIND, STREAM, HEIGHT>(j, e, g, table, w_stride, blockIdx.x, s0, s1, s2, s3);
+  rows_tile<T, O, BM, BN, WM, WN, S, SB, DB, B_COL, PAIR, KIND, STREAM, HEIGHT>(j, e, g, table, w_stride, sl, blockIdx.x, s0, s1, s2, s3);
 }
 
 template <typename T, int BM, int BN, int WM, int WN, int S, int SB, int DB>
@@ -165,16 +170,38 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void k_grouped_dw(DenseJob j, Dense
 // A backward pass's two products on 64 x 64 tiles in one launch: small ones leave the device half empty on their own.
 // The first `first` workgroups are dx's (dx_first) or the weight gradients', whichever's contraction is longer.
 template <typename T, int S, int DB>
-__global__ __launch_bounds__(256, 2) void k_grouped_two(DenseJob jx, DenseEpi ex, int64_t w_stride, DenseJob jw, DenseEpi ew,
-                                                        int first, bool dx_first, Groups g, const int4* __restrict__ table) {
+__global__ __launch_bounds__(256, 2) void k_grouped_two(DenseJob jx, DenseEpi ex, int64_t w_stride, MmSlices sl, DenseJob jw,
+                                                        DenseEpi ew, int first, bool dx_first, Groups g, const int4* __restrict__ table) {
   constexpr int STAGE = kMmStage<64, 64, 128>;
   __shared__ __attribute__((aligned(1024))) uint16_t s0[STAGE], s1[STAGE], s2[STAGE], s3[S > 3 ? STAGE : 1];
   const bool early = (int)blockIdx.x < first;
   const int block = early ? blockIdx.x : blockIdx.x - first;
   if (early == dx_first)
-    rows_tile<T, T, 64, 64, 2, 2, S, 128, DB, true, false, DENSE_STORE, false, 64>(jx, ex, g, table, w_stride, block, s0, s1, s2, s3);
+    rows_tile<T, T, 64, 64, 2, 2, S, 128, DB, true, false, DENSE_STORE, false, 64>(jx, ex, g, table, w_stride, sl, block, s0, s1, s2, s3);
   else
     dw_tile<T, 64, 64, 2, 2, S, 128, DB>(jw, ew, g, block, s0, s1, s2, s3);
+}
+
+// The slices' sums in ascending order, then the epilogue, for the rows of all experts; eight columns per thread.
+template <typename T, int KIND>
+__global__ __launch_bounds__(256) void k_grouped_join(DenseEpi e, MmSlices sl, int N, Groups g) {
+  const int first = min(max(g.offsets[0], 0), g.R), rows = min(g.offsets[g.E], g.R) - first, n8 = sl.ldp / 8;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < (int64_t)rows * n8; i += (int64_t)gridDim.x * 256) {
+    const int m = first + (int)(i / n8), n = (int)(i % n8) * 8;
+    float a[8] = {}, b[8] = {};
+#pragma unroll 4
+    for (int s = 0; s < sl.slices; ++s) {
+      const f32x4* p = sl.at(s, 0, m, n, sl.rows);
+      for (int k = 0; k < 8; ++k) a[k] += p[k >> 2][k & 3];
+      if (KIND == DENSE_GATED) {
+        p = sl.at(s, 1, m, n, sl.rows);
+        for (int k = 0; k < 8; ++k) b[k] += p[k >> 2][k & 3];
+      }
+    }
+    with_act<KIND>(e.act, [&](auto act) __attribute__((always_inline)) {
+      mm_out8<T, KIND, act()>(e, 0, 0, m, n, N, a, b, Raw8<T>{}, Raw8<T>{});
+    });
+  }
 }
 
 // m-tiles of bm rows that R rows of E experts can take at most.
@@ -191,10 +218,12 @@ static int64_t most_tiles(int R, int E, int bm) { return R / bm + (R < E ? R : E
 struct GroupedTile {
   int bm, bn, at_once;
   double step, fixed, step_alone, fixed_alone;
+  int slices = 1;   // of the contraction
 };
 constexpr GroupedTile kTiles[] = {{320, 256, 256, 2.0, 11.5, 2.0, 11.5},
                                   {128, 256, 512, 2.2, 7.0, 1.3, 6.0},
                                   {64, 64, 512, 0.42, 3.0, 0.19, 2.5}};
+constexpr GroupedTile kTileF32 = {64, 64, 512, 0.84, 2.0, 0.57, 2.5};
 // Besides, there is no activation to meet and no tile to look up.
 constexpr GroupedTile kTilesDw[] = {{256, 256, 256, 1.75, 5.6, 1.75, 11.5},
                                     {128, 256, 512, 2.2, 5.0, 1.3, 6.0},
@@ -221,22 +250,37 @@ static double mean_tiles(double rows, int bm) {
   return tiles;
 }
 
-// R rows of E experts by their N columns.
+// R rows of E experts by their N columns.  Products whose 64 x 64 tiles are too few for the device are cut along the
+// contraction, at least 4 steps a slice; the slices' sums are written and read again, and joined by a launch of their
+// own, at 4 us and 5 TB/s.  Whole and cut: 238 rows of 3 experts, 6960 -> 512, 34.1 and 14.8 us; 100 of 4, 2048 -> 768,
+// 11.4 and 9.4; dx and dw of 2 fp32 rows of 3, 192 -> 3328, 64.5 and 13.9.  Integer products are not cut: their sums are exact.
 static GroupedTile tile_of(GroupedType t, int R, int E, int N, int K, int segs, bool pair, bool b_col) {
-  if (t == GROUPED_F32) return kTiles[2];
-  if (!b_col && R <= (int64_t)kStreamRows * E && (int64_t)(R < E ? R : E) * ceil_div(N, pair ? 64 : 128) >= 512) return kStreamTile;
-  const double experts = R < E ? R : E, steps = ceil_div(K, t == GROUPED_INT8 ? 128 : 64) * segs;
-  const GroupedTile* best = nullptr;
+  if (t != GROUPED_F32 && !b_col && R <= (int64_t)kStreamRows * E && (int64_t)(R < E ? R : E) * ceil_div(N, pair ? 64 : 128) >= 512) return kStreamTile;
+  const double experts = R < E ? R : E, steps = ceil_div(K, t == GROUPED_INT8 ? 128 : t == GROUPED_BF16 ? 64 : 32) * segs;
+  GroupedTile best{};
   double least = 0;
-  for (const GroupedTile& c : kTiles) {
-    const double us = rounds_us(c, experts * mean_tiles(R / experts, c.bm) * ceil_div(N, pair ? c.bn / 2 : c.bn), steps);
-    if (!best || us < least) best = &c, least = us;
-  }
-  return *best;
+  auto consider = [&](GroupedTile c) {
+    const double items = experts * mean_tiles(R / experts, c.bm) * ceil_div(N, pair ? c.bn / 2 : c.bn);
+    const int most = c.bm == 64 && t != GROUPED_INT8 && items < 256 ? 32 : 1;
+    for (int s = 1; s == 1 || (s <= most && 4 * s <= steps); s += s < 4 ? 1 : s / 2) {
+      const double us = rounds_us(c, items * s, ceil(steps / s)) + (s > 1 ? 4.0 + (double)s * (pair ? 2 : 1) * R * N * 8 / 5e6 : 0.0);
+      if (best.bm && us >= least) continue;
+      least = us;
+      best = c;
+      best.slices = s;
+    }
+  };
+  if (t == GROUPED_F32) consider(kTileF32);
+  else for (const GroupedTile& c : kTiles) consider(c);
+  return best;
 }
 
-size_t grouped_table_bytes(GroupedType t, int R, int E, int N, int K, int segs, bool pair, bool b_col) {
-  return 16 * (size_t)(1 + most_tiles(R, E, tile_of(t, R, E, N, K, segs, pair, b_col).bm));
+static size_t table_bytes(const GroupedTile& c, int R, int E) { return (16 * (size_t)(1 + most_tiles(R, E, c.bm)) + 255) / 256 * 256; }
+static int row_of_sums(int N) { return (N + 7) / 8 * 8; }
+
+size_t grouped_scratch_bytes(GroupedType t, int R, int E, int N, int K, int segs, bool pair, bool b_col) {
+  const GroupedTile c = tile_of(t, R, E, N, K, segs, pair, b_col);
+  return table_bytes(c, R, E) + (c.slices > 1 ? (size_t)c.slices * (pair ? 2 : 1) * R * row_of_sums(N) * 4 : 0);
 }
 
 // Rows of the weights of experts that have rows, padded: eight elements of a row per thread; blockIdx.y the expert.
@@ -275,12 +319,15 @@ static unsigned whole_eights(int64_t items) { return (unsigned)((items + 7) / 8 
 struct RowsGrid {
   GroupedTile c;
   unsigned blocks;
+  MmSlices sl;
 };
 static hipError_t rows_grid(const DenseJob& j, GroupedType t, const Groups& g, RowsGrid* r, const int4** table, void* scratch,
                             hipStream_t st) {
   r->c = tile_of(t, g.R, g.E, j.N, j.K, j.segs, j.pair, j.b_col);
-  const int64_t tiles = most_tiles(g.R, g.E, r->c.bm), items = tiles * ceil_div(j.N, j.pair ? r->c.bn / 2 : r->c.bn);
+  const int64_t tiles = most_tiles(g.R, g.E, r->c.bm), items = tiles * ceil_div(j.N, j.pair ? r->c.bn / 2 : r->c.bn) * r->c.slices;
   r->blocks = whole_eights(items);
+  r->sl = MmSlices{nullptr, r->c.slices, j.pair ? 2 : 1, row_of_sums(j.N), g.R};
+  if (r->c.slices > 1) r->sl.part = reinterpret_cast<float*>(static_cast<char*>(scratch) + table_bytes(r->c, g.R, g.E));
   *table = nullptr;
   if (items <= 2 * r->c.at_once) return hipSuccess;
   *table = static_cast<int4*>(scratch);
@@ -290,23 +337,40 @@ static hipError_t rows_grid(const DenseJob& j, GroupedType t, const Groups& g, R
 }
 
 template <typename T, typename O, int BM, int BN, int WM, int WN, int S, int SB = 128, int DB = 16, bool STREAM = false, int HEIGHT = BM>
-static void go(const DenseJob& j, const DenseEpi& e, const Groups& g, const int4* t, unsigned grid, int64_t w_stride, hipStream_t st) {
+static void go(const DenseJob& j, const DenseEpi& e, const Groups& g, const int4* t, const RowsGrid& r, int64_t w_stride, hipStream_t st) {
+  const unsigned grid = r.blocks;
   const int block = WM * WN * 64;
-  if (j.pair) k_grouped_mm<T, O, BM, BN, WM, WN, S, SB, DB, false, true, DENSE_GATED, STREAM, HEIGHT><<<grid, block, 0, st>>>(j, e, g, t, w_stride);
-  else if constexpr (sizeof(T) == 1) k_grouped_mm<T, O, BM, BN, WM, WN, S, SB, DB, false, false, DENSE_STORE, STREAM, HEIGHT><<<grid, block, 0, st>>>(j, e, g, t, w_stride);
-  else if (!STREAM && j.b_col) k_grouped_mm<T, O, BM, BN, WM, WN, S, SB, DB, !STREAM, false, DENSE_STORE, STREAM, HEIGHT><<<grid, block, 0, st>>>(j, e, g, t, w_stride);
-  else k_grouped_mm<T, O, BM, BN, WM, WN, S, SB, DB, false, false, DENSE_STORE, STREAM, HEIGHT><<<grid, block, 0, st>>>(j, e, g, t, w_stride);
+  if (j.pair) k_grouped_mm<T, O, BM, BN, WM, WN, S, SB, DB, false, true, DENSE_GATED, STREAM, HEIGHT><<<grid, block, 0, st>>>(j, e, g, t, w_stride, r.sl);
+  else if constexpr (sizeof(T) == 1) k_grouped_mm<T, O, BM, BN, WM, WN, S, SB, DB, false, false, DENSE_STORE, STREAM, HEIGHT><<<grid, block, 0, st>>>(j, e, g, t, w_stride, r.sl);
+  else if (!STREAM && j.b_col) k_grouped_mm<T, O, BM, BN, WM, WN, S, SB, DB, !STREAM, false, DENSE_STORE, STREAM, HEIGHT><<<grid, block, 0, st>>>(j, e, g, t, w_stride, r.sl);
+  else k_grouped_mm<T, O, BM, BN, WM, WN, S, SB, DB, false, false, DENSE_STORE, STREAM, HEIGHT><<<grid, block, 0, st>>>(j, e, g, t, w_stride, r.sl);
 }
 template <typename T, typename O>
 static void go_tile(const DenseJob& j, const DenseEpi& e, const Groups& g, const int4* t, const RowsGrid& r, int64_t w_stride,
                     hipStream_t st) {
-  if (r.c.bm == 320) go<T, O, 384, 256, 2, 4, 4, 64, 16, false, 320>(j, e, g, t, r.blocks, w_stride, st);
-  else if (r.c.bm == 128) go<T, O, 128, 256, 2, 2, 3, 64>(j, e, g, t, r.blocks, w_stride, st);
-  else if (r.c.bn == kStreamTile.bn) go<T, O, 64, 128, 1, 4, 3, 128, 16, true>(j, e, g, t, r.blocks, w_stride, st);
-  else go<T, O, 64, 64, 2, 2, 4>(j, e, g, t, r.blocks, w_stride, st);
+  if (r.c.bm == 320) go<T, O, 384, 256, 2, 4, 4, 64, 16, false, 320>(j, e, g, t, r, w_stride, st);
+  else if (r.c.bm == 128) go<T, O, 128, 256, 2, 2, 3, 64>(j, e, g, t, r, w_stride, st);
+  else if (r.c.bn == kStreamTile.bn) go<T, O, 64, 128, 1, 4, 3, 128, 16, true>(j, e, g, t, r, w_stride, st);
+  else go<T, O, 64, 64, 2, 2, 4>(j, e, g, t, r, w_stride, st);
 }
 
 static bool whole_chunks(const DenseJob& j) { return j.lda % 4 == 0 && j.ldb % 4 == 0; }
+
+// The epilogue of a product's slices, if it was cut.
+template <typename T>
+static void join_kind(const DenseJob& j, const DenseEpi& e, const RowsGrid& r, const Groups& g, hipStream_t st) {
+  const int64_t want = ((int64_t)g.R * (r.sl.ldp / 8) + 255) / 256;
+  const unsigned grid = (unsigned)(want < 4096 ? want : 4096);
+  if (j.pair) k_grouped_join<T, DENSE_GATED><<<grid, 256, 0, st>>>(e, r.sl, j.N, g);
+  else k_grouped_join<T, DENSE_STORE><<<grid, 256, 0, st>>>(e, r.sl, j.N, g);
+}
+static hipError_t join(const DenseJob& j, const DenseEpi& e, GroupedType t, const RowsGrid& r, const Groups& g, hipStream_t st) {
+  hipError_t s = hipGetLastError();
+  if (s != hipSuccess || !r.sl.part) return s;
+  if (t == GROUPED_F32) join_kind<float>(j, e, r, g, st);
+  else join_kind<uint16_t>(j, e, r, g, st);
+  return hipGetLastError();
+}
 
 hipError_t launch_grouped(const DenseJob& j, const DenseEpi& e, GroupedType t, bool out_bf16, const Groups& g,
                           int64_t w_stride, void* scratch, hipStream_t st) {
@@ -314,8 +378,8 @@ hipError_t launch_grouped(const DenseJob& j, const DenseEpi& e, GroupedType t, b
   const int4* tab;
   if (hipError_t s = rows_grid(j, t, g, &r, &tab, scratch, st); s != hipSuccess) return s;
   if (t == GROUPED_F32) {
-    if (whole_chunks(j)) go<float, float, 64, 64, 2, 2, 3>(j, e, g, tab, r.blocks, w_stride, st);
-    else go<float, float, 64, 64, 2, 2, 3, 128, 4>(j, e, g, tab, r.blocks, w_stride, st);
+    if (whole_chunks(j)) go<float, float, 64, 64, 2, 2, 3>(j, e, g, tab, r, w_stride, st);
+    else go<float, float, 64, 64, 2, 2, 3, 128, 4>(j, e, g, tab, r, w_stride, st);
   } else if (t == GROUPED_BF16) {
     go_tile<uint16_t, uint16_t>(j, e, g, tab, r, w_stride, st);
   } else if (out_bf16) {
@@ -323,7 +387,7 @@ hipError_t launch_grouped(const DenseJob& j, const DenseEpi& e, GroupedType t, b
   } else {
     go_tile<int8_t, float>(j, e, g, tab, r, w_stride, st);
   }
-  return hipGetLastError();
+  return join(j, e, t, r, g, st);
 }
 
 // Tile of the weight gradients: as many rows for every expert (32768 rows of 128, 2048 -> 768 gated: 331 us on 256 x 256, 365
@@ -369,13 +433,13 @@ hipError_t launch_grouped_grads(const GroupedProduct* dx, const GroupedProduct* 
   RowsGrid r;
   const int4* tab;
   if (hipError_t s = rows_grid(dx->j, t, g, &r, &tab, scratch, st); s != hipSuccess) return s;
-  const bool dx_first = (int64_t)dx->j.K * dx->j.segs >= (int64_t)g.R / g.E * dw->j.segs;
+  const bool dx_first = (int64_t)dx->j.K * dx->j.segs / r.c.slices >= (int64_t)g.R / g.E * dw->j.segs;
   const unsigned blocks = dw_blocks(dw->j, c, g), first = dx_first ? r.blocks : blocks, all = r.blocks + blocks;
-  auto go = [&](auto kernel) { kernel<<<all, 256, 0, st>>>(dx->j, dx->e, w_stride, dw->j, dw->e, (int)first, dx_first, g, tab); };
+  auto go = [&](auto kernel) { kernel<<<all, 256, 0, st>>>(dx->j, dx->e, w_stride, r.sl, dw->j, dw->e, (int)first, dx_first, g, tab); };
   if (t == GROUPED_BF16) go(k_grouped_two<uint16_t, 4, 16>);
   else if (whole_chunks(dx->j) && whole_chunks(dw->j)) go(k_grouped_two<float, 3, 16>);
   else go(k_grouped_two<float, 3, 4>);
-  return hipGetLastError();
+  return join(dx->j, dx->e, t, r, g, st);
 }
 
 }  // namespace moe

@@ -187,6 +187,19 @@ def test_gated_backward(case, dtype, grad):
 
 
 # Sizes on the larger tiles; the 64-bit products run on the GPU.
+# long contractions with few tiles, which the products by rows cut into slices
+LONG = [([3, 0, 2], 1, 2, 2056, 1100), ([40, 1, 0, 70], 0, 5, 1100, 2048), ([238], 0, 0, 6960, 512), ([0, 33], 2, 0, 515, 3329),
+        ([1, 20], 0, 1, 4096, 64), ([0, 0], 3, 30, 2048, 72), ([65, 64, 0, 63], 1, 0, 1536, 40)]
+
+
+@pytest.mark.parametrize("dtype", ("bf16", "f32"))
+@pytest.mark.parametrize("case", LONG, ids=case_id)
+def test_cut_contractions(case, dtype):
+    test_linear(case, dtype)
+    test_gated(case, dtype)
+    test_gated_backward(case, dtype, "f32")
+
+
 def spread_cases(n):
     r = random.Random(31)
     log = lambda lo, hi: int(math.exp(r.uniform(math.log(lo), math.log(hi))))  # noqa: E731

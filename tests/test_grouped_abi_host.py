@@ -188,3 +188,15 @@ def test_binding_refuses_other_tensors():
         B.quantize_int8(x, torch.zeros(4, 16, dtype=torch.int8), torch.zeros(4))
     with pytest.raises(B.MoeError, match="not on a GPU"):
         B.combine_backward(x, x, off, x, x, x, B.MOE_F32, B.shape(4, 16, 2, 1, 64, dtype="f32"))
+
+
+@pytest.mark.parametrize("dtype", ("bf16", "f32"))
+def test_cut_contractions_have_room_for_their_sums(dtype):
+    """Few tiles with a long contraction: the sums of two slices at least, besides the tiles' table; none
+    where the contraction is short, or in integers."""
+    for call, R, K, N, planes, width in ((LF, 238, 6960, 512, 1, 512), (GF, 238, 4096, 64, 2, 64), (LB, 40, 128, 4096, 1, 128),
+                                         (GB, 40, 128, 4096, 1, 128)):
+        s = shape(call, R=R, K=K, N=N, E=2, dtype=dtype)
+        assert B.grouped_workspace_bytes(s, CALL[call]) > 2 * planes * R * width * 4
+    for call, K in ((LF, 64), (LI, 6960)):
+        assert B.grouped_workspace_bytes(shape(call, R=238, K=K, N=512, E=2, dtype=dtype), CALL[call]) <= 1024
