@@ -200,6 +200,35 @@ def test_cut_contractions(case, dtype):
     test_gated_backward(case, dtype, "f32")
 
 
+def test_cut_contraction_in_a_graph_reads_new_offsets():
+    """Replays with other row counts: every replay is the eager call's result, and rows of no expert stay."""
+    R, K, N, E = 150, 4096, 200, 3
+    gen = torch.Generator().manual_seed(3)
+    x, w = (rand(gen, *n, dtype="bf16").to(DEV) for n in ((R, K), (E, N, K)))
+    off = offsets_of([50, 50, 50]).to(DEV)
+    s = B.grouped_shape(R, K, N, E)
+    ws, y, eager = ws_for(s, B.MOE_CALL_GROUPED_LINEAR_FORWARD), out((R, N), "bf16"), out((R, N), "bf16")
+    B.grouped_linear_forward(x, off, w, y, s, ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        B.grouped_linear_forward(x, off, w, y, s, ws)
+    for counts, first in (([150, 0, 0], 0), ([0, 0, 1], 7), ([0, 0, 0], 4), ([64, 65, 3], 18), ([1, 0, 100], 2)):
+        now = offsets_of(counts, first)
+        off.copy_(now)
+        for t in (y, eager):
+            t.view(torch.uint8).fill_(gu.POISON)
+        B.grouped_linear_forward(x, off, w, eager, s, ws)
+        ws.fill_(0xFF)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y.view(torch.int16), eager.view(torch.int16))
+        rows_left(y, now, "y")
+        ref, tol = by_groups(now, x.cpu().double(), w.cpu().double(), K)
+        v = live(now)
+        check("y", f64(y, "bf16")[v], ref[v], (U["bf16"] * ref.abs() + 2 * tol)[v])
+
+
 def spread_cases(n):
     r = random.Random(31)
     log = lambda lo, hi: int(math.exp(r.uniform(math.log(lo), math.log(hi))))  # noqa: E731
