@@ -667,7 +667,8 @@ MOE_API moe_status moe_grouped_gated_backward(const void* dh, const void* x, con
  * first cols (a caller that makes codes itself, in -127 .. 127, leaves zeros there too: not checked).
  *
  * A product is row_scale col_scale sum(q_x q_w): the sum exactly (whole numbers in 32 bits), the
- * scales in fp32, then the activation and residual as in the bf16 and fp32 products, one rounding to s->dtype.
+ * scales in fp32 (no factor on the way leaves fp32's range where the product does not), then the activation and
+ * residual as in the bf16 and fp32 products, one rounding to s->dtype.
  *
  * Limits: as the dense and grouped products, and K <= 2^17, which keeps the sums in 32 bits.
  */

@@ -158,6 +158,13 @@ __device__ __forceinline__ void store8(T* p, int n, const float* f) {
 }
 
 
+// An integer product is sum row_scale col_scale in this order; a sum of up to 2^31 by a row scale beyond 2^96 could
+// leave fp32's range where the product does not (scales are up to 2^121).  Such a scale is taken as by, 2^-64 of it, and the
+// product multiplied by up = 2^64 at the end: powers of two change no bits, and the products between are normal numbers.
+constexpr float kWideScale = 0x1p96f;
+__device__ __forceinline__ float row_scale_by(float s) { return s > kWideScale ? s * 0x1p-64f : s; }
+__device__ __forceinline__ float row_scale_up(float s) { return s > kWideScale ? 0x1p64f : 1.f; }
+
 // Eight elements as they are in memory: what a load in flight costs in registers.
 template <typename T>
 struct Raw8 {

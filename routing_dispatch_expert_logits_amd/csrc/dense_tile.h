@@ -505,6 +505,16 @@ __device__ __forceinline__ void mm_body(const DenseJob& j, const DenseEpi& e, co
   }
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
+  // One of the wave's rows has a scale of two factors, the second of which follows on the way back.
+  bool wide = false;
+  if constexpr (INT8) {
+#pragma unroll
+    for (int a = 0; a < FM; ++a) {
+      wide |= by_row[a] > kWideScale;
+      by_row[a] = row_scale_by(by_row[a]);
+    }
+    wide = __ballot(wide) != 0;
+  }
   auto pass = [&](auto which) __attribute__((always_inline)) {
     constexpr int p = which();
 #pragma unroll
@@ -547,6 +557,10 @@ __device__ __forceinline__ void mm_body(const DenseJob& j, const DenseEpi& e, co
             if (m >= at.M || n >= j.N || (RPI > PM && r >= PM)) continue;
             f32x4 v[2] = {chunk(r, 2 * lc), chunk(r, 2 * lc + 1)}, u[2] = {v[0], v[1]};
             if (PAIR) u[0] = chunk(r, CH / 2 + 2 * lc), u[1] = chunk(r, CH / 2 + 2 * lc + 1);
+            if (INT8 && wide) {
+              const float up = row_scale_up(e.row_scale[at.row + m]);
+              for (int k = 0; k < 2; ++k) v[k] *= up, u[k] *= up;
+            }
             mm_out8<O, KIND, act(), GROUPED>(e, z, at.o, m, n, j.N, reinterpret_cast<float*>(v), reinterpret_cast<const float*>(u),
                                     bias, res[p][i]);
           }

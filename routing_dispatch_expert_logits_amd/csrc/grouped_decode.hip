@@ -117,8 +117,9 @@ __global__ __launch_bounds__(512) void k_grouped_decode(DenseJob j, DenseEpi e, 
       float v[2] = {(float)sum[0], (float)sum[1]};
       if constexpr (INT8) {
         const int64_t at = (int64_t)expert * j.N + n;
-        v[0] = v[0] * e.row_scale[row] * e.col_scale[0][at];
-        if (PAIR) v[1] = v[1] * e.row_scale[row] * e.col_scale[1][at];
+        const float by = row_scale_by(e.row_scale[row]), up = row_scale_up(e.row_scale[row]);
+        v[0] = v[0] * by * e.col_scale[0][at] * up;
+        if (PAIR) v[1] = v[1] * by * e.col_scale[1][at] * up;
       }
       constexpr bool FAST = sizeof(O) == 2;
       const int64_t idx = (int64_t)row * e.ldo + n;
