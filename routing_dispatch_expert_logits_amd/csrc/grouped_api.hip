@@ -272,6 +272,10 @@ moe_status moe_grouped_gated_backward(const void* dh, const void* x, const int32
     if (dw3) MOE_HIP(launch_fill_zero(dw3, gb, st));
     return MOE_OK;
   }
+  // dg and du enter the bf16 products rounded to bf16, as in the dense gated backward pass: a gradient is sqrt(2) of one
+  // rounding's error from its definition.  A second bf16 term of each would leave its own rounding alone, at twice the
+  // products (32768 rows of 128 experts, 2048 -> 768: 2.35e-3 of the gradients' norm in 634 us, 1.66e-3 in 1055).  Weight
+  // gradients asked for in fp32 take the terms that hold dg and du exactly; dx is rounded to bf16 in any case.
   const int terms = dw1 ? p.terms : 1;
   void *d0 = at<void>(ws, p.d0), *d1 = at<void>(ws, p.d1);
   MOE_HIP(launch_act_grad(dh, g, u, d.act, d.bf16, d.R, d.N, d0, d1, terms, p.lo, p.ldn, nullptr, nullptr, false, nullptr,
