@@ -141,8 +141,12 @@ __global__ __launch_bounds__(512) void k_grouped_decode(DenseJob j, DenseEpi e, 
   }
 }
 
-template <typename T, typename O, int SPLIT, int U = 8>
+template <typename T, typename O, int SPLIT>
 static void go(const DenseJob& j, const DenseEpi& e, const Groups& g, int64_t w_stride, int strips, int experts, hipStream_t st) {
+  // Chunks in flight.  16 take twice the registers, for two waves a SIMD (16 and 8: 8 rows in integers, 8192 -> 8192, 18.4 and
+  // 15.9 us, 7168 -> 2048 8.5 and 8.8; 8 bf16 rows of 4 experts, 4096 -> 2048, 16.1 and 14.0; 8 fp32 rows of 2, 7168 -> 4096,
+  // 59.8 and 52.6).
+  constexpr int U = 8;
   const dim3 grid(ceil_div(strips, 8 / SPLIT), experts);
   if (j.pair) k_grouped_decode<T, O, DENSE_GATED, SPLIT, U><<<grid, 512, 0, st>>>(j, e, g, w_stride);
   else if (e.kind == DENSE_STORE) k_grouped_decode<T, O, DENSE_STORE, SPLIT, U><<<grid, 512, 0, st>>>(j, e, g, w_stride);
@@ -161,8 +165,7 @@ static void go(const DenseJob& j, const DenseEpi& e, const Groups& g, int64_t w_
   if (split == 1) go<T, O, 1>(j, e, g, w_stride, strips, experts, st);
   else if (split == 2) go<T, O, 2>(j, e, g, w_stride, strips, experts, st);
   else if (split == 4) go<T, O, 4>(j, e, g, w_stride, strips, experts, st);
-  else if (chunks <= 64 || strips * experts > 512) go<T, O, 8>(j, e, g, w_stride, strips, experts, st);
-  else go<T, O, 8, 16>(j, e, g, w_stride, strips, experts, st);
+  else go<T, O, 8>(j, e, g, w_stride, strips, experts, st);
 }
 
 hipError_t launch_grouped_decode(const DenseJob& j, const DenseEpi& e, GroupedType t, bool out_bf16, const Groups& g,
