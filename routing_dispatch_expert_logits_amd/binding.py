@@ -9,6 +9,7 @@ import fails.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 from typing import Optional
@@ -484,9 +485,10 @@ def combine_backward(dout, y_perm, token_row, topk_w, dy_perm, dtopk_w, out_dtyp
 # ---- products in 8-bit integers with a scale for each token and channel
 
 
+@functools.lru_cache(maxsize=1024)   # a call into the library takes longer than the checks that ask
 def int8_row_bytes(cols: int) -> int:
-    """Length of a row of `cols` codes: moe_int8_row_bytes, in whole 16-byte chunks."""
-    return (cols + 15) // 16 * 16 if 1 <= cols <= 1 << 21 else 0
+    """Length of a row of `cols` codes: moe_int8_row_bytes."""
+    return int(lib.moe_int8_row_bytes(cols))
 
 
 def quantize_int8(src, q, scale, stream=None):

@@ -200,3 +200,13 @@ def test_cut_contractions_have_room_for_their_sums(dtype):
         assert B.grouped_workspace_bytes(s, CALL[call]) > 2 * planes * R * width * 4
     for call, K in ((LF, 64), (LI, 6960)):
         assert B.grouped_workspace_bytes(shape(call, R=238, K=K, N=512, E=2, dtype=dtype), CALL[call]) <= 1024
+
+
+def test_row_lengths_of_codes_are_the_library_s(monkeypatch):
+    """The binding has no rule of its own for them."""
+    B.int8_row_bytes.cache_clear()
+    monkeypatch.setattr(L, "moe_int8_row_bytes", lambda cols: 4 * cols)
+    assert B.int8_row_bytes(5) == 20
+    monkeypatch.undo()
+    B.int8_row_bytes.cache_clear()
+    assert B.int8_row_bytes(5) == 16
