@@ -10,7 +10,9 @@ namespace moe {
 // Bound by memory: each expert row is read once and its gradient written once, past the caches, which nothing will
 // read them from.  A workgroup per token (while the grid lasts) and part of its assignments: a token's gradient row is
 // read once for JB expert rows, whose loads are in flight together, eight elements per thread; the dot
-// products are summed per thread, then over the lanes of a wave, then over the waves in order.
+// products are summed per thread, then over the lanes of a wave, then over the waves in order.  Rows of fewer than 2048
+// elements leave lanes idle: 4096 tokens of 8 experts take 17 us for 64 columns, 25 for 256, 31 for 512, 35 for 1024 and 57 for
+// 2048, where the bytes are 2, 7, 14, 28 and 56 us.
 template <typename T>
 struct Piece {   // eight elements of a row of whole 16-byte chunks; fp32 rows may end after four
   u32x4 v[sizeof(T) / 2];

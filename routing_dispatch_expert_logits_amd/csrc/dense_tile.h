@@ -213,6 +213,15 @@ struct MmSlices {
 // [15:14]), no LDS operation (bits [11:8]), exports as they are.
 constexpr int mm_waitcnt(int n) { return (n & 0xF) | ((n >> 4) << 14) | (0x7 << 4); }
 
+// Passes of the epilogue: so many that W waves' sums of `tile` bytes find room in S stages of `stage` bytes.
+constexpr int mm_passes(int stage, int S, int tile, int W) {
+  int p = 1;
+  while (stage / (tile / p) * S < W) p *= 2;
+  return p;
+}
+template <int BM, int BN, int SB>
+constexpr int kMmStage = (BM + BN) * SB / 2;  // 16-bit words of a stage
+
 // Bound by the matrix cores where the device is full: 8192^3 in bf16 takes 819 us forward, 787 for
 // dx and 772 for dw (1.34, 1.40 and 1.43 PFLOP/s on 256 x 256 tiles; the library's products of
 // the three layouts run at 1.43, 1.34 and 1.18), 4096^3 in fp32 950 us (145 of the library's
@@ -228,19 +237,13 @@ constexpr int mm_waitcnt(int n) { return (n & 0xF) | ((n >> 4) << 14) | (0x7 << 
 // Steps of 128 bytes: all waves read a stage's operands and multiply at their own pace, one
 // barrier per step.  Steps of 64 bytes (8 waves, two per SIMD): the waves of a SIMD take turns,
 // one reading a step's operands while the other multiplies, a barrier after each turn.
-// Passes of the epilogue: so many that W waves' sums of `tile` bytes find room in S stages of `stage` bytes.
-constexpr int mm_passes(int stage, int S, int tile, int W) {
-  int p = 1;
-  while (stage / (tile / p) * S < W) p *= 2;
-  return p;
-}
-template <int BM, int BN, int SB>
-constexpr int kMmStage = (BM + BN) * SB / 2;  // 16-bit words of a stage
 //
 // T: the operands' type; O: that of what the epilogue reads and writes.  GROUPED: a wave with no row of the
 // product does not multiply (rows in groups of any number end inside most tiles), and outputs are written past the
-// caches, where the operands that other tiles read again stay (32768 rows of 128 experts, 2048 -> 768, both products of
-// a gated backward pass: 728 -> 708 us).  STREAM: so are B's loads, for weights that one tile reads.  HEIGHT: rows that the
+// caches, where the operands that other tiles read again stay (32768 rows of 128 experts, 2048 -> 768, a gated backward
+// pass: 642 us, 706 with ordinary stores).  A product that reads them next loses nothing by it: a gated product and the
+// linear one after it, 2048 / 768, take 393 us (429) for 32768 rows of 128 experts, 250 (251) for 4096 and 23 (23) for 64 of
+// 8; in integers, each after its codes, 302 (309), 163 (164) and 29 (29), and 8192 dense rows, 2048 / 7168, 371 (396).  STREAM: so are B's loads, for weights that one tile reads.  HEIGHT: rows that the
 // waves share, where A's tile in LDS is filled by whole instructions of every wave and has more (the rest reads 0); the
 // 16-row blocks without rows are not multiplied then.
 template <typename T, typename O, int BM, int BN, int WM, int WN, int S, int SB, int DB, bool A_COL, bool B_COL, bool PAIR,

@@ -230,6 +230,8 @@ constexpr GroupedTile kTilesDw[] = {{256, 256, 256, 1.75, 5.6, 1.75, 11.5},
                                     {64, 64, 512, 0.42, 3.0, 0.19, 2.5}};
 // Rows so few that an expert's mostly fit one tile: each weight is read once, in whole lines, and past the caches (2048
 // rows of 896 experts, 1024 -> 4096: 1191 us, 1299 on 64 x 64, which kept them; in integers 640, 763 and on 128 x 256 685).
+// The row counts are on the device, so the rule goes by their average: where one expert has most of the rows, its tiles read
+// its weights again each (8000 rows of one of 512 experts, 1024 -> 1024: 42 us, 25 as rows of one expert; in integers 36, 26).
 constexpr GroupedTile kStreamTile = {64, 128, 512};
 constexpr int kStreamRows = 16;   // an expert's, on average
 
@@ -250,10 +252,12 @@ static double mean_tiles(double rows, int bm) {
   return tiles;
 }
 
-// R rows of E experts by their N columns.  Products whose 64 x 64 tiles are too few for the device are cut along the
+// R rows of E experts by their N columns, spread evenly as far as the host knows (200 rows of one of 64 experts, 4096 -> 1024,
+// are not cut for it: 32 us, 13 as rows of one expert).  Products whose 64 x 64 tiles are too few for the device are cut along the
 // contraction, at least 4 steps a slice; the slices' sums are written and read again, and joined by a launch of their
 // own, at 4 us and 5 TB/s.  Whole and cut: 238 rows of 3 experts, 6960 -> 512, 34.1 and 14.8 us; 100 of 4, 2048 -> 768,
-// 11.4 and 9.4; dx and dw of 2 fp32 rows of 3, 192 -> 3328, 64.5 and 13.9.  Integer products are not cut: their sums are exact.
+// 11.4 and 9.4; dx and dw of 2 fp32 rows of 3, 192 -> 3328, 64.5 and 13.9.  Integer products are left whole (256 rows of one
+// expert, 7168 -> 2048: 23 us, of which the codes are 5).
 static GroupedTile tile_of(GroupedType t, int R, int E, int N, int K, int segs, bool pair, bool b_col) {
   if (t != GROUPED_F32 && !b_col && R <= (int64_t)kStreamRows * E && (int64_t)(R < E ? R : E) * ceil_div(N, pair ? 64 : 128) >= 512) return kStreamTile;
   const double experts = R < E ? R : E, steps = ceil_div(K, t == GROUPED_INT8 ? 128 : t == GROUPED_BF16 ? 64 : 32) * segs;
@@ -391,7 +395,9 @@ hipError_t launch_grouped(const DenseJob& j, const DenseEpi& e, GroupedType t, b
 }
 
 // Tile of the weight gradients: as many rows for every expert (32768 rows of 128, 2048 -> 768 gated: 331 us on 256 x 256, 365
-// on 128 x 256).
+// on 128 x 256).  Their contraction is not cut: few experts with small weights and many rows have too few tiles for the device,
+// each of which walks all rows of its expert (fp32, 32768 rows of one, 64 -> 64: one tile, 629 us; 14922 of 2, 2317 -> 64: 191;
+// bf16, 20000 of one, 256 -> 192: 92; 8000 of one of 64, 512 -> 512: 136).
 static const GroupedTile& dw_tile_of(const DenseJob& j, GroupedType t, const Groups& g) {
   if (t == GROUPED_F32) return kTilesDw[2];
   const double steps = (g.R / (double)g.E / 64 + 0.5) * j.segs;

@@ -30,7 +30,10 @@ static void go(const DenseJob& j, const DenseEpi& e, hipStream_t st) {
 // Tile by estimated time, from what a kernel takes per round of `at_once` workgroups: us per contraction step of 128
 // bytes and besides, measured (MI355X).  8192 x 8192 x 8192 / 8192 x 2048 x 7168 with a residual / 2048 x 4096 x 4096 /
 // 512 x 4096 x 4096 take 453 / 157 / 52 / 47 us on 256 x 256 (2.43 POP/s; the library's largest is 2.13), 532 / 177 / 39 / 33 on
-// 256 x 128, 812 / 272 / 58 / 17 on 64 x 64.
+// 256 x 128, 812 / 272 / 58 / 17 on 64 x 64.  All of it with bf16 outputs.  With fp32 ones the linear product's 256 x 256 tile
+// holds 128 registers of residual ahead and spills 300, also where there is none: with the codes, 8192 x 2048 -> 7168 takes 210 us
+// (with a residual 264) where no 256 x 256 tiles would take 190 (229), 8192 x 7168 -> 2048 182 (190) and 189 (200),
+// 4096 x 4096 -> 4096 103 (114) and 104 (117), 8192 x 512 -> 2048 52 (56) and 51 (57).
 struct Int8Tile {
   int bm, bn, at_once;
   double step, fixed;
