@@ -243,9 +243,10 @@ constexpr int kMmStage = (BM + BN) * SB / 2;  // 16-bit words of a stage
 // caches, where the operands that other tiles read again stay (32768 rows of 128 experts, 2048 -> 768, a gated backward
 // pass: 642 us, 706 with ordinary stores).  A product that reads them next loses nothing by it: a gated product and the
 // linear one after it, 2048 / 768, take 393 us (429) for 32768 rows of 128 experts, 250 (251) for 4096 and 23 (23) for 64 of
-// 8; in integers, each after its codes, 302 (309), 163 (164) and 29 (29), and 8192 dense rows, 2048 / 7168, 371 (396).  STREAM: so are B's loads, for weights that one tile reads.  HEIGHT: rows that the
-// waves share, where A's tile in LDS is filled by whole instructions of every wave and has more (the rest reads 0); the
-// 16-row blocks without rows are not multiplied then.
+// 8; in integers, each after its codes, 302 (309), 163 (164) and 29 (29), and 8192 dense rows, 2048 / 7168, 371 (396).
+// STREAM: past the caches go B's loads too, for weights that one tile reads.  HEIGHT: rows that the waves share, where A's
+// tile in LDS is filled by whole instructions of every wave and has more (the rest reads 0); the 16-row blocks without rows
+// are not multiplied then.
 template <typename T, typename O, int BM, int BN, int WM, int WN, int S, int SB, int DB, bool A_COL, bool B_COL, bool PAIR,
           int KIND, bool GROUPED = false, bool STREAM = false, int HEIGHT = BM>
 __device__ __forceinline__ void mm_body(const DenseJob& j, const DenseEpi& e, const MmSlices& sl, const MmWhere& w,
