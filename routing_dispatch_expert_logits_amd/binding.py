@@ -485,10 +485,14 @@ def combine_backward(dout, y_perm, token_row, topk_w, dy_perm, dtopk_w, out_dtyp
 # ---- products in 8-bit integers with a scale for each token and channel
 
 
-@functools.lru_cache(maxsize=1024)   # a call into the library takes longer than the checks that ask
+@functools.lru_cache(maxsize=1024)   # by the number alone: a call into the library takes longer than the checks that ask
+def _row_bytes(cols: int) -> int:
+    return int(lib.moe_int8_row_bytes(cols))
+
+
 def int8_row_bytes(cols: int) -> int:
     """Length of a row of `cols` codes: moe_int8_row_bytes."""
-    return int(lib.moe_int8_row_bytes(int(cols)))
+    return _row_bytes(int(cols))
 
 
 def quantize_int8(src, q, scale, stream=None):

@@ -204,9 +204,11 @@ def test_cut_contractions_have_room_for_their_sums(dtype):
 
 def test_row_lengths_of_codes_are_the_library_s(monkeypatch):
     """The binding has no rule of its own for them."""
-    B.int8_row_bytes.cache_clear()
+    B._row_bytes.cache_clear()
     monkeypatch.setattr(L, "moe_int8_row_bytes", lambda cols: 4 * cols)
     assert B.int8_row_bytes(5) == 20
     monkeypatch.undo()
-    B.int8_row_bytes.cache_clear()
-    assert B.int8_row_bytes(5) == B.int8_row_bytes(torch.tensor(5)) == 16   # any whole number
+    B._row_bytes.cache_clear()
+    n = torch.tensor(5)                         # any whole number, by its value
+    assert B.int8_row_bytes(5) == B.int8_row_bytes(n) == 16
+    assert B.int8_row_bytes(n.fill_(40)) == 48
